@@ -53,7 +53,8 @@ typedef enum {
     EXL3_ERR_DEVICE = 6     /* no sm_100-family device / device status set */
 } exl3_status;
 
-typedef enum { EXL3_F16 = 0, EXL3_BF16 = 1 } exl3_dtype;
+/* EXL3_E4M3 is a type of a key/value cache only (exl3_kv_cache). */
+typedef enum { EXL3_F16 = 0, EXL3_BF16 = 1, EXL3_E4M3 = 2 } exl3_dtype;
 
 /* Kernel path for the expert GEMMs.  AUTO picks the grouped GEMV for
  * decode-sized steps (few tokens per expert) and the tcgen05 grouped GEMM
@@ -296,6 +297,141 @@ exl3_status exl3_quantize_rows_e4m3(const float *a, int rows, int n, uint8_t *q,
  * process; a forward run with it gives an unspecified output.  Not thread
  * safe.  Errors: EXL3_ERR_ARG for values outside these ranges. */
 exl3_status exl3_test_set_wait_fault(int kernel, int ks, long long budget_cycles);
+
+/* ------------------------------------------------------------------------
+ * Attention over a paged key/value cache: the other half of the decoder layer
+ * that the MoE layer belongs to.  The pages have no counterpart; the three
+ * operators follow their formulas below.
+ *
+ * The device status word of these calls is sticky: kernels only set bits in
+ * it, so one word can serve every layer of a step.  The caller zeroes it once
+ * (the first 4 bytes of the attention workspace, or the word given to
+ * exl3_kv_append) and reads it with exl3_get_device_status.  Bits:
+ *   1  a page id outside [0, num_pages): the page's keys count as absent, an
+ *      append to it is skipped
+ *   2  an inconsistent batch: cu_q not ascending or past T, a length outside
+ *      [0, max_pages * page_size], an append before position 0.  A sequence
+ *      whose cu_q is inconsistent is left out; a length is clamped
+ *   4  a bounded wait ran out (outputs are unspecified)
+ */
+
+/* A paged cache: channel c of kv head h of the token in place i of page p is
+ * element p*page_stride + i*token_stride + h*head_stride + c of k and of v. */
+typedef struct {
+    void *k, *v;            /* device, 16-byte aligned */
+    int dtype;              /* exl3_dtype: the activations' type, or EXL3_E4M3 */
+    int num_pages;
+    int page_size;          /* tokens per page, a multiple of 16, at most 4096 */
+    int kv_heads;
+    int head_dim;
+    int64_t page_stride, token_stride, head_stride; /* elements, multiples of 16 bytes */
+    const float *k_scale;   /* device fp32 [kv_heads] or NULL (1): with EXL3_E4M3 a stored */
+    const float *v_scale;   /*   value x stands for x * scale; NULL with the other types */
+} exl3_kv_cache;
+
+/* The sequences of one step.  Sequence b has the new tokens cu_q[b] ..
+ * cu_q[b+1]-1 of the step (rows of q, k, v, out) and seq_lens[b] tokens in
+ * all, the new ones last: new token i of q_len stands at position
+ * seq_len - q_len + i.  Position p is in place p % page_size of page
+ * block_table[b*table_stride + p / page_size].  Table entries past a
+ * sequence's length are never used.  Rows past cu_q[num_seqs] are left alone
+ * (padding of a captured graph). */
+typedef struct {
+    int num_seqs;               /* 0 .. 65535 */
+    int max_q;                  /* the most new tokens of a sequence (a hint: it only picks
+                                   the kernel, results do not depend on it) */
+    int max_pages;              /* entries per row of the table */
+    int64_t table_stride;       /* elements */
+    const int32_t *cu_q;        /* device [num_seqs + 1] */
+    const int32_t *seq_lens;    /* device [num_seqs] */
+    const int32_t *block_table; /* device [num_seqs][max_pages] */
+} exl3_kv_batch;
+
+/* Head vectors of T tokens: channel c of head h of token t is element
+ * t*token_stride + h*head_stride + c of x and, where there is an out, element
+ * t*out_token_stride + h*out_head_stride + c of out.  out may be x itself
+ * (same strides), and may not overlap it otherwise. */
+typedef struct {
+    const void *x;              /* device, 16-byte aligned */
+    void *out;                  /* device, 16-byte aligned; unused where the cache takes them */
+    const void *weight;         /* device [head_dim], activations' type, 16-byte aligned: RMS
+                                   norm of every head vector times this; NULL: no norm */
+    int heads;
+    int64_t token_stride, head_stride;         /* elements, multiples of 8 */
+    int64_t out_token_stride, out_head_stride; /* elements, multiples of 8 */
+} exl3_heads;
+
+/* Rotary positions: pair i of the first rotary_dim channels turns by
+ * position * inv_freq[i] radians, (a, b) -> (a cos - b sin, a sin + b cos).
+ * Pair i is (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved.  The
+ * angle is kept as a 64-bit fraction of a turn, so far positions lose
+ * nothing.  0 <= inv_freq < 64 (radians per position). */
+typedef struct {
+    const double *inv_freq;     /* device [rotary_dim / 2] */
+    int rotary_dim;             /* a multiple of 16, at most head_dim */
+    int interleaved;            /* 0 or 1 */
+} exl3_rope;
+
+/* y = rotate(x / sqrt(mean(x^2) + eps) * weight), fp32 arithmetic, rounded
+ * once, for every query head and (k not NULL) every key head of T tokens.
+ *   positions  device int32 [T], may be negative
+ *   rope       NULL: no rotation (positions unused)
+ * head_dim a multiple of 8, at most 256.  Errors: EXL3_ERR_ARG (null or
+ * misaligned pointers, strides not multiples of 8, bad enum), EXL3_ERR_SHAPE
+ * (T < 0, heads < 1, head_dim or rotary_dim outside the above). */
+exl3_status exl3_qk_norm_rope(const exl3_heads *q, const exl3_heads *k, exl3_dtype dt, int T,
+                              int head_dim, const int32_t *positions, const exl3_rope *rope,
+                              float eps, void *stream);
+
+/* The new tokens' keys and values go to the cache: keys normed (k->weight)
+ * and rotated as in exl3_qk_norm_rope on the way, values as they are.  With
+ * q, the query heads are normed and rotated to q->out in the same launch.
+ * Everything is rounded once, from fp32; to E4M3 as
+ * E4M3_RNE(clamp(x / scale, -448, 448)), NaN staying NaN.
+ *   positions  device int32 [T] of the rotation, or NULL: the positions in the
+ *              sequence (where the token is stored never depends on it)
+ *   status     device int32, sticky (see above)
+ * k->out, v->out, v->weight are not used.  k and v have cache->kv_heads heads.
+ * Appending a token again overwrites it.  Errors: those of exl3_qk_norm_rope
+ * and, for cache and batch, EXL3_ERR_ARG (null or misaligned pointers,
+ * strides, a dtype neither dt nor EXL3_E4M3, scales without EXL3_E4M3) and
+ * EXL3_ERR_SHAPE (sizes outside the ranges stated there). */
+exl3_status exl3_kv_append(const exl3_kv_cache *cache, const exl3_kv_batch *batch,
+                           const exl3_heads *q, const exl3_heads *k, const exl3_heads *v,
+                           exl3_dtype dt, int T, const exl3_rope *rope, const int32_t *positions,
+                           float eps, int32_t *status, void *stream);
+
+/* Bytes of workspace exl3_paged_attention needs for T new tokens of up to
+ * num_seqs sequences. */
+size_t exl3_paged_attention_workspace_size(int T, int heads, int kv_heads, int head_dim,
+                                           int num_seqs);
+
+/* Attention of the new tokens over the cache, which already holds them:
+ *   out_t = sum_p softmax_p(scale * q_t . k_p) v_p
+ * over the positions p of t's sequence that t at position P sees: p <= P
+ * when causal (every p otherwise), p < seq_len, and p > P - window when
+ * window > 0 (requires causal).  Query head h reads kv head
+ * h / (heads / kv_heads).  A token that sees nothing gets out = 0 and
+ * lse = -inf.  What a token does not see (later tokens, keys before its
+ * window, places past the sequence's length) has no effect on it, NaN
+ * included.
+ *   q      device, element t*q_token_stride + h*q_head_stride + c, strides
+ *          multiples of 8
+ *   out    device [T][heads][head_dim] in dt; may not overlap q
+ *   lse    device fp32 [T][heads] or NULL: natural log of the sum of
+ *          exp(scale * q . k)
+ *   path   EXL3_PATH_AUTO, or a fixed kernel: 1 warp-level MMA (few rows),
+ *          2 tcgen05 (many rows)
+ * head_dim 64 or 128, heads a multiple of kv_heads.  Scores, the running
+ * maximum and sum and the output are fp32; softmax terms are rounded to the
+ * 16-bit type of the products (dt; fp16 with an E4M3 cache) before they meet
+ * the values.  Errors: as exl3_kv_append, EXL3_ERR_ARG for scale not finite
+ * and positive, window < 0 or without causal, and EXL3_ERR_WORKSPACE. */
+exl3_status exl3_paged_attention(const exl3_kv_cache *cache, const exl3_kv_batch *batch,
+                                 const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                 exl3_dtype dt, int T, int heads, float scale, int causal,
+                                 int window, void *out, float *lse, int path, void *ws,
+                                 size_t ws_bytes, void *stream);
 
 const char *exl3_status_string(exl3_status s);
 

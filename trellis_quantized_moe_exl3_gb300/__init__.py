@@ -12,7 +12,13 @@ def _api():
     return api
 
 
+_ATTENTION = ("PagedKVCache", "PagedBatch", "qk_norm_rope", "kv_append", "paged_attention")
+
+
 def __getattr__(name):
+    if name in _ATTENTION:
+        from . import attention
+        return getattr(attention, name)
     if name in ("Layer", "route", "rmsnorm", "device_status"):
         return getattr(_api(), name)
     raise AttributeError(name)

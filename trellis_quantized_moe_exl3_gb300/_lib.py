@@ -17,7 +17,7 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 
 EXL3_OK, EXL3_ERR_ARG, EXL3_ERR_SHAPE, EXL3_ERR_K, EXL3_ERR_WORKSPACE, EXL3_ERR_CUDA, \
     EXL3_ERR_DEVICE = range(7)
-EXL3_F16, EXL3_BF16 = 0, 1
+EXL3_F16, EXL3_BF16, EXL3_E4M3 = 0, 1, 2
 EXL3_PATH_AUTO, EXL3_PATH_GEMV, EXL3_PATH_GEMM = 0, 1, 2
 EXL3_NUM_STAGE_EVENTS = 8
 STAGE_NAMES = ("route", "gather", "gate_up", "down_prep", "down", "shared", "combine")
@@ -32,6 +32,38 @@ class LayerDesc(ctypes.Structure):
         ("hadamard", ctypes.c_int), ("shared_coded", ctypes.c_int),
         ("expert_K", ctypes.c_void_p), ("act_fp8", ctypes.c_int),
     ]
+
+
+class KVCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class KVBatch(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int), ("max_q", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("table_stride", ctypes.c_int64), ("cu_q", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+    ]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("heads", ctypes.c_int), ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+    ]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
 
 
 class Exl3Error(RuntimeError):
@@ -93,6 +125,15 @@ def lib():
     L.exl3_quantize_rows_e4m3.restype = i
     L.exl3_test_set_wait_fault.argtypes = [i, i, ctypes.c_longlong]
     L.exl3_test_set_wait_fault.restype = i
+    f, i64 = ctypes.c_float, ctypes.c_int64
+    L.exl3_qk_norm_rope.argtypes = [vp, vp, i, i, i, vp, vp, f, vp]
+    L.exl3_qk_norm_rope.restype = i
+    L.exl3_kv_append.argtypes = [vp, vp, vp, vp, vp, i, i, vp, vp, f, vp, vp]
+    L.exl3_kv_append.restype = i
+    L.exl3_paged_attention_workspace_size.argtypes = [i, i, i, i, i]
+    L.exl3_paged_attention_workspace_size.restype = sz
+    L.exl3_paged_attention.argtypes = [vp, vp, vp, i64, i64, i, i, i, f, i, i, vp, vp, i, vp, sz, vp]
+    L.exl3_paged_attention.restype = i
     L.exl3_status_string.argtypes = [i]
     L.exl3_status_string.restype = ctypes.c_char_p
     _lib = L

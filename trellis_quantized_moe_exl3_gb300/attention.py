@@ -1,0 +1,233 @@
+"""Attention over a paged key/value cache: Python API over the C ABI.
+
+    cache = PagedKVCache(k, v)                              # [pages, page_size, kv_heads, dim]
+    batch = PagedBatch(cu_q, seq_lens, block_table, max_q)  # the step's sequences
+    q = kv_append(cache, batch, k_new, v_new, inv_freq=f, k_weight=wk, q=q_new, q_weight=wq)
+    out = paged_attention(q, cache, batch)                  # [tokens, heads, dim]
+
+``qk_norm_rope`` is the norm and rotation alone, for keys that go to no cache.
+PyTorch supplies device memory and streams only; every call is one or two
+kernels of the library on the current stream, allocates nothing but its
+outputs, and can be captured in a CUDA graph.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import check
+from .api import _dtype_code, _ptr, _stream
+
+_ACT = (torch.float16, torch.bfloat16)
+_CODES = {torch.float16: _lib.EXL3_F16, torch.bfloat16: _lib.EXL3_BF16,
+          torch.float8_e4m3fn: _lib.EXL3_E4M3}
+
+
+def _cuda(t, name, dtype):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+def _dense(t, name, dtype, shape):
+    _cuda(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+class PagedKVCache:
+    """A paged cache: k and v [pages, page_size, kv_heads, head_dim], fp16, bf16
+    or float8_e4m3fn, channels contiguous, the other strides free but alike (a
+    permuted view of [pages, kv_heads, page_size, head_dim] works).  k_scale,
+    v_scale: fp32 [kv_heads], E4M3 only; a stored x stands for x * scale.
+    page_size is a multiple of 16.  The tensors must stay alive as long as the
+    handle.  `ws` is the workspace of its calls (grown as needed), whose first
+    word is the sticky device status: see `device_status`."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        _cuda(k, "k", tuple(_CODES))
+        _cuda(v, "v", k.dtype)
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError("k and v must be [pages, page_size, kv_heads, head_dim] with the "
+                             "same shape and strides")
+        if k.numel() and k.stride(3) != 1 and k.shape[3] > 1:
+            raise ValueError("the channels of k and v must be contiguous")
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                _dense(t, n, torch.float32, (k.shape[2],))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.kv_heads, self.head_dim, self.dtype = k.shape[2], k.shape[3], k.dtype
+        d = _lib.KVCache()
+        d.k, d.v, d.dtype = k.data_ptr(), v.data_ptr(), _CODES[k.dtype]
+        d.num_pages, d.page_size, d.kv_heads, d.head_dim = k.shape
+        d.page_stride, d.token_stride, d.head_stride = _strides(k)
+        d.k_scale = k_scale.data_ptr() if k_scale is not None else None
+        d.v_scale = v_scale.data_ptr() if v_scale is not None else None
+        self._d, self._ref = d, ctypes.byref(d)
+        self.ws = torch.zeros(256, dtype=torch.uint8, device=k.device)
+        self._need = {}
+
+    def workspace_size(self, tokens: int, heads: int, num_seqs: int) -> int:
+        return int(_lib.lib().exl3_paged_attention_workspace_size(
+            tokens, heads, self.kv_heads, self.head_dim, num_seqs))
+
+    def workspace(self, tokens: int, heads: int, num_seqs: int) -> torch.Tensor:
+        """The handle's workspace, grown to hold a call of this size (the first
+        call of a size inside a graph capture must not be the one that grows it)."""
+        key = (tokens, heads, num_seqs)
+        n = self._need.get(key)
+        if n is None:
+            n = self._need[key] = self.workspace_size(*key)
+        if self.ws.numel() < n:
+            ws = torch.zeros(n, dtype=torch.uint8, device=self.ws.device)
+            ws[:4].copy_(self.ws[:4])
+            self.ws = ws
+        return self.ws
+
+
+class PagedBatch:
+    """The sequences of one step.  Sequence b has the new tokens cu_q[b] ..
+    cu_q[b+1]-1 and seq_lens[b] tokens in all, the new ones last, so new token
+    i of n stands at position seq_lens[b] - n + i; position p is in place
+    p % page_size of page block_table[b, p // page_size].  int32 CUDA tensors
+    [B + 1], [B], [B, max_pages]; their values may change between calls (they
+    are read on the device).  max_q: the most new tokens of a sequence, a hint
+    that picks the kernel."""
+
+    def __init__(self, cu_q, seq_lens, block_table, max_q: int):
+        n = seq_lens.shape[0]
+        _dense(cu_q, "cu_q", torch.int32, (n + 1,))
+        _dense(seq_lens, "seq_lens", torch.int32, (n,))
+        _cuda(block_table, "block_table", torch.int32)
+        if block_table.dim() != 2 or block_table.shape[0] != n or \
+                (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError("block_table must be [sequences, pages] with contiguous rows")
+        self.cu_q, self.seq_lens, self.block_table = cu_q, seq_lens, block_table
+        self.num_seqs, self.max_q = n, int(max_q)
+        d = _lib.KVBatch()
+        d.num_seqs, d.max_q, d.max_pages = n, self.max_q, block_table.shape[1]
+        d.table_stride = block_table.stride(0)
+        d.cu_q, d.seq_lens = cu_q.data_ptr(), seq_lens.data_ptr()
+        d.block_table = block_table.data_ptr()
+        self._d, self._ref = d, ctypes.byref(d)
+
+
+def _strides(t):
+    """All strides but the last, 0 where a dimension of one leaves them open."""
+    return [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+
+
+def _heads(x, name, dim, weight=None, out=None):
+    """exl3_heads of a [tokens, heads, dim] tensor."""
+    _cuda(x, name, _ACT)
+    if x.dim() != 3 or x.shape[2] != dim or (x.stride(2) != 1 and x.numel()):
+        raise ValueError(f"{name} must be [tokens, heads, {dim}] with contiguous channels")
+    h = _lib.Heads()
+    h.x, h.heads = x.data_ptr(), x.shape[1]
+    h.token_stride, h.head_stride = _strides(x)
+    if weight is not None:
+        _dense(weight, f"{name}'s weight", x.dtype, (dim,))
+        h.weight = weight.data_ptr()
+    if out is not None:
+        _cuda(out, f"{name}'s out", x.dtype)
+        if out.shape != x.shape or (out.stride(2) != 1 and out.numel()):
+            raise ValueError(f"{name}'s out must be {tuple(x.shape)} with contiguous channels")
+        h.out = out.data_ptr()
+        h.out_token_stride, h.out_head_stride = _strides(out)
+    return h
+
+
+def _rope(inv_freq, interleaved):
+    if inv_freq is None:
+        return None
+    _cuda(inv_freq, "inv_freq", torch.float64)
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous [rotary_dim / 2] tensor")
+    return ctypes.byref(_lib.Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(bool(interleaved))))
+
+
+def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """(q, k) with every head vector RMS normed (where there is a weight) and
+    rotated by its token's position (where there is an inv_freq).
+
+    q [tokens, heads, dim] and k [tokens, kv_heads, dim] (or None), fp16 or
+    bf16, any strides that are multiples of 8 elements; positions int32
+    [tokens]; inv_freq float64 [rotary_dim / 2], radians per position of pair
+    (i, i + rotary_dim/2) of the first rotary_dim channels, or (2i, 2i + 1)
+    when interleaved.  q_out and k_out may be q and k."""
+    dim = q.shape[2]
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    hq = _heads(q, "q", dim, q_weight, q_out)
+    hk = None
+    if k is not None:
+        if k.dtype != q.dtype or k.shape[0] != q.shape[0]:
+            raise ValueError("q and k must have the same dtype and tokens")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        hk = ctypes.byref(_heads(k, "k", dim, k_weight, k_out))
+    if positions is not None:
+        _dense(positions, "positions", torch.int32, (q.shape[0],))
+    check(_lib.lib().exl3_qk_norm_rope(ctypes.byref(hq), hk, _dtype_code(q.dtype), q.shape[0], dim,
+                                       _ptr(positions), _rope(inv_freq, interleaved), eps,
+                                       _stream(stream)), "exl3_qk_norm_rope")
+    return q_out, k_out
+
+
+def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_weight=None, q=None,
+              q_weight=None, q_out=None, positions=None, eps: float = 1e-6,
+              interleaved: bool = False, stream=None):
+    """Writes the new tokens' keys (normed and rotated as by qk_norm_rope) and
+    values to the cache; with q, returns the normed and rotated queries, from
+    the same launch.  positions: those of the rotation (default: the positions
+    in the sequence).  A value past the E4M3 range saturates."""
+    if k.dtype != v.dtype or k.shape != v.shape or k.shape[1] != cache.kv_heads:
+        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
+    T, dim = k.shape[0], cache.head_dim
+    hk, hv, hq = _heads(k, "k", dim, k_weight), _heads(v, "v", dim), None
+    if q is not None:
+        if q.dtype != k.dtype or q.shape[0] != T:
+            raise ValueError("q and k must have the same dtype and tokens")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        hq = ctypes.byref(_heads(q, "q", dim, q_weight, q_out))
+    if positions is not None:
+        _dense(positions, "positions", torch.int32, (T,))
+    check(_lib.lib().exl3_kv_append(cache._ref, batch._ref, hq, ctypes.byref(hk), ctypes.byref(hv),
+                                    _dtype_code(k.dtype), T, _rope(inv_freq, interleaved),
+                                    _ptr(positions), eps, _ptr(cache.ws), _stream(stream)),
+          "exl3_kv_append")
+    return q_out
+
+
+def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causal: bool = True,
+                    window: int = 0, out=None, return_lse: bool = False, path: int = 0, ws=None,
+                    stream=None):
+    """Attention of the new tokens q [tokens, heads, head_dim] over the cache,
+    which already holds them.  A token at position P sees the positions p <= P
+    of its sequence (all of them when causal is false), and p > P - window when
+    window > 0.  scale defaults to head_dim ** -0.5.  Returns out [tokens,
+    heads, head_dim], or (out, lse fp32 [tokens, heads]) with return_lse; a
+    token that sees nothing gets out 0 and lse -inf."""
+    _cuda(q, "q", _ACT)
+    T, heads, dim = q.shape
+    if dim != cache.head_dim or (q.stride(2) != 1 and q.numel()):
+        raise ValueError(f"q must be [tokens, heads, {cache.head_dim}] with contiguous channels")
+    if out is None:
+        out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
+    else:
+        _dense(out, "out", q.dtype, (T, heads, dim))
+    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    if ws is None:
+        ws = cache.workspace(T, heads, batch.num_seqs)
+    check(_lib.lib().exl3_paged_attention(
+        cache._ref, batch._ref, _ptr(q), *_strides(q), _dtype_code(q.dtype), T, heads,
+        dim ** -0.5 if scale is None else scale, int(bool(causal)), int(window), _ptr(out),
+        _ptr(lse), int(path), _ptr(ws), ws.numel(), _stream(stream)), "exl3_paged_attention")
+    return (out, lse) if return_lse else out
