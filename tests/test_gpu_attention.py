@@ -302,7 +302,7 @@ def setup(c, seed=0, layout="NHD", pad=2):
     return cache, step, q
 
 
-PATHS = [1]
+PATHS = [1, 2]
 
 
 @pytest.mark.parametrize("path", PATHS)

@@ -7,6 +7,7 @@ using namespace exl3;
 
 namespace {
 
+constexpr int kRowsMost = 32;  // rows of a sequence that attn_rows takes
 constexpr size_t kHead = 256;  // bytes before the scratch: the status word
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -167,7 +168,9 @@ size_t exl3_paged_attention_workspace_size(int T, int heads, int kv_heads, int h
   if (T < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads ||
       (head_dim != 64 && head_dim != 128) || num_seqs < 0 || num_seqs > kMaxSeqs)
     return 0;
-  return kHead + attn_rows_scratch_bytes(head_dim);
+  const size_t a = attn_rows_scratch_bytes(head_dim);
+  const size_t b = attn_tiles_scratch_bytes((long long)T * (heads / kv_heads), num_seqs, head_dim);
+  return kHead + (a > b ? a : b);
 }
 
 exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch* batch,
@@ -211,8 +214,14 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   p.dim = cache->head_dim;
   p.status = static_cast<int32_t*>(ws);
   p.scratch = static_cast<uint8_t*>(ws) + kHead;
-  return launch_attn_rows(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXL3_OK
-                                                                              : EXL3_ERR_CUDA;
+  // Few rows per sequence and kv head: the cache's bytes bound the step.
+  bool tiles = (long long)batch->max_q * p.group > kRowsMost;
+  if (path != EXL3_PATH_AUTO) tiles = path == EXL3_PATH_GEMM;
+  if (tiles && !attn_tiles_can(p)) tiles = false;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return (tiles ? launch_attn_tiles(p, st) : launch_attn_rows(p, st)) == cudaSuccess
+             ? EXL3_OK
+             : EXL3_ERR_CUDA;
 }
 
 }  // extern "C"
