@@ -315,6 +315,8 @@ exl3_status exl3_test_set_wait_fault(int kernel, int ks, long long budget_cycles
  *   4  a bounded wait ran out (outputs are unspecified)
  */
 
+#define EXL3_ATTENTION_HEAD_BYTES 4096
+
 /* A paged cache: channel c of kv head h of the token in place i of page p is
  * element p*page_stride + i*token_stride + h*head_stride + c of k and of v. */
 typedef struct {

@@ -18,7 +18,8 @@ _ATTENTION = ("PagedKVCache", "PagedBatch", "qk_norm_rope", "kv_append", "paged_
 def __getattr__(name):
     if name in _ATTENTION:
         from . import attention
-        return getattr(attention, name)
+        value = globals()[name] = getattr(attention, name)  # found directly from now on
+        return value
     if name in ("Layer", "route", "rmsnorm", "device_status"):
         return getattr(_api(), name)
     raise AttributeError(name)

@@ -20,6 +20,7 @@ EXL3_OK, EXL3_ERR_ARG, EXL3_ERR_SHAPE, EXL3_ERR_K, EXL3_ERR_WORKSPACE, EXL3_ERR_
 EXL3_F16, EXL3_BF16, EXL3_E4M3 = 0, 1, 2
 EXL3_PATH_AUTO, EXL3_PATH_GEMV, EXL3_PATH_GEMM = 0, 1, 2
 EXL3_NUM_STAGE_EVENTS = 8
+EXL3_ATTENTION_HEAD_BYTES = 4096
 STAGE_NAMES = ("route", "gather", "gate_up", "down_prep", "down", "shared", "combine")
 
 

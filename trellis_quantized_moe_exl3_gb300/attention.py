@@ -13,29 +13,42 @@ outputs, and can be captured in a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
 from . import _lib
 from ._lib import check
-from .api import _dtype_code, _ptr, _stream
 
-_ACT = (torch.float16, torch.bfloat16)
+_ACT = {torch.float16: _lib.EXL3_F16, torch.bfloat16: _lib.EXL3_BF16}
 _CODES = {torch.float16: _lib.EXL3_F16, torch.bfloat16: _lib.EXL3_BF16,
           torch.float8_e4m3fn: _lib.EXL3_E4M3}
+
+
+# exl3_heads and exl3_rope as C lays them out.  Single-token calls last a few
+# microseconds on the GPU, so the call's own cost counts: the argument structs
+# are packed bytes, the stream is asked for by its raw handle.
+_HEADS = struct.Struct("@QQQiqqqq")
+_ROPE = struct.Struct("@Qii")
+assert _HEADS.size == ctypes.sizeof(_lib.Heads) and _ROPE.size == ctypes.sizeof(_lib.Rope)
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream(stream, t):
+    return _current_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _cuda(t, name, dtype):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype != dtype if isinstance(dtype, torch.dtype) else t.dtype not in dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
 
 
 def _dense(t, name, dtype, shape):
     _cuda(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
@@ -50,7 +63,7 @@ class PagedKVCache:
     word is the sticky device status: see `device_status`."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        _cuda(k, "k", tuple(_CODES))
+        _cuda(k, "k", _CODES)
         _cuda(v, "v", k.dtype)
         if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride():
             raise ValueError("k and v must be [pages, page_size, kv_heads, head_dim] with the "
@@ -69,7 +82,7 @@ class PagedKVCache:
         d.k_scale = k_scale.data_ptr() if k_scale is not None else None
         d.v_scale = v_scale.data_ptr() if v_scale is not None else None
         self._d, self._ref = d, ctypes.byref(d)
-        self.ws = torch.zeros(256, dtype=torch.uint8, device=k.device)
+        self.ws = torch.zeros(_lib.EXL3_ATTENTION_HEAD_BYTES, dtype=torch.uint8, device=k.device)
         self._need = {}
 
     def workspace_size(self, tokens: int, heads: int, num_seqs: int) -> int:
@@ -122,24 +135,30 @@ def _strides(t):
     return [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
 
 
+def _act(x, name, dim):
+    """Checks a [tokens, heads, dim] tensor; its token and head strides."""
+    code = _ACT.get(x.dtype)
+    if code is None or not x.is_cuda:
+        _cuda(x, name, _ACT)
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[2] != dim or (stride[2] != 1 and x.numel()):
+        raise ValueError(f"{name} must be [tokens, heads, {dim}] with contiguous channels")
+    return 0 if shape[0] == 1 else stride[0], 0 if shape[1] == 1 else stride[1]
+
+
 def _heads(x, name, dim, weight=None, out=None):
     """exl3_heads of a [tokens, heads, dim] tensor."""
-    _cuda(x, name, _ACT)
-    if x.dim() != 3 or x.shape[2] != dim or (x.stride(2) != 1 and x.numel()):
-        raise ValueError(f"{name} must be [tokens, heads, {dim}] with contiguous channels")
-    h = _lib.Heads()
-    h.x, h.heads = x.data_ptr(), x.shape[1]
-    h.token_stride, h.head_stride = _strides(x)
+    ts, hs = _act(x, name, dim)
+    o = ots = ohs = w = 0
     if weight is not None:
         _dense(weight, f"{name}'s weight", x.dtype, (dim,))
-        h.weight = weight.data_ptr()
+        w = weight.data_ptr()
     if out is not None:
-        _cuda(out, f"{name}'s out", x.dtype)
-        if out.shape != x.shape or (out.stride(2) != 1 and out.numel()):
-            raise ValueError(f"{name}'s out must be {tuple(x.shape)} with contiguous channels")
-        h.out = out.data_ptr()
-        h.out_token_stride, h.out_head_stride = _strides(out)
-    return h
+        if out.dtype != x.dtype or out.shape != x.shape:
+            raise ValueError(f"{name}'s out must be {tuple(x.shape)} {x.dtype}")
+        ots, ohs = _act(out, f"{name}'s out", dim)
+        o = out.data_ptr()
+    return _HEADS.pack(x.data_ptr(), o, w, x.shape[1], ts, hs, ots, ohs)
 
 
 def _rope(inv_freq, interleaved):
@@ -148,7 +167,7 @@ def _rope(inv_freq, interleaved):
     _cuda(inv_freq, "inv_freq", torch.float64)
     if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous [rotary_dim / 2] tensor")
-    return ctypes.byref(_lib.Rope(inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(bool(interleaved))))
+    return _ROPE.pack(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0)
 
 
 def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None,
@@ -161,22 +180,24 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     [tokens]; inv_freq float64 [rotary_dim / 2], radians per position of pair
     (i, i + rotary_dim/2) of the first rotary_dim channels, or (2i, 2i + 1)
     when interleaved.  q_out and k_out may be q and k."""
-    dim = q.shape[2]
+    T, _, dim = q.shape
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     hq = _heads(q, "q", dim, q_weight, q_out)
     hk = None
     if k is not None:
-        if k.dtype != q.dtype or k.shape[0] != q.shape[0]:
+        if k.dtype != q.dtype or k.shape[0] != T:
             raise ValueError("q and k must have the same dtype and tokens")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        hk = ctypes.byref(_heads(k, "k", dim, k_weight, k_out))
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        hk = _heads(k, "k", dim, k_weight, k_out)
+    pos = None
     if positions is not None:
-        _dense(positions, "positions", torch.int32, (q.shape[0],))
-    check(_lib.lib().exl3_qk_norm_rope(ctypes.byref(hq), hk, _dtype_code(q.dtype), q.shape[0], dim,
-                                       _ptr(positions), _rope(inv_freq, interleaved), eps,
-                                       _stream(stream)), "exl3_qk_norm_rope")
+        _dense(positions, "positions", torch.int32, (T,))
+        pos = positions.data_ptr()
+    check(_lib.lib().exl3_qk_norm_rope(hq, hk, _ACT[q.dtype], T, dim, pos,
+                                       _rope(inv_freq, interleaved), eps, _stream(stream, q)),
+          "exl3_qk_norm_rope")
     return q_out, k_out
 
 
@@ -195,14 +216,15 @@ def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_wei
         if q.dtype != k.dtype or q.shape[0] != T:
             raise ValueError("q and k must have the same dtype and tokens")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        hq = ctypes.byref(_heads(q, "q", dim, q_weight, q_out))
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        hq = _heads(q, "q", dim, q_weight, q_out)
+    pos = None
     if positions is not None:
         _dense(positions, "positions", torch.int32, (T,))
-    check(_lib.lib().exl3_kv_append(cache._ref, batch._ref, hq, ctypes.byref(hk), ctypes.byref(hv),
-                                    _dtype_code(k.dtype), T, _rope(inv_freq, interleaved),
-                                    _ptr(positions), eps, _ptr(cache.ws), _stream(stream)),
-          "exl3_kv_append")
+        pos = positions.data_ptr()
+    check(_lib.lib().exl3_kv_append(cache._ref, batch._ref, hq, hk, hv, _ACT[k.dtype], T,
+                                    _rope(inv_freq, interleaved), pos, eps, cache.ws.data_ptr(),
+                                    _stream(stream, k)), "exl3_kv_append")
     return q_out
 
 
@@ -215,19 +237,20 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
     window > 0.  scale defaults to head_dim ** -0.5.  Returns out [tokens,
     heads, head_dim], or (out, lse fp32 [tokens, heads]) with return_lse; a
     token that sees nothing gets out 0 and lse -inf."""
-    _cuda(q, "q", _ACT)
+    if not q.is_cuda:
+        _cuda(q, "q", _ACT)
+    ts, hs = _act(q, "q", cache.head_dim)
     T, heads, dim = q.shape
-    if dim != cache.head_dim or (q.stride(2) != 1 and q.numel()):
-        raise ValueError(f"q must be [tokens, heads, {cache.head_dim}] with contiguous channels")
     if out is None:
-        out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _dense(out, "out", q.dtype, (T, heads, dim))
     lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
     if ws is None:
         ws = cache.workspace(T, heads, batch.num_seqs)
     check(_lib.lib().exl3_paged_attention(
-        cache._ref, batch._ref, _ptr(q), *_strides(q), _dtype_code(q.dtype), T, heads,
-        dim ** -0.5 if scale is None else scale, int(bool(causal)), int(window), _ptr(out),
-        _ptr(lse), int(path), _ptr(ws), ws.numel(), _stream(stream)), "exl3_paged_attention")
+        cache._ref, batch._ref, q.data_ptr(), ts, hs, _ACT[q.dtype], T, heads,
+        dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), path, ws.data_ptr(), ws.numel(),
+        _stream(stream, q)), "exl3_paged_attention")
     return (out, lse) if return_lse else out

@@ -8,7 +8,8 @@ using namespace exl3;
 namespace {
 
 constexpr int kRowsMost = 32;  // rows of a sequence that attn_rows takes
-constexpr size_t kHead = 256;  // bytes before the scratch: the status word
+constexpr size_t kHead = EXL3_ATTENTION_HEAD_BYTES;  // status word, counters
+static_assert(256 + kRowsCounters * 4 <= kHead, "counters");
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool good(const void* p) { return p && aligned16(p); }
@@ -77,6 +78,7 @@ Cache cache_of(const exl3_kv_cache* c) {
   o.v = static_cast<const uint8_t*>(c->v);
   o.num_pages = c->num_pages;
   o.page_size = c->page_size;
+  o.page_shift = c->page_size & (c->page_size - 1) ? -1 : __builtin_ctz(c->page_size);
   o.page_bytes = c->page_stride * e;
   o.token_bytes = c->token_stride * e;
   o.head_bytes = c->head_stride * e;
@@ -113,6 +115,7 @@ exl3_status exl3_qk_norm_rope(const exl3_heads* q, const exl3_heads* k, exl3_dty
   p.bf16 = dt == EXL3_BF16;
   p.T = T;
   p.dim = head_dim;
+  p.inv_dim = 1.0f / (float)p.dim;
   p.positions = positions;
   if (rope) {
     p.inv_freq = rope->inv_freq;
@@ -149,6 +152,7 @@ exl3_status exl3_kv_append(const exl3_kv_cache* cache, const exl3_kv_batch* batc
   p.e4m3 = cache->dtype == EXL3_E4M3;
   p.T = T;
   p.dim = cache->head_dim;
+  p.inv_dim = 1.0f / (float)p.dim;
   p.positions = positions;
   if (rope) {
     p.inv_freq = rope->inv_freq;
@@ -213,6 +217,7 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   p.e4m3 = cache->dtype == EXL3_E4M3;
   p.dim = cache->head_dim;
   p.status = static_cast<int32_t*>(ws);
+  p.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
   p.scratch = static_cast<uint8_t*>(ws) + kHead;
   // Few rows per sequence and kv head: the cache's bytes bound the step.
   bool tiles = (long long)batch->max_q * p.group > kRowsMost;

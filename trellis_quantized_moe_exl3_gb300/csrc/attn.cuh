@@ -17,6 +17,7 @@ enum : int32_t { kStatusBadPage = 1, kStatusBadBatch = 2 };
 constexpr int kMaxSeqs = 65535;
 constexpr int kMaxPageSize = 4096;
 constexpr int kSms = 152;
+constexpr int kRowsCounters = 640;  // parts counters of attn_rows
 
 struct Batch {
   int num_seqs, max_q, max_pages, T;
@@ -56,6 +57,7 @@ struct Cache {
   const uint8_t* k;
   const uint8_t* v;
   int num_pages, page_size;
+  int page_shift;  // log2 of page_size, -1 if it is no power of two
   int64_t page_bytes, token_bytes, head_bytes;  // strides
   const float* k_scale;
   const float* v_scale;
@@ -76,7 +78,7 @@ struct NormRopeParams {
   const int32_t* positions;
   const double* inv_freq;
   int rot, inter;
-  float eps;
+  float eps, inv_dim;
   Cache cache;  // append
   Batch batch;
   int32_t* status;
@@ -96,6 +98,7 @@ struct AttnParams {
   int causal, window;
   int bf16, e4m3, dim;
   int32_t* status;
+  int32_t* counters;  // [kRowsCounters], zero between calls
   void* scratch;
 };
 size_t attn_rows_scratch_bytes(int dim);

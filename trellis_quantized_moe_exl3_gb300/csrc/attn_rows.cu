@@ -6,16 +6,22 @@
 //   when m grows; parts are joined by m and l.
 //
 // Rows.  The group = heads / kv_heads query heads of a kv head and the new
-// tokens are the rows of one matrix (row = token * group + head), 16 or 32 of
-// them per work unit, so a key is read once for all of them.
+// tokens are the rows of one matrix (row = token * group + head), 8, 16 or 32
+// of them per work unit, so a key is read once for all of them.  Both products
+// are formed transposed, S^T = K Q^T and O^T = V^T P^T: the rows are then the
+// MMA's N (8), not its M (16), so that 4 to 8 rows, the common case of
+// single-token steps, cost half the products and half the registers (32 fp32
+// of O per thread at head_dim 128), which leaves room for the warps that hide
+// the loads.
 //
 // Work.  A unit is (sequence, kv head, row chunk); its keys are counted in
 // granules of 64.  All units' granules form one line that is cut into equal
 // pieces, one per CTA, from the device-side lengths alone: ragged batches
 // balance, one long sequence fills the GPU, and nothing is planned on the
 // host.  A CTA whose piece holds a whole unit writes the output; parts of a
-// unit go to scratch (at most two per CTA) and attn_rows_join_kernel sums
-// them in order, so results do not depend on timing.
+// unit go to scratch (at most two per CTA), and the CTA that finishes the
+// unit's last part joins them in their order on the line, so that results do
+// not depend on timing.
 //
 // Inside a CTA the 4 warps take key tiles in turn, each with its own ring of
 // asynchronous copies, and meet only at the end of a unit.  Keys outside
@@ -37,28 +43,29 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
 constexpr int kGran = 64;            // keys per granule
-constexpr int kCtasPerSm = 2;
-constexpr int kGrid = kSms * kCtasPerSm;
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <int D_, int NQ_, int E8_, int BF_>
+template <int D_, int NB_, int E8_, int BF_>
 struct Cfg {
-  static constexpr int D = D_, NQ = NQ_, E8 = E8_, BF = BF_;
+  static constexpr int D = D_, NB = NB_, E8 = E8_, BF = BF_;
   static constexpr int RB = D * (E8 ? 1 : 2);       // bytes of a key row
   static constexpr int CPR = RB / 16;               // 16-byte chunks of it
-  static constexpr int KT = 4096 / RB;              // keys per tile: 4 KB of K, 4 KB of V
-  static constexpr int NT = KT / 8;                 // score tiles of 8 keys
-  static constexpr int SUB = KT / 16;               // 16-key groups (one page each)
+  static constexpr int kHalf = E8 ? 2048 : 4096;    // bytes of K (and of V) in a tile
+  static constexpr int KT = kHalf / RB;             // keys per tile, 16 or 32
+  static constexpr int MT = KT / 16;                // 16-key groups (one page each)
   static constexpr int RPI = 32 / CPR;              // rows per copy instruction
-  static constexpr int RT = 16 * NQ;                // rows of a unit
-  static constexpr int kStageBytes = 8192;
+  static constexpr int RT = 8 * NB;                 // rows of a unit
+  static constexpr int kStages = 3;
+  static constexpr int kStageBytes = 2 * kHalf;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int OS = D + 4;                  // floats per row of the join buffer
-  static constexpr int kSmem = kWarps * kWarpBytes + kWarps * RT * 8 + kWarps * kStages * 4 + 64;
+  static constexpr int kJoinBytes = RT * OS * 4;
+  static constexpr int kRing = kWarps * (kWarpBytes > kJoinBytes ? kWarpBytes : kJoinBytes);
+  static constexpr int kSmem = kRing + kWarps * RT * 8 + kWarps * kStages * 4 + 64;
+  static constexpr int kCtasPerSm = NB == 4 ? 2 : E8 ? (NB == 1 ? 4 : 3) : 2;
+  static constexpr int kGrid = kSms * kCtasPerSm;
 };
-static_assert(16 * 2 * (128 + 4) * 4 <= kStages * 8192, "join buffer fits a warp's ring");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -75,6 +82,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a));
 }
+// 8x8 transpose of 16-bit pairs over the warp
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -83,16 +96,16 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   return v;
 }
 template <int BF>
-__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                      uint32_t b1) {
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
   if (BF)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+    mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
 }
 template <int BF>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -127,12 +140,12 @@ __device__ __forceinline__ uint32_t v_off(int r, int j) {
   return r * C::RB + ((C::CPR >= 8 ? j ^ (r & 7) : j ^ ((r >> 1) & 3)) << 4);
 }
 
-// Whether this lane's eighth of a V tile holds an infinity or a NaN.
+// Whether this lane's share of a V tile holds an infinity or a NaN.
 template <class C>
 __device__ __forceinline__ bool not_finite(uint32_t vd, int lane) {
   constexpr uint32_t E = C::E8 ? 0x7F7F7F7Fu : C::BF ? 0x7F807F80u : 0x7C007C00u;
   bool r = false;
-  for (int i = 0; i < 8; i++) {
+  for (int i = 0; i < C::kHalf / 512; i++) {
     const uint4 v = lds16(vd + (i * 32 + lane) * 16);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -142,61 +155,61 @@ __device__ __forceinline__ bool not_finite(uint32_t vd, int lane) {
   return r;
 }
 
+// Value of channel d of key k in a V tile.
+template <class C>
+__device__ __forceinline__ float v_at(uint32_t vd, int k, int d) {
+  const int byte = d * (C::E8 ? 1 : 2);
+  uint32_t w;
+  asm volatile("ld.shared.u32 %0, [%1];"
+               : "=r"(w)
+               : "r"(vd + v_off<C>(k, byte >> 4) + (byte & 12)));
+  w >>= (byte & 3) * 8;
+  if (C::E8) {
+    const uint32_t h = e4m3_to_f16x2(w & 0xFFu);
+    return __low2float(*reinterpret_cast<const __half2*>(&h));
+  }
+  if (C::BF) return __uint_as_float(w << 16);
+  return __half2float(__ushort_as_half((unsigned short)w));
+}
+
+// Channel of accumulator row half hf (rows g, g + 8 of the MMA) in channel
+// tile x: 16-bit tiles hold 16 channels in order, E4M3 tiles even channels in
+// rows 0-7 and odd ones in rows 8-15.
+template <class C>
+__device__ __forceinline__ int o_channel(int x, int hf, int g) {
+  return C::E8 ? 16 * x + 2 * g + hf : 16 * x + 8 * hf + g;
+}
+
 // o += p v key by key for the rows that see the key.
 template <class C>
-__device__ __forceinline__ void add_seen(float (&o)[C::NQ][C::D / 8][4],
-                                         const float (&s)[C::NQ][C::NT][4], uint32_t vd, int key0,
-                                         uint32_t gone, const int (&hi)[C::NQ][2],
-                                         const int (&lo)[C::NQ][2], int g, int c) {
+__device__ __forceinline__ void add_seen(float (&o)[C::NB][C::D / 16][4],
+                                         const float (&s)[C::NB][C::MT][4], uint32_t vd, int key0,
+                                         uint32_t gone, const int (&hi)[C::NB][2],
+                                         const int (&lo)[C::NB][2], int g, int c) {
+#pragma unroll
+  for (int t = 0; t < C::MT; t++) {
+    if (gone >> t & 1) continue;
 #pragma unroll 1
-  for (int k = 0; k < C::KT; k++) {
-    float pr[C::NQ][2];
+    for (int k = 0; k < 16; k++) {
+      const int key = key0 + 16 * t + k;
+      float pr[C::NB][2];
 #pragma unroll
-    for (int q = 0; q < C::NQ; q++)
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        float x = 0.0f;
-#pragma unroll
-        for (int n = 0; n < C::NT; n++)
-          if (n == k >> 3) x = k & 1 ? s[q][n][2 * e + 1] : s[q][n][2 * e];
-        pr[q][e] = __shfl_sync(0xffffffffu, x, 4 * g + (k >> 1 & 3));
-      }
-    const int key = key0 + k;
-    if (gone >> (k >> 4) & 1) continue;
-#pragma unroll
-    for (int j = 0; j < C::CPR; j++) {
-      uint32_t w;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(vd + v_off<C>(k, j) + 4 * c));
-      float v[4];
-      if (C::E8) {
-        const uint32_t a = e4m3_to_f16x2(w), b = e4m3_to_f16x2(w >> 16);
-        const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
-        const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-        v[0] = fa.x;  // tile 2j: channels 4c, 4c + 2
-        v[1] = fb.x;
-        v[2] = fa.y;  // tile 2j + 1: channels 4c + 1, 4c + 3
-        v[3] = fb.y;
-      } else if (C::BF) {
-        v[0] = __uint_as_float(w << 16);
-        v[1] = __uint_as_float(w & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        v[0] = f.x;
-        v[1] = f.y;
-      }
-      constexpr int TP = C::E8 ? 2 : 1;  // score-column tiles of 8 channels per chunk
-#pragma unroll
-      for (int q = 0; q < C::NQ; q++)
+      for (int b = 0; b < C::NB; b++)
 #pragma unroll
         for (int e = 0; e < 2; e++)
-          if (key <= hi[q][e] && key >= lo[q][e]) {
+          pr[b][e] = __shfl_sync(0xffffffffu, k & 8 ? s[b][t][2 + e] : s[b][t][e], 4 * (k & 7) + c);
 #pragma unroll
-            for (int t = 0; t < TP; t++) {
-              float(&d)[4] = o[q][TP * j + t];
-              d[2 * e] = fmaf(pr[q][e], v[2 * t], d[2 * e]);
-              d[2 * e + 1] = fmaf(pr[q][e], v[2 * t + 1], d[2 * e + 1]);
-            }
-          }
+      for (int x = 0; x < C::D / 16; x++)
+#pragma unroll
+        for (int hf = 0; hf < 2; hf++) {
+          const float v = v_at<C>(vd, 16 * t + k, o_channel<C>(x, hf, g));
+#pragma unroll
+          for (int b = 0; b < C::NB; b++)
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+              if (key <= hi[b][e] && key >= lo[b][e])
+                o[b][x][2 * hf + e] = fmaf(pr[b][e], v, o[b][x][2 * hf + e]);
+        }
     }
   }
 }
@@ -274,12 +287,17 @@ __device__ __forceinline__ long long scan_line(const AttnParams& p, int rt, At a
   return total;
 }
 
-// The CTAs in use for a line of `total` granules, and where piece c starts.
+// The CTAs in use for a line of `total` granules, where piece c starts, and
+// the piece that holds granule x.
+template <class C>
 __device__ __forceinline__ int pieces_of(long long total) {
-  return total < kGrid ? (int)total : kGrid;
+  return total < C::kGrid ? (int)total : C::kGrid;
 }
 __device__ __forceinline__ long long piece_start(long long total, int pieces, int c) {
   return total * c / pieces;
+}
+__device__ __forceinline__ int piece_with(long long total, int pieces, long long x) {
+  return (int)(((x + 1) * pieces + total - 1) / total) - 1;
 }
 
 // scratch: [kGrid][2] parts of RT rows: fp32 O rows, then (m, l) pairs
@@ -306,36 +324,42 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_rows_kernel(AttnParams p) {
-  constexpr int D = C::D, NQ = C::NQ, KT = C::KT, NT = C::NT, RT = C::RT;
+__global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(AttnParams p) {
+  constexpr int D = C::D, NB = C::NB, KT = C::KT, MT = C::MT, RT = C::RT;
   constexpr int MBF = C::BF && !C::E8;  // type of the products
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  uint8_t* ring = smem + warp * C::kWarpBytes;
-  const uint32_t ring_s = smem_u32(ring);
-  float2* ml = reinterpret_cast<float2*>(smem + kWarps * C::kWarpBytes);  // [warp][RT]
-  uint32_t* absent = reinterpret_cast<uint32_t*>(ml + kWarps * RT) + warp * kStages;
+  const uint32_t ring_s = smem_u32(smem + warp * C::kWarpBytes);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kRing);  // [warp][RT]
+  uint32_t* absent = reinterpret_cast<uint32_t*>(ml + kWarps * RT) + warp * C::kStages;
 
   pdl_wait();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int32_t bad = 0;
   Place place;
   const long long total = scan_line(
       p, RT,
       [&](long long t) {
-        const int n = pieces_of(t);
+        const int n = pieces_of<C>(t);
         return (int)blockIdx.x < n ? piece_start(t, n, blockIdx.x) : -1LL;
       },
       &place, &bad);
   if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
-  const int pieces = pieces_of(total);
+  const int pieces = pieces_of<C>(total);
   if ((int)blockIdx.x >= pieces) return;
   long long pos = piece_start(total, pieces, blockIdx.x);
   const long long end = piece_start(total, pieces, blockIdx.x + 1);
   int b = place.b;
   long long base = place.base;
   bool first_part = true;
+
+  const int ps = p.cache.page_size, ps_shift = p.cache.page_shift;
+  const int64_t tb = p.cache.token_bytes;
+  // this lane's place in a group of rows that one copy instruction fetches
+  const int lrow = lane / C::CPR, lch = lane % C::CPR;
+  const int64_t lane_off = lrow * tb + lch * 16;
+  const int64_t it_off = C::RPI * tb;
 
   while (pos < end && b < p.batch.num_seqs) {
     const SeqWork sw = seq_work(p, RT, b, &bad);
@@ -345,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_rows_kernel(AttnPar
       continue;
     }
     const int u = (int)((pos - base) / sw.n), g0 = (int)((pos - base) % sw.n);
+    const long long u0 = base + (long long)u * sw.n;  // the unit's place on the line
     const int cnt = (int)min((long long)(sw.n - g0), end - pos);
     const int h = u / sw.rc, rc = u % sw.rc;
     pos += cnt;
@@ -355,15 +380,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_rows_kernel(AttnPar
     const int pos0 = sw.s.len - sw.s.n;
     auto vis_hi = [&](int tok) { return p.causal ? pos0 + tok : sw.s.len - 1; };
     auto vis_lo = [&](int tok) { return p.window > 0 ? max(0, pos0 + tok - p.window + 1) : 0; };
-    int hi[NQ][2], lo[NQ][2];
-#pragma unroll
-    for (int q = 0; q < NQ; q++)
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const int tok = min(rc * RT + 16 * q + 8 * e + g, rc * RT + nrows - 1) / p.group;
-        hi[q][e] = vis_hi(tok);
-        lo[q][e] = vis_lo(tok);
-      }
     // keys any row sees, and keys every row sees
     const int any0 = vis_lo(tok0), any1 = vis_hi(tok1) + 1;
     const int all0 = vis_lo(tok1), all1 = vis_hi(tok0) + 1;
@@ -374,202 +390,211 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_rows_kernel(AttnPar
     const int mine = ntile > warp ? (ntile - warp + kWarps - 1) / kWarps : 0;
 
     const int32_t* table = p.batch.table + (int64_t)b * p.batch.table_stride;
-    const int ps = p.cache.page_size;
     // page of 16-key group j of this warp's tile i (-1 past the end)
     auto page_of = [&](int i, int j) {
       const int key = (t_first + warp + i * kWarps) * KT + 16 * j;
-      return i < mine && key < any1 ? __ldg(table + key / ps) : -1;
+      if (i >= mine || key >= any1) return -1;
+      return __ldg(table + (ps_shift >= 0 ? key >> ps_shift : key / ps));
     };
-    int pg[C::SUB];
+    int pg[MT];
 #pragma unroll
-    for (int j = 0; j < C::SUB; j++) pg[j] = page_of(0, j);
+    for (int j = 0; j < MT; j++) pg[j] = page_of(0, j);
+    const uint8_t* const kh = p.cache.k + h * p.cache.head_bytes + lane_off;
+    const uint8_t* const vh = p.cache.v + h * p.cache.head_bytes + lane_off;
+    int ist = 0;  // stage of the next issue
     auto issue = [&](int i) {
       if (i < mine) {
-        const int st = i % kStages;
         const int key0 = (t_first + warp + i * kWarps) * KT;
-        const uint32_t kd = ring_s + st * C::kStageBytes, vd = kd + 4096;
-        const int ch = lane % C::CPR;
+        const uint32_t kd = ring_s + ist * C::kStageBytes, vd = kd + C::kHalf;
         uint32_t gone = 0;
 #pragma unroll
-        for (int j = 0; j < C::SUB; j++) {
+        for (int j = 0; j < MT; j++) {
           const int keyj = key0 + 16 * j;
-          const bool ok = pg[j] >= 0 && pg[j] < p.cache.num_pages;
+          const bool ok = (unsigned)pg[j] < (unsigned)p.cache.num_pages;
           if (!ok) {
             gone |= 1u << j;
             if (keyj < any1 && keyj + 16 > any0) bad |= kStatusBadPage;
           }
-          const int64_t at = (int64_t)(ok ? pg[j] : 0) * p.cache.page_bytes +
-                             (int64_t)(keyj % ps) * p.cache.token_bytes + h * p.cache.head_bytes +
-                             ch * 16;
+          const int in_page = ps_shift >= 0 ? keyj & (ps - 1) : keyj % ps;
+          int64_t at = (int64_t)pg[j] * p.cache.page_bytes + in_page * tb;
+          if (ok && keyj >= any0 && keyj + 16 <= any1) {
 #pragma unroll
-          for (int it = 0; it < 16 / C::RPI; it++) {
-            const int r = it * C::RPI + lane / C::CPR;  // row inside the group
-            const int key = keyj + r;
-            const int64_t off = at + (int64_t)r * p.cache.token_bytes;
-            const bool in = ok && key >= any0 && key < any1;
-            const int64_t o = in ? off : 0;
-            cp_async16(kd + k_off<C>(16 * j + r, ch), p.cache.k + o, in ? 16 : 0);
-            cp_async16(vd + v_off<C>(16 * j + r, ch), p.cache.v + o, in ? 16 : 0);
+            for (int it = 0; it < 16 / C::RPI; it++, at += it_off) {
+              const int r = 16 * j + it * C::RPI + lrow;
+              cp_async16(kd + k_off<C>(r, lch), kh + at, 16);
+              cp_async16(vd + v_off<C>(r, lch), vh + at, 16);
+            }
+          } else {
+#pragma unroll
+            for (int it = 0; it < 16 / C::RPI; it++, at += it_off) {
+              const int r = 16 * j + it * C::RPI + lrow;
+              const bool in = ok && key0 + r >= any0 && key0 + r < any1;
+              cp_async16(kd + k_off<C>(r, lch), in ? kh + at : p.cache.k, in ? 16 : 0);
+              cp_async16(vd + v_off<C>(r, lch), in ? vh + at : p.cache.v, in ? 16 : 0);
+            }
           }
         }
-        if (lane == 0) absent[st] = gone;
+        if (lane == 0) absent[ist] = gone;
 #pragma unroll
-        for (int j = 0; j < C::SUB; j++) pg[j] = page_of(i + 1, j);
+        for (int j = 0; j < MT; j++) pg[j] = page_of(i + 1, j);
       }
       cp_commit();
+      ist = ist == C::kStages - 1 ? 0 : ist + 1;
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; i++) issue(i);
+    for (int i = 0; i < C::kStages - 1; i++) issue(i);
 
-    // ---- queries to registers, in the channel order of the K operand
-    uint32_t qf[NQ][D / 16][4];
-    float cs[NQ][2];  // row factor of the scores, log2 units
+    // ---- queries to registers (B operand: lane g holds row g), in the
+    // channel order of the K operand
+    uint32_t qf[NB][D / 8];
+    float cs[NB][2];        // factor of the scores of rows 8 b + 2 c + e, log2 units
+    int hi[NB][2], lo[NB][2];
     const float cbase = p.scale_log2 * (C::E8 && p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f);
 #pragma unroll
-    for (int q = 0; q < NQ; q++)
+    for (int nb = 0; nb < NB; nb++) {
+      const int r = 8 * nb + g;
+      const int row = rc * RT + min(r, nrows - 1);
+      const uint16_t* src = p.q + (int64_t)(sw.s.q0 + row / p.group) * p.q_ts +
+                            (int64_t)(h * p.group + row % p.group) * p.q_hs;
+      // a 16-byte chunk of K holds 8 channels (16-bit) or 16 (E4M3)
+      constexpr int PC = C::E8 ? 2 : 1;
+#pragma unroll
+      for (int i = 0; i < C::CPR / 4; i++)
+#pragma unroll
+        for (int x = 0; x < PC; x++) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (r < nrows) v = *reinterpret_cast<const uint4*>(src + (c + 4 * i) * (8 * PC) + 8 * x);
+          qf[nb][(i * PC + x) * 4] = v.x;
+          qf[nb][(i * PC + x) * 4 + 1] = v.y;
+          qf[nb][(i * PC + x) * 4 + 2] = v.z;
+          qf[nb][(i * PC + x) * 4 + 3] = v.w;
+        }
+      float f_row = cbase;
+      if (C::E8 && C::BF) {
+        // bf16 to fp16: 2^s brings the row's largest value to [2^14, 2^15);
+        // values below 2^-38 of it lose bits
+        float am = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 8; i++)
+          am = fmaxf(am, fmaxf(fabsf(__uint_as_float(qf[nb][i] << 16)),
+                               fabsf(__uint_as_float(qf[nb][i] & 0xFFFF0000u))));
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        const int sh = fp16_scale_exp(am);
+        const float f = exp2f((float)sh);
+        f_row = cbase * exp2f((float)-sh);
+#pragma unroll
+        for (int i = 0; i < D / 8; i++)
+          qf[nb][i] = pack2<0>(__uint_as_float(qf[nb][i] << 16) * f,
+                               __uint_as_float(qf[nb][i] & 0xFFFF0000u) * f);
+      }
 #pragma unroll
       for (int e = 0; e < 2; e++) {
-        const int r = 16 * q + 8 * e + g;
-        const bool in = r < nrows;
-        const int row = rc * RT + (in ? r : 0);
-        const uint16_t* src = p.q + (int64_t)(sw.s.q0 + row / p.group) * p.q_ts +
-                              (int64_t)(h * p.group + row % p.group) * p.q_hs;
-        // chunk i: 16 bytes of K, 8 channels (16-bit) or 16 (E4M3)
-        uint32_t w[D / 8];  // this lane's words: 2 per MMA step
-        constexpr int PC = C::E8 ? 2 : 1;
-#pragma unroll
-        for (int i = 0; i < C::CPR / 4; i++)
-#pragma unroll
-          for (int x = 0; x < PC; x++) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (in)
-              v = *reinterpret_cast<const uint4*>(src + (c + 4 * i) * (8 * PC) + 8 * x);
-            w[(i * PC + x) * 4] = v.x;
-            w[(i * PC + x) * 4 + 1] = v.y;
-            w[(i * PC + x) * 4 + 2] = v.z;
-            w[(i * PC + x) * 4 + 3] = v.w;
-          }
-        cs[q][e] = cbase;
-        if (C::E8 && C::BF) {
-          // bf16 to fp16: 2^s brings the row's largest value to [2^14, 2^15);
-          // values below 2^-38 of it lose bits
-          float am = 0.0f;
-#pragma unroll
-          for (int i = 0; i < D / 8; i++)
-            am = fmaxf(am, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
-                                 fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-          const int sh = fp16_scale_exp(am);
-          const float f = exp2f((float)sh);
-          cs[q][e] = cbase * exp2f((float)-sh);
-#pragma unroll
-          for (int i = 0; i < D / 8; i++)
-            w[i] = pack2<0>(__uint_as_float(w[i] << 16) * f,
-                            __uint_as_float(w[i] & 0xFFFF0000u) * f);
-        }
-#pragma unroll
-        for (int s = 0; s < D / 16; s++) {
-          qf[q][s][e] = w[2 * s];
-          qf[q][s][2 + e] = w[2 * s + 1];
-        }
+        cs[nb][e] = __shfl_sync(0xffffffffu, f_row, 4 * (2 * c + e));
+        const int tok = (rc * RT + min(8 * nb + 2 * c + e, nrows - 1)) / p.group;
+        hi[nb][e] = vis_hi(tok);
+        lo[nb][e] = vis_lo(tok);
       }
-
-    float o[NQ][D / 8][4];
-    float m[NQ][2], l[NQ][2];
-#pragma unroll
-    for (int q = 0; q < NQ; q++) {
-#pragma unroll
-      for (int j = 0; j < D / 8; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) o[q][j][e] = 0.0f;
-      m[q][0] = m[q][1] = -INFINITY;
-      l[q][0] = l[q][1] = 0.0f;
     }
 
+    float o[NB][D / 16][4];
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; nb++) {
+#pragma unroll
+      for (int x = 0; x < D / 16; x++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[nb][x][e] = 0.0f;
+      m[nb][0] = m[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.0f;
+    }
+
+    int st = 0;
     for (int i = 0; i < mine; i++) {
-      cp_wait<kStages - 2>();
+      cp_wait<C::kStages - 2>();
       __syncwarp();
-      issue(i + kStages - 1);
-      const int st = i % kStages;
+      issue(i + C::kStages - 1);
       const int key0 = (t_first + warp + i * kWarps) * KT;
-      const uint32_t kd = ring_s + st * C::kStageBytes, vd = kd + 4096;
+      const uint32_t kd = ring_s + st * C::kStageBytes, vd = kd + C::kHalf;
       const uint32_t gone = absent[st];
+      st = st == C::kStages - 1 ? 0 : st + 1;
 
       // ---- scores
-      float s[NQ][NT][4];
+      float s[NB][MT][4];
 #pragma unroll
-      for (int n = 0; n < NT; n++) {
+      for (int t = 0; t < MT; t++) {
 #pragma unroll
-        for (int q = 0; q < NQ; q++)
+        for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-          for (int e = 0; e < 4; e++) s[q][n][e] = 0.0f;
+          for (int e = 0; e < 4; e++) s[nb][t][e] = 0.0f;
 #pragma unroll
         for (int x = 0; x < C::CPR / 4; x++) {
-          const uint4 kv = lds16(kd + k_off<C>(8 * n + g, c + 4 * x));
-          const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w};
+          const uint4 k0 = lds16(kd + k_off<C>(16 * t + g, c + 4 * x));
+          const uint4 k1 = lds16(kd + k_off<C>(16 * t + 8 + g, c + 4 * x));
+          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
           if (C::E8) {
 #pragma unroll
             for (int y = 0; y < 4; y++) {
-              const uint32_t b0 = e4m3_to_f16x2(kw[y]), b1 = e4m3_to_f16x2(kw[y] >> 16);
+              const uint32_t a0 = e4m3_to_f16x2(w0[y]), a2 = e4m3_to_f16x2(w0[y] >> 16);
+              const uint32_t a1 = e4m3_to_f16x2(w1[y]), a3 = e4m3_to_f16x2(w1[y] >> 16);
 #pragma unroll
-              for (int q = 0; q < NQ; q++) mma16<MBF>(s[q][n], qf[q][4 * x + y], b0, b1);
+              for (int nb = 0; nb < NB; nb++)
+                mma16<MBF>(s[nb][t], a0, a1, a2, a3, qf[nb][8 * x + 2 * y], qf[nb][8 * x + 2 * y + 1]);
             }
           } else {
 #pragma unroll
             for (int y = 0; y < 2; y++)
 #pragma unroll
-              for (int q = 0; q < NQ; q++)
-                mma16<MBF>(s[q][n], qf[q][2 * x + y], kw[2 * y], kw[2 * y + 1]);
+              for (int nb = 0; nb < NB; nb++)
+                mma16<MBF>(s[nb][t], w0[2 * y], w1[2 * y], w0[2 * y + 1], w1[2 * y + 1],
+                           qf[nb][4 * x + 2 * y], qf[nb][4 * x + 2 * y + 1]);
           }
         }
       }
-      const bool part = key0 < all0 || key0 + KT > all1 || gone;
-      if (part) {
+      if (key0 < all0 || key0 + KT > all1 || gone) {
 #pragma unroll
-        for (int q = 0; q < NQ; q++)
+        for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-          for (int n = 0; n < NT; n++)
+          for (int t = 0; t < MT; t++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-              const int key = key0 + 8 * n + 2 * c + (e & 1);
-              if (key > hi[q][e >> 1] || key < lo[q][e >> 1] || (gone >> (n >> 1) & 1))
-                s[q][n][e] = -INFINITY;
+              const int key = key0 + 16 * t + 8 * (e >> 1) + g;
+              if (key > hi[nb][e & 1] || key < lo[nb][e & 1] || (gone >> t & 1))
+                s[nb][t][e] = -INFINITY;
             }
       }
-      // ---- running maximum, terms, sum
+      // ---- running maximum, terms, sum (a row's keys lie over the 8 lanes g)
 #pragma unroll
-      for (int q = 0; q < NQ; q++)
+      for (int nb = 0; nb < NB; nb++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          float mx = s[q][0][2 * e];
+          float mx = fmaxf(s[nb][0][e], s[nb][0][2 + e]);
 #pragma unroll
-          for (int n = 0; n < NT; n++) mx = fmaxf(mx, fmaxf(s[q][n][2 * e], s[q][n][2 * e + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mx *= cs[q][e];
-          const float mn = fmaxf(m[q][e], mx);
+          for (int t = 1; t < MT; t++) mx = fmaxf(mx, fmaxf(s[nb][t][e], s[nb][t][2 + e]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          mx *= cs[nb][e];
+          const float mn = fmaxf(m[nb][e], mx);
           const float ms = mn == -INFINITY ? 0.0f : mn;
-          if (mn > m[q][e]) {
-            const float f = ex2(m[q][e] - ms);
-            l[q][e] *= f;
+          if (mn > m[nb][e]) {
+            const float f = ex2(m[nb][e] - ms);
+            l[nb][e] *= f;
 #pragma unroll
-            for (int j = 0; j < D / 8; j++) {
-              o[q][j][2 * e] *= f;
-              o[q][j][2 * e + 1] *= f;
+            for (int x = 0; x < D / 16; x++) {
+              o[nb][x][e] *= f;
+              o[nb][x][2 + e] *= f;
             }
-            m[q][e] = mn;
+            m[nb][e] = mn;
           }
-          float sum = 0.0f;
 #pragma unroll
-          for (int n = 0; n < NT; n++)
+          for (int t = 0; t < MT; t++)
 #pragma unroll
-            for (int x = 0; x < 2; x++) {
-              const float t = ex2(fmaf(s[q][n][2 * e + x], cs[q][e], -ms));
-              s[q][n][2 * e + x] = t;
-              sum += t;
+            for (int y = 0; y < 2; y++) {
+              const float v = ex2(fmaf(s[nb][t][2 * y + e], cs[nb][e], -ms));
+              s[nb][t][2 * y + e] = v;
+              l[nb][e] += v;
             }
-          l[q][e] += sum;
         }
       // ---- values
       // a tile with keys that only some rows see: a value there that is not
@@ -581,71 +606,56 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_rows_kernel(AttnPar
         continue;
       }
 #pragma unroll
-      for (int j = 0; j < KT / 16; j++) {
-        uint32_t pf[NQ][4];
+      for (int t = 0; t < MT; t++) {
+        uint32_t pf[NB][2];
 #pragma unroll
-        for (int q = 0; q < NQ; q++) {
-          pf[q][0] = pack2<MBF>(s[q][2 * j][0], s[q][2 * j][1]);
-          pf[q][1] = pack2<MBF>(s[q][2 * j][2], s[q][2 * j][3]);
-          pf[q][2] = pack2<MBF>(s[q][2 * j + 1][0], s[q][2 * j + 1][1]);
-          pf[q][3] = pack2<MBF>(s[q][2 * j + 1][2], s[q][2 * j + 1][3]);
+        for (int nb = 0; nb < NB; nb++) {
+          pf[nb][0] = movm_t(pack2<MBF>(s[nb][t][0], s[nb][t][1]));
+          pf[nb][1] = movm_t(pack2<MBF>(s[nb][t][2], s[nb][t][3]));
         }
 #pragma unroll
         for (int x = 0; x < C::CPR / 2; x++) {
-          uint32_t v[4];
-          ldsm4t(vd + v_off<C>(16 * j + (lane & 15), 2 * x + (lane >> 4)), v);
+          uint32_t v[4];  // keys 0-7 and 8-15 of chunks 2 x and 2 x + 1
+          ldsm4t(vd + v_off<C>(16 * t + (lane & 7) + (lane >> 4) * 8, 2 * x + (lane >> 3 & 1)), v);
           if (C::E8) {
 #pragma unroll
             for (int y = 0; y < 2; y++) {
-              const uint32_t a0 = e4m3_to_f16x2(v[2 * y]), a1 = e4m3_to_f16x2(v[2 * y] >> 16);
-              const uint32_t b0 = e4m3_to_f16x2(v[2 * y + 1]),
-                             b1 = e4m3_to_f16x2(v[2 * y + 1] >> 16);
+              const uint32_t a = e4m3_to_f16x2(v[y]), bq = e4m3_to_f16x2(v[y] >> 16);
+              const uint32_t d = e4m3_to_f16x2(v[2 + y]), e = e4m3_to_f16x2(v[2 + y] >> 16);
+              const uint32_t a0 = __byte_perm(a, bq, 0x5410), a1 = __byte_perm(a, bq, 0x7632);
+              const uint32_t a2 = __byte_perm(d, e, 0x5410), a3 = __byte_perm(d, e, 0x7632);
 #pragma unroll
-              for (int q = 0; q < NQ; q++) {
-                mma16<MBF>(o[q][4 * x + 2 * y], pf[q], __byte_perm(a0, a1, 0x5410),
-                           __byte_perm(b0, b1, 0x5410));
-                mma16<MBF>(o[q][4 * x + 2 * y + 1], pf[q], __byte_perm(a0, a1, 0x7632),
-                           __byte_perm(b0, b1, 0x7632));
-              }
+              for (int nb = 0; nb < NB; nb++)
+                mma16<MBF>(o[nb][2 * x + y], a0, a1, a2, a3, pf[nb][0], pf[nb][1]);
             }
           } else {
 #pragma unroll
-            for (int y = 0; y < 2; y++)
-#pragma unroll
-              for (int q = 0; q < NQ; q++)
-                mma16<MBF>(o[q][2 * x + y], pf[q], v[2 * y], v[2 * y + 1]);
+            for (int nb = 0; nb < NB; nb++)
+              mma16<MBF>(o[nb][x], v[0], v[1], v[2], v[3], pf[nb][0], pf[nb][1]);
           }
         }
       }
     }
     cp_wait<0>();
-    __syncwarp();
+    __syncthreads();  // every warp's ring is idle: the join buffers may cover it
 
-    // ---- join the warps: the ring is idle
-    float* buf = reinterpret_cast<float*>(ring);
+    // ---- join the warps
+    float* buf = reinterpret_cast<float*>(smem) + warp * (RT * C::OS);
 #pragma unroll
-    for (int q = 0; q < NQ; q++)
+    for (int nb = 0; nb < NB; nb++)
 #pragma unroll
       for (int e = 0; e < 2; e++) {
-        const int r = 16 * q + 8 * e + g;
-        float sum = l[q][e];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (c == 0) ml[warp * RT + r] = make_float2(m[q][e], sum);
-        if (C::E8) {
-          // even tiles hold channels 4c, 4c+2 of a 16-channel chunk, odd ones
-          // 4c+1, 4c+3
+        const int r = 8 * nb + 2 * c + e;
+        float sum = l[nb][e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (g == 0) ml[warp * RT + r] = make_float2(m[nb][e], sum);
 #pragma unroll
-          for (int j = 0; j < D / 16; j++)
-            *reinterpret_cast<float4*>(buf + r * C::OS + 16 * j + 4 * c) =
-                make_float4(o[q][2 * j][2 * e], o[q][2 * j + 1][2 * e], o[q][2 * j][2 * e + 1],
-                            o[q][2 * j + 1][2 * e + 1]);
-        } else {
+        for (int x = 0; x < D / 16; x++)
 #pragma unroll
-          for (int j = 0; j < D / 8; j++)
-            *reinterpret_cast<float2*>(buf + r * C::OS + 8 * j + 2 * c) =
-                make_float2(o[q][j][2 * e], o[q][j][2 * e + 1]);
-        }
+          for (int hf = 0; hf < 2; hf++)
+            buf[r * C::OS + o_channel<C>(x, hf, g)] = o[nb][x][2 * hf + e];
       }
     __syncthreads();
     const bool whole = cnt == sw.n;
@@ -654,21 +664,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_rows_kernel(AttnPar
     const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
     for (int i = threadIdx.x; i < nrows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d0 = (i % (D / 4)) * 4;
-      float2 st[kWarps];
+      float2 sl[kWarps];
       float mm = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; w++) {
-        st[w] = ml[w * RT + r];
-        mm = fmaxf(mm, st[w].x);
+        sl[w] = ml[w * RT + r];
+        mm = fmaxf(mm, sl[w].x);
       }
       const float ms = mm == -INFINITY ? 0.0f : mm;
       float ll = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int w = 0; w < kWarps; w++) {
-        const float f = ex2(st[w].x - ms);
-        ll += st[w].y * f;
-        const float4 x = *reinterpret_cast<const float4*>(
-            smem + w * C::kWarpBytes + (r * C::OS + d0) * 4);
+        const float f = ex2(sl[w].x - ms);
+        ll += sl[w].y * f;
+        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
+                                                          (w * RT + r) * C::OS + d0);
         acc[0] = fmaf(x.x, f, acc[0]);
         acc[1] = fmaf(x.y, f, acc[1]);
         acc[2] = fmaf(x.z, f, acc[2]);
@@ -688,78 +698,78 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_rows_kernel(AttnPar
       }
     }
     first_part = false;
+    if (!whole) {
+      // ---- the CTA that brings the unit's last part joins them all
+      const int c0 = piece_with(total, pieces, u0), c1 = piece_with(total, pieces, u0 + sw.n - 1);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) s_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        const float* parts = reinterpret_cast<const float*>(p.scratch);
+        // piece c0 holds the unit's first part as its second, unless the unit
+        // starts the piece; every other piece as its first
+        const size_t slot0 = (size_t)c0 * 2 + (piece_start(total, pieces, c0) < u0 ? 1 : 0);
+        const int np = c1 - c0 + 1;
+        auto part_of = [&](int i) {
+          return parts + (i == 0 ? slot0 : (size_t)(c0 + i) * 2) * part_floats(RT, D);
+        };
+        // weights of the parts, a warp per row: w = 2^(m - max m)
+        float* wt = reinterpret_cast<float*>(smem);  // [RT][np]
+        for (int r = warp; r < nrows; r += kWarps) {
+          float mm = -INFINITY;
+          for (int i = lane; i < np; i += 32) mm = fmaxf(mm, __ldcg(part_of(i) + RT * D + 2 * r));
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+          const float ms = mm == -INFINITY ? 0.0f : mm;
+          float ll = 0.0f;
+          for (int i = lane; i < np; i += 32) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(part_of(i) + RT * D + 2 * r));
+            const float f = ex2(x.x - ms);
+            wt[r * np + i] = f;
+            ll = fmaf(x.y, f, ll);
+          }
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, x);
+          if (lane == 0) ml[r] = make_float2(mm, ll);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < nrows * (D / 4); i += kThreads) {
+          const int r = i / (D / 4), d0 = (i % (D / 4)) * 4;
+          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+          for (int y = 0; y < np; y++) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(y) + r * D + d0));
+            const float f = wt[r * np + y];
+            acc[0] = fmaf(x.x, f, acc[0]);
+            acc[1] = fmaf(x.y, f, acc[1]);
+            acc[2] = fmaf(x.z, f, acc[2]);
+            acc[3] = fmaf(x.w, f, acc[3]);
+          }
+          const float2 sl = ml[r];
+          const int row = rc * RT + r;
+          const int token = sw.s.q0 + row / p.group, head = h * p.group + row % p.group;
+          const float inv = row_inverse(sl.y, vs);
+#pragma unroll
+          for (int e = 0; e < 4; e++) acc[e] *= inv;
+          store_out4<C>(p, token, head, d0, acc, C::BF);
+          if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(sl.x, sl.y);
+        }
+        if (threadIdx.x == 0) p.counters[c0] = 0;  // for the next call
+      }
+    }
     __syncthreads();  // the buffers are refilled by the next unit
   }
   if (bad) atomicOr(p.status, bad);
 }
 
-// Sums the parts of every unit that a cut of the line goes through.  Block
-// (x, y): cut x + 1; the block of a unit's first cut does the unit.  Rows are
-// spread over the warps and over y.
-template <class C>
-__global__ void __launch_bounds__(kThreads) attn_rows_join_kernel(AttnParams p) {
-  constexpr int D = C::D, RT = C::RT;
-  const int cut = blockIdx.x + 1;
-  int32_t bad = 0;
-  Place place;
-  const long long total = scan_line(
-      p, RT,
-      [&](long long t) {
-        const int n = pieces_of(t);
-        return cut < n ? piece_start(t, n, cut) : -1LL;
-      },
-      &place, &bad);
-  const int pieces = pieces_of(total);
-  const bool live = cut < pieces;
-  const SeqWork sw = live ? seq_work(p, RT, place.b, &bad) : SeqWork{};
-  const long long at = live ? piece_start(total, pieces, cut) : 0;
-  pdl_wait();
-  if (!live) return;
-  const int u = (int)((at - place.base) / sw.n);
-  const long long u0 = place.base + (long long)u * sw.n, u1 = u0 + sw.n;
-  if (at == u0 || piece_start(total, pieces, cut - 1) > u0) return;
-  // pieces first .. last hold the unit's parts
-  const int first = cut - 1;
-  int last = cut;
-  while (last + 1 < pieces && piece_start(total, pieces, last + 1) < u1) last++;
-  const int h = u / sw.rc, rc = u % sw.rc;
-  const int nrows = min(RT, sw.s.n * p.group - rc * RT);
-  const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
-  constexpr int LR = D / 4;  // threads of a row
-  const int d0 = (threadIdx.x % LR) * 4;
-  const float* parts = reinterpret_cast<const float*>(p.scratch);
-  // the first piece's part is its second one, unless the unit starts it
-  const size_t slot0 = (size_t)first * 2 + (piece_start(total, pieces, first) < u0 ? 1 : 0);
-  for (int r = blockIdx.y * (kThreads / LR) + threadIdx.x / LR; r < nrows;
-       r += gridDim.y * (kThreads / LR)) {
-    float mm = -INFINITY, ll = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int c = first; c <= last; c++) {
-      const float* part = parts + (c == first ? slot0 : (size_t)c * 2) * part_floats(RT, D);
-      const float2 st = *reinterpret_cast<const float2*>(part + RT * D + 2 * r);
-      const float4 x = *reinterpret_cast<const float4*>(part + r * D + d0);
-      const float mn = fmaxf(mm, st.x);
-      const float ms = mn == -INFINITY ? 0.0f : mn;
-      const float f0 = ex2(mm - ms), f1 = ex2(st.x - ms);
-      mm = mn;
-      ll = ll * f0 + st.y * f1;
-      acc[0] = acc[0] * f0 + x.x * f1;
-      acc[1] = acc[1] * f0 + x.y * f1;
-      acc[2] = acc[2] * f0 + x.z * f1;
-      acc[3] = acc[3] * f0 + x.w * f1;
-    }
-    const int row = rc * RT + r;
-    const int token = sw.s.q0 + row / p.group, head = h * p.group + row % p.group;
-    const float inv = row_inverse(ll, vs);
-#pragma unroll
-    for (int e = 0; e < 4; e++) acc[e] *= inv;
-    store_out4<C>(p, token, head, d0, acc, C::BF);
-    if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(mm, ll);
-  }
-}
-
 template <class C>
 cudaError_t launch_cfg(const AttnParams& p, cudaStream_t st) {
+  // the join's weights, and the resident CTAs, fit the shared memory
+  static_assert(C::RT * C::kGrid * 4 <= C::kRing, "join weights");
+  static_assert(C::kCtasPerSm * (C::kSmem + 1200) <= 227 * 1024, "resident CTAs");
+  static_assert(C::kGrid <= kRowsCounters, "counters");
   static bool init = false;
   if (!init) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -767,32 +777,37 @@ cudaError_t launch_cfg(const AttnParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     init = true;
   }
-  cudaError_t err =
-      launch_pdl(attn_rows_kernel<C>, dim3(kGrid), dim3(kThreads), C::kSmem, st, p);
-  note_launches(1);
-  if (err != cudaSuccess) return err;
-  err = launch_pdl(attn_rows_join_kernel<C>, dim3(kGrid - 1, 1), dim3(kThreads), 0, st, p);
+  const cudaError_t err =
+      launch_pdl(attn_rows_kernel<C>, dim3(C::kGrid), dim3(kThreads), C::kSmem, st, p);
   note_launches(1);
   return err;
 }
 
-template <int D, int NQ>
+template <int D, int NB>
 cudaError_t launch_types(const AttnParams& p, cudaStream_t st) {
   if (p.e4m3)
-    return p.bf16 ? launch_cfg<Cfg<D, NQ, 1, 1>>(p, st) : launch_cfg<Cfg<D, NQ, 1, 0>>(p, st);
-  return p.bf16 ? launch_cfg<Cfg<D, NQ, 0, 1>>(p, st) : launch_cfg<Cfg<D, NQ, 0, 0>>(p, st);
+    return p.bf16 ? launch_cfg<Cfg<D, NB, 1, 1>>(p, st) : launch_cfg<Cfg<D, NB, 1, 0>>(p, st);
+  return p.bf16 ? launch_cfg<Cfg<D, NB, 0, 1>>(p, st) : launch_cfg<Cfg<D, NB, 0, 0>>(p, st);
+}
+
+template <int D>
+cudaError_t launch_dim(const AttnParams& p, cudaStream_t st) {
+  // the fewest rows per unit that hold one sequence's new tokens; 32 where
+  // none does (half the reads of the cache per row)
+  const long long rows = (long long)p.batch.max_q * p.group;
+  return rows <= 8    ? launch_types<D, 1>(p, st)
+         : rows <= 16 ? launch_types<D, 2>(p, st)
+                      : launch_types<D, 4>(p, st);
 }
 
 }  // namespace
 
-size_t attn_rows_scratch_bytes(int dim) { return (size_t)kGrid * 2 * part_floats(32, dim) * 4; }
+size_t attn_rows_scratch_bytes(int dim) {
+  return (size_t)kSms * 2 * 2 * part_floats(32, dim) * 4;  // 2 CTAs of 32 rows, or 4 of 8
+}
 
 cudaError_t launch_attn_rows(const AttnParams& p, cudaStream_t st) {
-  // 16 rows per unit while one sequence's new tokens fit them, 32 otherwise
-  // (half the reads of the cache per row)
-  const bool wide = (long long)p.batch.max_q * p.group > 16;
-  if (p.dim == 64) return wide ? launch_types<64, 2>(p, st) : launch_types<64, 1>(p, st);
-  return wide ? launch_types<128, 2>(p, st) : launch_types<128, 1>(p, st);
+  return p.dim == 64 ? launch_dim<64>(p, st) : launch_dim<128>(p, st);
 }
 
 }  // namespace exl3
