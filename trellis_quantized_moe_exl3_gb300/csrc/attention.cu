@@ -216,6 +216,7 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   p.bf16 = dt == EXL3_BF16;
   p.e4m3 = cache->dtype == EXL3_E4M3;
   p.dim = cache->head_dim;
+  p.out32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   p.status = static_cast<int32_t*>(ws);
   p.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
   p.scratch = static_cast<uint8_t*>(ws) + kHead;

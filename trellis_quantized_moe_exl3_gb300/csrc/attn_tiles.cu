@@ -12,13 +12,18 @@
 // tensor core works on one row tile while the other's softmax runs.
 //
 // Roles of a CTA (one per SM, persistent): two softmax warpgroups (one row
-// tile each, one thread per row: no shuffles), one warp that issues the MMAs,
-// one that issues the TMA loads, and for E4M3 caches four warps that widen
-// the 8-bit tiles to fp16 (exact) in shared memory.
+// tile each, one thread per row: no shuffles); one thread that issues the MMAs
+// and nothing else, since the tensor core idles whenever it is late; a warp
+// that walks the work, publishes each unit to the others and issues the TMA
+// loads; a warp that brings in the next unit's queries; and a warp that cleans
+// the few V tiles that need it, or, for E4M3 caches, four warps that widen the
+// 8-bit tiles to fp16 (exact) in shared memory and clean them on the way.
 //   S = Q K^T   A, B from shared memory, S (128 fp32 columns) in TMEM
 //   P           written over S as 16-bit pairs, the A operand of
 //   O += P V    B = V as it lies in memory (keys are the K dimension, so V is
 //               the MN-major operand), O (head_dim fp32 columns) in TMEM
+// P is handed over in two halves of 64 keys, so that the product starts while
+// the second half's exponentials are taken.
 // A row's O is rescaled only when its maximum has grown by more than 2^8
 // since the last time (P stays below 2^8, in range for both 16-bit types, and
 // the final division removes the common factor), which leaves almost no
@@ -51,6 +56,8 @@ constexpr int kMinSteps = 4;        // key tiles per piece, where there are enou
 constexpr float kRescale = 8.0f;    // log2 growth of the maximum that rescales O
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kGone = 16;           // ring of absent-page masks (steps)
+constexpr int kUnits = 4;           // ring of published units
+constexpr int kRecInts = 24;
 
 template <int D_, int E8_, int BF_>
 struct Cfg {
@@ -63,9 +70,11 @@ struct Cfg {
   static constexpr int kOffKV = 2 * kOp;
   static constexpr int kOffRaw = kOffKV + kStages * kOp;
   static constexpr int kOffBar = kOffRaw + kRawStages * kRaw;
-  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 9;
+  static constexpr int kBars = 3 * kStages + 2 * kRawStages + 13 + 2 * kUnits;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
-  static constexpr int kSmem = kOffMisc + kGone * 4 + 32 + 1024;
+  static constexpr int kOffUnits = kOffMisc + kGone * 4 + 16;
+  static constexpr int kOffScale = kOffUnits + kUnits * kRecInts * 4;
+  static constexpr int kSmem = kOffScale + (E8 && BF ? 2 * 2 * kTile : 0) + 1024;
   static constexpr int kThreads = E8 ? 512 : 384;
   // registers of a softmax thread and of the others (their sum over the CTA
   // is what the launch holds: 128 or 168 a thread)
@@ -74,12 +83,33 @@ struct Cfg {
 };
 
 // ------------------------------------------------------------ PTX helpers
+// MMAs and commits are issued by a converged warp, one elected lane each (the
+// same one for the same mask): the operands then stay in uniform registers.
+// From a one-lane branch the issue of 8 MMAs takes 370 cycles, this way 90 to
+// 160, of the 512 they run; operands in ordinary registers cost as much again,
+// so what varies (the ring's stage) passes through a warp reduction, whose
+// result is uniform.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
@@ -118,6 +148,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
       "r"(r[30]), "r"(r[31]), "r"(a)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t a, const float* v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -135,18 +176,50 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// two fp32 lanes at once
-__device__ __forceinline__ void fma2(float& x, float& y, float c, float d) {
-  asm("{\n\t.reg .b64 a, b, e;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
-      "mov.b64 e, {%3, %3};\n\tfma.rn.f32x2 a, a, b, e;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(c), "f"(d));
+// two fp32 operations at once
+__device__ __forceinline__ uint64_t both(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
 }
-__device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+__device__ __forceinline__ void fma2(float& x, float& y, uint64_t c, uint64_t d) {
+  asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {%0, %1};\n\tfma.rn.f32x2 a, a, %2, %3;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
       : "+f"(x), "+f"(y)
+      : "l"(c), "l"(d));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, uint64_t c) {
+  asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {%0, %1};\n\tmul.rn.f32x2 a, a, %2;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "l"(c));
+}
+__device__ __forceinline__ void add2(uint64_t& acc, float u, float v) {
+  asm("{\n\t.reg .b64 b;\n\tmov.b64 b, {%1, %2};\n\tadd.rn.f32x2 %0, %0, b;\n\t}"
+      : "+l"(acc)
       : "f"(u), "f"(v));
+}
+__device__ __forceinline__ float sum2(uint64_t a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+  return x + y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 32 bytes, one sector
+__device__ __forceinline__ void stg32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                      uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b),
+               "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(bytes)
+               : "memory");
 }
 template <int BF>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -360,20 +433,29 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p, P
   }
 }
 
-// The pieces of one CTA, unit by unit.  Every role walks them by itself.
+// A part of a unit as the TMA warp publishes it (in shared memory).
+struct Rec {
+  int live;           // 0: no more
+  int b, h;           // sequence, kv head
+  int q0, n, len;     // its new tokens and length
+  int row0, nrows;    // packed rows
+  int any0, any1, all0, all1;
+  int first;          // key tile that j counts from
+  int s0, s1;         // the part's key tiles
+  int j0, j1;         // those that some row needs
+  int t0a, t0e, t1a, t1e;  // those that row tile 0, 1 needs (empty: a >= e)
+  int c0, c1;         // key tiles that every row sees whole
+  int flags;          // 1: the whole unit, 2: not the first part of the piece
+};
+static_assert(sizeof(Rec) == kRecInts * 4, "record");
+
+// The piece of this CTA, part by part.
 struct Walk {
   const AttnParams& p;
   const Plan& pl;
   int unit, head, off, units;
   long long left;
   bool first;
-  // the current part
-  Unit u;
-  int h, s0, s1;   // kv head, key tiles [s0, s1) counted from u.first
-  int j0, j1;      // those of them that a row tile needs (a row tile's are a
-                   // run, and the two runs meet)
-  bool whole;
-  int slot;        // 0: the first part of the piece
   __device__ Walk(const AttnParams& p_, const Plan& pl_) : p(p_), pl(pl_) {
     const PlanHead hd = *pl.head;
     const int c = blockIdx.x;
@@ -389,44 +471,53 @@ struct Walk {
       off = st.off;
     }
   }
-  __device__ bool next() {
-    if (left <= 0) return false;
-    const int2 r = pl.rec[unit];
+  __device__ Rec next() {
+    Rec r{};
+    if (left <= 0) return r;
+    const int2 id = pl.rec[unit];
     int32_t ignored = 0;
-    u = make_unit(p, r.x, load_seq(p.batch, r.x, &ignored), r.y);
-    h = head;
-    s0 = off;
-    s1 = (int)min((long long)u.n, off + left);
-    if (s1 <= s0) return false;
-    whole = s0 == 0 && s1 == u.n;
-    const bool has0 = u.e0 > u.a0, has1 = u.e1 > u.a1;
-    j0 = max(s0, (has0 ? u.a0 : u.a1) - u.first);
-    j1 = min(s1, (has1 ? u.e1 : u.e0) - u.first);
-    if (j1 < j0) j1 = j0;
-    slot = first ? 0 : 1;
+    const Unit u = make_unit(p, id.x, load_seq(p.batch, id.x, &ignored), id.y);
+    r.s0 = off;
+    r.s1 = (int)min((long long)u.n, off + left);
+    if (r.s1 <= r.s0) return r;
+    r.live = 1;
+    r.b = u.b;
+    r.h = head;
+    r.q0 = u.s.q0;
+    r.n = u.s.n;
+    r.len = u.s.len;
+    r.row0 = u.row0;
+    r.nrows = u.nrows;
+    r.any0 = u.any0;
+    r.any1 = u.any1;
+    r.all0 = u.all0;
+    r.all1 = u.all1;
+    r.first = u.first;
+    r.t0a = max(r.s0, u.a0 - u.first);
+    r.t0e = min(r.s1, u.e0 - u.first);
+    r.t1a = max(r.s0, u.a1 - u.first);
+    r.t1e = min(r.s1, u.e1 - u.first);
+    // (the two runs meet: row tile 1 starts no later than one past tile 0's end)
+    const bool has0 = r.t0e > r.t0a, has1 = r.t1e > r.t1a;
+    r.j0 = has0 ? r.t0a : r.t1a;
+    r.j1 = has1 ? r.t1e : r.t0e;
+    if (!has0 && !has1) r.j0 = r.j1 = 0;
+    r.c0 = (u.all0 + kTile - 1) / kTile - u.first;
+    r.c1 = min(u.all1, u.any1) / kTile - u.first;
+    r.flags = (r.s0 == 0 && r.s1 == u.n ? 1 : 0) | (first ? 0 : 2);
     first = false;
-    left -= s1 - s0;
+    left -= r.s1 - r.s0;
     off = 0;
     if (++unit == units) {
       unit = 0;
       head++;
     }
-    return true;
-  }
-  // whether row tile t needs key tile j (counted from u.first)
-  __device__ __forceinline__ bool act(int t, int j) const {
-    return u.first + j >= (t ? u.a1 : u.a0) && u.first + j < (t ? u.e1 : u.e0);
-  }
-  // keys of tile j that only some rows see, some of them held
-  __device__ __forceinline__ bool mixed(int j) const {
-    const int k0 = (u.first + j) * kTile, k1 = k0 + kTile;
-    return max(k0, u.any0) < u.all0 || min(k1, u.any1) > u.all1;
-  }
-  __device__ __forceinline__ bool ragged(int j) const {
-    const int k0 = (u.first + j) * kTile;
-    return k0 < u.any0 || k0 + kTile > u.any1;
+    return r;
   }
 };
+// A V tile that needs cleaning, scores that need masking: not every row sees
+// all of the tile's keys.
+__device__ __forceinline__ bool edge(const Rec& r, int j) { return j < r.c0 || j >= r.c1; }
 
 // 16-byte chunk of operand row r, channels 8 ch .. 8 ch + 7
 template <int D>
@@ -446,25 +537,35 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   return v;
 }
 
-// Zeroes the rows of a V tile outside [r0, r1) and, where `mixed`, replaces
-// values that are not finite by zero; returns whether there were any.  The
-// rows that see them get them back at the end (add_poison).
+// Zeroes the rows of a V tile outside [r0, r1) and replaces values that are
+// not finite by zero; returns whether there were any.  The rows that see them
+// get them back at the end (add_poison).
 template <class C>
-__device__ __forceinline__ bool clean_v(uint32_t v, int r0, int r1, bool mixed, int lane) {
+__device__ __forceinline__ bool clean_v(uint32_t v, int r0, int r1, int lane) {
   constexpr uint32_t E = C::BF ? 0x7F807F80u : 0x7C007C00u;
+  constexpr int CH = C::D / 8;
   bool hit = false;
-  for (int i = lane; i < kTile * (C::D / 8); i += 32) {
-    const int r = i / (C::D / 8), ch = i % (C::D / 8);
-    const uint32_t a = v + op_off<C::D>(r, ch);
-    if (r < r0 || r >= r1) {
-      sts16(a, 0, 0, 0, 0);
-    } else if (mixed) {
-      uint4 x = lds16(a);
-      const uint32_t m0 = __vcmpeq2(x.x & E, E), m1 = __vcmpeq2(x.y & E, E),
-                     m2 = __vcmpeq2(x.z & E, E), m3 = __vcmpeq2(x.w & E, E);
-      if (m0 | m1 | m2 | m3) {
-        hit = true;
-        sts16(a, x.x & ~m0, x.y & ~m1, x.z & ~m2, x.w & ~m3);
+#pragma unroll 1
+  for (int i0 = lane; i0 < kTile * CH; i0 += 32 * 8) {
+    uint4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const int i = i0 + 32 * k;
+      x[k] = lds16(v + op_off<C::D>(i / CH, i % CH));
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const int i = i0 + 32 * k, r = i / CH;
+      const uint32_t a = v + op_off<C::D>(r, i % CH);
+      if (r < r0 || r >= r1) {
+        sts16(a, 0, 0, 0, 0);
+      } else {
+        const uint32_t m0 = __vcmpeq2(x[k].x & E, E), m1 = __vcmpeq2(x[k].y & E, E),
+                       m2 = __vcmpeq2(x[k].z & E, E), m3 = __vcmpeq2(x[k].w & E, E);
+        if (m0 | m1 | m2 | m3) {
+          hit = true;
+          sts16(a, x[k].x & ~m0, x[k].y & ~m1, x[k].z & ~m2, x[k].w & ~m3);
+        }
       }
     }
   }
@@ -515,38 +616,53 @@ template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ Maps maps, AttnParams p, Plan pl) {
   constexpr int D = C::D;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~(uintptr_t)1023);
+  // (aligned by its declaration, not by arithmetic, so that operand addresses
+  // are known to be uniform; checked below)
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* kv_empty = kv_full + C::kStages;
-  uint64_t* raw_full = kv_empty + C::kStages;
+  uint64_t* edge_full = kv_empty + C::kStages;   // V tiles on their way to the cleaner
+  uint64_t* raw_full = edge_full + C::kStages;
   uint64_t* raw_empty = raw_full + C::kRawStages;
-  uint64_t* q_full = raw_empty + C::kRawStages;  // [2] each from here on
-  uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
-  uint64_t* all_done = o_full + 2;
+  uint64_t* q_full = raw_empty + C::kRawStages;  // [2] each: row tiles
+  uint64_t* q_free = q_full + 2;
+  uint64_t* s_full = q_free + 2;
+  uint64_t* o_full = s_full + 2;
+  uint64_t* p_full = o_full + 2;                 // [row tile][half]
+  uint64_t* u_full = p_full + 4;
+  uint64_t* u_empty = u_full + kUnits;
+  uint64_t* all_done = u_empty + kUnits;
   volatile uint32_t* gone = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc) + kGone;
-  volatile uint32_t* poison = tmem_slot + 1;  // a count of cleaned values' parts
+  volatile uint32_t* poison = tmem_slot + 1;     // a V tile held an infinity or a NaN
+  Rec* recs = reinterpret_cast<Rec*>(smem + C::kOffUnits);
+  // exponents of the queries' row scales, [use parity][tile][row]
+  int8_t* qscale = reinterpret_cast<int8_t*>(smem + C::kOffScale);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; i++) {
       mbar_init(&kv_full[i], C::E8 ? 4 : 1);
       mbar_init(&kv_empty[i], 1);
+      mbar_init(&edge_full[i], 1);
     }
     for (int i = 0; i < C::kRawStages; i++) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
     }
     for (int t = 0; t < 2; t++) {
-      mbar_init(&q_full[t], 4);
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_free[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
       mbar_init(&o_full[t], 1);
+      mbar_init(&p_full[2 * t], 4);
+      mbar_init(&p_full[2 * t + 1], 4);
+    }
+    for (int i = 0; i < kUnits; i++) {
+      mbar_init(&u_full[i], 1);
+      // softmax warps, MMA, queries, cleaner or converters
+      mbar_init(&u_empty[i], 8 + 1 + 1 + (C::E8 ? 4 : 1));
     }
     mbar_init(all_done, 1);
     *poison = 0;
@@ -556,12 +672,27 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // all 512 columns are this CTA's, so its TMEM addresses are constants
+  constexpr uint32_t tmem = 0;
+  if (*tmem_slot != 0 || (sbase & 1023)) {
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+    return;
+  }
   pdl_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, p.status)) != 0;
+  };
+  // the next published part, for a whole warp; live = 0 at the end or on abort
+  auto next_rec = [&](uint32_t& n) {
+    const uint32_t i = n % kUnits;
+    if (!wait(&u_full[i], (n / kUnits) & 1)) return Rec{};
+    const Rec r = recs[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&u_empty[i]);
+    n++;
+    return r;
   };
 
   if (warp < 8) {
@@ -572,57 +703,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const uint32_t s_col = tmem + lane_base + t * kTile;
     const uint32_t o_col = tmem + lane_base + 2 * kTile + t * D;
-    const uint32_t q_s = sbase + t * C::kOp;
     uint32_t steps = 0;  // key tiles this row tile has gone through
     uint32_t base = 0;   // key tiles the CTA has loaded before this unit
+    uint32_t nrec = 0, uses = 0;  // parts seen, those of them with keys for this tile
     bool ok = true;
-    Walk w(p, pl);
-    while (ok && w.next()) {
-      const int nt = min(kTile, w.u.nrows - t * kTile);  // rows of the tile
-      const int j0 = max(w.s0, (t ? w.u.a1 : w.u.a0) - w.u.first);
-      const int j1 = min(w.s1, (t ? w.u.e1 : w.u.e0) - w.u.first);
-      const int prow = w.u.row0 + t * kTile + min(row, max(nt, 1) - 1);
-      const int tok = min(prow, w.u.row0 + w.u.nrows - 1) / p.group;
-      const int token = w.u.s.q0 + tok;
-      const int head = w.h * p.group + min(prow, w.u.row0 + w.u.nrows - 1) % p.group;
-      const int hi = vis_hi(p, w.u.s, tok), lo = vis_lo(p, w.u.s, tok);
-      float c = p.scale_log2 * (C::E8 && p.cache.k_scale ? __ldg(p.cache.k_scale + w.h) : 1.0f);
-      if (j0 < j1) {
-        // ---- queries to shared memory (the last product that read the
-        // previous ones is done: its scores were seen)
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)token * p.q_ts +
-                                                          (int64_t)head * p.q_hs);
-        uint4 v[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; i++) v[i] = row < nt ? src[i] : make_uint4(0, 0, 0, 0);
-        if (C::E8 && C::BF) {
-          // bf16 to fp16 by a power of two per row
-          float am = 0.0f;
-#pragma unroll
-          for (int i = 0; i < D / 8; i++) {
-            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int y = 0; y < 4; y++)
-              am = fmaxf(am, fmaxf(fabsf(__uint_as_float(x[y] << 16)),
-                                   fabsf(__uint_as_float(x[y] & 0xFFFF0000u))));
-          }
-          const int sh = fp16_scale_exp(am);
-          const float f = exp2f((float)sh);
-          c *= exp2f((float)-sh);
-          auto cv = [&](uint32_t x) {
-            return pack2<0>(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f);
-          };
-#pragma unroll
-          for (int i = 0; i < D / 8; i++)
-            v[i] = make_uint4(cv(v[i].x), cv(v[i].y), cv(v[i].z), cv(v[i].w));
-        }
-#pragma unroll
-        for (int i = 0; i < D / 8; i++)
-          sts16(q_s + op_off<D>(row, i), v[i].x, v[i].y, v[i].z, v[i].w);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[t]);
-      }
+    while (ok) {
+      const Rec r = next_rec(nrec);
+      if (!r.live) break;
+      const int nt = min(kTile, r.nrows - t * kTile);  // rows of the tile
+      const int j0 = t ? r.t1a : r.t0a, j1 = t ? r.t1e : r.t0e;
+      const int prow = min(r.row0 + t * kTile + row, r.row0 + r.nrows - 1);
+      const int tok = prow / p.group;
+      const int token = r.q0 + tok, head = r.h * p.group + (prow - tok * p.group);
+      const int pos = r.len - r.n + tok;
+      const int hi = p.causal ? pos : r.len - 1;
+      const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      float c = p.scale_log2 * (C::E8 && p.cache.k_scale ? __ldg(p.cache.k_scale + r.h) : 1.0f);
       float m = -INFINITY, l = 0.0f;
       for (int j = j0; j < j1; j++, steps++) {
         if (!(ok = wait(&s_full[t], steps & 1))) break;
@@ -631,11 +727,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         uint32_t* sr = reinterpret_cast<uint32_t*>(s);
 #pragma unroll
         for (int i = 0; i < 4; i++) tmem_ld32(s_col + 32 * i, sr + 32 * i);
+        if (C::E8 && C::BF && j == j0) c *= exp2f(-(float)qscale[((uses & 1) * 2 + t) * kTile + row]);
+        const uint32_t gm = gone[(base + j - r.j0) % kGone];
 #pragma unroll
         for (int i = 0; i < 4; i++) tmem_ld32_wait(sr + 32 * i);
-        const int k0 = (w.u.first + j) * kTile;
-        const uint32_t gm = gone[(base + j - w.j0) % kGone];
-        if (k0 < w.u.all0 || k0 + kTile > w.u.all1 || gm) {
+        if (edge(r, j) || gm) {
+          const int k0 = (r.first + j) * kTile;
           const int h0 = hi - k0, l0 = lo - k0;
 #pragma unroll
           for (int i = 0; i < kTile; i++)
@@ -643,10 +740,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < kTile; i += 4)
+        for (int i = 4; i + 8 <= kTile; i += 8)
 #pragma unroll
-          for (int e = 0; e < 4; e++) mx[e] = fmaxf(mx[e], s[i + e]);
-        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c);
+          for (int e = 0; e < 4; e++) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; e++) mx[e] = fmaxf(mx[e], s[kTile - 4 + e]);
+        const float mn = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c);
         if (j == j0) {
           m = mn;
         } else {
@@ -655,54 +754,60 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const float f = grow ? ex2(m - mn) : 1.0f;
             if (grow) m = mn;
             l *= f;
-            // the product that last added to O is done
-            if (!(ok = wait(&o_full[t], (steps - 1) & 1))) break;
-            tc_fence_after();
+            // (the scores of this tile are complete, so the product before
+            // them, the last that added to O, is too)
+            const uint64_t f2 = both(f);
 #pragma unroll
-            for (int i = 0; i < D / 32; i++) {
-              uint32_t o[32];
-              tmem_ld32(o_col + 32 * i, o);
-              tmem_ld32_wait(o);
+            for (int i = 0; i < D / 16; i++) {
+              float o[16];
+              tmem_ld16(o_col + 16 * i, o);
+              tmem_ld_wait(o);
 #pragma unroll
-              for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_col + 32 * i, o);
+              for (int e = 0; e < 8; e++) mul2(o[2 * e], o[2 * e + 1], f2);
+              tmem_st16(o_col + 16 * i, o);
             }
           }
         }
         const float ms = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t c2 = both(c), n2 = both(-ms);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int half = 0; half < 2; half++) {
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; i++) {
             float &x = s[64 * half + 2 * i], &y = s[64 * half + 2 * i + 1];
-            fma2(x, y, c, -ms);
+            fma2(x, y, c2, n2);
             x = ex2(x);
             y = ex2(y);
-            add2(sum[(i & 1) * 2], sum[(i & 1) * 2 + 1], x, y);
+            add2(sum[i & 1], x, y);
             pk[i] = pack2<C::MBF>(x, y);
           }
           tmem_st32(s_col + 32 * half, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        l += sum2(sum[0]) + sum2(sum[1]);
       }
       if (!ok) break;
+      base += r.j1 - r.j0;
       // ---- output
       if (j0 < j1) {
-        if (!(ok = wait(&o_full[t], (steps - 1) & 1))) break;
+        if (!(ok = wait(&o_full[t], uses & 1))) break;
+        uses++;
         tc_fence_after();
       }
-      const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + w.h) : 1.0f;
-      const float inv = w.whole ? row_inverse(l, vs) : 1.0f;
+      const bool whole = r.flags & 1;
+      const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + r.h) : 1.0f;
+      const float inv = whole ? row_inverse(l, vs) : 1.0f;
+      const uint64_t inv2 = both(inv);
       const bool bad_v = *poison != 0;
-      float* part = pl.parts + ((size_t)blockIdx.x * 2 + w.slot) * part_floats(D);
       const int prt = t * kTile + row;
-#pragma unroll 1
+      float* part = pl.parts + ((size_t)blockIdx.x * 2 + (r.flags >> 1)) * part_floats(D);
+      uint16_t* out = p.out + ((int64_t)token * p.heads + head) * D;
+#pragma unroll
       for (int i = 0; i < D / 32; i++) {
         float o[32];
         uint32_t* orr = reinterpret_cast<uint32_t*>(o);
@@ -719,132 +824,132 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             float tmp[32];
 #pragma unroll
             for (int e = 0; e < 32; e++) tmp[e] = o[e];
-            add_poison<C>(p.cache, p.batch.table + (int64_t)w.u.b * p.batch.table_stride, w.h,
-                          (w.u.first + w.s0) * kTile, (w.u.first + w.s1) * kTile, w.u.any0, w.u.any1,
-                          w.u.all0, w.u.all1, lo, hi, 32 * i, tmp);
+            add_poison<C>(p.cache, p.batch.table + (int64_t)r.b * p.batch.table_stride, r.h,
+                          (r.first + r.s0) * kTile, (r.first + r.s1) * kTile, r.any0, r.any1,
+                          r.all0, r.all1, lo, hi, 32 * i, tmp);
 #pragma unroll
             for (int e = 0; e < 32; e++) o[e] = tmp[e];
           }
-          if (w.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)token * p.heads + head) * D + 32 * i);
+          if (whole) {
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-              dst[e] = make_uint4(pack2<C::BF>(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                  pack2<C::BF>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                  pack2<C::BF>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                  pack2<C::BF>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            for (int e = 0; e < 16; e++) {
+              mul2(o[2 * e], o[2 * e + 1], inv2);
+              w[e] = pack2<C::BF>(o[2 * e], o[2 * e + 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+              if (p.out32)
+                stg32(out + 32 * i + 2 * e, w[e], w[e + 1], w[e + 2], w[e + 3], w[e + 4], w[e + 5],
+                      w[e + 6], w[e + 7]);
+              else {
+                uint4* d = reinterpret_cast<uint4*>(out + 32 * i + 2 * e);
+                d[0] = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                d[1] = make_uint4(w[e + 4], w[e + 5], w[e + 6], w[e + 7]);
+              }
+            }
           } else {
-            float4* dst = reinterpret_cast<float4*>(part + (size_t)prt * D + 32 * i);
+            float* dst = part + (size_t)prt * D + 32 * i;
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 32; e += 8)
+              stg32(dst + e, orr[e], orr[e + 1], orr[e + 2], orr[e + 3], orr[e + 4], orr[e + 5],
+                    orr[e + 6], orr[e + 7]);
           }
         }
       }
       tc_fence_before();  // O is read before the next unit's first product writes it
       if (row < nt) {
-        if (!w.whole)
+        if (!whole)
           *reinterpret_cast<float2*>(part + (size_t)kUnitRows * D + 2 * prt) = make_float2(m, l);
         else if (p.lse)
           p.lse[(int64_t)token * p.heads + head] = row_lse(m, l);
       }
-      base += w.j1 - w.j0;
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------------ MMA
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
-    const uint32_t bf = C::MBF ? (1u << 7) | (1u << 10) : 0u;
-    const uint32_t id_qk = umma_idesc_f16(kTile, kTile, 0, 0) | bf;
-    const uint32_t id_pv = umma_idesc_f16(kTile, D, 0, 1) | bf;
-    uint64_t qd[2];
-    for (int t = 0; t < 2; t++) qd[t] = umma_desc(sbase + t * C::kOp, 16, 1024);
-    // V: rows of 128 bytes hold 64 channels of one key; 8 keys 1024 B, the
-    // second 64 channels kTile * 128 B on
-    const uint64_t kd0 = umma_desc(sbase + C::kOffKV, 16, 1024);
-    const uint64_t vd0 = umma_desc(sbase + C::kOffKV, kTile * 128, 1024);
-    uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
-    uint32_t load = 0;  // loads of the steps so far (K then V of each)
-    bool ok = true;
-    Walk w(p, pl);
-    while (ok && w.next()) {
-      uint32_t lk = 0, lk_prev = 0;    // load index of K of step j, j - 1
-      bool started[2] = {false, false};
-      bool any_prev = false;
-      for (int j = w.j0; ok && j <= w.j1; j++) {
-        const bool any = j < w.j1;
-        if (any) {
-          lk = load;
-          load += 2;
+    {
+      const uint32_t bf = C::MBF ? (1u << 7) | (1u << 10) : 0u;
+      const uint32_t id_qk = umma_idesc_f16(kTile, kTile, 0, 0) | bf;
+      const uint32_t id_pv = umma_idesc_f16(kTile, D, 0, 1) | bf;
+      const uint64_t qd = umma_desc(sbase, 16, 1024);
+      // V: rows of 128 bytes hold 64 channels of one key; 8 keys 1024 B, the
+      // second 64 channels kTile * 128 B on
+      const uint64_t kd0 = umma_desc(sbase + C::kOffKV, 16, 1024);
+      const uint64_t vd0 = umma_desc(sbase + C::kOffKV, kTile * 128, 1024);
+      uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0, nrec = 0;
+      uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // stage and parity of the next K, V
+      bool ok = true;
+      auto pv = [&](int t, uint32_t& np, bool acc) {
+        const uint32_t o = 2 * kTile + t * D, a = t * kTile;
+        const uint64_t vd = vd0 + (uint64_t)(__reduce_max_sync(0xffffffffu, vs) * (C::kOp >> 4));
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          if (!wait(&p_full[2 * t + half], np & 1)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 4 * half; k < 4 * half + 4; k++)
+            umma_ts(o, a + 8 * k, vd + k * (2048 >> 4), id_pv, acc || k > 0);
         }
-        const uint32_t kst = lk % C::kStages, vst = (lk_prev + 1) % C::kStages;
-        if (any_prev) {
-          if (!(ok = wait(&kv_full[vst], ((lk_prev + 1) / C::kStages) & 1))) break;
-          if (!C::E8) {
-            const bool mix = w.mixed(j - 1);
-            if (mix || w.ragged(j - 1)) {
-              const int k0 = (w.u.first + j - 1) * kTile;
-              const bool hit = clean_v<C>(sbase + C::kOffKV + vst * C::kOp, w.u.any0 - k0,
-                                          w.u.any1 - k0, mix, lane);
-              if (__any_sync(0xffffffffu, hit) && lane == 0) *poison = 1;
-              __threadfence_block();
-              fence_async_smem();
-              __syncwarp();
+        np++;
+        return true;
+      };
+      auto qk = [&](int t, uint32_t& nq, bool first, bool last) {
+        if (first && !wait(&q_full[t], nq++ & 1)) return false;
+        tc_fence_after();
+        const uint64_t kd = kd0 + (uint64_t)(__reduce_max_sync(0xffffffffu, ks) * (C::kOp >> 4)), q = qd + t * (C::kOp >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; k++) {
+          const uint64_t off = (uint64_t)(((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4);
+          umma_ss(t * kTile, q + off, kd + off, id_qk, k > 0);
+        }
+        commit(&s_full[t]);
+        if (last) commit(&q_free[t]);
+        return true;
+      };
+      while (ok) {
+        const Rec r = next_rec(nrec);
+        if (!r.live) break;
+        const int j0 = r.j0, j1 = r.j1, a0 = r.t0a, e0 = r.t0e, a1 = r.t1a, e1 = r.t1e;
+        if (j1 <= j0) continue;
+        for (int j = j0; j <= j1; j++) {
+          const bool has_v = j > j0, has_k = j < j1;
+          if (has_v && !(ok = wait(&kv_full[vs], vp))) break;
+          if (has_v && j > a0 && j <= e0) {
+            if (!(ok = pv(0, np0, j - 1 > a0))) break;
+            if (j == e0) commit(&o_full[0]);
+          }
+          if (has_k) {
+            if (!(ok = wait(&kv_full[ks], kp))) break;
+            if (j >= a0 && j < e0 && !(ok = qk(0, nq0, j == a0, j == e0 - 1))) break;
+          }
+          if (has_v) {
+            if (j > a1 && j <= e1) {
+              if (!(ok = pv(1, np1, j - 1 > a1))) break;
+              if (j == e1) commit(&o_full[1]);
+            }
+            commit(&kv_empty[vs]);
+            vs += 2;
+            if (vs >= C::kStages) {
+              vs -= C::kStages;
+              vp ^= 1;
+            }
+          }
+          if (has_k) {
+            if (j >= a1 && j < e1 && !(ok = qk(1, nq1, j == a1, j == e1 - 1))) break;
+            commit(&kv_empty[ks]);
+            ks += 2;
+            if (ks >= C::kStages) {
+              ks -= C::kStages;
+              kp ^= 1;
             }
           }
         }
-        bool k_here = false;
-#pragma unroll
-        for (int t = 0; t < 2; t++) {
-          if (any_prev && w.act(t, j - 1)) {
-            if (!(ok = wait(&p_full[t], n_p[t] & 1))) break;
-            n_p[t]++;
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t o = tmem + 2 * kTile + t * D, a = tmem + t * kTile;
-              const uint64_t vd = vd0 + (uint64_t)(vst * (C::kOp >> 4));
-#pragma unroll
-              for (int k = 0; k < kTile / 16; k++)
-                umma_ts(o, a + 8 * k, vd + k * (2048 >> 4), id_pv, started[t] || k > 0);
-              umma_commit(&o_full[t]);
-            }
-            started[t] = true;
-            __syncwarp();
-          }
-          if (any && w.act(t, j)) {
-            if (!k_here) {
-              if (!(ok = wait(&kv_full[kst], (lk / C::kStages) & 1))) break;
-              k_here = true;
-            }
-            if (j == max(w.s0, (t ? w.u.a1 : w.u.a0) - w.u.first)) {
-              if (!(ok = wait(&q_full[t], n_q[t] & 1))) break;
-              n_q[t]++;
-            }
-            tc_fence_after();
-            if (lane == 0) {
-              const uint64_t kd = kd0 + (uint64_t)(kst * (C::kOp >> 4));
-#pragma unroll
-              for (int k = 0; k < D / 16; k++) {
-                const uint64_t off = (uint64_t)(((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4);
-                umma_f16(tmem + t * kTile, qd[t] + off, kd + off, id_qk, k > 0);
-              }
-              umma_commit(&s_full[t]);
-            }
-            __syncwarp();
-          }
-        }
-        if (!ok) break;
-        if (lane == 0) {
-          if (any_prev) umma_commit(&kv_empty[vst]);
-          if (any) umma_commit(&kv_empty[kst]);
-        }
-        __syncwarp();
-        any_prev = any;
-        lk_prev = lk;
       }
+      commit(all_done);
     }
-    if (lane == 0) umma_commit(all_done);
   } else if (warp == 9) {
-    // ------------------------------------------------------------------ TMA
+    // ------------------------------------------------------------ work, TMA
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
     constexpr int ST = C::E8 ? C::kRawStages : C::kStages;
     constexpr int HALF = C::E8 ? 1 : D / 64;      // boxes across the channels
@@ -855,32 +960,54 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int nbox = kTile / maps.box;
     const int bx = lane / HALF, half = lane % HALF;
     const bool mine = bx < nbox;
-    uint32_t load = 0;
+    const int ps = p.cache.page_size, ps_shift = p.cache.page_shift;
+    uint32_t load = 0, nrec = 0;
+    uint32_t to_edge = 0, edge_par = 0;  // per stage: its last load went to the cleaner; its parity
     int32_t bad = 0;
     bool ok = true;
     Walk w(p, pl);
-    while (ok && w.next()) {
-      const int32_t* table = p.batch.table + (int64_t)w.u.b * p.batch.table_stride;
-      for (int j = w.j0; ok && j < w.j1; j++) {
-        const int key = (w.u.first + j) * kTile + bx * maps.box;
-        int page = p.cache.num_pages;  // out of range: zeros
-        bool absent = false;
-        if (mine && key < w.u.any1 && key + maps.box > w.u.any0) {
-          const int id = __ldg(table + key / p.cache.page_size);
-          absent = id < 0 || id >= p.cache.num_pages;
-          if (!absent) page = id;
-        }
+    while (ok) {
+      const Rec r = w.next();
+      const uint32_t slot = nrec % kUnits;
+      if (!(ok = wait(&u_empty[slot], ((nrec / kUnits) & 1) ^ 1))) break;
+      if (lane == 0) {
+        recs[slot] = r;
+        mbar_arrive(&u_full[slot]);
+      }
+      __syncwarp();
+      nrec++;
+      if (!r.live) break;
+      const int32_t* table = p.batch.table + (int64_t)r.b * p.batch.table_stride;
+      // page of this lane's box of key tile j; num_pages, out of range, reads zeros
+      auto page_of = [&](int j) {
+        const int key = (r.first + j) * kTile + bx * maps.box;
+        if (!mine || j >= r.j1 || key >= r.any1 || key + maps.box <= r.any0) return p.cache.num_pages;
+        return __ldg(table + (ps_shift >= 0 ? key >> ps_shift : key / ps));
+      };
+      int nxt = page_of(r.j0);
+      for (int j = r.j0; ok && j < r.j1; j++) {
+        const int key = (r.first + j) * kTile + bx * maps.box;
+        const int id = nxt;
+        nxt = page_of(j + 1);
+        const bool absent = (unsigned)id > (unsigned)p.cache.num_pages ||
+                            (id == p.cache.num_pages && mine && key < r.any1 &&
+                             key + maps.box > r.any0);
+        const int page = absent ? p.cache.num_pages : id;
         // 16-key groups of absent pages
         uint32_t g = absent ? ((1u << (maps.box / 16)) - 1) << (bx * (maps.box / 16)) : 0u;
         g = __reduce_or_sync(0xffffffffu, g);
         if (g) bad |= kStatusBadPage;
-        const int at = key % p.cache.page_size;
+        const int at = ps_shift >= 0 ? key & (ps - 1) : key % ps;
         for (int x = 0; x < 2; x++) {  // K, V
           const uint32_t st = load % ST;
           if (!(ok = wait(&empty[st], ((load / ST) & 1) ^ 1))) break;
+          const bool cleaner = !C::E8 && x == 1 && edge(r, j);
+          uint64_t* bar = cleaner ? &edge_full[st] : &full[st];
+          to_edge = cleaner ? to_edge | (1u << st) : to_edge & ~(1u << st);
+          if (cleaner) edge_par ^= 1u << st;
           if (lane == 0) {
             if (x == 0) gone[(load >> 1) % kGone] = g;
-            mbar_arrive_expect_tx(&full[st], BYTES);
+            mbar_arrive_expect_tx(bar, BYTES);
           }
           __syncwarp();
           if (mine) {
@@ -888,9 +1015,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                                  bx * maps.box * (C::E8 ? D : 128);
             const CUtensorMap* m = x == 0 ? &maps.k : &maps.v;
             if (maps.heads_first)
-              tma_load_4d(dst, m, half * 64, w.h, at, page, &full[st]);
+              tma_load_4d(dst, m, half * 64, r.h, at, page, bar);
             else
-              tma_load_4d(dst, m, half * 64, at, w.h, page, &full[st]);
+              tma_load_4d(dst, m, half * 64, at, r.h, page, bar);
           }
           load++;
         }
@@ -898,22 +1025,124 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     if (bad && lane == 0) atomicOr(p.status, bad);
     // every box this warp requested has landed before the CTA may exit
-    for (uint32_t i = load < ST ? 0 : load - ST; i < load; i++)
-      mbar_drain(&full[i % ST], (i / ST) & 1, kWaitBudgetCycles);
-  } else if (warp < 12) {
+    for (uint32_t i = load < ST ? 0 : load - ST; i < load; i++) {
+      const uint32_t st = i % ST;
+      if (to_edge >> st & 1)
+        mbar_drain(&edge_full[st], (edge_par >> st & 1) ^ 1, kWaitBudgetCycles);
+      else
+        mbar_drain(&full[st], (i / ST) & 1, kWaitBudgetCycles);
+    }
+  } else if (warp == 11) {
+    // -------------------------------------------------------------- queries
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
+    constexpr int LR = D / 8;        // lanes of a row
+    constexpr int RI = 32 / LR;      // rows at a time
+    const int ch = lane % LR;
+    uint32_t nrec = 0, n[2] = {0, 0};
+    bool ok = true;
+    while (ok) {
+      const Rec r = next_rec(nrec);
+      if (!r.live) break;
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        if (!ok || (t ? r.t1e <= r.t1a : r.t0e <= r.t0a)) continue;
+        const int nt = min(kTile, r.nrows - t * kTile);
+        // the last product that reads this tile's previous queries is done
+        if (n[t] > 0 && !(ok = wait(&q_free[t], (n[t] - 1) & 1))) continue;
+        const uint32_t dst = sbase + t * C::kOp;
+        auto src_of = [&](int row) {
+          const int prow = r.row0 + t * kTile + min(row, nt - 1);
+          const int tok = prow / p.group;
+          return p.q + (int64_t)(r.q0 + tok) * p.q_ts +
+                 (int64_t)(r.h * p.group + prow - tok * p.group) * p.q_hs + ch * 8;
+        };
+        if constexpr (C::E8 && C::BF) {
+          // bf16 to fp16 by a power of two per row: 2^s brings the row's
+          // largest value to [2^14, 2^15); values below 2^-38 of it lose bits
+          constexpr int UN = 4;
+          int8_t* sc = qscale + ((n[t] & 1) * 2 + t) * kTile;
+          for (int r0 = 0; r0 < kTile; r0 += RI * UN) {
+            uint4 v[UN];
+#pragma unroll
+            for (int k = 0; k < UN; k++) {
+              const int row = r0 + k * RI + lane / LR;
+              v[k] = make_uint4(0, 0, 0, 0);
+              if (row < nt) v[k] = *reinterpret_cast<const uint4*>(src_of(row));
+            }
+#pragma unroll
+            for (int k = 0; k < UN; k++) {
+              const int row = r0 + k * RI + lane / LR;
+              uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+              float am = 0.0f;
+#pragma unroll
+              for (int y = 0; y < 4; y++)
+                am = fmaxf(am, fmaxf(fabsf(__uint_as_float(x[y] << 16)),
+                                     fabsf(__uint_as_float(x[y] & 0xFFFF0000u))));
+#pragma unroll
+              for (int y = LR / 2; y > 0; y >>= 1)
+                am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, y));
+              const int sh = fp16_scale_exp(am);
+              const float f = exp2f((float)sh);
+#pragma unroll
+              for (int y = 0; y < 4; y++)
+                x[y] = pack2<0>(__uint_as_float(x[y] << 16) * f,
+                                __uint_as_float(x[y] & 0xFFFF0000u) * f);
+              sts16(dst + op_off<D>(row, ch), x[0], x[1], x[2], x[3]);
+              if (ch == 0) sc[row] = (int8_t)sh;
+            }
+          }
+        } else {
+#pragma unroll 4
+          for (int r0 = 0; r0 < kTile; r0 += RI) {
+            const int row = r0 + lane / LR;
+            cp_async16(dst + op_off<D>(row, ch), src_of(row), row < nt ? 16 : 0);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[t]);
+        n[t]++;
+      }
+    }
+  } else if (warp == 10) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
+    if constexpr (!C::E8) {
+      // ---------------------------------------------------- clean V tiles
+      uint32_t nrec = 0, load = 0, par = 0;
+      bool ok = true;
+      while (ok) {
+        const Rec r = next_rec(nrec);
+        if (!r.live) break;
+        for (int j = r.j0; ok && j < r.j1; j++, load += 2) {
+          if (!edge(r, j)) continue;
+          const uint32_t st = (load + 1) % C::kStages;
+          if (!(ok = wait(&edge_full[st], par >> st & 1))) break;
+          par ^= 1u << st;
+          const int k0 = (r.first + j) * kTile;
+          if (__any_sync(0xffffffffu, clean_v<C>(sbase + C::kOffKV + st * C::kOp, r.any0 - k0,
+                                                 r.any1 - k0, lane)) &&
+              lane == 0)
+            *poison = 1;
+          __threadfence_block();
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kv_full[st]);
+        }
+      }
+    }
   } else if constexpr (C::E8) {
     // -------------------------------------------------- widen E4M3 to fp16
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
     const int tid = threadIdx.x - 12 * 32;
-    uint32_t load = 0;
+    uint32_t load = 0, nrec = 0;
     bool ok = true;
-    Walk w(p, pl);
-    while (ok && w.next()) {
-      for (int j = w.j0; ok && j < w.j1; j++) {
-        const int k0 = (w.u.first + j) * kTile;
-        const int r0 = w.u.any0 - k0, r1 = w.u.any1 - k0;
-        const bool mix = w.mixed(j);
+    while (ok) {
+      const Rec rc = next_rec(nrec);
+      if (!rc.live) break;
+      for (int j = rc.j0; ok && j < rc.j1; j++) {
+        const int k0 = (rc.first + j) * kTile;
+        const int r0 = rc.any0 - k0, r1 = rc.any1 - k0;
         for (int x = 0; x < 2; x++) {
           const uint32_t rs = load % C::kRawStages, cs = load % C::kStages;
           if (!(ok = wait(&raw_full[rs], (load / C::kRawStages) & 1) &&
@@ -921,34 +1150,37 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             break;
           const uint32_t src = sbase + C::kOffRaw + rs * C::kRaw;
           const uint32_t dst = sbase + C::kOffKV + cs * C::kOp;
+          const bool clean = x == 1 && edge(rc, j);
           bool hit = false;
-#pragma unroll 4
-          for (int i = tid; i < C::kRaw / 16; i += 128) {
-            const int r = i / (D / 16), ch = i % (D / 16);
-            uint4 v = lds16(src + i * 16);
-            if (x == 1) {
-              if (r < r0 || r >= r1) v = make_uint4(0, 0, 0, 0);
-              if (mix) {
+          constexpr int CH = D / 16, UN = 4;
+#pragma unroll 1
+          for (int i0 = tid; i0 < C::kRaw / 16; i0 += 128 * UN) {
+            uint4 v[UN];
+#pragma unroll
+            for (int k = 0; k < UN; k++) v[k] = lds16(src + (i0 + 128 * k) * 16);
+#pragma unroll
+            for (int k = 0; k < UN; k++) {
+              const int i = i0 + 128 * k, r = i / CH, ch = i % CH;
+              if (clean) {
                 constexpr uint32_t E = 0x7F7F7F7Fu;
-                const uint32_t m0 = __vcmpeq4(v.x & E, E), m1 = __vcmpeq4(v.y & E, E),
-                               m2 = __vcmpeq4(v.z & E, E), m3 = __vcmpeq4(v.w & E, E);
+                if (r < r0 || r >= r1) v[k] = make_uint4(0, 0, 0, 0);
+                const uint32_t m0 = __vcmpeq4(v[k].x & E, E), m1 = __vcmpeq4(v[k].y & E, E),
+                               m2 = __vcmpeq4(v[k].z & E, E), m3 = __vcmpeq4(v[k].w & E, E);
                 hit |= (m0 | m1 | m2 | m3) != 0;
-                v = make_uint4(v.x & ~m0, v.y & ~m1, v.z & ~m2, v.w & ~m3);
+                v[k] = make_uint4(v[k].x & ~m0, v[k].y & ~m1, v[k].z & ~m2, v[k].w & ~m3);
               }
-            }
-            const uint32_t y[8] = {e4m3_to_f16x2(v.x), e4m3_to_f16x2(v.x >> 16),
-                                   e4m3_to_f16x2(v.y), e4m3_to_f16x2(v.y >> 16),
-                                   e4m3_to_f16x2(v.z), e4m3_to_f16x2(v.z >> 16),
-                                   e4m3_to_f16x2(v.w), e4m3_to_f16x2(v.w >> 16)};
-            // lanes of the upper channels store their second chunk first: 8
-            // lanes then cover all banks
-            const uint32_t a0 = dst + op_off<D>(r, 2 * ch), a1 = dst + op_off<D>(r, 2 * ch + 1);
-            if (ch & (D / 32)) {
-              sts16(a1, y[4], y[5], y[6], y[7]);
-              sts16(a0, y[0], y[1], y[2], y[3]);
-            } else {
-              sts16(a0, y[0], y[1], y[2], y[3]);
-              sts16(a1, y[4], y[5], y[6], y[7]);
+              const uint32_t y[8] = {e4m3_to_f16x2(v[k].x), e4m3_to_f16x2(v[k].x >> 16),
+                                     e4m3_to_f16x2(v[k].y), e4m3_to_f16x2(v[k].y >> 16),
+                                     e4m3_to_f16x2(v[k].z), e4m3_to_f16x2(v[k].z >> 16),
+                                     e4m3_to_f16x2(v[k].w), e4m3_to_f16x2(v[k].w >> 16)};
+              // lanes of the upper channels store their second chunk first: 8
+              // lanes then cover all banks
+              const uint32_t a0 = dst + op_off<D>(r, 2 * ch), a1 = dst + op_off<D>(r, 2 * ch + 1);
+              const bool sw = ch & (D / 32);
+              sts16(sw ? a1 : a0, sw ? y[4] : y[0], sw ? y[5] : y[1], sw ? y[6] : y[2],
+                    sw ? y[7] : y[3]);
+              sts16(sw ? a0 : a1, sw ? y[0] : y[4], sw ? y[1] : y[5], sw ? y[2] : y[6],
+                    sw ? y[3] : y[7]);
             }
           }
           if (hit) *poison = 1;
@@ -964,6 +1196,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
