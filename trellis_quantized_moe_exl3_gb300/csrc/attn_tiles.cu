@@ -12,12 +12,15 @@
 // tensor core works on one row tile while the other's softmax runs.
 //
 // Roles of a CTA (one per SM, persistent): two softmax warpgroups (one row
-// tile each, one thread per row: no shuffles); one thread that issues the MMAs
-// and nothing else, since the tensor core idles whenever it is late; a warp
-// that walks the work, publishes each unit to the others and issues the TMA
-// loads; a warp that brings in the next unit's queries; and a warp that cleans
-// the few V tiles that need it, or, for E4M3 caches, four warps that widen the
-// 8-bit tiles to fp16 (exact) in shared memory and clean them on the way.
+// tile each, one thread per row: no shuffles); a warp that issues the MMAs and
+// nothing else, since the tensor core idles whenever it is late (one warp, not
+// one per row tile: it keeps the row tiles in turn, and two free-running ones
+// fall into step, both in softmax, then both in products, 1.5 times slower); a
+// warp that walks the work, publishes each unit to the others and issues the
+// TMA loads; a warp that brings in the next unit's queries; and a warp that
+// cleans the few V tiles that need it, or, for E4M3 caches, four warps that
+// widen the 8-bit tiles to fp16 (exact) in shared memory and clean them on the
+// way.
 //   S = Q K^T   A, B from shared memory, S (128 fp32 columns) in TMEM
 //   P           written over S as 16-bit pairs, the A operand of
 //   O += P V    B = V as it lies in memory (keys are the K dimension, so V is
@@ -70,11 +73,11 @@ struct Cfg {
   static constexpr int kOffKV = 2 * kOp;
   static constexpr int kOffRaw = kOffKV + kStages * kOp;
   static constexpr int kOffBar = kOffRaw + kRawStages * kRaw;
-  static constexpr int kBars = 3 * kStages + 2 * kRawStages + 13 + 2 * kUnits;
+  static constexpr int kBars = 3 * kStages + 2 * kRawStages + 15 + 2 * kUnits;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffUnits = kOffMisc + kGone * 4 + 16;
-  static constexpr int kOffScale = kOffUnits + kUnits * kRecInts * 4;
-  static constexpr int kSmem = kOffScale + (E8 && BF ? 2 * 2 * kTile : 0) + 1024;
+  static constexpr int kSmem = kOffUnits + kUnits * kRecInts * 4;
+  static constexpr int kCvtQ = E8 && BF;   // queries are brought to fp16
   static constexpr int kThreads = E8 ? 512 : 384;
   // registers of a softmax thread and of the others (their sum over the CTA
   // is what the launch holds: 128 or 168 a thread)
@@ -170,6 +173,55 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
       "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+// A whole warp waits for a phase of a barrier: the lanes' answers are voted
+// on, so that the warp never diverges and a ready barrier costs a few
+// instructions (the MMA warp's waits are on the critical path of every tile).
+// False once a wait ran out of budget, here or (status word) anywhere.
+__device__ __forceinline__ bool wait_some(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
+      "WAIT:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "vote.sync.all.pred p, p, 0xffffffff;\n\t"
+      "@p bra.uni DONE;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.ge.u32 p, n, 64;\n\t"
+      "@p bra.uni FAIL;\n\t"
+      "bra.uni WAIT;\n\t"
+      "DONE:\n\tsetp.eq.u32 p, 0, 0;\n\t"
+      "bra.uni END;\n\t"
+      "FAIL:\n\tsetp.ne.u32 p, 0, 0;\n\t"
+      "END:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, int32_t* status) {
+  const long long t0 = clock64();
+  while (!wait_some(bar, parity)) {
+    bool stop = *reinterpret_cast<volatile int32_t*>(status) & kStatusTimeout;
+    if (clock64() - t0 > kWaitBudgetCycles) {
+      atomicOr(status, kStatusTimeout);
+      stop = true;
+    }
+    if (__any_sync(0xffffffffu, stop)) return false;
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  return wait_some(a, parity) || wait_long(a, parity, status);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -609,6 +661,8 @@ struct Maps {
   CUtensorMap k, v;
   int box;          // tokens of a box
   int heads_first;  // dimension 1 is the heads (else the tokens of a page)
+  CUtensorMap q;    // channels, heads, tokens; boxes of a row tile
+  int q_boxes;      // 0: the group does not divide a row tile, no such boxes
 };
 
 // ------------------------------------------------------------ main kernel
@@ -626,7 +680,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint64_t* raw_full = edge_full + C::kStages;
   uint64_t* raw_empty = raw_full + C::kRawStages;
   uint64_t* q_full = raw_empty + C::kRawStages;  // [2] each: row tiles
-  uint64_t* q_free = q_full + 2;
+  uint64_t* q_raw = q_full + 2;                  // queries still in bf16
+  uint64_t* q_free = q_raw + 2;
   uint64_t* s_full = q_free + 2;
   uint64_t* o_full = s_full + 2;
   uint64_t* p_full = o_full + 2;                 // [row tile][half]
@@ -637,8 +692,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc) + kGone;
   volatile uint32_t* poison = tmem_slot + 1;     // a V tile held an infinity or a NaN
   Rec* recs = reinterpret_cast<Rec*>(smem + C::kOffUnits);
-  // exponents of the queries' row scales, [use parity][tile][row]
-  int8_t* qscale = reinterpret_cast<int8_t*>(smem + C::kOffScale);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -652,7 +705,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       mbar_init(&raw_empty[i], 4);
     }
     for (int t = 0; t < 2; t++) {
-      mbar_init(&q_full[t], 1);
+      mbar_init(&q_full[t], C::kCvtQ ? 4 : 1);
+      mbar_init(&q_raw[t], 1);
       mbar_init(&q_free[t], 1);
       mbar_init(&s_full[t], 1);
       mbar_init(&o_full[t], 1);
@@ -682,7 +736,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, p.status)) != 0;
+    return wait_warp(bar, parity, p.status);
   };
   // the next published part, for a whole warp; live = 0 at the end or on abort
   auto next_rec = [&](uint32_t& n) {
@@ -719,32 +773,75 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int hi = p.causal ? pos : r.len - 1;
       const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
       float c = p.scale_log2 * (C::E8 && p.cache.k_scale ? __ldg(p.cache.k_scale + r.h) : 1.0f);
+      if (C::kCvtQ && j0 < j1) {
+        // bf16 queries to fp16, in place, by a power of two per row: 2^s
+        // brings the row's largest value to [2^14, 2^15); values below 2^-38
+        // of it lose bits
+        if (!(ok = wait(&q_raw[t], uses & 1))) break;
+        const uint32_t q = sbase + t * C::kOp;
+        float am = 0.0f;
+#pragma unroll 8
+        for (int i = 0; i < D / 8; i++) {
+          const uint4 v = lds16(q + op_off<D>(row, i));
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int y = 0; y < 4; y++)
+            am = max3(am, fabsf(__uint_as_float(x[y] << 16)),
+                      fabsf(__uint_as_float(x[y] & 0xFFFF0000u)));
+        }
+        const int sh = fp16_scale_exp(am);
+        const float f = exp2f((float)sh);
+        c *= exp2f((float)-sh);
+#pragma unroll 4
+        for (int i = 0; i < D / 8; i++) {
+          const uint4 v = lds16(q + op_off<D>(row, i));
+          uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int y = 0; y < 4; y++)
+            x[y] = pack2<0>(__uint_as_float(x[y] << 16) * f,
+                            __uint_as_float(x[y] & 0xFFFF0000u) * f);
+          sts16(q + op_off<D>(row, i), x[0], x[1], x[2], x[3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[t]);
+      }
       float m = -INFINITY, l = 0.0f;
       for (int j = j0; j < j1; j++, steps++) {
         if (!(ok = wait(&s_full[t], steps & 1))) break;
         tc_fence_after();
         float s[kTile];
         uint32_t* sr = reinterpret_cast<uint32_t*>(s);
-#pragma unroll
-        for (int i = 0; i < 4; i++) tmem_ld32(s_col + 32 * i, sr + 32 * i);
-        if (C::E8 && C::BF && j == j0) c *= exp2f(-(float)qscale[((uses & 1) * 2 + t) * kTile + row]);
+        tmem_ld32(s_col, sr);
+        tmem_ld32(s_col + 32, sr + 32);
         const uint32_t gm = gone[(base + j - r.j0) % kGone];
+        const bool masked = edge(r, j) || gm;
+        const int k0 = (r.first + j) * kTile;
+        const int h0 = hi - k0, l0 = lo - k0;
+        float mx[4];
+        // the second half is on its way while the first is looked through
 #pragma unroll
-        for (int i = 0; i < 4; i++) tmem_ld32_wait(sr + 32 * i);
-        if (edge(r, j) || gm) {
-          const int k0 = (r.first + j) * kTile;
-          const int h0 = hi - k0, l0 = lo - k0;
+        for (int half = 0; half < 2; half++) {
+          tmem_ld32_wait(sr + 64 * half);
+          tmem_ld32_wait(sr + 64 * half + 32);
+          if (half == 0) {
+            tmem_ld32(s_col + 64, sr + 64);
+            tmem_ld32(s_col + 96, sr + 96);
+          }
+          if (masked) {
 #pragma unroll
-          for (int i = 0; i < kTile; i++)
-            if (i > h0 || i < l0 || (gm >> (i >> 4) & 1)) s[i] = -INFINITY;
+            for (int i = 64 * half; i < 64 * half + 64; i++)
+              if (i > h0 || i < l0 || (gm >> (i >> 4) & 1)) s[i] = -INFINITY;
+          }
+          if (half == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) mx[e] = fmaxf(s[2 * e], s[2 * e + 1]);
+          }
+#pragma unroll
+          for (int i = 64 * half + (half ? 0 : 8); i < 64 * half + 64; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; e++) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int i = 4; i + 8 <= kTile; i += 8)
-#pragma unroll
-          for (int e = 0; e < 4; e++) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
-#pragma unroll
-        for (int e = 0; e < 4; e++) mx[e] = fmaxf(mx[e], s[kTile - 4 + e]);
         const float mn = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c);
         if (j == j0) {
           m = mn;
@@ -1035,9 +1132,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   } else if (warp == 11) {
     // -------------------------------------------------------------- queries
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
-    constexpr int LR = D / 8;        // lanes of a row
-    constexpr int RI = 32 / LR;      // rows at a time
-    const int ch = lane % LR;
     uint32_t nrec = 0, n[2] = {0, 0};
     bool ok = true;
     while (ok) {
@@ -1050,60 +1144,51 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         // the last product that reads this tile's previous queries is done
         if (n[t] > 0 && !(ok = wait(&q_free[t], (n[t] - 1) & 1))) continue;
         const uint32_t dst = sbase + t * C::kOp;
-        auto src_of = [&](int row) {
-          const int prow = r.row0 + t * kTile + min(row, nt - 1);
-          const int tok = prow / p.group;
-          return p.q + (int64_t)(r.q0 + tok) * p.q_ts +
-                 (int64_t)(r.h * p.group + prow - tok * p.group) * p.q_hs + ch * 8;
-        };
-        if constexpr (C::E8 && C::BF) {
-          // bf16 to fp16 by a power of two per row: 2^s brings the row's
-          // largest value to [2^14, 2^15); values below 2^-38 of it lose bits
-          constexpr int UN = 4;
-          int8_t* sc = qscale + ((n[t] & 1) * 2 + t) * kTile;
-          for (int r0 = 0; r0 < kTile; r0 += RI * UN) {
-            uint4 v[UN];
+        uint64_t* const bar = C::kCvtQ ? &q_raw[t] : &q_full[t];
+        if (maps.q_boxes) {
+          // rows past the sequence's end are other tokens' (or zeros): they
+          // are computed and dropped
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, C::kOp);
+            const int tok = r.q0 + (r.row0 + t * kTile) / p.group;
 #pragma unroll
-            for (int k = 0; k < UN; k++) {
-              const int row = r0 + k * RI + lane / LR;
-              v[k] = make_uint4(0, 0, 0, 0);
-              if (row < nt) v[k] = *reinterpret_cast<const uint4*>(src_of(row));
-            }
-#pragma unroll
-            for (int k = 0; k < UN; k++) {
-              const int row = r0 + k * RI + lane / LR;
-              uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-              float am = 0.0f;
-#pragma unroll
-              for (int y = 0; y < 4; y++)
-                am = fmaxf(am, fmaxf(fabsf(__uint_as_float(x[y] << 16)),
-                                     fabsf(__uint_as_float(x[y] & 0xFFFF0000u))));
-#pragma unroll
-              for (int y = LR / 2; y > 0; y >>= 1)
-                am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, y));
-              const int sh = fp16_scale_exp(am);
-              const float f = exp2f((float)sh);
-#pragma unroll
-              for (int y = 0; y < 4; y++)
-                x[y] = pack2<0>(__uint_as_float(x[y] << 16) * f,
-                                __uint_as_float(x[y] & 0xFFFF0000u) * f);
-              sts16(dst + op_off<D>(row, ch), x[0], x[1], x[2], x[3]);
-              if (ch == 0) sc[row] = (int8_t)sh;
-            }
+            for (int x = 0; x < D / 64; x++)
+              tma_load_3d(dst + x * (kTile * 128), &maps.q, 64 * x, r.h * p.group, tok, bar);
           }
+          __syncwarp();
         } else {
+          constexpr int LR = D / 8, RI = 32 / LR;  // lanes of a row, rows at a time
+          const int ch = lane % LR;
+          int row = lane / LR;
+          const int first = r.row0 + t * kTile + row;
+          int tok = first / p.group, hd = first - tok * p.group;
+          const uint16_t* q = p.q + (int64_t)(r.q0 + tok) * p.q_ts +
+                              (int64_t)(r.h * p.group + hd) * p.q_hs + ch * 8;
+          const int64_t wrap = p.q_ts - p.group * p.q_hs;
 #pragma unroll 4
-          for (int r0 = 0; r0 < kTile; r0 += RI) {
-            const int row = r0 + lane / LR;
-            cp_async16(dst + op_off<D>(row, ch), src_of(row), row < nt ? 16 : 0);
+          for (; row < kTile; row += RI) {
+            cp_async16(dst + op_off<D>(row, ch), row < nt ? q : p.q, row < nt ? 16 : 0);
+            q += RI * p.q_hs;
+            hd += RI;
+            while (hd >= p.group) {
+              hd -= p.group;
+              q += wrap;
+            }
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[t]);
         n[t]++;
       }
+    }
+    // the last queries requested have landed before the CTA may exit
+    if (maps.q_boxes) {
+#pragma unroll
+      for (int t = 0; t < 2; t++)
+        if (n[t] > 0)
+          mbar_drain(C::kCvtQ ? &q_raw[t] : &q_full[t], (n[t] - 1) & 1, kWaitBudgetCycles);
     }
   } else if (warp == 10) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
@@ -1310,6 +1395,20 @@ bool make_maps(const AttnParams& p, Maps* m) {
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return false;
+  // queries: a row tile is a box of group heads x 128 / group tokens, where
+  // the group divides it
+  m->q_boxes = 0;
+  if (kTile % p.group == 0) {
+    const int64_t qh = p.heads > 1 ? p.q_hs * 2 : (int64_t)p.dim * 2;
+    const int64_t qt = p.batch.T > 1 ? p.q_ts * 2 : (int64_t)p.dim * 2;
+    const cuuint64_t qdims[3] = {(cuuint64_t)p.dim, (cuuint64_t)p.heads, (cuuint64_t)p.batch.T};
+    const cuuint64_t qstr[2] = {(cuuint64_t)qh, (cuuint64_t)qt};
+    const cuuint32_t qbox[3] = {64u, (cuuint32_t)p.group, (cuuint32_t)(kTile / p.group)};
+    m->q_boxes = fn(&m->q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<uint16_t*>(p.q), qdims,
+                    qstr, qbox, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   return true;
 }
 
