@@ -30,7 +30,9 @@
 // A row's O is rescaled only when its maximum has grown by more than 2^8
 // since the last time (P stays below 2^8, in range for both 16-bit types, and
 // the final division removes the common factor), which leaves almost no
-// rescales after a row's first tiles.
+// rescales after a row's first tiles.  So the exponentials are taken against
+// the maximum of the tiles before, while this tile's is being looked for, and
+// taken again in the rare case that it has grown too much.
 //
 // Work.  All units' key tiles form one line (heads outermost) that
 // plan_kernel measures from the device-side lengths and cuts into equal
@@ -189,19 +191,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
 __device__ __forceinline__ bool wait_some(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\tmov.u32 %0, 1;\n\t"
       "WAIT:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "vote.sync.all.pred p, p, 0xffffffff;\n\t"
-      "@p bra.uni DONE;\n\t"
+      "@p bra.uni END;\n\t"
       "add.u32 n, n, 1;\n\t"
-      "setp.ge.u32 p, n, 64;\n\t"
-      "@p bra.uni FAIL;\n\t"
-      "bra.uni WAIT;\n\t"
-      "DONE:\n\tsetp.eq.u32 p, 0, 0;\n\t"
-      "bra.uni END;\n\t"
-      "FAIL:\n\tsetp.ne.u32 p, 0, 0;\n\t"
-      "END:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "setp.lt.u32 p, n, 64;\n\t"
+      "@p bra.uni WAIT;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "END:\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
@@ -657,6 +656,33 @@ __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.0f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
+// Scores of keys that the row does not see (before l0, after h0, in absent
+// pages) to -inf.
+template <int I0, int I1>
+__device__ __forceinline__ void mask_scores(float* s, int h0, int l0, uint32_t gm) {
+#pragma unroll
+  for (int i = I0; i < I1; i++)
+    if (i > h0 || i < l0 || (gm >> (i >> 4) & 1)) s[i] = -INFINITY;
+}
+
+// 64 softmax terms 2^(s c + n), their sum, and their 16-bit pairs.
+template <int MBF>
+__device__ __forceinline__ void take_terms(const float* s, uint32_t* pk, uint64_t& sum, uint64_t c,
+                                           uint64_t n) {
+  uint64_t part[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 32; i++) {
+    float x = s[2 * i], y = s[2 * i + 1];
+    fma2(x, y, c, n);
+    x = ex2(x);
+    y = ex2(y);
+    add2(part[i & 1], x, y);
+    pk[i] = pack2<MBF>(x, y);
+  }
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(part[0]) : "l"(part[1]));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(part[0]));
+}
+
 struct Maps {
   CUtensorMap k, v;
   int box;          // tokens of a box
@@ -812,45 +838,33 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         tc_fence_after();
         float s[kTile];
         uint32_t* sr = reinterpret_cast<uint32_t*>(s);
-        tmem_ld32(s_col, sr);
-        tmem_ld32(s_col + 32, sr + 32);
+#pragma unroll
+        for (int i = 0; i < 4; i++) tmem_ld32(s_col + 32 * i, sr + 32 * i);
         const uint32_t gm = gone[(base + j - r.j0) % kGone];
-        const bool masked = edge(r, j) || gm;
+#pragma unroll
+        for (int i = 0; i < 4; i++) tmem_ld32_wait(sr + 32 * i);
         const int k0 = (r.first + j) * kTile;
         const int h0 = hi - k0, l0 = lo - k0;
-        float mx[4];
-        // the second half is on its way while the first is looked through
+        const bool masked = edge(r, j) || gm;
+        if (masked) mask_scores<0, kTile>(s, h0, l0, gm);
+        // the first half's terms against the old maximum, and the new maximum
+        uint32_t pk[32];
+        uint64_t sum = 0;
+        take_terms<C::MBF>(s, pk, sum, both(c), both(-(m == -INFINITY ? 0.0f : m)));
+        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int half = 0; half < 2; half++) {
-          tmem_ld32_wait(sr + 64 * half);
-          tmem_ld32_wait(sr + 64 * half + 32);
-          if (half == 0) {
-            tmem_ld32(s_col + 64, sr + 64);
-            tmem_ld32(s_col + 96, sr + 96);
-          }
-          if (masked) {
+        for (int i = 4; i + 8 <= kTile; i += 8)
 #pragma unroll
-            for (int i = 64 * half; i < 64 * half + 64; i++)
-              if (i > h0 || i < l0 || (gm >> (i >> 4) & 1)) s[i] = -INFINITY;
-          }
-          if (half == 0) {
+          for (int e = 0; e < 4; e++) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
 #pragma unroll
-            for (int e = 0; e < 4; e++) mx[e] = fmaxf(s[2 * e], s[2 * e + 1]);
-          }
-#pragma unroll
-          for (int i = 64 * half + (half ? 0 : 8); i < 64 * half + 64; i += 8)
-#pragma unroll
-            for (int e = 0; e < 4; e++) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
-        }
+        for (int e = 0; e < 4; e++) mx[e] = fmaxf(mx[e], s[kTile - 4 + e]);
         const float mn = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c);
-        if (j == j0) {
-          m = mn;
-        } else {
-          const bool grow = mn > m + kRescale || (m == -INFINITY && mn > m);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? ex2(m - mn) : 1.0f;
-            if (grow) m = mn;
-            l *= f;
+        const bool grow = mn > m + kRescale || (m == -INFINITY && mn > m);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2(m - mn) : 1.0f;
+          if (grow) m = mn;
+          l *= f;
+          if (j > j0) {
             // (the scores of this tile are complete, so the product before
             // them, the last that added to O, is too)
             const uint64_t f2 = both(f);
@@ -864,29 +878,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               tmem_st16(o_col + 16 * i, o);
             }
           }
+          sum = 0;
+          take_terms<C::MBF>(s, pk, sum, both(c), both(-(m == -INFINITY ? 0.0f : m)));
         }
-        const float ms = m == -INFINITY ? 0.0f : m;
-        const uint64_t c2 = both(c), n2 = both(-ms);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int half = 0; half < 2; half++) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; i++) {
-            float &x = s[64 * half + 2 * i], &y = s[64 * half + 2 * i + 1];
-            fma2(x, y, c2, n2);
-            x = ex2(x);
-            y = ex2(y);
-            add2(sum[i & 1], x, y);
-            pk[i] = pack2<C::MBF>(x, y);
-          }
+        auto hand_over = [&](int half) {
           tmem_st32(s_col + 32 * half, pk);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
-        }
-        l += sum2(sum[0]) + sum2(sum[1]);
+        };
+        hand_over(0);
+        take_terms<C::MBF>(s + 64, pk, sum, both(c), both(-(m == -INFINITY ? 0.0f : m)));
+        l += sum2(sum);
+        hand_over(1);
       }
       if (!ok) break;
       base += r.j1 - r.j0;
@@ -977,70 +982,115 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0, nrec = 0;
       uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // stage and parity of the next K, V
       bool ok = true;
-      auto pv = [&](int t, uint32_t& np, bool acc) {
-        const uint32_t o = 2 * kTile + t * D, a = t * kTile;
-        const uint64_t vd = vd0 + (uint64_t)(__reduce_max_sync(0xffffffffu, vs) * (C::kOp >> 4));
+      // operands of a ring stage, in uniform registers
+      auto v_desc = [&] {
+        return vd0 + (uint64_t)(__reduce_max_sync(0xffffffffu, vs) * (C::kOp >> 4));
+      };
+      auto k_desc = [&] {
+        return kd0 + (uint64_t)(__reduce_max_sync(0xffffffffu, ks) * (C::kOp >> 4));
+      };
+      auto step = [&](uint32_t& st, uint32_t& par) {
+        st += 2;
+        if (st >= C::kStages) {
+          st -= C::kStages;
+          par ^= 1;
+        }
+      };
+      // O += P V of row tile t; P comes in two halves of the keys
+      auto pv = [&](int t, uint32_t par, uint64_t vd, uint32_t acc) {
 #pragma unroll
         for (int half = 0; half < 2; half++) {
-          if (!wait(&p_full[2 * t + half], np & 1)) return false;
+          ok &= wait(&p_full[2 * t + half], par);
           tc_fence_after();
 #pragma unroll
           for (int k = 4 * half; k < 4 * half + 4; k++)
-            umma_ts(o, a + 8 * k, vd + k * (2048 >> 4), id_pv, acc || k > 0);
+            umma_ts(2 * kTile + t * D, t * kTile + 8 * k, vd + k * (2048 >> 4), id_pv,
+                    k > 0 ? 1u : acc);
         }
-        np++;
-        return true;
       };
-      auto qk = [&](int t, uint32_t& nq, bool first, bool last) {
-        if (first && !wait(&q_full[t], nq++ & 1)) return false;
-        tc_fence_after();
-        const uint64_t kd = kd0 + (uint64_t)(__reduce_max_sync(0xffffffffu, ks) * (C::kOp >> 4)), q = qd + t * (C::kOp >> 4);
+      // S = Q K^T of row tile t, its MMAs k0 .. k1
+      auto qk = [&](int t, uint64_t kd, int k0, int k1) {
 #pragma unroll
         for (int k = 0; k < D / 16; k++) {
           const uint64_t off = (uint64_t)(((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4);
-          umma_ss(t * kTile, q + off, kd + off, id_qk, k > 0);
+          if (k >= k0 && k < k1)
+            umma_ss(t * kTile, qd + t * (C::kOp >> 4) + off, kd + off, id_qk, k > 0);
         }
-        commit(&s_full[t]);
-        if (last) commit(&q_free[t]);
-        return true;
       };
+      constexpr int kHalfK = D / 32;
       while (ok) {
         const Rec r = next_rec(nrec);
         if (!r.live) break;
         const int j0 = r.j0, j1 = r.j1, a0 = r.t0a, e0 = r.t0e, a1 = r.t1a, e1 = r.t1e;
         if (j1 <= j0) continue;
+        bool pv0 = false, pv1 = false;      // row tiles whose P V of j - 1 is due
+        // steps in which both row tiles have a P V, not their first, and a Q K,
+        // not their last
+        const int f0 = max(a0, a1) + 2, f1 = min(e0, e1) - 1;
         for (int j = j0; j <= j1; j++) {
+          if (j >= f0 && j < f1) {
+            // the steady state: between the MMAs only the waits for P.  The
+            // issue of MMAs blocks while the tensor core is busy and leaves it
+            // a few MMAs ahead at most, so every other wait, and whatever else
+            // there is to do, goes between the MMAs of the second Q K.
+            ok = wait(&kv_full[vs], vp) && wait(&kv_full[ks], kp);
+            uint64_t vd = v_desc(), kd = k_desc();
+            for (; ok && j < f1; j++) {
+              pv(0, np0++ & 1, vd, 1);
+              qk(0, kd, 0, D / 16);
+              commit(&s_full[0]);
+              pv(1, np1++ & 1, vd, 1);
+              commit(&kv_empty[vs]);
+              qk(1, kd, 0, kHalfK);
+              step(vs, vp);
+              const uint32_t k_old = ks;
+              const uint64_t kd_old = kd;
+              step(ks, kp);
+              if (j + 1 < f1) {
+                ok &= wait(&kv_full[vs], vp) && wait(&kv_full[ks], kp);
+                vd = v_desc();
+                kd = k_desc();
+              }
+              qk(1, kd_old, kHalfK, D / 16);
+              commit(&s_full[1]);
+              commit(&kv_empty[k_old]);
+            }
+            if (!ok) break;
+          }
           const bool has_v = j > j0, has_k = j < j1;
+          const bool qk0 = has_k && j >= a0 && j < e0, qk1 = has_k && j >= a1 && j < e1;
           if (has_v && !(ok = wait(&kv_full[vs], vp))) break;
-          if (has_v && j > a0 && j <= e0) {
-            if (!(ok = pv(0, np0, j - 1 > a0))) break;
-            if (j == e0) commit(&o_full[0]);
+          const uint64_t vd = v_desc(), kd = k_desc();
+          if (pv0) pv(0, np0++ & 1, vd, j - 1 > a0);
+          if (pv0 && !qk0) commit(&o_full[0]);
+          if (has_k) ok &= wait(&kv_full[ks], kp);
+          if (qk0) {
+            if (j == a0) ok &= wait(&q_full[0], nq0++ & 1);
+            tc_fence_after();
+            qk(0, kd, 0, D / 16);
+            commit(&s_full[0]);
+            if (j == e0 - 1) commit(&q_free[0]);
           }
-          if (has_k) {
-            if (!(ok = wait(&kv_full[ks], kp))) break;
-            if (j >= a0 && j < e0 && !(ok = qk(0, nq0, j == a0, j == e0 - 1))) break;
-          }
+          if (pv1) pv(1, np1++ & 1, vd, j - 1 > a1);
+          if (pv1 && !qk1) commit(&o_full[1]);
           if (has_v) {
-            if (j > a1 && j <= e1) {
-              if (!(ok = pv(1, np1, j - 1 > a1))) break;
-              if (j == e1) commit(&o_full[1]);
-            }
             commit(&kv_empty[vs]);
-            vs += 2;
-            if (vs >= C::kStages) {
-              vs -= C::kStages;
-              vp ^= 1;
-            }
+            step(vs, vp);
+          }
+          if (qk1) {
+            if (j == a1) ok &= wait(&q_full[1], nq1++ & 1);
+            tc_fence_after();
+            qk(1, kd, 0, D / 16);
+            commit(&s_full[1]);
+            if (j == e1 - 1) commit(&q_free[1]);
           }
           if (has_k) {
-            if (j >= a1 && j < e1 && !(ok = qk(1, nq1, j == a1, j == e1 - 1))) break;
             commit(&kv_empty[ks]);
-            ks += 2;
-            if (ks >= C::kStages) {
-              ks -= C::kStages;
-              kp ^= 1;
-            }
+            step(ks, kp);
           }
+          pv0 = qk0;
+          pv1 = qk1;
+          if (!ok) break;
         }
       }
       commit(all_done);
