@@ -419,7 +419,8 @@ size_t exl3_paged_attention_workspace_size(int T, int heads, int kv_heads, int h
  * included.
  *   q      device, element t*q_token_stride + h*q_head_stride + c, strides
  *          multiples of 8
- *   out    device [T][heads][head_dim] in dt; may not overlap q
+ *   out    device [T][heads][head_dim] in dt, 32-byte aligned; may not
+ *          overlap q
  *   lse    device fp32 [T][heads] or NULL: natural log of the sum of
  *          exp(scale * q . k)
  *   path   EXL3_PATH_AUTO, or a fixed kernel: 1 warp-level MMA (few rows),

@@ -195,7 +195,9 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   if (q_token_stride % 8 || q_head_stride % 8 || q_token_stride < 0 || q_head_stride < 0)
     return EXL3_ERR_ARG;
   if (T == 0 || batch->num_seqs == 0) return EXL3_OK;
-  if (!good(q) || !good(out) || (reinterpret_cast<uintptr_t>(lse) & 3)) return EXL3_ERR_ARG;
+  if (!good(q) || !out || (reinterpret_cast<uintptr_t>(out) & 31) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3))
+    return EXL3_ERR_ARG;
   if (!good(ws) || ws_bytes < exl3_paged_attention_workspace_size(T, heads, cache->kv_heads,
                                                                   cache->head_dim, batch->num_seqs))
     return EXL3_ERR_WORKSPACE;
@@ -216,7 +218,6 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   p.bf16 = dt == EXL3_BF16;
   p.e4m3 = cache->dtype == EXL3_E4M3;
   p.dim = cache->head_dim;
-  p.out32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   p.status = static_cast<int32_t*>(ws);
   p.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
   p.scratch = static_cast<uint8_t*>(ws) + kHead;

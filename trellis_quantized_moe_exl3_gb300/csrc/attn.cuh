@@ -97,7 +97,6 @@ struct AttnParams {
   float scale_log2;  // scale * log2(e)
   int causal, window;
   int bf16, e4m3, dim;
-  int out32;  // out is 32-byte aligned
   int32_t* status;
   int32_t* counters;  // [kRowsCounters], zero between calls
   void* scratch;

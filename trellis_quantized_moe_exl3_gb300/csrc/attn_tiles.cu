@@ -70,12 +70,13 @@ struct Cfg {
   static constexpr int MBF = BF && !E8;                  // type of the products
   static constexpr int kOp = kTile * D * 2;              // bytes of a 16-bit operand tile
   static constexpr int kRaw = kTile * D;                 // bytes of an E4M3 tile
-  static constexpr int kStages = E8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
-  static constexpr int kRawStages = E8 ? 4 : 0;
-  static constexpr int kOffKV = 2 * kOp;
-  static constexpr int kOffRaw = kOffKV + kStages * kOp;
-  static constexpr int kOffBar = kOffRaw + kRawStages * kRaw;
-  static constexpr int kBars = 3 * kStages + 2 * kRawStages + 15 + 2 * kUnits;
+  // two stages of K and two of V, so that a step's operands are known from the
+  // parity of its number (constants of the code for that parity)
+  static constexpr int kOffK = 2 * kOp;
+  static constexpr int kOffV = kOffK + 2 * kOp;
+  static constexpr int kOffRaw = kOffV + 2 * kOp;        // E4M3: one K and one V tile
+  static constexpr int kOffBar = kOffRaw + (E8 ? 2 * kRaw : 0);
+  static constexpr int kBars = 10 + 4 + 15 + 2 * kUnits;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffUnits = kOffMisc + kGone * 4 + 16;
   static constexpr int kSmem = kOffUnits + kUnits * kRecInts * 4;
@@ -218,9 +219,16 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, int32_t
   }
   return true;
 }
+// The long wait out of line (the roles' code has to stay in the instruction
+// caches): not for the softmax warps, whose registers a call would have to save.
+__device__ __noinline__ bool wait_long_call(uint32_t bar, uint32_t parity, int32_t* status) {
+  return wait_long(bar, parity, status);
+}
+template <bool CALL>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* status) {
   const uint32_t a = smem_u32(bar);
-  return wait_some(a, parity) || wait_long(a, parity, status);
+  if (__builtin_expect(wait_some(a, parity), 1)) return true;
+  return CALL ? wait_long_call(a, parity, status) : wait_long(a, parity, status);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -588,35 +596,45 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   return v;
 }
 
+// Top bits of the 16-bit values of w (of the bytes, E4M3) that are infinite or
+// NaN: adding one to an exponent of all ones carries into the sign's place.
+template <class C>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  if (C::E8) return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return C::BF ? ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u
+               : ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+}
+// The same values as a mask of all their bits.
+template <class C>
+__device__ __forceinline__ uint32_t whole_mask(uint32_t top) {
+  return C::E8 ? (top >> 7) * 0xFFu : (top >> 15) * 0xFFFFu;
+}
+
 // Zeroes the rows of a V tile outside [r0, r1) and replaces values that are
 // not finite by zero; returns whether there were any.  The rows that see them
 // get them back at the end (add_poison).
 template <class C>
 __device__ __forceinline__ bool clean_v(uint32_t v, int r0, int r1, int lane) {
-  constexpr uint32_t E = C::BF ? 0x7F807F80u : 0x7C007C00u;
-  constexpr int CH = C::D / 8;
+  constexpr int CH = C::D / 8, RI = 32 / CH;
   bool hit = false;
+  const int ch = lane % CH;
 #pragma unroll 1
-  for (int i0 = lane; i0 < kTile * CH; i0 += 32 * 8) {
-    uint4 x[8];
+  for (int rb = lane / CH; rb < kTile; rb += 4 * RI) {
+    uint4 x[4];
 #pragma unroll
-    for (int k = 0; k < 8; k++) {
-      const int i = i0 + 32 * k;
-      x[k] = lds16(v + op_off<C::D>(i / CH, i % CH));
-    }
+    for (int k = 0; k < 4; k++) x[k] = lds16(v + op_off<C::D>(rb + k * RI, ch));
 #pragma unroll
-    for (int k = 0; k < 8; k++) {
-      const int i = i0 + 32 * k, r = i / CH;
-      const uint32_t a = v + op_off<C::D>(r, i % CH);
+    for (int k = 0; k < 4; k++) {
+      const int r = rb + k * RI;
+      const uint32_t a = v + op_off<C::D>(r, ch);
+      const uint32_t m0 = not_finite<C>(x[k].x), m1 = not_finite<C>(x[k].y),
+                     m2 = not_finite<C>(x[k].z), m3 = not_finite<C>(x[k].w);
       if (r < r0 || r >= r1) {
         sts16(a, 0, 0, 0, 0);
-      } else {
-        const uint32_t m0 = __vcmpeq2(x[k].x & E, E), m1 = __vcmpeq2(x[k].y & E, E),
-                       m2 = __vcmpeq2(x[k].z & E, E), m3 = __vcmpeq2(x[k].w & E, E);
-        if (m0 | m1 | m2 | m3) {
-          hit = true;
-          sts16(a, x[k].x & ~m0, x[k].y & ~m1, x[k].z & ~m2, x[k].w & ~m3);
-        }
+      } else if (m0 | m1 | m2 | m3) {
+        hit = true;
+        sts16(a, x[k].x & ~whole_mask<C>(m0), x[k].y & ~whole_mask<C>(m1),
+              x[k].z & ~whole_mask<C>(m2), x[k].w & ~whole_mask<C>(m3));
       }
     }
   }
@@ -624,12 +642,12 @@ __device__ __forceinline__ bool clean_v(uint32_t v, int r0, int r1, int lane) {
 }
 
 // Adds the values that are not finite, in the mixed tiles of a part, of the
-// keys a row sees, to channels d0 .. d0 + 31 of its O.  keys0, keys1: the
+// keys a row sees, to its O as written: fp32 part, or out.  keys0, keys1: the
 // part's keys; all0, all1: those every row sees.
 template <class C>
 __device__ __noinline__ void add_poison(const Cache c, const int32_t* table, int h, int keys0,
                                         int keys1, int any0, int any1, int all0, int all1, int lo,
-                                        int hi, int d0, float* o) {
+                                        int hi, float* part, uint16_t* out) {
   for (int k0 = keys0; k0 < keys1; k0 += kTile) {
     if (!(max(k0, any0) < all0 || min(k0 + kTile, any1) > all1)) continue;
     for (int key = max(k0, lo); key <= min(k0 + kTile - 1, hi); key++) {
@@ -637,15 +655,17 @@ __device__ __noinline__ void add_poison(const Cache c, const int32_t* table, int
       if (page < 0 || page >= c.num_pages) continue;
       const uint8_t* v = c.v + page * c.page_bytes + (int64_t)(key % c.page_size) * c.token_bytes +
                          h * c.head_bytes;
-      for (int i = 0; i < 32; i++) {
+      for (int d = 0; d < C::D; d++) {
         float x;
-        if (C::E8) {
-          x = (v[d0 + i] & 0x7F) == 0x7F ? NAN : 0.0f;
-        } else {
-          x = load_act(v, C::BF, d0 + i);
-          if (isfinite(x)) x = 0.0f;
-        }
-        o[i] += x;
+        if (C::E8)
+          x = (v[d] & 0x7F) == 0x7F ? NAN : 0.0f;
+        else
+          x = load_act(v, C::BF, d);
+        if (isfinite(x)) continue;
+        if (part)
+          part[d] += x;
+        else
+          out[d] = (uint16_t)pack2<C::BF>(load_act(out, C::BF, d) + x, 0.0f);
       }
     }
   }
@@ -658,11 +678,16 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 
 // Scores of keys that the row does not see (before l0, after h0, in absent
 // pages) to -inf.
-template <int I0, int I1>
 __device__ __forceinline__ void mask_scores(float* s, int h0, int l0, uint32_t gm) {
 #pragma unroll
-  for (int i = I0; i < I1; i++)
-    if (i > h0 || i < l0 || (gm >> (i >> 4) & 1)) s[i] = -INFINITY;
+  for (int w = 0; w < kTile / 32; w++) {
+    const int a = min(max(l0 - 32 * w, 0), 32), b = min(max(h0 + 1 - 32 * w, 0), 32);
+    uint32_t seen = a < b ? (0xffffffffu << a) & (0xffffffffu >> (32 - b)) : 0u;
+    seen &= ~((gm >> (2 * w) & 1 ? 0x0000ffffu : 0u) | (gm >> (2 * w) & 2 ? 0xffff0000u : 0u));
+#pragma unroll
+    for (int i = 0; i < 32; i++)
+      if (!(seen >> i & 1)) s[32 * w + i] = -INFINITY;
+  }
 }
 
 // 64 softmax terms 2^(s c + n), their sum, and their 16-bit pairs.
@@ -700,12 +725,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   // are known to be uniform; checked below)
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* kv_empty = kv_full + C::kStages;
-  uint64_t* edge_full = kv_empty + C::kStages;   // V tiles on their way to the cleaner
-  uint64_t* raw_full = edge_full + C::kStages;
-  uint64_t* raw_empty = raw_full + C::kRawStages;
-  uint64_t* q_full = raw_empty + C::kRawStages;  // [2] each: row tiles
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [2] each: stages
+  uint64_t* k_empty = k_full + 2;
+  uint64_t* v_full = k_empty + 2;
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* edge_full = v_empty + 2;             // V tiles on their way to the cleaner
+  uint64_t* raw_full = edge_full + 2;            // E4M3 tiles: K, V
+  uint64_t* raw_empty = raw_full + 2;
+  uint64_t* q_full = raw_empty + 2;              // [2] each: row tiles
   uint64_t* q_raw = q_full + 2;                  // queries still in bf16
   uint64_t* q_free = q_raw + 2;
   uint64_t* s_full = q_free + 2;
@@ -721,12 +748,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; i++) {
-      mbar_init(&kv_full[i], C::E8 ? 4 : 1);
-      mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&k_full[i], C::E8 ? 4 : 1);
+      mbar_init(&v_full[i], C::E8 ? 4 : 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_empty[i], 1);
       mbar_init(&edge_full[i], 1);
-    }
-    for (int i = 0; i < C::kRawStages; i++) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
     }
@@ -761,11 +788,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   pdl_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return wait_warp(bar, parity, p.status);
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp<true>(bar, parity, p.status); };
   // the next published part, for a whole warp; live = 0 at the end or on abort
-  auto next_rec = [&](uint32_t& n) {
+  auto next_rec = [&](uint32_t& n, auto wait) {
     const uint32_t i = n % kUnits;
     if (!wait(&u_full[i], (n / kUnits) & 1)) return Rec{};
     const Rec r = recs[i];
@@ -778,6 +803,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if (warp < 8) {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return wait_warp<false>(bar, parity, p.status);
+    };
     const int t = warp >> 2, q4 = warp & 3;
     const int row = 32 * q4 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
@@ -788,7 +816,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     uint32_t nrec = 0, uses = 0;  // parts seen, those of them with keys for this tile
     bool ok = true;
     while (ok) {
-      const Rec r = next_rec(nrec);
+      const Rec r = next_rec(nrec, wait);
       if (!r.live) break;
       const int nt = min(kTile, r.nrows - t * kTile);  // rows of the tile
       const int j0 = t ? r.t1a : r.t0a, j1 = t ? r.t1e : r.t0e;
@@ -846,7 +874,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int k0 = (r.first + j) * kTile;
         const int h0 = hi - k0, l0 = lo - k0;
         const bool masked = edge(r, j) || gm;
-        if (masked) mask_scores<0, kTile>(s, h0, l0, gm);
+        if (masked) mask_scores(s, h0, l0, gm);
         // the first half's terms against the old maximum, and the new maximum
         uint32_t pk[32];
         uint64_t sum = 0;
@@ -905,11 +933,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + r.h) : 1.0f;
       const float inv = whole ? row_inverse(l, vs) : 1.0f;
       const uint64_t inv2 = both(inv);
-      const bool bad_v = *poison != 0;
       const int prt = t * kTile + row;
       float* part = pl.parts + ((size_t)blockIdx.x * 2 + (r.flags >> 1)) * part_floats(D);
       uint16_t* out = p.out + ((int64_t)token * p.heads + head) * D;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < D / 32; i++) {
         float o[32];
         uint32_t* orr = reinterpret_cast<uint32_t*>(o);
@@ -922,16 +949,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           for (int e = 0; e < 32; e++) o[e] = 0.0f;
         }
         if (row < nt) {
-          if (bad_v) {
-            float tmp[32];
-#pragma unroll
-            for (int e = 0; e < 32; e++) tmp[e] = o[e];
-            add_poison<C>(p.cache, p.batch.table + (int64_t)r.b * p.batch.table_stride, r.h,
-                          (r.first + r.s0) * kTile, (r.first + r.s1) * kTile, r.any0, r.any1,
-                          r.all0, r.all1, lo, hi, 32 * i, tmp);
-#pragma unroll
-            for (int e = 0; e < 32; e++) o[e] = tmp[e];
-          }
           if (whole) {
             uint32_t w[16];
 #pragma unroll
@@ -940,16 +957,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               w[e] = pack2<C::BF>(o[2 * e], o[2 * e + 1]);
             }
 #pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              if (p.out32)
-                stg32(out + 32 * i + 2 * e, w[e], w[e + 1], w[e + 2], w[e + 3], w[e + 4], w[e + 5],
-                      w[e + 6], w[e + 7]);
-              else {
-                uint4* d = reinterpret_cast<uint4*>(out + 32 * i + 2 * e);
-                d[0] = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
-                d[1] = make_uint4(w[e + 4], w[e + 5], w[e + 6], w[e + 7]);
-              }
-            }
+            for (int e = 0; e < 16; e += 8)
+              stg32(out + 32 * i + 2 * e, w[e], w[e + 1], w[e + 2], w[e + 3], w[e + 4], w[e + 5],
+                    w[e + 6], w[e + 7]);
           } else {
             float* dst = part + (size_t)prt * D + 32 * i;
 #pragma unroll
@@ -961,6 +971,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       tc_fence_before();  // O is read before the next unit's first product writes it
       if (row < nt) {
+        if (*poison != 0)
+          add_poison<C>(p.cache, p.batch.table + (int64_t)r.b * p.batch.table_stride, r.h,
+                        (r.first + r.s0) * kTile, (r.first + r.s1) * kTile, r.any0, r.any1, r.all0,
+                        r.all1, lo, hi, whole ? nullptr : part + (size_t)prt * D, out);
         if (!whole)
           *reinterpret_cast<float2*>(part + (size_t)kUnitRows * D + 2 * prt) = make_float2(m, l);
         else if (p.lse)
@@ -970,146 +984,115 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   } else if (warp == 8) {
     // ------------------------------------------------------------------ MMA
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
-    {
-      const uint32_t bf = C::MBF ? (1u << 7) | (1u << 10) : 0u;
-      const uint32_t id_qk = umma_idesc_f16(kTile, kTile, 0, 0) | bf;
-      const uint32_t id_pv = umma_idesc_f16(kTile, D, 0, 1) | bf;
-      const uint64_t qd = umma_desc(sbase, 16, 1024);
-      // V: rows of 128 bytes hold 64 channels of one key; 8 keys 1024 B, the
-      // second 64 channels kTile * 128 B on
-      const uint64_t kd0 = umma_desc(sbase + C::kOffKV, 16, 1024);
-      const uint64_t vd0 = umma_desc(sbase + C::kOffKV, kTile * 128, 1024);
-      uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0, nrec = 0;
-      uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // stage and parity of the next K, V
-      bool ok = true;
-      // operands of a ring stage, in uniform registers
-      auto v_desc = [&] {
-        return vd0 + (uint64_t)(__reduce_max_sync(0xffffffffu, vs) * (C::kOp >> 4));
-      };
-      auto k_desc = [&] {
-        return kd0 + (uint64_t)(__reduce_max_sync(0xffffffffu, ks) * (C::kOp >> 4));
-      };
-      auto step = [&](uint32_t& st, uint32_t& par) {
-        st += 2;
-        if (st >= C::kStages) {
-          st -= C::kStages;
-          par ^= 1;
-        }
-      };
-      // O += P V of row tile t; P comes in two halves of the keys
-      auto pv = [&](int t, uint32_t par, uint64_t vd, uint32_t acc) {
+    // (no call in this role: a call would cost the operands their uniform
+    // registers)
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return wait_warp<false>(bar, parity, p.status);
+    };
+    constexpr uint32_t bf = C::MBF ? (1u << 7) | (1u << 10) : 0u;
+    const uint32_t id_qk = umma_idesc_f16(kTile, kTile, 0, 0) | bf;
+    const uint32_t id_pv = umma_idesc_f16(kTile, D, 0, 1) | bf;
+    uint32_t nq = 0, np = 0;        // bit t: parity of row tile t's next queries, P
+    uint32_t n = 0, nrec = 0;       // steps so far: K and V of step n are in stage n & 1
+    bool ok = true;
+    const uint64_t qd0 = umma_desc(sbase, 16, 1024);
+    auto uni = [](uint32_t x) { return __reduce_max_sync(0xffffffffu, x); };
+    const uint32_t q_lo = (uint32_t)qd0;
+    const uint32_t k_lo = q_lo + (C::kOffK >> 4);
+    constexpr uint32_t kHi = (1024 >> 4) | (1u << 14) | (2u << 29);  // high word of all three
+    auto desc = [&](uint32_t lo) {
+      uint64_t d;
+      asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kHi));
+      return d;
+    };
+    // V: rows of 128 bytes hold 64 channels of one key; 8 keys 1024 B, the
+    // second 64 channels kTile * 128 B on
+    const uint32_t v_lo = (uint32_t)umma_desc(sbase + C::kOffV, kTile * 128, 1024);
+    // (an MMA takes ~30 instructions in the code, few of them executed; a step
+    // is written once, with 8 of them, so that it stays in the instruction
+    // caches beside the softmax)
+    auto wait_kv = [&](uint64_t* full, uint32_t i) { return wait(&full[i & 1], (i >> 1) & 1); };
+    while (ok) {
+      const Rec r = next_rec(nrec, wait);
+      if (!r.live) break;
+      if (r.j1 <= r.j0) continue;
+      uint32_t due = 0;             // bit t: row tile t's P V of the step before is due
+      ok = wait_kv(k_full, n);
+#pragma unroll 1
+      for (int j = r.j0; ok && j <= r.j1; j++) {
+        const bool has_v = j > r.j0, has_k = j < r.j1;
+        const uint32_t now = (has_k && j >= r.t0a && j < r.t0e ? 1u : 0u) |
+                             (has_k && j >= r.t1a && j < r.t1e ? 2u : 0u);
+        const uint32_t vd = v_lo + ((n - 1) & 1) * (C::kOp >> 4);
+        const uint32_t kd = k_lo + (n & 1) * (C::kOp >> 4);
+#pragma unroll 1
+        for (int t = 0; t < 2; t++) {
+          const int a = t ? r.t1a : r.t0a, e = t ? r.t1e : r.t0e;
+          if (due >> t & 1) {
+            // O += P V; P comes in two halves of the keys
+            uint32_t acc = j - 1 > a;
+            const uint32_t o = uni(2 * kTile + t * D);
+#pragma unroll 1
+            for (int half = 0; half < 2; half++) {
+              const uint32_t pa = uni(t * kTile + 32 * half);
+              const uint32_t v = uni(vd + half * (4 * 2048 >> 4)), ac = uni(acc);
+              ok &= wait(&p_full[2 * t + half], np >> t & 1);
+              tc_fence_after();
 #pragma unroll
-        for (int half = 0; half < 2; half++) {
-          ok &= wait(&p_full[2 * t + half], par);
-          tc_fence_after();
-#pragma unroll
-          for (int k = 4 * half; k < 4 * half + 4; k++)
-            umma_ts(2 * kTile + t * D, t * kTile + 8 * k, vd + k * (2048 >> 4), id_pv,
-                    k > 0 ? 1u : acc);
-        }
-      };
-      // S = Q K^T of row tile t, its MMAs k0 .. k1
-      auto qk = [&](int t, uint64_t kd, int k0, int k1) {
-#pragma unroll
-        for (int k = 0; k < D / 16; k++) {
-          const uint64_t off = (uint64_t)(((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4);
-          if (k >= k0 && k < k1)
-            umma_ss(t * kTile, qd + t * (C::kOp >> 4) + off, kd + off, id_qk, k > 0);
-        }
-      };
-      constexpr int kHalfK = D / 32;
-      while (ok) {
-        const Rec r = next_rec(nrec);
-        if (!r.live) break;
-        const int j0 = r.j0, j1 = r.j1, a0 = r.t0a, e0 = r.t0e, a1 = r.t1a, e1 = r.t1e;
-        if (j1 <= j0) continue;
-        bool pv0 = false, pv1 = false;      // row tiles whose P V of j - 1 is due
-        // steps in which both row tiles have a P V, not their first, and a Q K,
-        // not their last
-        const int f0 = max(a0, a1) + 2, f1 = min(e0, e1) - 1;
-        for (int j = j0; j <= j1; j++) {
-          if (j >= f0 && j < f1) {
-            // the steady state: between the MMAs only the waits for P.  The
-            // issue of MMAs blocks while the tensor core is busy and leaves it
-            // a few MMAs ahead at most, so every other wait, and whatever else
-            // there is to do, goes between the MMAs of the second Q K.
-            ok = wait(&kv_full[vs], vp) && wait(&kv_full[ks], kp);
-            uint64_t vd = v_desc(), kd = k_desc();
-            for (; ok && j < f1; j++) {
-              pv(0, np0++ & 1, vd, 1);
-              qk(0, kd, 0, D / 16);
-              commit(&s_full[0]);
-              pv(1, np1++ & 1, vd, 1);
-              commit(&kv_empty[vs]);
-              qk(1, kd, 0, kHalfK);
-              step(vs, vp);
-              const uint32_t k_old = ks;
-              const uint64_t kd_old = kd;
-              step(ks, kp);
-              if (j + 1 < f1) {
-                ok &= wait(&kv_full[vs], vp) && wait(&kv_full[ks], kp);
-                vd = v_desc();
-                kd = k_desc();
-              }
-              qk(1, kd_old, kHalfK, D / 16);
-              commit(&s_full[1]);
-              commit(&kv_empty[k_old]);
+              for (int k = 0; k < 4; k++)
+                umma_ts(o, pa + 8 * k, desc(v + k * (2048 >> 4)), id_pv, k > 0 ? 1u : ac);
+              acc = 1;
             }
-            if (!ok) break;
+            np ^= 1u << t;
+            if (!(now >> t & 1)) commit(&o_full[t]);
           }
-          const bool has_v = j > j0, has_k = j < j1;
-          const bool qk0 = has_k && j >= a0 && j < e0, qk1 = has_k && j >= a1 && j < e1;
-          if (has_v && !(ok = wait(&kv_full[vs], vp))) break;
-          const uint64_t vd = v_desc(), kd = k_desc();
-          if (pv0) pv(0, np0++ & 1, vd, j - 1 > a0);
-          if (pv0 && !qk0) commit(&o_full[0]);
-          if (has_k) ok &= wait(&kv_full[ks], kp);
-          if (qk0) {
-            if (j == a0) ok &= wait(&q_full[0], nq0++ & 1);
+          if (t == 1 && has_v) commit(&v_empty[(n - 1) & 1]);
+          if (now >> t & 1) {
+            if (j == a) {
+              ok &= wait(&q_full[t], nq >> t & 1);
+              nq ^= 1u << t;
+            }
+            // S = Q K^T, 64 channels at a time
             tc_fence_after();
-            qk(0, kd, 0, D / 16);
-            commit(&s_full[0]);
-            if (j == e0 - 1) commit(&q_free[0]);
+#pragma unroll 1
+            for (int x = 0; x < D / 64; x++) {
+              const uint32_t off = x * (kTile * 128 >> 4);
+              const uint32_t qd = uni(q_lo + t * (C::kOp >> 4) + off), kx = uni(kd + off);
+              const uint32_t sc = uni(t * kTile), ac = uni(x);
+#pragma unroll
+              for (int k = 0; k < 4; k++)
+                umma_ss(sc, desc(qd + 2 * k), desc(kx + 2 * k), id_qk, k > 0 ? 1u : ac);
+              // The issue of MMAs blocks while the tensor core is busy and
+              // leaves it a few MMAs ahead at most: the next step's waits go
+              // here, between MMAs.
+              if (x == 0 && t == 1)
+                ok = ok && wait_kv(v_full, n) && (j + 1 >= r.j1 || wait_kv(k_full, n + 1));
+            }
+            commit(&s_full[t]);
+            if (j == e - 1) commit(&q_free[t]);
+          } else if (t == 1 && j < r.j1) {
+            ok = ok && wait_kv(v_full, n) && (j + 1 >= r.j1 || wait_kv(k_full, n + 1));
           }
-          if (pv1) pv(1, np1++ & 1, vd, j - 1 > a1);
-          if (pv1 && !qk1) commit(&o_full[1]);
-          if (has_v) {
-            commit(&kv_empty[vs]);
-            step(vs, vp);
-          }
-          if (qk1) {
-            if (j == a1) ok &= wait(&q_full[1], nq1++ & 1);
-            tc_fence_after();
-            qk(1, kd, 0, D / 16);
-            commit(&s_full[1]);
-            if (j == e1 - 1) commit(&q_free[1]);
-          }
-          if (has_k) {
-            commit(&kv_empty[ks]);
-            step(ks, kp);
-          }
-          pv0 = qk0;
-          pv1 = qk1;
-          if (!ok) break;
         }
+        if (has_k) {
+          commit(&k_empty[n & 1]);
+          n++;
+        }
+        due = now;
       }
-      commit(all_done);
     }
+    commit(all_done);
   } else if (warp == 9) {
     // ------------------------------------------------------------ work, TMA
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
-    constexpr int ST = C::E8 ? C::kRawStages : C::kStages;
     constexpr int HALF = C::E8 ? 1 : D / 64;      // boxes across the channels
     constexpr uint32_t BYTES = C::E8 ? C::kRaw : C::kOp;
-    uint64_t* full = C::E8 ? raw_full : kv_full;
-    uint64_t* empty = C::E8 ? raw_empty : kv_empty;
-    const uint32_t ring = sbase + (C::E8 ? C::kOffRaw : C::kOffKV);
     const int nbox = kTile / maps.box;
     const int bx = lane / HALF, half = lane % HALF;
     const bool mine = bx < nbox;
     const int ps = p.cache.page_size, ps_shift = p.cache.page_shift;
-    uint32_t load = 0, nrec = 0;
-    uint32_t to_edge = 0, edge_par = 0;  // per stage: its last load went to the cleaner; its parity
+    uint32_t n = 0, nrec = 0;            // steps so far
+    uint32_t to_edge = 0, edge_par = 0;  // per V stage: its last load went to the cleaner; its parity
     int32_t bad = 0;
     bool ok = true;
     Walk w(p, pl);
@@ -1145,39 +1128,53 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         g = __reduce_or_sync(0xffffffffu, g);
         if (g) bad |= kStatusBadPage;
         const int at = ps_shift >= 0 ? key & (ps - 1) : key % ps;
+        const uint32_t st = n & 1, par = (n >> 1) & 1;
+#pragma unroll 1
         for (int x = 0; x < 2; x++) {  // K, V
-          const uint32_t st = load % ST;
-          if (!(ok = wait(&empty[st], ((load / ST) & 1) ^ 1))) break;
-          const bool cleaner = !C::E8 && x == 1 && edge(r, j);
-          uint64_t* bar = cleaner ? &edge_full[st] : &full[st];
-          to_edge = cleaner ? to_edge | (1u << st) : to_edge & ~(1u << st);
-          if (cleaner) edge_par ^= 1u << st;
+          uint64_t* const full = C::E8 ? &raw_full[x] : x ? &v_full[st] : &k_full[st];
+          uint64_t* const empty = C::E8 ? &raw_empty[x] : x ? &v_empty[st] : &k_empty[st];
+          if (!(ok = wait(empty, (C::E8 ? n & 1 : par) ^ 1))) break;
+          uint64_t* bar = full;
+          if (!C::E8 && x == 1) {
+            to_edge &= ~(1u << st);
+            if (edge(r, j)) {
+              bar = &edge_full[st];
+              to_edge |= 1u << st;
+              edge_par ^= 1u << st;
+            }
+          }
           if (lane == 0) {
-            if (x == 0) gone[(load >> 1) % kGone] = g;
+            if (x == 0) gone[n % kGone] = g;
             mbar_arrive_expect_tx(bar, BYTES);
           }
           __syncwarp();
           if (mine) {
-            const uint32_t dst = ring + st * BYTES + half * (kTile * 128) +
-                                 bx * maps.box * (C::E8 ? D : 128);
+            const uint32_t ring = sbase + (C::E8 ? C::kOffRaw + x * C::kRaw
+                                                 : (x ? C::kOffV : C::kOffK) + st * C::kOp);
+            const uint32_t dst = ring + half * (kTile * 128) + bx * maps.box * (C::E8 ? D : 128);
             const CUtensorMap* m = x == 0 ? &maps.k : &maps.v;
             if (maps.heads_first)
               tma_load_4d(dst, m, half * 64, r.h, at, page, bar);
             else
               tma_load_4d(dst, m, half * 64, at, r.h, page, bar);
           }
-          load++;
         }
+        if (!ok) break;
+        n++;
       }
     }
     if (bad && lane == 0) atomicOr(p.status, bad);
-    // every box this warp requested has landed before the CTA may exit
-    for (uint32_t i = load < ST ? 0 : load - ST; i < load; i++) {
-      const uint32_t st = i % ST;
-      if (to_edge >> st & 1)
-        mbar_drain(&edge_full[st], (edge_par >> st & 1) ^ 1, kWaitBudgetCycles);
-      else
-        mbar_drain(&full[st], (i / ST) & 1, kWaitBudgetCycles);
+    // every box this warp requested has landed before the CTA may exit (after
+    // a wait that ran out, a step's K may be under way without its V)
+#pragma unroll 1
+    for (uint32_t i = n < 2 ? 0 : n - (C::E8 ? 1 : 2); i < n + (ok ? 0 : 1); i++) {
+      const uint32_t st = i & 1, par = (i >> 1) & 1;
+      const long long budget = i < n ? kWaitBudgetCycles : 100000;
+      mbar_drain(C::E8 ? &raw_full[0] : &k_full[st], C::E8 ? i & 1 : par, budget);
+      if (i == n) break;
+      const bool e = to_edge >> st & 1;
+      mbar_drain(C::E8 ? &raw_full[1] : e ? &edge_full[st] : &v_full[st],
+                 C::E8 ? i & 1 : e ? (edge_par >> st & 1) ^ 1 : par, budget);
     }
   } else if (warp == 11) {
     // -------------------------------------------------------------- queries
@@ -1185,7 +1182,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     uint32_t nrec = 0, n[2] = {0, 0};
     bool ok = true;
     while (ok) {
-      const Rec r = next_rec(nrec);
+      const Rec r = next_rec(nrec, wait);
       if (!r.live) break;
 #pragma unroll
       for (int t = 0; t < 2; t++) {
@@ -1244,25 +1241,25 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
     if constexpr (!C::E8) {
       // ---------------------------------------------------- clean V tiles
-      uint32_t nrec = 0, load = 0, par = 0;
+      uint32_t nrec = 0, n = 0, par = 0;
       bool ok = true;
       while (ok) {
-        const Rec r = next_rec(nrec);
+        const Rec r = next_rec(nrec, wait);
         if (!r.live) break;
-        for (int j = r.j0; ok && j < r.j1; j++, load += 2) {
+        for (int j = r.j0; ok && j < r.j1; j++, n++) {
           if (!edge(r, j)) continue;
-          const uint32_t st = (load + 1) % C::kStages;
+          const uint32_t st = n & 1;
           if (!(ok = wait(&edge_full[st], par >> st & 1))) break;
           par ^= 1u << st;
           const int k0 = (r.first + j) * kTile;
-          if (__any_sync(0xffffffffu, clean_v<C>(sbase + C::kOffKV + st * C::kOp, r.any0 - k0,
+          if (__any_sync(0xffffffffu, clean_v<C>(sbase + C::kOffV + st * C::kOp, r.any0 - k0,
                                                  r.any1 - k0, lane)) &&
               lane == 0)
             *poison = 1;
           __threadfence_block();
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&kv_full[st]);
+          if (lane == 0) mbar_arrive(&v_full[st]);
         }
       }
     }
@@ -1270,21 +1267,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     // -------------------------------------------------- widen E4M3 to fp16
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
     const int tid = threadIdx.x - 12 * 32;
-    uint32_t load = 0, nrec = 0;
+    uint32_t n = 0, nrec = 0;
     bool ok = true;
     while (ok) {
-      const Rec rc = next_rec(nrec);
+      const Rec rc = next_rec(nrec, wait);
       if (!rc.live) break;
-      for (int j = rc.j0; ok && j < rc.j1; j++) {
+      for (int j = rc.j0; ok && j < rc.j1; j++, n++) {
         const int k0 = (rc.first + j) * kTile;
         const int r0 = rc.any0 - k0, r1 = rc.any1 - k0;
         for (int x = 0; x < 2; x++) {
-          const uint32_t rs = load % C::kRawStages, cs = load % C::kStages;
-          if (!(ok = wait(&raw_full[rs], (load / C::kRawStages) & 1) &&
-                     wait(&kv_empty[cs], ((load / C::kStages) & 1) ^ 1)))
+          const uint32_t st = n & 1;
+          uint64_t* const full = x ? &v_full[st] : &k_full[st];
+          if (!(ok = wait(&raw_full[x], n & 1) &&
+                     wait(x ? &v_empty[st] : &k_empty[st], ((n >> 1) & 1) ^ 1)))
             break;
-          const uint32_t src = sbase + C::kOffRaw + rs * C::kRaw;
-          const uint32_t dst = sbase + C::kOffKV + cs * C::kOp;
+          const uint32_t src = sbase + C::kOffRaw + x * C::kRaw;
+          const uint32_t dst = sbase + (x ? C::kOffV : C::kOffK) + st * C::kOp;
           const bool clean = x == 1 && edge(rc, j);
           bool hit = false;
           constexpr int CH = D / 16, UN = 4;
@@ -1297,12 +1295,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             for (int k = 0; k < UN; k++) {
               const int i = i0 + 128 * k, r = i / CH, ch = i % CH;
               if (clean) {
-                constexpr uint32_t E = 0x7F7F7F7Fu;
                 if (r < r0 || r >= r1) v[k] = make_uint4(0, 0, 0, 0);
-                const uint32_t m0 = __vcmpeq4(v[k].x & E, E), m1 = __vcmpeq4(v[k].y & E, E),
-                               m2 = __vcmpeq4(v[k].z & E, E), m3 = __vcmpeq4(v[k].w & E, E);
+                const uint32_t m0 = not_finite<C>(v[k].x), m1 = not_finite<C>(v[k].y),
+                               m2 = not_finite<C>(v[k].z), m3 = not_finite<C>(v[k].w);
                 hit |= (m0 | m1 | m2 | m3) != 0;
-                v[k] = make_uint4(v[k].x & ~m0, v[k].y & ~m1, v[k].z & ~m2, v[k].w & ~m3);
+                v[k] = make_uint4(v[k].x & ~whole_mask<C>(m0), v[k].y & ~whole_mask<C>(m1),
+                                  v[k].z & ~whole_mask<C>(m2), v[k].w & ~whole_mask<C>(m3));
               }
               const uint32_t y[8] = {e4m3_to_f16x2(v[k].x), e4m3_to_f16x2(v[k].x >> 16),
                                      e4m3_to_f16x2(v[k].y), e4m3_to_f16x2(v[k].y >> 16),
@@ -1323,10 +1321,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&raw_empty[rs]);
-            mbar_arrive(&kv_full[cs]);
+            mbar_arrive(&raw_empty[x]);
+            mbar_arrive(full);
           }
-          load++;
         }
       }
     }
