@@ -610,32 +610,30 @@ __device__ __forceinline__ uint32_t whole_mask(uint32_t top) {
   return C::E8 ? (top >> 7) * 0xFFu : (top >> 15) * 0xFFFFu;
 }
 
-// Zeroes the rows of a V tile outside [r0, r1) and replaces values that are
-// not finite by zero; returns whether there were any.  The rows that see them
-// get them back at the end (add_poison).
+// Rows ra .. rb - 1 of a V tile: those outside [r0, r1) are zeroed, values in
+// the others that are not finite replaced by zero; returns whether there were
+// any.  The rows that see them get them back at the end (add_poison).
 template <class C>
-__device__ __forceinline__ bool clean_v(uint32_t v, int r0, int r1, int lane) {
-  constexpr int CH = C::D / 8, RI = 32 / CH;
+__device__ __forceinline__ bool clean_v(uint32_t v, int ra, int rb, int r0, int r1, int lane) {
+  constexpr int CH = C::D / 8, RI = 32 / CH, UN = 4;
   bool hit = false;
   const int ch = lane % CH;
 #pragma unroll 1
-  for (int rb = lane / CH; rb < kTile; rb += 4 * RI) {
-    uint4 x[4];
+  for (int r = ra + lane / CH; r < rb; r += UN * RI) {
+    uint4 x[UN];
 #pragma unroll
-    for (int k = 0; k < 4; k++) x[k] = lds16(v + op_off<C::D>(rb + k * RI, ch));
+    for (int k = 0; k < UN; k++) x[k] = lds16(v + op_off<C::D>(min(r + k * RI, kTile - 1), ch));
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const int r = rb + k * RI;
-      const uint32_t a = v + op_off<C::D>(r, ch);
-      const uint32_t m0 = not_finite<C>(x[k].x), m1 = not_finite<C>(x[k].y),
-                     m2 = not_finite<C>(x[k].z), m3 = not_finite<C>(x[k].w);
-      if (r < r0 || r >= r1) {
-        sts16(a, 0, 0, 0, 0);
-      } else if (m0 | m1 | m2 | m3) {
-        hit = true;
-        sts16(a, x[k].x & ~whole_mask<C>(m0), x[k].y & ~whole_mask<C>(m1),
-              x[k].z & ~whole_mask<C>(m2), x[k].w & ~whole_mask<C>(m3));
-      }
+    for (int k = 0; k < UN; k++) {
+      const int rk = min(r + k * RI, kTile - 1);
+      uint32_t m0 = not_finite<C>(x[k].x), m1 = not_finite<C>(x[k].y),
+               m2 = not_finite<C>(x[k].z), m3 = not_finite<C>(x[k].w);
+      const bool in = rk >= r0 && rk < r1;
+      if (in && !(m0 | m1 | m2 | m3)) continue;
+      hit |= in;
+      sts16(v + op_off<C::D>(rk, ch), in ? x[k].x & ~whole_mask<C>(m0) : 0u,
+            in ? x[k].y & ~whole_mask<C>(m1) : 0u, in ? x[k].z & ~whole_mask<C>(m2) : 0u,
+            in ? x[k].w & ~whole_mask<C>(m3) : 0u);
     }
   }
   return hit;
@@ -813,21 +811,86 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const uint32_t o_col = tmem + lane_base + 2 * kTile + t * D;
     uint32_t steps = 0;  // key tiles this row tile has gone through
     uint32_t base = 0;   // key tiles the CTA has loaded before this unit
-    uint32_t nrec = 0, uses = 0;  // parts seen, those of them with keys for this tile
+    uint32_t nrec = 0;   // parts seen
+    uint32_t uses = 0;   // those of them with keys for this tile
     bool ok = true;
+    // the part before, whose O is written once the next part's first products
+    // are under way: its row, statistics, and place in the record ring
+    bool owed = false, o_keys = false;
+    float o_m = 0.0f, o_l = 0.0f;
+    int o_row = 0, o_hi = 0, o_lo = 0;
+    auto put_out = [&]() {
+      const Rec& r = recs[(nrec - 1) % kUnits];
+      if (o_keys) {
+        if (!(ok = wait(&o_full[t], (uses - 1) & 1))) return;
+        tc_fence_after();
+      }
+      const bool whole = r.flags & 1, in = row < r.nrows - t * kTile;
+      const int tok = o_row / p.group;
+      const int64_t at = (int64_t)(r.q0 + tok) * p.heads + r.h * p.group + (o_row - tok * p.group);
+      const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + r.h) : 1.0f;
+      const uint64_t inv2 = both(whole ? row_inverse(o_l, vs) : 1.0f);
+      const int prt = t * kTile + row;
+      float* part = pl.parts + ((size_t)blockIdx.x * 2 + (r.flags >> 1)) * part_floats(D);
+      uint16_t* out = p.out + at * D;
+#pragma unroll 1
+      for (int i = 0; i < D / 32; i++) {
+        float o[32];
+        uint32_t* orr = reinterpret_cast<uint32_t*>(o);
+        __syncwarp();
+        if (o_keys) {
+          tmem_ld32(o_col + 32 * i, orr);
+          tmem_ld32_wait(orr);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e++) o[e] = 0.0f;
+        }
+        if (!in) continue;
+        if (whole) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            mul2(o[2 * e], o[2 * e + 1], inv2);
+            w[e] = pack2<C::BF>(o[2 * e], o[2 * e + 1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            stg32(out + 32 * i + 2 * e, w[e], w[e + 1], w[e + 2], w[e + 3], w[e + 4], w[e + 5],
+                  w[e + 6], w[e + 7]);
+        } else {
+          float* dst = part + (size_t)prt * D + 32 * i;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            stg32(dst + e, orr[e], orr[e + 1], orr[e + 2], orr[e + 3], orr[e + 4], orr[e + 5],
+                  orr[e + 6], orr[e + 7]);
+        }
+      }
+      tc_fence_before();  // O is read before the next unit's first product writes it
+      if (in) {
+        if (*poison != 0)
+          add_poison<C>(p.cache, p.batch.table + (int64_t)r.b * p.batch.table_stride, r.h,
+                        (r.first + r.s0) * kTile, (r.first + r.s1) * kTile, r.any0, r.any1, r.all0,
+                        r.all1, o_lo, o_hi, whole ? nullptr : part + (size_t)prt * D, out);
+        if (!whole)
+          *reinterpret_cast<float2*>(part + (size_t)kUnitRows * D + 2 * prt) = make_float2(o_m, o_l);
+        else if (p.lse)
+          p.lse[at] = row_lse(o_m, o_l);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&u_empty[(nrec - 1) % kUnits]);
+    };
     while (ok) {
-      const Rec r = next_rec(nrec, wait);
-      if (!r.live) break;
+      const uint32_t slot = nrec % kUnits;
+      if (!(ok = wait(&u_full[slot], (nrec / kUnits) & 1))) break;
+      const Rec r = recs[slot];
       const int nt = min(kTile, r.nrows - t * kTile);  // rows of the tile
       const int j0 = t ? r.t1a : r.t0a, j1 = t ? r.t1e : r.t0e;
       const int prow = min(r.row0 + t * kTile + row, r.row0 + r.nrows - 1);
-      const int tok = prow / p.group;
-      const int token = r.q0 + tok, head = r.h * p.group + (prow - tok * p.group);
-      const int pos = r.len - r.n + tok;
+      const int pos = r.len - r.n + prow / p.group;
       const int hi = p.causal ? pos : r.len - 1;
       const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
       float c = p.scale_log2 * (C::E8 && p.cache.k_scale ? __ldg(p.cache.k_scale + r.h) : 1.0f);
-      if (C::kCvtQ && j0 < j1) {
+      if (C::kCvtQ && r.live && j0 < j1) {
         // bf16 queries to fp16, in place, by a power of two per row: 2^s
         // brings the row's largest value to [2^14, 2^15); values below 2^-38
         // of it lose bits
@@ -860,6 +923,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
       }
+      if (owed) {
+        put_out();
+        if (!ok) break;
+      }
+      if (!r.live) break;
+      nrec++;
       float m = -INFINITY, l = 0.0f;
       for (int j = j0; j < j1; j++, steps++) {
         if (!(ok = wait(&s_full[t], steps & 1))) break;
@@ -923,63 +992,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       if (!ok) break;
       base += r.j1 - r.j0;
-      // ---- output
-      if (j0 < j1) {
-        if (!(ok = wait(&o_full[t], uses & 1))) break;
-        uses++;
-        tc_fence_after();
-      }
-      const bool whole = r.flags & 1;
-      const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + r.h) : 1.0f;
-      const float inv = whole ? row_inverse(l, vs) : 1.0f;
-      const uint64_t inv2 = both(inv);
-      const int prt = t * kTile + row;
-      float* part = pl.parts + ((size_t)blockIdx.x * 2 + (r.flags >> 1)) * part_floats(D);
-      uint16_t* out = p.out + ((int64_t)token * p.heads + head) * D;
-#pragma unroll 1
-      for (int i = 0; i < D / 32; i++) {
-        float o[32];
-        uint32_t* orr = reinterpret_cast<uint32_t*>(o);
-        __syncwarp();
-        if (j0 < j1) {
-          tmem_ld32(o_col + 32 * i, orr);
-          tmem_ld32_wait(orr);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e++) o[e] = 0.0f;
-        }
-        if (row < nt) {
-          if (whole) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; e++) {
-              mul2(o[2 * e], o[2 * e + 1], inv2);
-              w[e] = pack2<C::BF>(o[2 * e], o[2 * e + 1]);
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              stg32(out + 32 * i + 2 * e, w[e], w[e + 1], w[e + 2], w[e + 3], w[e + 4], w[e + 5],
-                    w[e + 6], w[e + 7]);
-          } else {
-            float* dst = part + (size_t)prt * D + 32 * i;
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              stg32(dst + e, orr[e], orr[e + 1], orr[e + 2], orr[e + 3], orr[e + 4], orr[e + 5],
-                    orr[e + 6], orr[e + 7]);
-          }
-        }
-      }
-      tc_fence_before();  // O is read before the next unit's first product writes it
-      if (row < nt) {
-        if (*poison != 0)
-          add_poison<C>(p.cache, p.batch.table + (int64_t)r.b * p.batch.table_stride, r.h,
-                        (r.first + r.s0) * kTile, (r.first + r.s1) * kTile, r.any0, r.any1, r.all0,
-                        r.all1, lo, hi, whole ? nullptr : part + (size_t)prt * D, out);
-        if (!whole)
-          *reinterpret_cast<float2*>(part + (size_t)kUnitRows * D + 2 * prt) = make_float2(m, l);
-        else if (p.lse)
-          p.lse[(int64_t)token * p.heads + head] = row_lse(m, l);
-      }
+      owed = true;
+      o_keys = j0 < j1;
+      uses += o_keys;
+      o_m = m;
+      o_l = l;
+      o_row = prow;
+      o_hi = hi;
+      o_lo = lo;
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------------ MMA
@@ -1251,11 +1271,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const uint32_t st = n & 1;
           if (!(ok = wait(&edge_full[st], par >> st & 1))) break;
           par ^= 1u << st;
+          // keys that every row sees need no look
           const int k0 = (r.first + j) * kTile;
-          if (__any_sync(0xffffffffu, clean_v<C>(sbase + C::kOffV + st * C::kOp, r.any0 - k0,
-                                                 r.any1 - k0, lane)) &&
-              lane == 0)
-            *poison = 1;
+          const int m0 = min(max(r.all0 - k0, 0), kTile), m1 = min(max(r.all1 - k0, m0), kTile);
+          bool hit = false;
+#pragma unroll 1
+          for (int x = 0; x < 2; x++)
+            hit |= clean_v<C>(sbase + C::kOffV + st * C::kOp, x ? m1 : 0, x ? kTile : m0,
+                              r.any0 - k0, r.any1 - k0, lane);
+          if (__any_sync(0xffffffffu, hit) && lane == 0) *poison = 1;
           __threadfence_block();
           fence_async_smem();
           __syncwarp();
