@@ -51,7 +51,7 @@ struct Cfg {
   static constexpr int D = D_, NB = NB_, E8 = E8_, BF = BF_;
   static constexpr int RB = D * (E8 ? 1 : 2);       // bytes of a key row
   static constexpr int CPR = RB / 16;               // 16-byte chunks of it
-  static constexpr int kHalf = E8 ? 2048 : 4096;    // bytes of K (and of V) in a tile
+  static constexpr int kHalf = RB > 128 ? 4096 : 2048;  // bytes of K (and of V) in a tile
   static constexpr int KT = kHalf / RB;             // keys per tile, 16 or 32
   static constexpr int MT = KT / 16;                // 16-key groups (one page each)
   static constexpr int RPI = 32 / CPR;              // rows per copy instruction
@@ -63,7 +63,7 @@ struct Cfg {
   static constexpr int kJoinBytes = RT * OS * 4;
   static constexpr int kRing = kWarps * (kWarpBytes > kJoinBytes ? kWarpBytes : kJoinBytes);
   static constexpr int kSmem = kRing + kWarps * RT * 8 + kWarps * kStages * 4 + 64;
-  static constexpr int kCtasPerSm = NB == 4 ? 2 : E8 ? (NB == 1 ? 4 : 3) : 2;
+  static constexpr int kCtasPerSm = NB == 4 || RB > 128 ? 2 : NB == 2 && D == 128 ? 3 : 4;
   static constexpr int kGrid = kSms * kCtasPerSm;
 };
 
