@@ -16,6 +16,9 @@ _ATTENTION = ("PagedKVCache", "PagedBatch", "qk_norm_rope", "kv_append", "paged_
 
 
 def __getattr__(name):
+    if name == "DecoderBlock":
+        from .block import DecoderBlock
+        return DecoderBlock
     if name in _ATTENTION:
         from . import attention
         value = globals()[name] = getattr(attention, name)  # found directly from now on
