@@ -1309,15 +1309,24 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const uint32_t dst = sbase + (x ? C::kOffV : C::kOffK) + st * C::kOp;
           const bool clean = x == 1 && edge(rc, j);
           bool hit = false;
-          constexpr int CH = D / 16, UN = 4;
+          // 8 lanes take 4 chunks of a row and 4 of the next one, of the other
+          // half of the channels where there are two, so that their loads and
+          // their stores cover all banks
+          constexpr int HALVES = D / 64, UN = 2;
+          const int r8 = 2 * (tid >> 3) + (tid >> 2 & 1);
 #pragma unroll 1
-          for (int i0 = tid; i0 < C::kRaw / 16; i0 += 128 * UN) {
+          for (int i0 = 0; i0 < 4 * HALVES; i0 += UN) {
             uint4 v[UN];
 #pragma unroll
-            for (int k = 0; k < UN; k++) v[k] = lds16(src + (i0 + 128 * k) * 16);
+            for (int k = 0; k < UN; k++) {
+              const int r = r8 + 32 * ((i0 + k) / HALVES);
+              const int ch = (tid & 3) + (HALVES == 2 ? 4 * ((r ^ k) & 1) : 0);
+              v[k] = lds16(src + r * D + ch * 16);
+            }
 #pragma unroll
             for (int k = 0; k < UN; k++) {
-              const int i = i0 + 128 * k, r = i / CH, ch = i % CH;
+              const int r = r8 + 32 * ((i0 + k) / HALVES);
+              const int ch = (tid & 3) + (HALVES == 2 ? 4 * ((r ^ k) & 1) : 0);
               if (clean) {
                 if (r < r0 || r >= r1) v[k] = make_uint4(0, 0, 0, 0);
                 const uint32_t m0 = not_finite<C>(v[k].x), m1 = not_finite<C>(v[k].y),
@@ -1326,18 +1335,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 v[k] = make_uint4(v[k].x & ~whole_mask<C>(m0), v[k].y & ~whole_mask<C>(m1),
                                   v[k].z & ~whole_mask<C>(m2), v[k].w & ~whole_mask<C>(m3));
               }
-              const uint32_t y[8] = {e4m3_to_f16x2(v[k].x), e4m3_to_f16x2(v[k].x >> 16),
-                                     e4m3_to_f16x2(v[k].y), e4m3_to_f16x2(v[k].y >> 16),
-                                     e4m3_to_f16x2(v[k].z), e4m3_to_f16x2(v[k].z >> 16),
-                                     e4m3_to_f16x2(v[k].w), e4m3_to_f16x2(v[k].w >> 16)};
-              // lanes of the upper channels store their second chunk first: 8
-              // lanes then cover all banks
-              const uint32_t a0 = dst + op_off<D>(r, 2 * ch), a1 = dst + op_off<D>(r, 2 * ch + 1);
-              const bool sw = ch & (D / 32);
-              sts16(sw ? a1 : a0, sw ? y[4] : y[0], sw ? y[5] : y[1], sw ? y[6] : y[2],
-                    sw ? y[7] : y[3]);
-              sts16(sw ? a0 : a1, sw ? y[0] : y[4], sw ? y[1] : y[5], sw ? y[2] : y[6],
-                    sw ? y[3] : y[7]);
+              sts16(dst + op_off<D>(r, 2 * ch), e4m3_to_f16x2(v[k].x), e4m3_to_f16x2(v[k].x >> 16),
+                    e4m3_to_f16x2(v[k].y), e4m3_to_f16x2(v[k].y >> 16));
+              sts16(dst + op_off<D>(r, 2 * ch + 1), e4m3_to_f16x2(v[k].z),
+                    e4m3_to_f16x2(v[k].z >> 16), e4m3_to_f16x2(v[k].w), e4m3_to_f16x2(v[k].w >> 16));
             }
           }
           if (hit) *poison = 1;
