@@ -6,7 +6,7 @@
 //   when m grows; parts are joined by m and l.
 //
 // Rows.  The group = heads / kv_heads query heads of a kv head and the new
-// tokens are the rows of one matrix (row = token * group + head), 8, 16 or 32
+// tokens are the rows of one matrix (row = token * group + head), 8 or 16
 // of them per work unit, so a key is read once for all of them.  Both products
 // are formed transposed, S^T = K Q^T and O^T = V^T P^T: the rows are then the
 // MMA's N (8), not its M (16), so that 4 to 8 rows, the common case of
@@ -63,7 +63,7 @@ struct Cfg {
   static constexpr int kJoinBytes = RT * OS * 4;
   static constexpr int kRing = kWarps * (kWarpBytes > kJoinBytes ? kWarpBytes : kJoinBytes);
   static constexpr int kSmem = kRing + kWarps * RT * 8 + kWarps * kStages * 4 + 64;
-  static constexpr int kCtasPerSm = NB == 4 || RB > 128 ? 2 : NB == 2 && D == 128 ? 3 : 4;
+  static constexpr int kCtasPerSm = RB > 128 ? 2 : NB == 2 && D == 128 ? 3 : 4;
   static constexpr int kGrid = kSms * kCtasPerSm;
 };
 
@@ -792,18 +792,17 @@ cudaError_t launch_types(const AttnParams& p, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_dim(const AttnParams& p, cudaStream_t st) {
-  // the fewest rows per unit that hold one sequence's new tokens; 32 where
-  // none does (half the reads of the cache per row)
-  const long long rows = (long long)p.batch.max_q * p.group;
-  return rows <= 8    ? launch_types<D, 1>(p, st)
-         : rows <= 16 ? launch_types<D, 2>(p, st)
-                      : launch_types<D, 4>(p, st);
+  // the fewest rows per unit that hold one sequence's new tokens; 16 where
+  // neither does (units of 32, whose registers leave no room for the warps
+  // that hide the loads, took as long as two of 16)
+  return (long long)p.batch.max_q * p.group <= 8 ? launch_types<D, 1>(p, st)
+                                                 : launch_types<D, 2>(p, st);
 }
 
 }  // namespace
 
 size_t attn_rows_scratch_bytes(int dim) {
-  return (size_t)kSms * 2 * 2 * part_floats(32, dim) * 4;  // 2 CTAs of 32 rows, or 4 of 8
+  return (size_t)kSms * 4 * 2 * part_floats(16, dim) * 4;  // 4 CTAs of 16 rows at most
 }
 
 cudaError_t launch_attn_rows(const AttnParams& p, cudaStream_t st) {

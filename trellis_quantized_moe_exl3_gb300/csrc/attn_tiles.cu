@@ -345,13 +345,22 @@ __device__ __forceinline__ Unit make_unit(const AttnParams& p, int b, const Seq&
 struct PlanHead {
   long long line;   // key tiles of one kv head
   int units, pieces;
+  int splits;       // units that cuts go through
+  int split_rows;   // the most rows of one
 };
 struct Start {
   int unit, head, off, pad;
 };
+// A unit that cuts go through: its parts are in the first part slots of the
+// pieces first .. last, but for the first one's, slot0.
+struct Split {
+  int first, last, slot0;
+  int row0, nrows, q0, head, pad;
+};
 struct Plan {
   PlanHead* head;
   Start* start;     // [kGrid]
+  Split* split;     // [kGrid], in no particular order
   int2* rec;        // [units] {sequence, index of the unit in it}
   int* seq_unit;    // [num_seqs + 1]
   long long* pre;   // [units + 1]
@@ -370,6 +379,8 @@ __host__ __device__ inline size_t carve(void* base, long long rows, int seqs, Pl
   at += 256;
   p.start = reinterpret_cast<Start*>(b + at);
   at += align256(sizeof(Start) * kGrid);
+  p.split = reinterpret_cast<Split*>(b + at);
+  at += align256(sizeof(Split) * kGrid);
   p.rec = reinterpret_cast<int2*>(b + at);
   at += align256(sizeof(int2) * mu);
   p.seq_unit = reinterpret_cast<int*>(b + at);
@@ -475,7 +486,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p, P
   const long long all = run * p.kv_heads;
   const long long want = (all + kMinSteps - 1) / kMinSteps;
   const int pieces = want < kGrid ? (int)want : kGrid;
-  if (threadIdx.x == 0) *pl.head = PlanHead{run, units, pieces};
+  __shared__ int splits, split_rows;
+  if (threadIdx.x == 0) splits = split_rows = 0;
+  __syncthreads();
   if (threadIdx.x < pieces) {
     const long long at = piece_start(all, pieces, threadIdx.x);
     const long long s = at % run;
@@ -487,9 +500,25 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p, P
       else
         hi = mid;
     }
-    pl.start[threadIdx.x] =
-        Start{lo, (int)(at / run), (int)(s - (pre_cached ? pre_s[lo] : pl.pre[lo])), 0};
+    const int off = (int)(s - (pre_cached ? pre_s[lo] : pl.pre[lo]));
+    pl.start[threadIdx.x] = Start{lo, (int)(at / run), off, 0};
+    const long long u0 = at - off;  // the unit's place on the line
+    if (off > 0 && piece_start(all, pieces, threadIdx.x - 1) <= u0) {
+      // the first cut inside its unit
+      const int2 rec = pl.rec[lo];
+      int32_t ignored = 0;
+      const Unit u = make_unit(p, rec.x, load_seq(p.batch, rec.x, &ignored), rec.y);
+      const int first = threadIdx.x - 1;
+      // the piece that holds the unit's last key tile
+      const int last = (int)(((u0 + u.n) * pieces + all - 1) / all) - 1;
+      const int slot0 = 2 * first + (piece_start(all, pieces, first) < u0 ? 1 : 0);
+      pl.split[atomicAdd(&splits, 1)] =
+          Split{first, last, slot0, u.row0, u.nrows, u.s.q0, (int)(at / run), 0};
+      atomicMax(&split_rows, u.nrows);
+    }
   }
+  __syncthreads();
+  if (threadIdx.x == 0) *pl.head = PlanHead{run, units, pieces, splits, split_rows};
 }
 
 // A part of a unit as the TMA warp publishes it (in shared memory).
@@ -1363,36 +1392,24 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   }
 }
 
-// Sums the parts of every unit that a cut goes through: block (x, y) takes
-// cut x + 1 (if it is its unit's first) and rows 8 y .. of every 8 gridDim.y.
+// Sums the parts of the units that cuts go through, 256 / (head_dim / 4) rows
+// of a unit at a time.
+constexpr int kJoinBlocks = 8 * kSms;
 template <class C>
 __global__ void __launch_bounds__(256) attn_tiles_join_kernel(AttnParams p, Plan pl) {
-  constexpr int D = C::D;
+  constexpr int D = C::D, LR = D / 4, kRows = 256 / LR;
   pdl_wait();
-  const PlanHead hd = *pl.head;
-  const int cut = blockIdx.x + 1;
-  if (cut >= hd.pieces) return;
-  const long long all = hd.line * p.kv_heads;
-  const Start st = pl.start[cut];
-  if (st.off == 0) return;
-  const long long u0 = piece_start(all, hd.pieces, cut) - st.off;
-  if (piece_start(all, hd.pieces, cut - 1) > u0) return;
-  const int2 rec = pl.rec[st.unit];
-  int32_t ignored = 0;
-  const Unit u = make_unit(p, rec.x, load_seq(p.batch, rec.x, &ignored), rec.y);
-  const int first = cut - 1;
-  int last = cut;
-  while (last + 1 < hd.pieces && piece_start(all, hd.pieces, last + 1) < u0 + u.n) last++;
-  const size_t slot0 = (size_t)first * 2 + (piece_start(all, hd.pieces, first) < u0 ? 1 : 0);
-  const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + st.head) : 1.0f;
-  constexpr int LR = D / 4;
+  const int splits = pl.head->splits, groups = (pl.head->split_rows + kRows - 1) / kRows;
   const int d0 = (threadIdx.x % LR) * 4;
-  for (int r = blockIdx.y * (256 / LR) + threadIdx.x / LR; r < u.nrows;
-       r += gridDim.y * (256 / LR)) {
+  for (int i = blockIdx.x; i < splits * groups; i += gridDim.x) {
+    const Split u = pl.split[i % splits];
+    const int r = i / splits * kRows + threadIdx.x / LR;
+    if (r >= u.nrows) continue;
+    const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + u.head) : 1.0f;
     float mm = -INFINITY, ll = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int c = first; c <= last; c++) {
-      const float* part = pl.parts + (c == first ? slot0 : (size_t)c * 2) * part_floats(D);
+#pragma unroll 8
+    for (int c = u.first; c <= u.last; c++) {
+      const float* part = pl.parts + (size_t)(c == u.first ? u.slot0 : 2 * c) * part_floats(D);
       const float2 s = *reinterpret_cast<const float2*>(part + (size_t)kUnitRows * D + 2 * r);
       const float4 x = *reinterpret_cast<const float4*>(part + (size_t)r * D + d0);
       const float mn = fmaxf(mm, s.x);
@@ -1406,7 +1423,7 @@ __global__ void __launch_bounds__(256) attn_tiles_join_kernel(AttnParams p, Plan
       acc[3] = acc[3] * f0 + x.w * f1;
     }
     const int prow = u.row0 + r;
-    const int token = u.s.q0 + prow / p.group, head = st.head * p.group + prow % p.group;
+    const int token = u.q0 + prow / p.group, head = u.head * p.group + prow % p.group;
     const float inv = row_inverse(ll, vs);
     uint2 o;
     o.x = pack2<C::BF>(acc[0] * inv, acc[1] * inv);
@@ -1501,7 +1518,7 @@ cudaError_t launch_cfg(const AttnParams& p, const Maps& maps, const Plan& pl, in
   e = launch_pdl(attn_tiles_kernel<C>, dim3(kGrid), dim3(C::kThreads), C::kSmem, st, maps, p, pl);
   note_launches(1);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_tiles_join_kernel<C>, dim3(kGrid - 1, 8), dim3(256), 0, st, p, pl);
+  e = launch_pdl(attn_tiles_join_kernel<C>, dim3(kJoinBlocks), dim3(256), 0, st, p, pl);
   note_launches(1);
   return e;
 }
