@@ -13,7 +13,7 @@ import numpy as np
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from trellis_quantized_moe_exl3_gb300 import DecoderBlock, Layer, PagedBatch, PagedKVCache, device_status, synth  # noqa: E402
+from trellis_quantized_moe_exl3_gb300 import DecoderBlock, Layer, PagedBatch, PagedKVCache, synth  # noqa: E402
 
 
 def build_block(spec, heads, kv_heads, dim, top_k, seed=0):
@@ -95,7 +95,7 @@ def main():
     print(f"decode: {a.steps} steps of {a.seqs} sequences, {dt / a.steps * 1e6:.1f} us per step, "
           f"{a.steps * a.seqs / dt:.0f} tokens/s, lengths now {batch.seq_lens.tolist()}, "
           f"output norm {float(y.float().norm()):.3e}")
-    print("device status", device_status(cache.ws))
+    print("device status", cache.status())
 
 
 if __name__ == "__main__":

@@ -17,8 +17,8 @@ import pytest
 import torch
 
 import _attention_ref as R
-from trellis_quantized_moe_exl3_gb300 import (PagedBatch, PagedKVCache, device_status, kv_append,
-                                              paged_attention, qk_norm_rope)
+from trellis_quantized_moe_exl3_gb300 import (PagedBatch, PagedKVCache, kv_append, paged_attention,
+                                              qk_norm_rope)
 
 pytestmark = pytest.mark.gpu
 
@@ -146,7 +146,7 @@ def test_append(qs, lens, page, H, Hk, D, rot, inter, dtype, cdt, layout):
     batch = PagedBatch(step.cu_q, step.seq_lens, step.table, step.max_q)
     kv_append(cache, batch, k, v, inv_freq=f, k_weight=wk, q=q, q_weight=wq, q_out=q_out,
               interleaved=inter)
-    assert device_status(cache.ws) == 0
+    assert cache.status() == 0
     pos = torch.cat([torch.arange(L - n, L) for n, L in zip(qs, lens)]).int()
     close_rotated(q_out[:T], R.norm_rope(q[:T], pos, f, wq, 1e-6, inter), dtype)
     assert bool((q_out[T:] == 7.0).all())
@@ -203,7 +203,7 @@ def test_append_reports_bad_pages_and_batches():
         cache = make_cache(g, 4, 16, 1, 16, BF, fill=0.0)
         b = PagedBatch(*[torch.tensor(x, dtype=torch.int32, device="cuda") for x in (cu, lens, table)], 3)
         kv_append(cache, b, k, k)
-        return device_status(cache.ws), cache.k.float().sum().item() / 16
+        return cache.status(), cache.k.float().sum().item() / 16
 
     assert run([0, 3], [3], [[1, 2]]) == (0, 3)
     assert run([0, 3], [18], [[1, 4]]) == (1, 1)        # the second page does not exist
@@ -230,7 +230,7 @@ def check_attention(cache, step, q, page, scale, causal, window, path=0, pad=0):
     batch = PagedBatch(step.cu_q, step.seq_lens, step.table, step.max_q)
     got, lse = paged_attention(q, cache, batch, scale=scale, causal=causal, window=window, out=out,
                                return_lse=True, path=path)
-    assert device_status(cache.ws) == 0
+    assert cache.status() == 0
     k, v = values(cache)
     ref, mag, rlse = R.attention(q[:T], k, v, step.table.cpu(), step.qs, step.lens, page, scale,
                                  causal, window)
@@ -391,8 +391,8 @@ def test_attention_reports_bad_pages(path):
     step.table[0, 2] = 1 << 20
     step.table[1, 0] = -3
     got = paged_attention(q, cache, PagedBatch(step.cu_q, step.seq_lens, step.table, 2), path=path)
-    assert device_status(cache.ws) == 1
-    cache.ws.zero_()
+    assert cache.status() == 1
+    cache.clear_status()
     # the same with the page's keys at a score of -inf: a cache without them
     k, v = values(cache)
     tab = step.table.cpu()
@@ -413,13 +413,13 @@ def test_attention_reports_bad_batches():
         cu = torch.tensor([0, 2, 1, 5], dtype=torch.int32, device="cuda")   # sequence 1 runs backwards
         out = torch.full_like(q, 7.0)
         paged_attention(q, cache, PagedBatch(cu, step.seq_lens, step.table, 4), path=path, out=out)
-        assert device_status(cache.ws) == 2
+        assert cache.status() == 2
         assert torch.equal(out[0], want[0]) and bool((out[5:] == 7.0).all())
-        cache.ws.zero_()
+        cache.clear_status()
         lens = step.seq_lens.clone()
         lens[1] = 100000
         out = paged_attention(q, cache, PagedBatch(step.cu_q, lens, step.table, 4), path=path)
-        assert device_status(cache.ws) & 2
+        assert cache.status() & 2
         assert torch.equal(out[:2], want[:2]) and torch.equal(out[5:], want[5:])
 
 
@@ -456,7 +456,7 @@ def test_offsets_past_32_bits(cdt, path):
     q = randn(g, sum(qs), 16, D).to(BF).cuda()
     step = PagedBatch(torch.tensor([0, 1, 41], dtype=torch.int32, device="cuda"), full.seq_lens, table, 40)
     got = paged_attention(q, cache, step, path=path).double().cpu()
-    assert device_status(cache.ws) == 0
+    assert cache.status() == 0
     kk, vv = [x.to(cdt).float().cpu().double() for x in (kn, vn)]
     seq = [torch.arange(200), torch.arange(200, 350)]
     t = 0
@@ -505,7 +505,7 @@ def test_step_in_a_graph_follows_device_lengths():
         torch.cuda.synchronize()
         got = out.clone()
         assert torch.equal(got, step())
-        assert device_status(cache.ws) == 0
+        assert cache.status() == 0
 
 
 def test_other_streams():
@@ -524,3 +524,22 @@ def test_other_streams():
     assert got is not None
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_a_graph_outlives_a_larger_workspace():
+    """A graph captured before the handle's workspace grew replays on the old one."""
+    c = ([1, 1], [300, 90], 16, 4, 2, 64, BF, BF, True, 0)
+    cache, step, q = setup(c, pad=0)
+    batch = PagedBatch(step.cu_q, step.seq_lens, step.table, 1)
+    want = paged_attention(q, cache, batch)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = paged_attention(q, cache, batch)
+    small = cache.ws
+    big = torch.zeros(20000, 4, 64, dtype=BF, device="cuda")  # padding rows: the workspace of a larger call
+    paged_attention(big, cache, batch)
+    assert cache.ws.numel() > small.numel()
+    junk = torch.full((small.numel(),), 0xFF, dtype=torch.uint8, device="cuda")
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and bool((junk == 0xFF).all()) and cache.status() == 0

@@ -12,8 +12,7 @@ import torch
 
 import _attention_ref as R
 from _helpers import FRO_REL, MAX_REL, HostLayer, act_to_f64
-from trellis_quantized_moe_exl3_gb300 import (DecoderBlock, PagedBatch, PagedKVCache, device_status,
-                                              rmsnorm, synth)
+from trellis_quantized_moe_exl3_gb300 import DecoderBlock, PagedBatch, PagedKVCache, rmsnorm, synth
 
 pytestmark = pytest.mark.gpu
 
@@ -65,7 +64,7 @@ def test_block_as_prompt_chunks_and_tokens(heads, kv, dim):
                            torch.tensor([at + n], dtype=torch.int32, device="cuda"), table, n)
             out.append(method(x[at:at + n], cache, b))
             at += n
-        assert at == T and device_status(cache.ws) == 0
+        assert at == T and cache.status() == 0
         return torch.cat(out)
 
     ol = host.oracle()

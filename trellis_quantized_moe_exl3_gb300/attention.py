@@ -19,6 +19,7 @@ import torch
 
 from . import _lib
 from ._lib import check
+from .api import device_status
 
 _ACT = {torch.float16: _lib.EXL3_F16, torch.bfloat16: _lib.EXL3_BF16}
 _CODES = {torch.float16: _lib.EXL3_F16, torch.bfloat16: _lib.EXL3_BF16,
@@ -59,8 +60,9 @@ class PagedKVCache:
     permuted view of [pages, kv_heads, page_size, head_dim] works).  k_scale,
     v_scale: fp32 [kv_heads], E4M3 only; a stored x stands for x * scale.
     page_size is a multiple of 16.  The tensors must stay alive as long as the
-    handle.  `ws` is the workspace of its calls (grown as needed), whose first
-    word is the sticky device status: see `device_status`."""
+    handle.  `ws` is the workspace of its calls, grown as needed; earlier, smaller
+    ones stay alive for the graphs captured with them.  `status()` is the sticky
+    device status of all calls on the handle (it synchronises)."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         _cuda(k, "k", _CODES)
@@ -82,8 +84,24 @@ class PagedKVCache:
         d.k_scale = k_scale.data_ptr() if k_scale is not None else None
         d.v_scale = v_scale.data_ptr() if v_scale is not None else None
         self._d, self._ref = d, ctypes.byref(d)
-        self.ws = torch.zeros(_lib.EXL3_ATTENTION_HEAD_BYTES, dtype=torch.uint8, device=k.device)
-        self._need = {}
+        self._held = []
+        self._hold(torch.zeros(_lib.EXL3_ATTENTION_HEAD_BYTES, dtype=torch.uint8, device=k.device))
+
+    def _hold(self, ws):
+        self._held.append(ws)
+        self.ws, self._ws_ptr, self._ws_bytes = ws, ws.data_ptr(), ws.numel()
+        self._ws_for = None  # the size of call last found to fit
+
+    def status(self, stream=None) -> int:
+        """The status bits set so far (0: fine); see exl3.h."""
+        bits = 0
+        for ws in self._held:
+            bits |= device_status(ws, stream)
+        return bits
+
+    def clear_status(self):
+        for ws in self._held:
+            ws[:4].zero_()
 
     def workspace_size(self, tokens: int, heads: int, num_seqs: int) -> int:
         return int(_lib.lib().exl3_paged_attention_workspace_size(
@@ -92,14 +110,10 @@ class PagedKVCache:
     def workspace(self, tokens: int, heads: int, num_seqs: int) -> torch.Tensor:
         """The handle's workspace, grown to hold a call of this size (the first
         call of a size inside a graph capture must not be the one that grows it)."""
-        key = (tokens, heads, num_seqs)
-        n = self._need.get(key)
-        if n is None:
-            n = self._need[key] = self.workspace_size(*key)
-        if self.ws.numel() < n:
-            ws = torch.zeros(n, dtype=torch.uint8, device=self.ws.device)
-            ws[:4].copy_(self.ws[:4])
-            self.ws = ws
+        n = self.workspace_size(tokens, heads, num_seqs)
+        if self._ws_bytes < n:
+            self._hold(torch.zeros(n, dtype=torch.uint8, device=self.ws.device))
+        self._ws_for = (tokens, heads, num_seqs)
         return self.ws
 
 
@@ -136,35 +150,57 @@ def _strides(t):
 
 
 def _act(x, name, dim):
-    """Checks a [tokens, heads, dim] tensor; its token and head strides."""
-    code = _ACT.get(x.dtype)
-    if code is None or not x.is_cuda:
-        _cuda(x, name, _ACT)
+    """Checks a [tokens, heads, dim] tensor; its shape and the strides of a
+    token and a head."""
     shape, stride = x.shape, x.stride()
+    if x.dtype not in _ACT or not x.is_cuda:
+        _cuda(x, name, _ACT)
     if len(shape) != 3 or shape[2] != dim or (stride[2] != 1 and x.numel()):
         raise ValueError(f"{name} must be [tokens, heads, {dim}] with contiguous channels")
-    return 0 if shape[0] == 1 else stride[0], 0 if shape[1] == 1 else stride[1]
+    T, H, _ = shape
+    return T, H, 0 if T == 1 else stride[0], 0 if H == 1 else stride[1]
 
 
-def _heads(x, name, dim, weight=None, out=None):
-    """exl3_heads of a [tokens, heads, dim] tensor."""
-    ts, hs = _act(x, name, dim)
-    o = ots = ohs = w = 0
-    if weight is not None:
-        _dense(weight, f"{name}'s weight", x.dtype, (dim,))
-        w = weight.data_ptr()
-    if out is not None:
-        if out.dtype != x.dtype or out.shape != x.shape:
-            raise ValueError(f"{name}'s out must be {tuple(x.shape)} {x.dtype}")
-        ots, ohs = _act(out, f"{name}'s out", dim)
-        o = out.data_ptr()
-    return _HEADS.pack(x.data_ptr(), o, w, x.shape[1], ts, hs, ots, ohs)
+def _like(x):
+    """An uninitialised contiguous tensor of x's shape."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype,
+                                                                     device=x.device)
+
+
+def _weight(w, name, dtype, dim):
+    if w is None:
+        return 0
+    if w.dtype != dtype or w.shape != (dim,) or not w.is_cuda or not w.is_contiguous():
+        _dense(w, name, dtype, (dim,))
+    return w.data_ptr()
+
+
+def _out(out, x, T, H, dim, name):
+    """(out, exl3_heads' out pointer and strides): a new tensor, or the given
+    one checked."""
+    if out is None:
+        out = _like(x)
+        return out, out.data_ptr(), H * dim, dim
+    if out.dtype != x.dtype or out.shape != x.shape:
+        raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype}")
+    _, _, ts, hs = _act(out, name, dim)
+    return out, out.data_ptr(), ts, hs
+
+
+def _positions(positions, T):
+    if positions is None:
+        return None
+    if positions.dtype != torch.int32 or positions.shape != (T,) or not positions.is_cuda or \
+            not positions.is_contiguous():
+        _dense(positions, "positions", torch.int32, (T,))
+    return positions.data_ptr()
 
 
 def _rope(inv_freq, interleaved):
     if inv_freq is None:
         return None
-    _cuda(inv_freq, "inv_freq", torch.float64)
+    if inv_freq.dtype != torch.float64 or not inv_freq.is_cuda:
+        _cuda(inv_freq, "inv_freq", torch.float64)
     if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous [rotary_dim / 2] tensor")
     return _ROPE.pack(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0)
@@ -180,22 +216,20 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     [tokens]; inv_freq float64 [rotary_dim / 2], radians per position of pair
     (i, i + rotary_dim/2) of the first rotary_dim channels, or (2i, 2i + 1)
     when interleaved.  q_out and k_out may be q and k."""
-    T, _, dim = q.shape
-    if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    hq = _heads(q, "q", dim, q_weight, q_out)
+    dim = q.shape[-1]
+    T, H, ts, hs = _act(q, "q", dim)
+    dtype = q.dtype
+    q_out, p, ots, ohs = _out(q_out, q, T, H, dim, "q_out")
+    hq = _HEADS.pack(q.data_ptr(), p, _weight(q_weight, "q_weight", dtype, dim), H, ts, hs, ots, ohs)
     hk = None
     if k is not None:
-        if k.dtype != q.dtype or k.shape[0] != T:
+        Tk, Hk, ts, hs = _act(k, "k", dim)
+        if Tk != T or k.dtype != dtype:
             raise ValueError("q and k must have the same dtype and tokens")
-        if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        hk = _heads(k, "k", dim, k_weight, k_out)
-    pos = None
-    if positions is not None:
-        _dense(positions, "positions", torch.int32, (T,))
-        pos = positions.data_ptr()
-    check(_lib.lib().exl3_qk_norm_rope(hq, hk, _ACT[q.dtype], T, dim, pos,
+        k_out, p, ots, ohs = _out(k_out, k, T, Hk, dim, "k_out")
+        hk = _HEADS.pack(k.data_ptr(), p, _weight(k_weight, "k_weight", dtype, dim), Hk, ts, hs, ots,
+                         ohs)
+    check(_lib.lib().exl3_qk_norm_rope(hq, hk, _ACT[dtype], T, dim, _positions(positions, T),
                                        _rope(inv_freq, interleaved), eps, _stream(stream, q)),
           "exl3_qk_norm_rope")
     return q_out, k_out
@@ -208,23 +242,24 @@ def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_wei
     values to the cache; with q, returns the normed and rotated queries, from
     the same launch.  positions: those of the rotation (default: the positions
     in the sequence).  A value past the E4M3 range saturates."""
-    if k.dtype != v.dtype or k.shape != v.shape or k.shape[1] != cache.kv_heads:
+    dim, dtype = cache.head_dim, k.dtype
+    T, H, ts, hs = _act(k, "k", dim)
+    Tv, Hv, tv, hv = _act(v, "v", dim)
+    if v.dtype != dtype or Tv != T or H != cache.kv_heads or Hv != H:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
-    T, dim = k.shape[0], cache.head_dim
-    hk, hv, hq = _heads(k, "k", dim, k_weight), _heads(v, "v", dim), None
+    pk = _HEADS.pack(k.data_ptr(), 0, _weight(k_weight, "k_weight", dtype, dim), H, ts, hs, 0, 0)
+    pv = _HEADS.pack(v.data_ptr(), 0, 0, H, tv, hv, 0, 0)
+    pq = None
     if q is not None:
-        if q.dtype != k.dtype or q.shape[0] != T:
+        Tq, Hq, ts, hs = _act(q, "q", dim)
+        if Tq != T or q.dtype != dtype:
             raise ValueError("q and k must have the same dtype and tokens")
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        hq = _heads(q, "q", dim, q_weight, q_out)
-    pos = None
-    if positions is not None:
-        _dense(positions, "positions", torch.int32, (T,))
-        pos = positions.data_ptr()
-    check(_lib.lib().exl3_kv_append(cache._ref, batch._ref, hq, hk, hv, _ACT[k.dtype], T,
-                                    _rope(inv_freq, interleaved), pos, eps, cache.ws.data_ptr(),
-                                    _stream(stream, k)), "exl3_kv_append")
+        q_out, p, ots, ohs = _out(q_out, q, T, Hq, dim, "q_out")
+        pq = _HEADS.pack(q.data_ptr(), p, _weight(q_weight, "q_weight", dtype, dim), Hq, ts, hs, ots,
+                         ohs)
+    check(_lib.lib().exl3_kv_append(cache._ref, batch._ref, pq, pk, pv, _ACT[dtype], T,
+                                    _rope(inv_freq, interleaved), _positions(positions, T), eps,
+                                    cache._ws_ptr, _stream(stream, k)), "exl3_kv_append")
     return q_out
 
 
@@ -239,18 +274,23 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
     token that sees nothing gets out 0 and lse -inf."""
     if not q.is_cuda:
         _cuda(q, "q", _ACT)
-    ts, hs = _act(q, "q", cache.head_dim)
-    T, heads, dim = q.shape
+    dim = cache.head_dim
+    T, heads, ts, hs = _act(q, "q", dim)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _like(q)
     else:
         _dense(out, "out", q.dtype, (T, heads, dim))
     lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
     if ws is None:
-        ws = cache.workspace(T, heads, batch.num_seqs)
+        size = (T, heads, batch.num_seqs)
+        if size != cache._ws_for:
+            cache.workspace(*size)
+        ws_ptr, ws_bytes = cache._ws_ptr, cache._ws_bytes
+    else:
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     check(_lib.lib().exl3_paged_attention(
         cache._ref, batch._ref, q.data_ptr(), ts, hs, _ACT[q.dtype], T, heads,
         dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), path, ws.data_ptr(), ws.numel(),
-        _stream(stream, q)), "exl3_paged_attention")
+        None if lse is None else lse.data_ptr(), path, ws_ptr, ws_bytes, _stream(stream, q)),
+        "exl3_paged_attention")
     return (out, lse) if return_lse else out

@@ -227,11 +227,11 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   // Few rows per sequence and kv head: the cache's bytes bound the step.
   bool tiles = (long long)batch->max_q * p.group > kRowsMost;
   if (path != EXL3_PATH_AUTO) tiles = path == EXL3_PATH_GEMM;
-  if (tiles && !attn_tiles_can(p)) tiles = false;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return (tiles ? launch_attn_tiles(p, st) : launch_attn_rows(p, st)) == cudaSuccess
-             ? EXL3_OK
-             : EXL3_ERR_CUDA;
+  cudaError_t err = cudaErrorNotSupported;  // a cache that cannot be a TMA source
+  if (tiles) err = launch_attn_tiles(p, st);
+  if (err == cudaErrorNotSupported) err = launch_attn_rows(p, st);
+  return err == cudaSuccess ? EXL3_OK : EXL3_ERR_CUDA;
 }
 
 }  // extern "C"

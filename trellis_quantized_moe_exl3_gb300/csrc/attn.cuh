@@ -105,8 +105,8 @@ size_t attn_rows_scratch_bytes(int dim);
 cudaError_t launch_attn_rows(const AttnParams& p, cudaStream_t st);
 // rows: new tokens times group
 size_t attn_tiles_scratch_bytes(long long rows, int seqs, int dim);
-// whether the cache can be a TMA source (it has pages, the driver takes its strides)
-bool attn_tiles_can(const AttnParams& p);
+// cudaErrorNotSupported, before any launch, where the cache cannot be a TMA
+// source (it has no pages, the driver does not take its strides)
 cudaError_t launch_attn_tiles(const AttnParams& p, cudaStream_t st);
 
 }  // namespace exl3

@@ -1539,11 +1539,6 @@ size_t attn_tiles_scratch_bytes(long long rows, int seqs, int dim) {
   return carve(nullptr, rows, seqs, nullptr) + (size_t)kGrid * 2 * part_floats(dim) * 4;
 }
 
-bool attn_tiles_can(const AttnParams& p) {
-  Maps m;
-  return make_maps(p, &m);
-}
-
 cudaError_t launch_attn_tiles(const AttnParams& p, cudaStream_t st) {
   Maps m;
   if (!make_maps(p, &m)) return cudaErrorNotSupported;
