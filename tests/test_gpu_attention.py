@@ -313,6 +313,27 @@ def test_attention(c, path):
 
 
 @pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("c", [
+    ([1], [9000], 32, 16, 1, 128, BF, BF, True, 0),
+    ([1, 2], [3333, 5001], 64, 4, 1, 128, FP, FP, True, 0),    # units that begin inside a piece
+    ([1], [2600], 16, 8, 1, 64, BF, E4, True, 0),
+    ([3, 1, 0, 1], [4000, 70, 9, 12345], 64, 12, 2, 64, FP, FP, True, 0),
+    ([1], [20000], 64, 5, 1, 128, BF, E4, True, 7000),
+    ([2], [41000], 64, 2, 2, 64, BF, BF, True, 0),             # 600 pieces
+], ids=ident)
+def test_units_of_many_parts(c, path):
+    """Long sequences alone on the GPU: tens to hundreds of parts per unit,
+    joined in one step and in two; a second call finds the counts at zero."""
+    cache, step, q = setup(c)
+    o, lse = check_attention(cache, step, q, c[2], c[5] ** -0.5, c[8], c[9], path)
+    for _ in range(3):
+        o2, lse2 = paged_attention(q, cache, PagedBatch(step.cu_q, step.seq_lens, step.table, step.max_q),
+                                   window=c[9], return_lse=True, path=path)
+        n = sum(c[0])
+        assert torch.equal(o2[:n], o[:n]) and torch.equal(lse2[:n], lse[:n])
+
+
+@pytest.mark.parametrize("path", PATHS)
 def test_attention_layouts_and_strides(path):
     """Heads before places in a page; queries out of a fused projection."""
     c = ([1, 20], [200, 90], 16, 8, 2, 128, BF, BF, True, 0)

@@ -51,7 +51,10 @@ struct Cfg {
   static constexpr int D = D_, NB = NB_, E8 = E8_, BF = BF_;
   static constexpr int RB = D * (E8 ? 1 : 2);       // bytes of a key row
   static constexpr int CPR = RB / 16;               // 16-byte chunks of it
-  static constexpr int kHalf = RB > 128 ? 4096 : 2048;  // bytes of K (and of V) in a tile
+  // bytes of K (and of V) in a tile: 2 KB at 64 channels let 4 CTAs share an
+  // SM; E4M3 tiles of 128 channels took 89 us with 2 KB (16 keys) where they
+  // take 83 with 4 KB (one token over 4 x 110,000 keys)
+  static constexpr int kHalf = D == 128 ? 4096 : 2048;
   static constexpr int KT = kHalf / RB;             // keys per tile, 16 or 32
   static constexpr int MT = KT / 16;                // 16-key groups (one page each)
   static constexpr int RPI = 32 / CPR;              // rows per copy instruction
@@ -63,8 +66,9 @@ struct Cfg {
   static constexpr int kJoinBytes = RT * OS * 4;
   static constexpr int kRing = kWarps * (kWarpBytes > kJoinBytes ? kWarpBytes : kJoinBytes);
   static constexpr int kSmem = kRing + kWarps * RT * 8 + kWarps * kStages * 4 + 64;
-  static constexpr int kCtasPerSm = RB > 128 ? 2 : NB == 2 && D == 128 ? 3 : 4;
+  static constexpr int kCtasPerSm = D == 128 ? 2 : 4;
   static constexpr int kGrid = kSms * kCtasPerSm;
+  static constexpr int kFlat = D == 128 ? 40 : 24;  // most parts that are joined in one step
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -620,10 +624,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
           if (C::E8) {
 #pragma unroll
             for (int y = 0; y < 2; y++) {
-              const uint32_t a = e4m3_to_f16x2(v[y]), bq = e4m3_to_f16x2(v[y] >> 16);
-              const uint32_t d = e4m3_to_f16x2(v[2 + y]), e = e4m3_to_f16x2(v[2 + y] >> 16);
-              const uint32_t a0 = __byte_perm(a, bq, 0x5410), a1 = __byte_perm(a, bq, 0x7632);
-              const uint32_t a2 = __byte_perm(d, e, 0x5410), a3 = __byte_perm(d, e, 0x7632);
+              // bytes (key 0: even, odd channel; key 1: even, odd) to pairs of keys
+              const uint32_t w0 = __byte_perm(v[y], 0, 0x3120), w1 = __byte_perm(v[2 + y], 0, 0x3120);
+              const uint32_t a0 = e4m3_to_f16x2(w0), a1 = e4m3_to_f16x2(w0 >> 16);
+              const uint32_t a2 = e4m3_to_f16x2(w1), a3 = e4m3_to_f16x2(w1 >> 16);
 #pragma unroll
               for (int nb = 0; nb < NB; nb++)
                 mma16<MBF>(o[nb][2 * x + y], a0, a1, a2, a3, pf[nb][0], pf[nb][1]);
@@ -699,35 +703,45 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
     }
     first_part = false;
     if (!whole) {
-      // ---- the CTA that brings the unit's last part joins them all
+      // ---- the CTA that brings a unit's last part joins them all.  Many
+      // parts are joined in two steps, groups of about sqrt(parts) first, so
+      // that no CTA reads them all.  One token of 16 heads per kv head over
+      // 8000 keys (2 units of 125 parts of 16 x 128): 33.5 us with one step,
+      // 20.2 with two; but 38 parts of 4 rows 15.6 and 17.0, and units of 19
+      // parts of 16 x 64 18.0 and 25.0.
       const int c0 = piece_with(total, pieces, u0), c1 = piece_with(total, pieces, u0 + sw.n - 1);
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) s_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        const float* parts = reinterpret_cast<const float*>(p.scratch);
-        // piece c0 holds the unit's first part as its second, unless the unit
-        // starts the piece; every other piece as its first
-        const size_t slot0 = (size_t)c0 * 2 + (piece_start(total, pieces, c0) < u0 ? 1 : 0);
-        const int np = c1 - c0 + 1;
-        auto part_of = [&](int i) {
-          return parts + (i == 0 ? slot0 : (size_t)(c0 + i) * 2) * part_floats(RT, D);
-        };
+      const float* parts = reinterpret_cast<const float*>(p.scratch);
+      // piece c0 holds the unit's first part as its second, unless the unit
+      // starts the piece; every other piece as its first
+      const size_t slot0 = (size_t)c0 * 2 + (piece_start(total, pieces, c0) < u0 ? 1 : 0);
+      auto part_of = [&](int i) {
+        return parts + (i == 0 ? slot0 : (size_t)(c0 + i) * 2) * part_floats(RT, D);
+      };
+      const int np = c1 - c0 + 1;
+      const int per = np <= C::kFlat ? np : (int)ceilf(sqrtf((float)np));  // parts of a group
+      const int ng = (np + per - 1) / per;
+      const int lead = ((int)blockIdx.x - c0) / per * per;  // first part of this one's group
+      const int members = min(per, np - lead);
+
+      // Joins the n parts from + y * step into the output, or in place into
+      // the first of them (every thread writes what it alone reads).
+      auto join = [&](int from, int step, int n, bool to_out) {
         // weights of the parts, a warp per row: w = 2^(m - max m)
-        float* wt = reinterpret_cast<float*>(smem);  // [RT][np]
+        float* wt = reinterpret_cast<float*>(smem);  // [RT][n]
         for (int r = warp; r < nrows; r += kWarps) {
+          auto at = [&](int y) {
+            return reinterpret_cast<const float2*>(part_of(from + y * step) + RT * D + 2 * r);
+          };
           float mm = -INFINITY;
-          for (int i = lane; i < np; i += 32) mm = fmaxf(mm, __ldcg(part_of(i) + RT * D + 2 * r));
+          for (int y = lane; y < n; y += 32) mm = fmaxf(mm, __ldcg(at(y)).x);
 #pragma unroll
           for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
           const float ms = mm == -INFINITY ? 0.0f : mm;
           float ll = 0.0f;
-          for (int i = lane; i < np; i += 32) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(part_of(i) + RT * D + 2 * r));
+          for (int y = lane; y < n; y += 32) {
+            const float2 x = __ldcg(at(y));
             const float f = ex2(x.x - ms);
-            wt[r * np + i] = f;
+            wt[r * n + y] = f;
             ll = fmaf(x.y, f, ll);
           }
 #pragma unroll
@@ -735,28 +749,67 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
           if (lane == 0) ml[r] = make_float2(mm, ll);
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < nrows * (D / 4); i += kThreads) {
-          const int r = i / (D / 4), d0 = (i % (D / 4)) * 4;
-          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-          for (int y = 0; y < np; y++) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(y) + r * D + d0));
-            const float f = wt[r * np + y];
-            acc[0] = fmaf(x.x, f, acc[0]);
-            acc[1] = fmaf(x.y, f, acc[1]);
-            acc[2] = fmaf(x.z, f, acc[2]);
-            acc[3] = fmaf(x.w, f, acc[3]);
-          }
-          const float2 sl = ml[r];
-          const int row = rc * RT + r;
-          const int token = sw.s.q0 + row / p.group, head = h * p.group + row % p.group;
-          const float inv = row_inverse(sl.y, vs);
+        constexpr int IPT = RT * (D / 4) / kThreads;  // 16-byte columns per thread
+        constexpr int U = 16 / IPT;                   // loads in flight
+        float acc[IPT][4] = {};
+        const int d0 = threadIdx.x % (D / 4) * 4, r0 = threadIdx.x / (D / 4);
+        constexpr int RS = kThreads / (D / 4);
+#pragma unroll U
+        for (int y = 0; y < n; y++) {
+          const float* src = part_of(from + y * step) + d0;
 #pragma unroll
-          for (int e = 0; e < 4; e++) acc[e] *= inv;
-          store_out4<C>(p, token, head, d0, acc, C::BF);
-          if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(sl.x, sl.y);
+          for (int k = 0; k < IPT; k++) {
+            const int r = r0 + k * RS;
+            if (r < nrows) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(src + r * D));
+              const float f = wt[r * n + y];
+              acc[k][0] = fmaf(x.x, f, acc[k][0]);
+              acc[k][1] = fmaf(x.y, f, acc[k][1]);
+              acc[k][2] = fmaf(x.z, f, acc[k][2]);
+              acc[k][3] = fmaf(x.w, f, acc[k][3]);
+            }
+          }
         }
-        if (threadIdx.x == 0) p.counters[c0] = 0;  // for the next call
+#pragma unroll
+        for (int k = 0; k < IPT; k++) {
+          const int r = r0 + k * RS;
+          if (r >= nrows) break;
+          const float2 sl = ml[r];
+          if (to_out) {
+            const int row = rc * RT + r;
+            const int token = sw.s.q0 + row / p.group, head = h * p.group + row % p.group;
+            const float inv = row_inverse(sl.y, vs);
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[k][e] *= inv;
+            store_out4<C>(p, token, head, d0, acc[k], C::BF);
+            if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(sl.x, sl.y);
+          } else {
+            float* dst = const_cast<float*>(part_of(from));
+            *reinterpret_cast<float4*>(dst + r * D + d0) =
+                make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+            if (d0 == 0) *reinterpret_cast<float2*>(dst + RT * D + 2 * r) = sl;
+          }
+        }
+      };
+      // Counts one arrival; true in every thread for the last of `all`.  A
+      // piece's word has three counts of 10 bits: the first group (0) and the
+      // groups (10) of the unit that begins in it, and the later group (20)
+      // of the unit that reaches into it.
+      auto arrive = [&](int piece, int shift, int all) {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          const int was = atomicAdd(p.counters + piece, 1 << shift) >> shift & 1023;
+          s_last = was == all - 1;
+          if (s_last) atomicSub(p.counters + piece, all << shift);  // for the next call
+        }
+        __syncthreads();
+        if (s_last) __threadfence();
+        return s_last != 0;
+      };
+      if (arrive(c0 + lead, lead ? 20 : 0, members)) {
+        join(lead, 1, members, ng == 1);
+        if (ng > 1 && arrive(c0, 10, ng)) join(0, per, ng, true);
       }
     }
     __syncthreads();  // the buffers are refilled by the next unit
