@@ -44,6 +44,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGran = 64;            // keys per granule
+constexpr float kRescale = 8.0f;     // log2 growth of the maximum that rescales O
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D_, int NB_, int E8_, int BF_>
@@ -357,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
   int b = place.b;
   long long base = place.base;
   bool first_part = true;
+  int done = 0;  // granules of the piece so far
 
   const int ps = p.cache.page_size, ps_shift = p.cache.page_shift;
   const int64_t tb = p.cache.token_bytes;
@@ -392,11 +394,28 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
     const int t_first = kbeg / KT;
     const int ntile = kend > kbeg ? (kend + KT - 1) / KT - t_first : 0;
     const int mine = ntile > warp ? (ntile - warp + kWarps - 1) / kWarps : 0;
+    // The tiles are taken in a circle that begins where the piece would be by
+    // now if all pieces had begun at multiples of their length: pieces of a
+    // sequence's other heads then read the same tokens at about the same time,
+    // neighbours in memory.
+    int turn;
+    {
+      const float len = (float)total / pieces, e = (float)done;
+      const int x0 = (int)(ceilf((g0 - e) / len) * len + e) - g0;
+      turn = x0 * (kGran / KT);
+      if (x0 < 0 || turn >= ntile) turn = 0;
+      done += cnt;
+      turn += warp;
+    }
+    auto key_of = [&](int i) {  // first key of this warp's tile i
+      const int x = turn + i * kWarps;
+      return (t_first + (x < ntile ? x : x - ntile)) * KT;
+    };
 
     const int32_t* table = p.batch.table + (int64_t)b * p.batch.table_stride;
     // page of 16-key group j of this warp's tile i (-1 past the end)
     auto page_of = [&](int i, int j) {
-      const int key = (t_first + warp + i * kWarps) * KT + 16 * j;
+      const int key = key_of(i) + 16 * j;
       if (i >= mine || key >= any1) return -1;
       return __ldg(table + (ps_shift >= 0 ? key >> ps_shift : key / ps));
     };
@@ -408,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
     int ist = 0;  // stage of the next issue
     auto issue = [&](int i) {
       if (i < mine) {
-        const int key0 = (t_first + warp + i * kWarps) * KT;
+        const int key0 = key_of(i);
         const uint32_t kd = ring_s + ist * C::kStageBytes, vd = kd + C::kHalf;
         uint32_t gone = 0;
 #pragma unroll
@@ -518,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
       cp_wait<C::kStages - 2>();
       __syncwarp();
       issue(i + C::kStages - 1);
-      const int key0 = (t_first + warp + i * kWarps) * KT;
+      const int key0 = key_of(i);
       const uint32_t kd = ring_s + st * C::kStageBytes, vd = kd + C::kHalf;
       const uint32_t gone = absent[st];
       st = st == C::kStages - 1 ? 0 : st + 1;
@@ -567,30 +586,49 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
                 s[nb][t][e] = -INFINITY;
             }
       }
-      // ---- running maximum, terms, sum (a row's keys lie over the 8 lanes g)
+      // ---- terms, sum (a row's keys lie over the 8 lanes g).  m is brought
+      // up to the maximum only when some row's has grown past 2^8 of it (terms
+      // stay in range of both 16-bit types, and m goes out with l), so that
+      // most tiles need one vote and no shuffles.
+      float mx[NB][2];
+      bool grow = false;
 #pragma unroll
       for (int nb = 0; nb < NB; nb++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          float mx = fmaxf(s[nb][0][e], s[nb][0][2 + e]);
+          mx[nb][e] = fmaxf(s[nb][0][e], s[nb][0][2 + e]);
 #pragma unroll
-          for (int t = 1; t < MT; t++) mx = fmaxf(mx, fmaxf(s[nb][t][e], s[nb][t][2 + e]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          mx *= cs[nb][e];
-          const float mn = fmaxf(m[nb][e], mx);
-          const float ms = mn == -INFINITY ? 0.0f : mn;
-          if (mn > m[nb][e]) {
-            const float f = ex2(m[nb][e] - ms);
-            l[nb][e] *= f;
+          for (int t = 1; t < MT; t++)
+            mx[nb][e] = fmaxf(mx[nb][e], fmaxf(s[nb][t][e], s[nb][t][2 + e]));
+          mx[nb][e] *= cs[nb][e];
+          grow |= mx[nb][e] > m[nb][e] + kRescale;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int x = 0; x < D / 16; x++) {
-              o[nb][x][e] *= f;
-              o[nb][x][2 + e] *= f;
+        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float x = mx[nb][e];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            if (x > m[nb][e]) {
+              const float f = ex2(m[nb][e] - x);
+              l[nb][e] *= f;
+#pragma unroll
+              for (int y = 0; y < D / 16; y++) {
+                o[nb][y][e] *= f;
+                o[nb][y][2 + e] *= f;
+              }
+              m[nb][e] = x;
             }
-            m[nb][e] = mn;
           }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const float ms = m[nb][e] == -INFINITY ? 0.0f : m[nb][e];
 #pragma unroll
           for (int t = 0; t < MT; t++)
 #pragma unroll
