@@ -30,9 +30,15 @@
 // A row's O is rescaled only when its maximum has grown by more than 2^8
 // since the last time (P stays below 2^8, in range for both 16-bit types, and
 // the final division removes the common factor), which leaves almost no
-// rescales after a row's first tiles.  So the exponentials are taken against
-// the maximum of the tiles before, while this tile's is being looked for, and
-// taken again in the rare case that it has grown too much.
+// rescales after a row's first tiles.
+// What a step takes the longest for is not the products (2048 cycles of the
+// tensor core at head_dim 128) but this code around them, and first of all the
+// fetching of it: the MMA warp waited for almost nothing and still took 3000
+// cycles a step (chunks of 512 at 16384 keys, 205 us), 2450 with the steps in
+// the middle of a unit written out from uniform registers (188 us).  So there
+// is one copy of everything (terms against the maximum of the tiles before,
+// which need a second one for the first tile and for rescales, were as fast
+// over long units and 20 % slower over short ones).
 //
 // Work.  All units' key tiles form one line (heads outermost) that
 // plan_kernel measures from the device-side lengths and cuts into equal
@@ -70,13 +76,13 @@ struct Cfg {
   static constexpr int MBF = BF && !E8;                  // type of the products
   static constexpr int kOp = kTile * D * 2;              // bytes of a 16-bit operand tile
   static constexpr int kRaw = kTile * D;                 // bytes of an E4M3 tile
-  // two stages of K and two of V, so that a step's operands are known from the
-  // parity of its number (constants of the code for that parity)
+  // stages of K and of V
+  static constexpr int kStages = D == 64 ? 4 : 2, kStageBits = D == 64 ? 2 : 1;
   static constexpr int kOffK = 2 * kOp;
-  static constexpr int kOffV = kOffK + 2 * kOp;
-  static constexpr int kOffRaw = kOffV + 2 * kOp;        // E4M3: one K and one V tile
+  static constexpr int kOffV = kOffK + kStages * kOp;
+  static constexpr int kOffRaw = kOffV + kStages * kOp;  // E4M3: one K and one V tile
   static constexpr int kOffBar = kOffRaw + (E8 ? 2 * kRaw : 0);
-  static constexpr int kBars = 10 + 4 + 15 + 2 * kUnits;
+  static constexpr int kBars = 5 * kStages + 4 + 15 + 2 * kUnits;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffUnits = kOffMisc + kGone * 4 + 16;
   static constexpr int kSmem = kOffUnits + kUnits * kRecInts * 4;
@@ -91,24 +97,46 @@ struct Cfg {
 // ------------------------------------------------------------ PTX helpers
 // MMAs and commits are issued by a converged warp, one elected lane each (the
 // same one for the same mask): the operands then stay in uniform registers.
-// From a one-lane branch the issue of 8 MMAs takes 370 cycles, this way 90 to
-// 160, of the 512 they run; operands in ordinary registers cost as much again,
-// so what varies (the ring's stage) passes through a warp reduction, whose
-// result is uniform.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// From a one-lane branch the issue of 8 MMAs takes 370 cycles, this way 90, of
+// the 512 they run.  What comes from memory passes through a warp reduction and
+// every branch hangs on a vote, so that all of it is uniform.
+// (a, b: low words of the operands' descriptors, whose high word is kDescHi)
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+// Four products over 16 channels each, both operands 32 bytes on per product.
+__device__ __forceinline__ void umma_ss4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 x<3>, y<3>;\n\t.reg .b64 a<4>, b<4>;\n\t"
+      "add.u32 x0, %1, 2;\n\tadd.u32 x1, %1, 4;\n\tadd.u32 x2, %1, 6;\n\t"
+      "add.u32 y0, %2, 2;\n\tadd.u32 y1, %2, 4;\n\tadd.u32 y2, %2, 6;\n\t"
+      "mov.b64 a0, {%1, %5};\n\tmov.b64 a1, {x0, %5};\n\t"
+      "mov.b64 a2, {x1, %5};\n\tmov.b64 a3, {x2, %5};\n\t"
+      "mov.b64 b0, {%2, %5};\n\tmov.b64 b1, {y0, %5};\n\t"
+      "mov.b64 b2, {y1, %5};\n\tmov.b64 b3, {y2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// Four products over 16 keys each: A 8 columns of TMEM on per product, B 16
+// rows of 128 bytes.
+__device__ __forceinline__ void umma_ts4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 x<3>, y<3>;\n\t.reg .b64 b<4>;\n\t"
+      "add.u32 x0, %1, 8;\n\tadd.u32 x1, %1, 16;\n\tadd.u32 x2, %1, 24;\n\t"
+      "add.u32 y0, %2, 128;\n\tadd.u32 y1, %2, 256;\n\tadd.u32 y2, %2, 384;\n\t"
+      "mov.b64 b0, {%2, %5};\n\tmov.b64 b1, {y0, %5};\n\t"
+      "mov.b64 b2, {y1, %5};\n\tmov.b64 b3, {y2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x0], b1, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x1], b2, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x2], b3, %3, 1;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -218,6 +246,26 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, int32_t
     if (__any_sync(0xffffffffu, stop)) return false;
   }
   return true;
+}
+// As wait_warp, written so that the compiler sees the warp stay together (the
+// MMA warp's loops and operands then live in uniform registers) and short: at
+// most `limit` looks of up to 1 us each, after which the limit is 1.
+constexpr uint32_t kLooks = 1u << 21;
+__device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, uint32_t& limit) {
+  uint32_t looks = 0;
+  do {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+  } while (++looks < limit);
+  limit = 1;
+  return false;
 }
 // The long wait out of line (the roles' code has to stay in the instruction
 // caches): not for the softmax warps, whose registers a call would have to save.
@@ -752,12 +800,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   // are known to be uniform; checked below)
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [2] each: stages
-  uint64_t* k_empty = k_full + 2;
-  uint64_t* v_full = k_empty + 2;
-  uint64_t* v_empty = v_full + 2;
-  uint64_t* edge_full = v_empty + 2;             // V tiles on their way to the cleaner
-  uint64_t* raw_full = edge_full + 2;            // E4M3 tiles: K, V
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [kStages] each
+  uint64_t* k_empty = k_full + C::kStages;
+  uint64_t* v_full = k_empty + C::kStages;
+  uint64_t* v_empty = v_full + C::kStages;
+  uint64_t* edge_full = v_empty + C::kStages;    // V tiles on their way to the cleaner
+  uint64_t* raw_full = edge_full + C::kStages;   // E4M3 tiles: K, V
   uint64_t* raw_empty = raw_full + 2;
   uint64_t* q_full = raw_empty + 2;              // [2] each: row tiles
   uint64_t* q_raw = q_full + 2;                  // queries still in bf16
@@ -773,14 +821,17 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   volatile uint32_t* poison = tmem_slot + 1;     // a V tile held an infinity or a NaN
   Rec* recs = reinterpret_cast<Rec*>(smem + C::kOffUnits);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the same in all lanes, known to the compiler as such)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < C::kStages; i++) {
       mbar_init(&k_full[i], C::E8 ? 4 : 1);
       mbar_init(&v_full[i], C::E8 ? 4 : 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&edge_full[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
     }
@@ -973,10 +1024,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int h0 = hi - k0, l0 = lo - k0;
         const bool masked = edge(r, j) || gm;
         if (masked) mask_scores(s, h0, l0, gm);
-        // the first half's terms against the old maximum, and the new maximum
-        uint32_t pk[32];
-        uint64_t sum = 0;
-        take_terms<C::MBF>(s, pk, sum, both(c), both(-(m == -INFINITY ? 0.0f : m)));
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
         for (int i = 4; i + 8 <= kTile; i += 8)
@@ -994,7 +1041,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             // (the scores of this tile are complete, so the product before
             // them, the last that added to O, is too)
             const uint64_t f2 = both(f);
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < D / 16; i++) {
               float o[16];
               tmem_ld16(o_col + 16 * i, o);
@@ -1004,9 +1051,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               tmem_st16(o_col + 16 * i, o);
             }
           }
-          sum = 0;
-          take_terms<C::MBF>(s, pk, sum, both(c), both(-(m == -INFINITY ? 0.0f : m)));
         }
+        uint32_t pk[32];
+        uint64_t sum = 0;
+        const uint64_t c2 = both(c), n2 = both(-(m == -INFINITY ? 0.0f : m));
+        take_terms<C::MBF>(s, pk, sum, c2, n2);
         auto hand_over = [&](int half) {
           tmem_st32(s_col + 32 * half, pk);
           tmem_st_wait();
@@ -1015,7 +1064,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
         };
         hand_over(0);
-        take_terms<C::MBF>(s + 64, pk, sum, both(c), both(-(m == -INFINITY ? 0.0f : m)));
+        take_terms<C::MBF>(s + 64, pk, sum, c2, n2);
         l += sum2(sum);
         hand_over(1);
       }
@@ -1035,101 +1084,165 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
     // (no call in this role: a call would cost the operands their uniform
     // registers)
+    uint32_t looks = kLooks;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return wait_warp<false>(bar, parity, p.status);
+      return wait_uniform(smem_u32(bar), parity, looks);
     };
     constexpr uint32_t bf = C::MBF ? (1u << 7) | (1u << 10) : 0u;
     const uint32_t id_qk = umma_idesc_f16(kTile, kTile, 0, 0) | bf;
     const uint32_t id_pv = umma_idesc_f16(kTile, D, 0, 1) | bf;
     uint32_t nq = 0, np = 0;        // bit t: parity of row tile t's next queries, P
-    uint32_t n = 0, nrec = 0;       // steps so far: K and V of step n are in stage n & 1
+    uint32_t n = 0, nrec = 0;       // steps so far: K and V of step n are in stage n % kStages
     bool ok = true;
     const uint64_t qd0 = umma_desc(sbase, 16, 1024);
     auto uni = [](uint32_t x) { return __reduce_max_sync(0xffffffffu, x); };
     const uint32_t q_lo = (uint32_t)qd0;
     const uint32_t k_lo = q_lo + (C::kOffK >> 4);
-    constexpr uint32_t kHi = (1024 >> 4) | (1u << 14) | (2u << 29);  // high word of all three
-    auto desc = [&](uint32_t lo) {
-      uint64_t d;
-      asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kHi));
-      return d;
-    };
     // V: rows of 128 bytes hold 64 channels of one key; 8 keys 1024 B, the
     // second 64 channels kTile * 128 B on
     const uint32_t v_lo = (uint32_t)umma_desc(sbase + C::kOffV, kTile * 128, 1024);
-    // (an MMA takes ~30 instructions in the code, few of them executed; a step
-    // is written once, with 8 of them, so that it stays in the instruction
-    // caches beside the softmax)
-    auto wait_kv = [&](uint64_t* full, uint32_t i) { return wait(&full[i & 1], (i >> 1) & 1); };
+    auto wait_kv = [&](uint64_t* full, uint32_t i) {
+      return wait(&full[i % C::kStages], (i >> C::kStageBits) & 1);
+    };
+    // Step by step: the scores of key tile j (S) and the product with the
+    // values of the tile before (V).  A unit's last product goes with the next
+    // unit's first scores.
+    int t0a = 0, t0e = 0, t1a = 0, t1e = 0;
+    int j = 0, j1 = 0;              // the unit's steps to come
+    uint32_t due = 0;               // bit t: row tile t's product is due,
+    uint32_t add = 0, last = 0;     // adds to O, is its unit's last
+    bool v_due = false, end = false;
     while (ok) {
-      const Rec r = next_rec(nrec, wait);
-      if (!r.live) break;
-      if (r.j1 <= r.j0) continue;
-      uint32_t due = 0;             // bit t: row tile t's P V of the step before is due
-      ok = wait_kv(k_full, n);
+      if (j >= j1 && !end) {
+        const uint32_t slot = nrec % kUnits;
+        ok = wait(&u_full[slot], (nrec / kUnits) & 1);
+        const Rec& r = recs[slot];
+        end = !ok || !uni(r.live);
+        j = end ? 0 : uni(r.j0);
+        j1 = end ? 0 : uni(r.j1);
+        t0a = uni(r.t0a);
+        t0e = uni(r.t0e);
+        t1a = uni(r.t1a);
+        t1e = uni(r.t1e);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&u_empty[slot]);
+        __syncwarp();
+        nrec++;
+        if (j < j1) ok = wait_kv(k_full, n);
+      }
+      const bool has_k = j < j1;
+      if (!has_k && !v_due) {
+        if (end) break;
+        continue;
+      }
+      // The run of steps in the middle of a unit, written out: both row tiles
+      // take part in all of it.  (This warp's instructions, not the products,
+      // are what a step takes the longest for.)
+      const int mid = min(t0e, t1e) - 1;
+      if (j >= max(t0a, t1a) + 2 && j < mid) {
 #pragma unroll 1
-      for (int j = r.j0; ok && j <= r.j1; j++) {
-        const bool has_v = j > r.j0, has_k = j < r.j1;
-        const uint32_t now = (has_k && j >= r.t0a && j < r.t0e ? 1u : 0u) |
-                             (has_k && j >= r.t1a && j < r.t1e ? 2u : 0u);
-        const uint32_t vd = v_lo + ((n - 1) & 1) * (C::kOp >> 4);
-        const uint32_t kd = k_lo + (n & 1) * (C::kOp >> 4);
+        for (; ok && j < mid; j++) {
+          const uint32_t kd = k_lo + n % C::kStages * (C::kOp >> 4);
+          const uint32_t vd = v_lo + (n - 1) % C::kStages * (C::kOp >> 4);
+          const uint32_t np0 = np & 1, np1 = np >> 1;
+          auto scores = [&](int t, int y) {
+            umma_ss4(t * kTile, q_lo + t * (C::kOp >> 4) + y * (kTile * 128 >> 4),
+                     kd + y * (kTile * 128 >> 4), id_qk, y > 0);
+          };
+          auto values = [&](int t, int half) {
+            umma_ts4(2 * kTile + t * D, t * kTile + 32 * half, vd + half * (4 * 2048 >> 4), id_pv, 1);
+          };
+          ok &= wait_kv(v_full, n - 1);
+          ok &= wait(&p_full[0], np0);
+          tc_fence_after();
+          values(0, 0);
+          ok &= wait(&p_full[1], np0);
+          tc_fence_after();
+          values(0, 1);
+          ok &= wait_kv(k_full, n);
+#pragma unroll
+          for (int y = 0; y < D / 64; y++) scores(0, y);
+          commit(&s_full[0]);
+          ok &= wait(&p_full[2], np1);
+          tc_fence_after();
+          values(1, 0);
+          ok &= wait(&p_full[3], np1);
+          tc_fence_after();
+          values(1, 1);
+          commit(&v_empty[(n - 1) % C::kStages]);
+#pragma unroll
+          for (int y = 0; y < D / 64; y++) scores(1, y);
+          commit(&s_full[1]);
+          commit(&k_empty[n % C::kStages]);
+          np ^= 3;
+          n++;
+        }
+        ok = ok && wait_kv(v_full, n - 1) && wait_kv(k_full, n);
+        if (!ok) break;
+      }
+      const uint32_t now = (has_k && j >= t0a && j < t0e ? 1u : 0u) |
+                           (has_k && j >= t1a && j < t1e ? 2u : 0u);
+      const uint32_t vd = v_lo + (n - 1) % C::kStages * (C::kOp >> 4);
+      const uint32_t kd = k_lo + n % C::kStages * (C::kOp >> 4);
+      // The issue of MMAs blocks while the tensor core is busy and leaves it a
+      // few MMAs ahead at most: the next step's waits go between MMAs.
+      auto wait_next = [&]() {
+        if (has_k) ok = ok && wait_kv(v_full, n) && (j + 1 >= j1 || wait_kv(k_full, n + 1));
+      };
+      // (scores overwrite P, so they go after its product)
 #pragma unroll 1
-        for (int t = 0; t < 2; t++) {
-          const int a = t ? r.t1a : r.t0a, e = t ? r.t1e : r.t0e;
+      for (int x = 0; x < 4; x++) {
+        const int t = x >> 1;
+        if (!(x & 1)) {
           if (due >> t & 1) {
             // O += P V; P comes in two halves of the keys
-            uint32_t acc = j - 1 > a;
-            const uint32_t o = uni(2 * kTile + t * D);
+            uint32_t acc = add >> t & 1;
+            const uint32_t o = 2 * kTile + t * D;
 #pragma unroll 1
             for (int half = 0; half < 2; half++) {
-              const uint32_t pa = uni(t * kTile + 32 * half);
-              const uint32_t v = uni(vd + half * (4 * 2048 >> 4)), ac = uni(acc);
+              const uint32_t pa = t * kTile + 32 * half;
+              const uint32_t v = vd + half * (4 * 2048 >> 4);
               ok &= wait(&p_full[2 * t + half], np >> t & 1);
               tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < 4; k++)
-                umma_ts(o, pa + 8 * k, desc(v + k * (2048 >> 4)), id_pv, k > 0 ? 1u : ac);
+              umma_ts4(o, pa, v, id_pv, acc);
               acc = 1;
             }
             np ^= 1u << t;
-            if (!(now >> t & 1)) commit(&o_full[t]);
+            if (last >> t & 1) commit(&o_full[t]);
           }
-          if (t == 1 && has_v) commit(&v_empty[(n - 1) & 1]);
-          if (now >> t & 1) {
-            if (j == a) {
-              ok &= wait(&q_full[t], nq >> t & 1);
-              nq ^= 1u << t;
-            }
-            // S = Q K^T, 64 channels at a time
-            tc_fence_after();
+          if (t == 1 && v_due) commit(&v_empty[(n - 1) % C::kStages]);
+        } else if (now >> t & 1) {
+          if (j == (t ? t1a : t0a)) {
+            ok &= wait(&q_full[t], nq >> t & 1);
+            nq ^= 1u << t;
+          }
+          // S = Q K^T, 64 channels at a time
+          tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < D / 64; x++) {
-              const uint32_t off = x * (kTile * 128 >> 4);
-              const uint32_t qd = uni(q_lo + t * (C::kOp >> 4) + off), kx = uni(kd + off);
-              const uint32_t sc = uni(t * kTile), ac = uni(x);
-#pragma unroll
-              for (int k = 0; k < 4; k++)
-                umma_ss(sc, desc(qd + 2 * k), desc(kx + 2 * k), id_qk, k > 0 ? 1u : ac);
-              // The issue of MMAs blocks while the tensor core is busy and
-              // leaves it a few MMAs ahead at most: the next step's waits go
-              // here, between MMAs.
-              if (x == 0 && t == 1)
-                ok = ok && wait_kv(v_full, n) && (j + 1 >= r.j1 || wait_kv(k_full, n + 1));
-            }
-            commit(&s_full[t]);
-            if (j == e - 1) commit(&q_free[t]);
-          } else if (t == 1 && j < r.j1) {
-            ok = ok && wait_kv(v_full, n) && (j + 1 >= r.j1 || wait_kv(k_full, n + 1));
+          for (int y = 0; y < D / 64; y++) {
+            const uint32_t off = y * (kTile * 128 >> 4);
+            const uint32_t qd = q_lo + t * (C::kOp >> 4) + off, kx = kd + off;
+            const uint32_t sc = t * kTile;
+            umma_ss4(sc, qd, kx, id_qk, y > 0);
+            if (y == 0 && t == 1) wait_next();
           }
+          commit(&s_full[t]);
+          if (j == (t ? t1e : t0e) - 1) commit(&q_free[t]);
+        } else if (t == 1) {
+          wait_next();
         }
-        if (has_k) {
-          commit(&k_empty[n & 1]);
-          n++;
-        }
-        due = now;
+      }
+      add = (j > t0a ? 1u : 0u) | (j > t1a ? 2u : 0u);
+      last = (j == t0e - 1 ? 1u : 0u) | (j == t1e - 1 ? 2u : 0u);
+      due = now;
+      v_due = has_k;
+      if (has_k) {
+        commit(&k_empty[n % C::kStages]);
+        n++;
+        j++;
       }
     }
+    if (looks != kLooks && lane == 0) atomicOr(p.status, kStatusTimeout);
     commit(all_done);
   } else if (warp == 9) {
     // ------------------------------------------------------------ work, TMA
@@ -1177,7 +1290,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         g = __reduce_or_sync(0xffffffffu, g);
         if (g) bad |= kStatusBadPage;
         const int at = ps_shift >= 0 ? key & (ps - 1) : key % ps;
-        const uint32_t st = n & 1, par = (n >> 1) & 1;
+        const uint32_t st = n % C::kStages, par = (n >> C::kStageBits) & 1;
 #pragma unroll 1
         for (int x = 0; x < 2; x++) {  // K, V
           uint64_t* const full = C::E8 ? &raw_full[x] : x ? &v_full[st] : &k_full[st];
@@ -1215,9 +1328,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (bad && lane == 0) atomicOr(p.status, bad);
     // every box this warp requested has landed before the CTA may exit (after
     // a wait that ran out, a step's K may be under way without its V)
+    constexpr uint32_t kBack = C::E8 ? 1 : C::kStages;
 #pragma unroll 1
-    for (uint32_t i = n < 2 ? 0 : n - (C::E8 ? 1 : 2); i < n + (ok ? 0 : 1); i++) {
-      const uint32_t st = i & 1, par = (i >> 1) & 1;
+    for (uint32_t i = n < kBack ? 0 : n - kBack; i < n + (ok ? 0 : 1); i++) {
+      const uint32_t st = i % C::kStages, par = (i >> C::kStageBits) & 1;
       const long long budget = i < n ? kWaitBudgetCycles : 100000;
       mbar_drain(C::E8 ? &raw_full[0] : &k_full[st], C::E8 ? i & 1 : par, budget);
       if (i == n) break;
@@ -1297,7 +1411,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (!r.live) break;
         for (int j = r.j0; ok && j < r.j1; j++, n++) {
           if (!edge(r, j)) continue;
-          const uint32_t st = n & 1;
+          const uint32_t st = n % C::kStages;
           if (!(ok = wait(&edge_full[st], par >> st & 1))) break;
           par ^= 1u << st;
           // keys that every row sees need no look
@@ -1329,10 +1443,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int k0 = (rc.first + j) * kTile;
         const int r0 = rc.any0 - k0, r1 = rc.any1 - k0;
         for (int x = 0; x < 2; x++) {
-          const uint32_t st = n & 1;
+          const uint32_t st = n % C::kStages;
           uint64_t* const full = x ? &v_full[st] : &k_full[st];
           if (!(ok = wait(&raw_full[x], n & 1) &&
-                     wait(x ? &v_empty[st] : &k_empty[st], ((n >> 1) & 1) ^ 1)))
+                     wait(x ? &v_empty[st] : &k_empty[st], ((n >> C::kStageBits) & 1) ^ 1)))
             break;
           const uint32_t src = sbase + C::kOffRaw + x * C::kRaw;
           const uint32_t dst = sbase + (x ? C::kOffV : C::kOffK) + st * C::kOp;
