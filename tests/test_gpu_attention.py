@@ -564,3 +564,14 @@ def test_a_graph_outlives_a_larger_workspace():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and bool((junk == 0xFF).all()) and cache.status() == 0
+
+
+@pytest.mark.parametrize("q", [4, 5, 8, 9])
+@pytest.mark.parametrize("dtype,cdt,D", [(BF, BF, 128), (BF, E4, 128), (FP, E4, 64)],
+                         ids=["bf16_128", "e4m3_128", "e4m3_64"])
+def test_both_sides_of_the_choice_of_kernel(q, dtype, cdt, D):
+    """4 heads per kv head and 4 to 9 drafted tokens: 16 to 36 rows, where the
+    choice between the two kernels changes."""
+    c = ([q, q - 1, 1], [700, q, 65], 32, 8, 2, D, dtype, cdt, True, 0)
+    cache, step, q_ = setup(c)
+    check_attention(cache, step, q_, c[2], D ** -0.5, True, 0)

@@ -8,9 +8,11 @@ using namespace exl3;
 namespace {
 
 // Rows of a sequence and kv head up to which attn_rows is taken.  8 kv heads of
-// 128, bf16, us against attn_tiles: 16 sequences of 4000: 59 / 60 at 16 rows,
-// 81 / 60 at 32; 256 of 1000: 178 / 204, 333 / 205; one of 500: 12 / 15, 13 / 15.
-constexpr int kRowsMost = 16;
+// 128, us against attn_tiles at 16 and 32 rows.  bf16: 16 sequences of 4000
+// 54 / 60, 67 / 60; 256 of 1000 174 / 198, 326 / 200; one of 500 12 / 15,
+// 12 / 15.  E4M3 (which attn_tiles has to widen): 40 / 59, 54 / 59; 123 / 205,
+// 222 / 205; 13 / 16, 13 / 16; at 48 rows 77 / 60, 319 / 207.
+constexpr int kRowsMost = 16, kRowsMostE4m3 = 32;
 constexpr size_t kHead = EXL3_ATTENTION_HEAD_BYTES;  // status word, counters
 static_assert(256 + kRowsCounters * 4 <= kHead, "counters");
 
@@ -225,7 +227,7 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   p.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
   p.scratch = static_cast<uint8_t*>(ws) + kHead;
   // Few rows per sequence and kv head: the cache's bytes bound the step.
-  bool tiles = (long long)batch->max_q * p.group > kRowsMost;
+  bool tiles = (long long)batch->max_q * p.group > (p.e4m3 ? kRowsMostE4m3 : kRowsMost);
   if (path != EXL3_PATH_AUTO) tiles = path == EXL3_PATH_GEMM;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t err = cudaErrorNotSupported;  // a cache that cannot be a TMA source
