@@ -1,0 +1,49 @@
+"""Edges of the attention operators: values that are not finite in places that
+every row of a unit sees, scales of zero, workspaces, streams, inconsistent
+batches.  Tolerances are those of test_gpu_attention.py."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_attention import BF, E4, FP, PATHS, check_attention, setup
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------ values that are not finite
+def plant(cache, step, page, spots):
+    """NaN (infinities too in a 16-bit cache) in V of the given (sequence,
+    position) places, a channel of its own for each, in kv head 0."""
+    tab = step.table.cpu()
+    for i, (b, pos) in enumerate(spots):
+        at = (int(tab[b, pos // page]), pos % page, 0, (7 * i + 3) % cache.head_dim)
+        if cache.dtype == E4:
+            cache.v.view(torch.uint8)[at] = 0x7F
+        else:
+            cache.v[at] = (math.nan, math.inf, -math.inf)[i % 3]
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype,cdt", [(BF, BF), (FP, FP), (BF, E4), (FP, E4)],
+                         ids=["bf16", "fp16", "bf16_e4m3", "fp16_e4m3"])
+@pytest.mark.parametrize("c,spots", [
+    # one token: the last tile is part filled, and every row sees what it holds
+    (([1], [300], 16, 4, 1, 128), [(0, 299), (0, 256), (0, 130)]),
+    (([1, 2], [70, 513], 32, 8, 2, 64), [(0, 69), (0, 0), (1, 512), (1, 511)]),
+    # 65 tokens of 4 heads: a unit of 256 rows and one of 4, of one token
+    (([65], [420], 16, 4, 1, 128), [(0, 419), (0, 384), (0, 400), (0, 355)]),
+    # every row sees every key
+    (([40, 7], [333, 150], 16, 8, 2, 128, False), [(0, 332), (0, 260), (1, 149), (1, 128), (0, 5)]),
+    (([70], [200], 48, 4, 4, 64, False), [(0, 199), (0, 129)]),
+    # a window that begins inside a tile, seen by one token and by several
+    (([1], [500], 16, 4, 1, 128, True, 200), [(0, 299), (0, 300), (0, 303), (0, 499)]),
+    (([1, 1], [459, 260], 16, 4, 1, 64, True, 150), [(0, 308), (0, 309), (0, 315), (0, 319), (1, 110), (1, 111)]),
+    (([3, 80], [700, 300], 16, 4, 1, 64, True, 130), [(0, 567), (0, 570), (0, 699), (1, 91), (1, 120), (1, 299)]),
+], ids=lambda x: f"q{x[0]}_len{x[1]}_d{x[5]}{'_full' if len(x) == 7 else ''}{'_w' if len(x) > 7 else ''}"
+    .replace(" ", "") if isinstance(x, tuple) else "")
+def test_nonfinite_values_reach_those_that_see_them(c, spots, dtype, cdt, path):
+    c = c[:6] + (dtype, cdt) + (c[6:] + (True, 0)[len(c) - 6:])
+    cache, step, q = setup(c)
+    plant(cache, step, c[2], spots)
+    check_attention(cache, step, q, c[2], c[5] ** -0.5, c[8], c[9], path)

@@ -654,6 +654,13 @@ struct Walk {
 // A V tile that needs cleaning, scores that need masking: not every row sees
 // all of the tile's keys.
 __device__ __forceinline__ bool edge(const Rec& r, int j) { return j < r.c0 || j >= r.c1; }
+// The rows [m0, m1) of the V tile from key k0 on that every row sees.  Their
+// values stay as they are, whatever they are: add_poison gives back only what
+// some rows see and others do not.
+__device__ __forceinline__ void seen_by_all(const Rec& r, int k0, int* m0, int* m1) {
+  *m0 = min(max(r.all0 - k0, 0), kTile);
+  *m1 = min(max(r.all1 - k0, *m0), kTile);
+}
 
 // 16-byte chunk of operand row r, channels 8 ch .. 8 ch + 7
 template <int D>
@@ -702,8 +709,9 @@ __device__ __forceinline__ bool clean_v(uint32_t v, int ra, int rb, int r0, int 
     for (int k = 0; k < UN; k++) x[k] = lds16(v + op_off<C::D>(min(r + k * RI, kTile - 1), ch));
 #pragma unroll
     for (int k = 0; k < UN; k++) {
-      const int rk = min(r + k * RI, kTile - 1);
-      uint32_t m0 = not_finite<C>(x[k].x), m1 = not_finite<C>(x[k].y),
+      const int rk = r + k * RI;
+      if (rk >= rb) continue;
+      const uint32_t m0 = not_finite<C>(x[k].x), m1 = not_finite<C>(x[k].y),
                m2 = not_finite<C>(x[k].z), m3 = not_finite<C>(x[k].w);
       const bool in = rk >= r0 && rk < r1;
       if (in && !(m0 | m1 | m2 | m3)) continue;
@@ -1416,7 +1424,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           par ^= 1u << st;
           // keys that every row sees need no look
           const int k0 = (r.first + j) * kTile;
-          const int m0 = min(max(r.all0 - k0, 0), kTile), m1 = min(max(r.all1 - k0, m0), kTile);
+          int m0, m1;
+          seen_by_all(r, k0, &m0, &m1);
           bool hit = false;
 #pragma unroll 1
           for (int x = 0; x < 2; x++)
@@ -1451,6 +1460,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const uint32_t src = sbase + C::kOffRaw + x * C::kRaw;
           const uint32_t dst = sbase + (x ? C::kOffV : C::kOffK) + st * C::kOp;
           const bool clean = x == 1 && edge(rc, j);
+          int m0, m1;
+          seen_by_all(rc, k0, &m0, &m1);
           bool hit = false;
           // 8 lanes take 4 chunks of a row and 4 of the next one, of the other
           // half of the channels where there are two, so that their loads and
@@ -1472,11 +1483,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               const int ch = (tid & 3) + (HALVES == 2 ? 4 * ((r ^ k) & 1) : 0);
               if (clean) {
                 if (r < r0 || r >= r1) v[k] = make_uint4(0, 0, 0, 0);
-                const uint32_t m0 = not_finite<C>(v[k].x), m1 = not_finite<C>(v[k].y),
-                               m2 = not_finite<C>(v[k].z), m3 = not_finite<C>(v[k].w);
-                hit |= (m0 | m1 | m2 | m3) != 0;
-                v[k] = make_uint4(v[k].x & ~whole_mask<C>(m0), v[k].y & ~whole_mask<C>(m1),
-                                  v[k].z & ~whole_mask<C>(m2), v[k].w & ~whole_mask<C>(m3));
+                const uint32_t some = r < m0 || r >= m1 ? 0xffffffffu : 0u;
+                const uint32_t f0 = not_finite<C>(v[k].x) & some, f1 = not_finite<C>(v[k].y) & some,
+                               f2 = not_finite<C>(v[k].z) & some, f3 = not_finite<C>(v[k].w) & some;
+                hit |= (f0 | f1 | f2 | f3) != 0;
+                v[k] = make_uint4(v[k].x & ~whole_mask<C>(f0), v[k].y & ~whole_mask<C>(f1),
+                                  v[k].z & ~whole_mask<C>(f2), v[k].w & ~whole_mask<C>(f3));
               }
               sts16(dst + op_off<D>(r, 2 * ch), e4m3_to_f16x2(v[k].x), e4m3_to_f16x2(v[k].x >> 16),
                     e4m3_to_f16x2(v[k].y), e4m3_to_f16x2(v[k].y >> 16));
