@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from test_gpu_attention import BF, E4, FP, PATHS, check_attention, setup
+from trellis_quantized_moe_exl3_gb300 import PagedBatch, PagedKVCache, kv_append
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,32 @@ def test_nonfinite_values_reach_those_that_see_them(c, spots, dtype, cdt, path):
     cache, step, q = setup(c)
     plant(cache, step, c[2], spots)
     check_attention(cache, step, q, c[2], c[5] ** -0.5, c[8], c[9], path)
+
+
+# ------------------------------------------------------------ inconsistent batches
+def test_append_of_tokens_outside_the_sequence_found():
+    """cu_q that does not ascend: a token whose sequence cannot be told is
+    dropped and reported; nothing is read or written past a sequence's end."""
+    pages, table = 8, [[0, 1], [2, 3], [4, 5], [6, 7]]
+    k, v = [torch.zeros(pages, 16, 1, 16, dtype=BF, device="cuda") for _ in range(2)]
+    cache = PagedKVCache(k, v)
+    new = (1 + torch.arange(12, device="cuda")).view(12, 1, 1).expand(12, 1, 16).to(BF).contiguous()
+
+    def run(cu, lens):
+        k.zero_()
+        v.zero_()
+        b = PagedBatch(*[torch.tensor(x, dtype=torch.int32, device="cuda") for x in (cu, lens, table)], 12)
+        kv_append(cache, b, new, new)
+        bits = cache.status()
+        cache.clear_status()
+        assert torch.equal(k, v)
+        at = k[:, :, 0, 0].flatten().cpu()
+        return bits, {int(i): int(at[i]) for i in at.nonzero()[:, 0]}
+
+    # sequences [0, 10), backwards, [2, 3), [3, 12): tokens 0, 1 fall to the
+    # first, 2 to the second, 3 to 9 to the third, past its end, the rest to the last
+    assert run([0, 10, 2, 3, 12], [10, 5, 32, 31]) == (2, {0: 1, 1: 2, 96 + 29: 11, 96 + 30: 12})
+    assert run([0, 0, 9, 1, 12], [0, 31, 32, 32])[0] == 2
+    # (ascending, the same tokens find their places)
+    assert run([0, 3, 3, 5, 12], [3, 0, 32, 7]) == \
+        (0, {0: 1, 1: 2, 2: 3, 64 + 30: 4, 64 + 31: 5, **{96 + i: 6 + i for i in range(7)}})

@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeParams p, i
       if (b < p.batch.num_seqs) {
         const Seq s = load_seq(p.batch, b, &bad);
         pos = s.len - s.n + (t - s.q0);
-        if (s.n <= 0 || t < s.q0 || pos < 0) {
+        // (where cu_q does not ascend, the sequence found need not hold t)
+        if (t < s.q0 || t - s.q0 >= s.n || pos < 0) {
           bad |= kStatusBadBatch;
         } else {
           const int pi = pos / p.cache.page_size;
