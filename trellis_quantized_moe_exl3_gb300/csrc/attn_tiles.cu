@@ -706,11 +706,10 @@ __device__ __forceinline__ bool clean_v(uint32_t v, int ra, int rb, int r0, int 
   for (int r = ra + lane / CH; r < rb; r += UN * RI) {
     uint4 x[UN];
 #pragma unroll
-    for (int k = 0; k < UN; k++) x[k] = lds16(v + op_off<C::D>(min(r + k * RI, kTile - 1), ch));
+    for (int k = 0; k < UN; k++) x[k] = lds16(v + op_off<C::D>(min(r + k * RI, rb - 1), ch));
 #pragma unroll
     for (int k = 0; k < UN; k++) {
-      const int rk = r + k * RI;
-      if (rk >= rb) continue;
+      const int rk = min(r + k * RI, rb - 1);  // (the last row more than once)
       const uint32_t m0 = not_finite<C>(x[k].x), m1 = not_finite<C>(x[k].y),
                m2 = not_finite<C>(x[k].z), m3 = not_finite<C>(x[k].w);
       const bool in = rk >= r0 && rk < r1;
