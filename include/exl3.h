@@ -328,7 +328,8 @@ typedef struct {
     int head_dim;
     int64_t page_stride, token_stride, head_stride; /* elements, multiples of 16 bytes */
     const float *k_scale;   /* device fp32 [kv_heads] or NULL (1): with EXL3_E4M3 a stored */
-    const float *v_scale;   /*   value x stands for x * scale; NULL with the other types */
+    const float *v_scale;   /*   value x stands for x * scale (a scale may be 0 or negative);
+                                 NULL with the other types */
 } exl3_kv_cache;
 
 /* The sequences of one step.  Sequence b has the new tokens cu_q[b] ..
@@ -389,7 +390,8 @@ exl3_status exl3_qk_norm_rope(const exl3_heads *q, const exl3_heads *k, exl3_dty
  * and rotated as in exl3_qk_norm_rope on the way, values as they are.  With
  * q, the query heads are normed and rotated to q->out in the same launch.
  * Everything is rounded once, from fp32; to E4M3 as
- * E4M3_RNE(clamp(x / scale, -448, 448)), NaN staying NaN.
+ * E4M3_RNE(clamp(x / scale, -448, 448)), or 0 where the scale is 0, NaN
+ * staying NaN.
  *   positions  device int32 [T] of the rotation, or NULL: the positions in the
  *              sequence (where the token is stored never depends on it)
  *   status     device int32, sticky (see above)

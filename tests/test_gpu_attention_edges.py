@@ -50,6 +50,36 @@ def test_nonfinite_values_reach_those_that_see_them(c, spots, dtype, cdt, path):
     check_attention(cache, step, q, c[2], c[5] ** -0.5, c[8], c[9], path)
 
 
+# ------------------------------------------------------------ scales
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("ks,vs", [(0.0, 0.02), (-0.02, -0.01), (1e-45, 0.0)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scales_of_zero_and_below(D, ks, vs, dtype, path):
+    """A stored x stands for x * scale whatever the scale: with 0 every key a
+    token sees weighs the same, and what it does not see weighs nothing."""
+    c = ([1, 70, 3], [77, 301, 200], 16, 8, 2, D, dtype, E4, True, 0)
+    cache, step, q = setup(c)
+    cache.k_scale[0], cache.v_scale[1] = ks, vs
+    check_attention(cache, step, q, c[2], D ** -0.5, True, 0, path)
+
+
+def test_append_with_a_scale_of_zero():
+    """A head whose scale is 0 holds zeros (a NaN stays one), not 0 / 0."""
+    cache = PagedKVCache(*[torch.zeros(1, 16, 2, 16, dtype=E4, device="cuda") for _ in range(2)],
+                         *[torch.tensor([0.0, 0.5], device="cuda") for _ in range(2)])
+    one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    batch = PagedBatch(one, one[1:], one[:1].view(1, 1), 1)
+    x = torch.tensor([0.0, 1.0, -2.0, math.inf, math.nan] + [0.5] * 11, dtype=BF, device="cuda")
+    x = x.expand(1, 2, 16).contiguous()
+    kv_append(cache, batch, x, x)
+    for t in (cache.k, cache.v):
+        got = t[0, 0].float().cpu()
+        assert got[0, :4].tolist() == [0, 0, 0, 0] and math.isnan(got[0, 4]) and not got[0, 5:].any()
+        assert got[1, :4].tolist() == [0, 2, -4, 448] and math.isnan(got[1, 4])
+        assert bool((got[1, 5:] == 1).all())
+
+
 # ------------------------------------------------------------ inconsistent batches
 def test_append_of_tokens_outside_the_sequence_found():
     """cu_q that does not ascend: a token whose sequence cannot be told is

@@ -58,7 +58,8 @@ class PagedKVCache:
     """A paged cache: k and v [pages, page_size, kv_heads, head_dim], fp16, bf16
     or float8_e4m3fn, channels contiguous, the other strides free but alike (a
     permuted view of [pages, kv_heads, page_size, head_dim] works).  k_scale,
-    v_scale: fp32 [kv_heads], E4M3 only; a stored x stands for x * scale.
+    v_scale: fp32 [kv_heads], E4M3 only; a stored x stands for x * scale (0 and
+    negative scales are fine).
     page_size is a multiple of 16.  The tensors must stay alive as long as the
     handle.  `ws` is the workspace of its calls, grown as needed; earlier, smaller
     ones stay alive for the graphs captured with them.  `status()` is the sticky

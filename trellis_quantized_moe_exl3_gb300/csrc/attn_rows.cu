@@ -511,6 +511,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
           qf[nb][i] = pack2<0>(__uint_as_float(qf[nb][i] << 16) * f,
                                __uint_as_float(qf[nb][i] & 0xFFFF0000u) * f);
       }
+      if (C::E8 && !(f_row > 0.0f)) {
+        // a factor that is not positive (a k_scale of 0 or below) would turn
+        // the -inf of masked scores: its sign, or its 0, goes to the queries
+        const __half2 x = __float2half2_rn(f_row < 0.0f ? -1.0f : f_row == 0.0f ? 0.0f : NAN);
+#pragma unroll
+        for (int i = 0; i < D / 8; i++) {
+          const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&qf[nb][i]), x);
+          qf[nb][i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        f_row = f_row < 0.0f ? -f_row : 1.0f;
+      }
 #pragma unroll
       for (int e = 0; e < 2; e++) {
         cs[nb][e] = __shfl_sync(0xffffffffu, f_row, 4 * (2 * c + e));

@@ -1010,6 +1010,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
       }
+      // a factor that is not positive (a k_scale of 0 or below) would turn the
+      // -inf of masked scores: it is applied before the mask then
+      const float pre = c;
+      const bool odd = C::E8 && __any_sync(0xffffffffu, !(c > 0.0f));
+      if (odd) c = 1.0f;
       if (owed) {
         put_out();
         if (!ok) break;
@@ -1029,6 +1034,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         for (int i = 0; i < 4; i++) tmem_ld32_wait(sr + 32 * i);
         const int k0 = (r.first + j) * kTile;
         const int h0 = hi - k0, l0 = lo - k0;
+        if (odd) {
+          const uint64_t pre2 = both(pre);
+#pragma unroll
+          for (int i = 0; i < kTile / 2; i++) mul2(s[2 * i], s[2 * i + 1], pre2);
+        }
         const bool masked = edge(r, j) || gm;
         if (masked) mask_scores(s, h0, l0, gm);
         float mx[4] = {s[0], s[1], s[2], s[3]};

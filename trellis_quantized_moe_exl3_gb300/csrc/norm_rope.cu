@@ -281,7 +281,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeParams p, i
           uint8_t* base = const_cast<uint8_t*>(s == 1 ? p.cache.k : p.cache.v) + dst_k[t] +
                           h * p.cache.head_bytes;
           if (p.e4m3) {
-            if (scale != 1.0f) {
+            if (scale == 0.0f) {  // (whatever is stored stands for 0; a NaN stays one)
+#pragma unroll
+              for (int e = 0; e < 8; e++) v[e] = v[e] != v[e] ? v[e] : 0.0f;
+            } else if (scale != 1.0f) {
 #pragma unroll
               for (int e = 0; e < 8; e++) v[e] = __fdiv_rn(v[e], scale);
             }
