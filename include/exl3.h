@@ -305,16 +305,22 @@ exl3_status exl3_test_set_wait_fault(int kernel, int ks, long long budget_cycles
  *
  * The device status word of these calls is sticky: kernels only set bits in
  * it, so one word can serve every layer of a step.  The caller zeroes it once
- * (the first 4 bytes of the attention workspace, or the word given to
- * exl3_kv_append) and reads it with exl3_get_device_status.  Bits:
+ * (it is the first word of the attention workspace's head, see below, and the
+ * word given to exl3_kv_append) and reads it with exl3_get_device_status.  Bits:
  *   1  a page id outside [0, num_pages): the page's keys count as absent, an
  *      append to it is skipped
  *   2  an inconsistent batch: cu_q not ascending or past T, a length outside
  *      [0, max_pages * page_size], an append before position 0.  A sequence
  *      whose cu_q is inconsistent is left out; a length is clamped
- *   4  a bounded wait ran out (outputs are unspecified)
+ *   4  a bounded wait ran out: outputs are unspecified, those of later calls
+ *      too until the caller clears the bit
  */
 
+/* The head of an attention workspace: the status word, and counters that every
+ * call expects at zero and leaves at zero.  The caller zeroes these bytes once,
+ * before the workspace's first call; what the rest holds does not matter.  A
+ * workspace serves one call at a time: calls that may run at once (on other
+ * streams, in replayed graphs) need one each. */
 #define EXL3_ATTENTION_HEAD_BYTES 4096
 
 /* A paged cache: channel c of kv head h of the token in place i of page p is
@@ -427,6 +433,8 @@ size_t exl3_paged_attention_workspace_size(int T, int heads, int kv_heads, int h
  *          exp(scale * q . k)
  *   path   EXL3_PATH_AUTO, or a fixed kernel: 1 warp-level MMA (few rows),
  *          2 tcgen05 (many rows)
+ *   ws     device, 16-byte aligned, its first EXL3_ATTENTION_HEAD_BYTES zeroed
+ *          once before its first call (see there)
  * head_dim 64 or 128, heads a multiple of kv_heads.  Scores, the running
  * maximum and sum and the output are fp32; softmax terms are rounded to the
  * 16-bit type of the products (dt; fp16 with an E4M3 cache) before they meet

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from test_gpu_attention import BF, E4, FP, PATHS, check_attention, setup
-from trellis_quantized_moe_exl3_gb300 import PagedBatch, PagedKVCache, kv_append
+from trellis_quantized_moe_exl3_gb300 import (PagedBatch, PagedKVCache, _lib, device_status, kv_append,
+                                              paged_attention)
 
 pytestmark = pytest.mark.gpu
 
@@ -78,6 +79,48 @@ def test_append_with_a_scale_of_zero():
         assert got[0, :4].tolist() == [0, 0, 0, 0] and math.isnan(got[0, 4]) and not got[0, 5:].any()
         assert got[1, :4].tolist() == [0, 2, -4, 448] and math.isnan(got[1, 4])
         assert bool((got[1, 5:] == 1).all())
+
+
+# ------------------------------------------------------------ workspaces and streams
+LONG = ([1, 2], [9000, 4000], 32, 16, 1, 128, BF, BF, True, 0)  # units of many parts
+
+
+def batch_of(step):
+    return PagedBatch(step.cu_q, step.seq_lens, step.table, step.max_q)
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_workspace_needs_its_head_zeroed_and_no_more(path):
+    """Through the ABI and with ws=: 0xFF everywhere but in the first
+    EXL3_ATTENTION_HEAD_BYTES."""
+    cache, step, q = setup(LONG, pad=0)
+    batch = batch_of(step)
+    want, lse = paged_attention(q, cache, batch, return_lse=True, path=path)
+    n = cache.workspace_size(3, 16, 2)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:_lib.EXL3_ATTENTION_HEAD_BYTES] = 0
+    for _ in range(2):
+        got, glse = paged_attention(q, cache, batch, return_lse=True, path=path, ws=ws)
+        assert torch.equal(got, want) and torch.equal(glse, lse) and device_status(ws) == 0
+    out = torch.full_like(q, 7.0)
+    torch.cuda.synchronize()
+    assert _lib.lib().exl3_paged_attention(
+        cache._ref, batch._ref, q.data_ptr(), q.stride(0), q.stride(1), _lib.EXL3_BF16, 3, 16, 128 ** -0.5,
+        1, 0, out.data_ptr(), None, path, ws.data_ptr(), n, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_workspaces_that_are_refused():
+    cache, step, q = setup(LONG, pad=0)
+    batch = batch_of(step)
+    n = cache.workspace_size(3, 16, 2)
+    for ws, error in ((torch.zeros(n, dtype=torch.uint8), ValueError),
+                      (torch.zeros(n, dtype=torch.float32, device="cuda"), TypeError),
+                      (torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2], ValueError),
+                      (torch.zeros(n - 1, dtype=torch.uint8, device="cuda"), _lib.Exl3Error)):
+        with pytest.raises(error):
+            paged_attention(q, cache, batch, ws=ws)
 
 
 # ------------------------------------------------------------ inconsistent batches

@@ -272,7 +272,13 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
     of its sequence (all of them when causal is false), and p > P - window when
     window > 0.  scale defaults to head_dim ** -0.5.  Returns out [tokens,
     heads, head_dim], or (out, lse fp32 [tokens, heads]) with return_lse; a
-    token that sees nothing gets out 0 and lse -inf."""
+    token that sees nothing gets out 0 and lse -inf.
+
+    ws: a workspace of the caller's instead of the handle's, uint8, of at least
+    cache.workspace_size(tokens, heads, sequences) bytes, whose first 4096
+    (exl3.h: EXL3_ATTENTION_HEAD_BYTES) were zeroed before its first call.  It
+    serves one call at a time, and holds the status of its own calls
+    (device_status(ws))."""
     if not q.is_cuda:
         _cuda(q, "q", _ACT)
     dim = cache.head_dim
@@ -288,6 +294,7 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
             cache.workspace(*size)
         ws_ptr, ws_bytes = cache._ws_ptr, cache._ws_bytes
     else:
+        _dense(ws, "ws", torch.uint8, ws.shape)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     check(_lib.lib().exl3_paged_attention(
         cache._ref, batch._ref, q.data_ptr(), ts, hs, _ACT[q.dtype], T, heads,
