@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_attention import BF, E4, FP, PATHS, check_attention, setup
+from test_gpu_attention import BF, E4, FP, PATHS, check_attention, freqs, setup
 from trellis_quantized_moe_exl3_gb300 import (PagedBatch, PagedKVCache, _lib, device_status, kv_append,
                                               paged_attention)
 
@@ -121,6 +121,156 @@ def test_workspaces_that_are_refused():
                       (torch.zeros(n - 1, dtype=torch.uint8, device="cuda"), _lib.Exl3Error)):
         with pytest.raises(error):
             paged_attention(q, cache, batch, ws=ws)
+
+
+def dirty(*sizes):
+    """Blocks of 0xFF that the allocator will hand out next."""
+    torch.cuda.empty_cache()
+    junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    del junk
+
+
+def test_first_call_on_another_stream():
+    """stream= on a new handle, while the current stream is busy: the workspace
+    is zeroed, and the output belongs, where the kernels run."""
+    cache, step, q = setup(LONG, pad=0)
+    batch = batch_of(step)
+    want, wlse = paged_attention(q, cache, batch, return_lse=True, path=1)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    dirty(64 << 20, 8 << 20, 4096, q.numel() * 2)
+    fresh = PagedKVCache(cache.k, cache.v)
+    late = torch.empty_like(q)  # freed while a write to it is still to come
+    torch.cuda._sleep(40_000_000)
+    late.fill_(5.0)
+    del late
+    got, lse = paged_attention(q, fresh, batch, return_lse=True, path=1, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(lse, wlse)
+    assert fresh.status() == 0
+
+
+def test_append_on_another_stream():
+    cache, step, q = setup(LONG, pad=0)
+    batch = batch_of(step)
+    k, v = [torch.randn(3, 1, 128, device="cuda").to(BF) for _ in range(2)]
+    want = kv_append(cache, batch, k, v, q=q, inv_freq=freqs(128))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    dirty(8 << 20, 8192, 4096, q.numel() * 2)
+    fresh = PagedKVCache(cache.k, cache.v)
+    late = torch.empty_like(q)
+    torch.cuda._sleep(40_000_000)
+    late.fill_(5.0)
+    del late
+    got = kv_append(fresh, batch, k, v, q=q, inv_freq=freqs(128), stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and fresh.status() == 0
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_one_handle_on_two_streams(path):
+    """Calls in flight on two streams do not meet in the handle's workspace."""
+    cases = [setup(c, pad=0) for c in (LONG, ([2, 1, 1, 40], [3000, 5000, 12000, 700], 32, 16, 1, 128, BF, BF,
+                                              True, 0))]
+    cache, n0 = cases[0][0], cases[0][0].k.shape[0]
+    # one cache with the pages of both cases
+    k, v = [torch.cat([getattr(c[0], x) for c in cases]) for x in "kv"]
+    cache = PagedKVCache(k, v)
+    cases[1][1].table.add_(n0)
+    work = [(q, batch_of(step)) for _, step, q in cases]
+    want = [paged_attention(q, cache, b, path=path) for q, b in work]
+    streams = [torch.cuda.Stream() for _ in work]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for i, (q, b) in enumerate(work):
+            got[i].append(paged_attention(q, cache, b, path=path, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+    assert cache.status() == 0
+    assert torch.equal(paged_attention(work[0][0], cache, work[0][1], path=path), want[0])
+
+
+def test_growth_inside_a_capture_is_refused():
+    cache, step, q = setup(LONG, pad=0)
+    batch = batch_of(step)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="workspace"):
+        with torch.cuda.graph(graph):
+            paged_attention(q, cache, batch)
+    torch.cuda.synchronize()
+    want = paged_attention(q, cache, batch)   # the handle is as good as before
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = paged_attention(q, cache, batch)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and cache.status() == 0
+
+
+def test_append_captured_first():
+    """An append needs no workspace but its status word: a new handle's first
+    call may be a captured one."""
+    cache, step, q = setup(LONG, pad=0)
+    k, v = [torch.randn(3, 1, 128, device="cuda").to(BF) for _ in range(2)]
+    batch, f = batch_of(step), freqs(128)
+    want = kv_append(cache, batch, k, v, q=q, inv_freq=f)
+    fresh = PagedKVCache(torch.zeros_like(cache.k), torch.zeros_like(cache.v))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = kv_append(fresh, batch, k, v, q=q, inv_freq=f)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and fresh.status() == 0
+    step.table[0, 0] = 1 << 20
+    step.table[0, (9000 - 1) // 32] = 1 << 20
+    graph.replay()
+    graph.replay()
+    assert fresh.status() == 1
+
+
+def test_a_graph_beside_calls_on_the_stream_it_was_warmed_up_on():
+    """A replay on one stream and calls on another, both in flight."""
+    cache, step, q = setup(LONG, pad=0)
+    batch, q2 = batch_of(step), q.flip(0).contiguous()
+    want = [paged_attention(x, cache, batch, path=1) for x in (q, q2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = paged_attention(q, cache, batch, path=1)
+    paged_attention(q2, cache, batch, path=1)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs, got = [], []
+    for _ in range(30):
+        with torch.cuda.stream(s):
+            graph.replay()
+            outs.append(out.clone())
+        got.append(paged_attention(q2, cache, batch, path=1))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[0]) for g in outs) and all(torch.equal(g, want[1]) for g in got)
+    assert cache.status() == 0
+
+
+def test_a_growing_step_holds_one_workspace():
+    """Steps of more and more tokens: the handle does not keep a block for each."""
+    k = torch.zeros(64, 16, 2, 64, dtype=BF, device="cuda")
+    cache = PagedKVCache(k, k.clone())
+    table = torch.arange(64, dtype=torch.int32, device="cuda").view(1, 64)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for n in range(8):
+        T = 100 << n
+        q = torch.zeros(T, 8, 64, dtype=BF, device="cuda")
+        cu = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+        paged_attention(q, cache, PagedBatch(cu, cu[1:], table, 100))
+    del q, cu
+    need = cache.workspace_size(T, 8, 1)
+    assert torch.cuda.memory_allocated() - before <= need + (2 << 20) + 65536
 
 
 # ------------------------------------------------------------ inconsistent batches

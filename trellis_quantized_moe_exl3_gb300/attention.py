@@ -6,12 +6,14 @@
     out = paged_attention(q, cache, batch)                  # [tokens, heads, dim]
 
 ``qk_norm_rope`` is the norm and rotation alone, for keys that go to no cache.
-PyTorch supplies device memory and streams only; every call is one or two
-kernels of the library on the current stream, allocates nothing but its
-outputs, and can be captured in a CUDA graph.
+PyTorch supplies device memory and streams only; every call is one or a few
+kernels of the library on the current stream (or on stream=, which the inputs
+must then be ready on), allocates nothing but its outputs, and can be captured
+in a CUDA graph.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import struct
 
@@ -33,10 +35,30 @@ _HEADS = struct.Struct("@QQQiqqqq")
 _ROPE = struct.Struct("@Qii")
 assert _HEADS.size == ctypes.sizeof(_lib.Heads) and _ROPE.size == ctypes.sizeof(_lib.Rope)
 _current_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _stream(stream, t):
     return _current_stream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _on(stream):
+    """Makes stream, where there is one, torch's current stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """An uninitialised contiguous tensor that the launch stream may write at
+    once, for use on the current stream later."""
+    with _on(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _cuda(t, name, dtype):
@@ -61,9 +83,15 @@ class PagedKVCache:
     v_scale: fp32 [kv_heads], E4M3 only; a stored x stands for x * scale (0 and
     negative scales are fine).
     page_size is a multiple of 16.  The tensors must stay alive as long as the
-    handle.  `ws` is the workspace of its calls, grown as needed; earlier, smaller
-    ones stay alive for the graphs captured with them.  `status()` is the sticky
-    device status of all calls on the handle (it synchronises)."""
+    handle.  `status()` is the sticky device status of all calls on the handle
+    (it synchronises).
+
+    The handle keeps a workspace per stream, grown as needed, so calls on
+    different streams may overlap; `ws` is the current stream's.  Captured calls
+    have one of their own: the largest that earlier calls left, for good, so run
+    a step (or call `workspace()`) once before its capture, which raises a
+    RuntimeError where none is large enough.  The graphs of a handle share it:
+    their replays must not overlap unless ws= keeps them apart."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         _cuda(k, "k", _CODES)
@@ -85,37 +113,88 @@ class PagedKVCache:
         d.k_scale = k_scale.data_ptr() if k_scale is not None else None
         d.v_scale = v_scale.data_ptr() if v_scale is not None else None
         self._d, self._ref = d, ctypes.byref(d)
-        self._held = []
-        self._hold(torch.zeros(_lib.EXL3_ATTENTION_HEAD_BYTES, dtype=torch.uint8, device=k.device))
+        self._spaces = {}                    # raw stream -> the workspace of its calls
+        self._graph, self._kept = None, []   # captured calls' workspace, and earlier ones
+        if _capturing():
+            self._graph = self._space(_lib.EXL3_ATTENTION_HEAD_BYTES)
+        else:
+            self._spaces[_current_stream(k.get_device())] = self._space(_lib.EXL3_ATTENTION_HEAD_BYTES)
 
-    def _hold(self, ws):
-        self._held.append(ws)
-        self.ws, self._ws_ptr, self._ws_bytes = ws, ws.data_ptr(), ws.numel()
-        self._ws_for = None  # the size of call last found to fit
+    def _space(self, n):
+        ws = torch.empty(n, dtype=torch.uint8, device=self.k.device)
+        ws[:_lib.EXL3_ATTENTION_HEAD_BYTES].zero_()
+        return _Space(ws, torch.cuda.current_stream(ws.device))
+
+    def _room(self, stream, raw, size):
+        """The workspace of a call of size (tokens, heads, num_seqs), or of one
+        that needs the status word only (None), on a stream."""
+        if stream is None:
+            graph = _capturing()
+        else:
+            with _on(stream):
+                graph = _capturing()
+        w = self._graph if graph else self._spaces.get(raw)
+        if w is None or (size is not None and size != w.fits):
+            n = _lib.EXL3_ATTENTION_HEAD_BYTES if size is None else self.workspace_size(*size)
+            if w is None or w.bytes < n:
+                w = self._take(n) if graph else self._grow(stream, raw, n)
+            w.fits = size
+        return w
+
+    def _grow(self, stream, raw, n):
+        old = self._spaces.get(raw)
+        with _on(stream):
+            # 1 MiB over: each 256 rows more take tens of bytes more
+            w = self._spaces[raw] = self._space(n + (1 << 20 if n > _lib.EXL3_ATTENTION_HEAD_BYTES else 0))
+            if old is not None:
+                w.ws[:4].copy_(old.ws[:4])
+        return w
+
+    def _take(self, n):
+        raw = max(self._spaces, key=lambda r: self._spaces[r].bytes, default=None)
+        if raw is None or self._spaces[raw].bytes < n:
+            raise RuntimeError(f"no workspace of {n} bytes to capture this call with: run it once, or "
+                               "call workspace() for its size, before the capture")
+        if self._graph is not None:
+            self._kept.append(self._graph)
+        self._graph = self._spaces.pop(raw)
+        return self._graph
+
+    def _all(self):
+        return [*self._kept, *([self._graph] if self._graph else []), *self._spaces.values()]
+
+    @property
+    def ws(self) -> torch.Tensor:
+        return (self._spaces.get(_current_stream(self.k.get_device())) or self._all()[-1]).ws
 
     def status(self, stream=None) -> int:
         """The status bits set so far (0: fine); see exl3.h."""
+        torch.cuda.synchronize(self.k.device)
         bits = 0
-        for ws in self._held:
-            bits |= device_status(ws, stream)
+        for w in self._all():
+            bits |= device_status(w.ws, stream)
         return bits
 
     def clear_status(self):
-        for ws in self._held:
-            ws[:4].zero_()
+        for w in self._all():
+            with _on(w.stream if w in self._spaces.values() else None):
+                w.ws[:4].zero_()
 
     def workspace_size(self, tokens: int, heads: int, num_seqs: int) -> int:
         return int(_lib.lib().exl3_paged_attention_workspace_size(
             tokens, heads, self.kv_heads, self.head_dim, num_seqs))
 
     def workspace(self, tokens: int, heads: int, num_seqs: int) -> torch.Tensor:
-        """The handle's workspace, grown to hold a call of this size (the first
-        call of a size inside a graph capture must not be the one that grows it)."""
-        n = self.workspace_size(tokens, heads, num_seqs)
-        if self._ws_bytes < n:
-            self._hold(torch.zeros(n, dtype=torch.uint8, device=self.ws.device))
-        self._ws_for = (tokens, heads, num_seqs)
-        return self.ws
+        """The current stream's workspace, grown to hold a call of this size."""
+        return self._room(None, _current_stream(self.k.get_device()), (tokens, heads, num_seqs)).ws
+
+
+class _Space:
+    """A workspace: of the calls on one stream, or of graphs."""
+    __slots__ = ("ws", "ptr", "bytes", "stream", "fits")
+
+    def __init__(self, ws, stream):
+        self.ws, self.ptr, self.bytes, self.stream, self.fits = ws, ws.data_ptr(), ws.numel(), stream, None
 
 
 class PagedBatch:
@@ -162,10 +241,11 @@ def _act(x, name, dim):
     return T, H, 0 if T == 1 else stride[0], 0 if H == 1 else stride[1]
 
 
-def _like(x):
+def _like(x, stream):
     """An uninitialised contiguous tensor of x's shape."""
-    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype,
-                                                                     device=x.device)
+    if stream is None and x.is_contiguous():
+        return torch.empty_like(x)
+    return _empty(x.shape, x.dtype, x.device, stream)
 
 
 def _weight(w, name, dtype, dim):
@@ -176,11 +256,11 @@ def _weight(w, name, dtype, dim):
     return w.data_ptr()
 
 
-def _out(out, x, T, H, dim, name):
+def _out(out, x, T, H, dim, name, stream):
     """(out, exl3_heads' out pointer and strides): a new tensor, or the given
     one checked."""
     if out is None:
-        out = _like(x)
+        out = _like(x, stream)
         return out, out.data_ptr(), H * dim, dim
     if out.dtype != x.dtype or out.shape != x.shape:
         raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype}")
@@ -220,14 +300,14 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     dim = q.shape[-1]
     T, H, ts, hs = _act(q, "q", dim)
     dtype = q.dtype
-    q_out, p, ots, ohs = _out(q_out, q, T, H, dim, "q_out")
+    q_out, p, ots, ohs = _out(q_out, q, T, H, dim, "q_out", stream)
     hq = _HEADS.pack(q.data_ptr(), p, _weight(q_weight, "q_weight", dtype, dim), H, ts, hs, ots, ohs)
     hk = None
     if k is not None:
         Tk, Hk, ts, hs = _act(k, "k", dim)
         if Tk != T or k.dtype != dtype:
             raise ValueError("q and k must have the same dtype and tokens")
-        k_out, p, ots, ohs = _out(k_out, k, T, Hk, dim, "k_out")
+        k_out, p, ots, ohs = _out(k_out, k, T, Hk, dim, "k_out", stream)
         hk = _HEADS.pack(k.data_ptr(), p, _weight(k_weight, "k_weight", dtype, dim), Hk, ts, hs, ots,
                          ohs)
     check(_lib.lib().exl3_qk_norm_rope(hq, hk, _ACT[dtype], T, dim, _positions(positions, T),
@@ -255,12 +335,13 @@ def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_wei
         Tq, Hq, ts, hs = _act(q, "q", dim)
         if Tq != T or q.dtype != dtype:
             raise ValueError("q and k must have the same dtype and tokens")
-        q_out, p, ots, ohs = _out(q_out, q, T, Hq, dim, "q_out")
+        q_out, p, ots, ohs = _out(q_out, q, T, Hq, dim, "q_out", stream)
         pq = _HEADS.pack(q.data_ptr(), p, _weight(q_weight, "q_weight", dtype, dim), Hq, ts, hs, ots,
                          ohs)
+    raw = _stream(stream, k)
     check(_lib.lib().exl3_kv_append(cache._ref, batch._ref, pq, pk, pv, _ACT[dtype], T,
                                     _rope(inv_freq, interleaved), _positions(positions, T), eps,
-                                    cache._ws_ptr, _stream(stream, k)), "exl3_kv_append")
+                                    cache._room(stream, raw, None).ptr, raw), "exl3_kv_append")
     return q_out
 
 
@@ -283,22 +364,20 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
         _cuda(q, "q", _ACT)
     dim = cache.head_dim
     T, heads, ts, hs = _act(q, "q", dim)
-    if out is None:
-        out = _like(q)
-    else:
-        _dense(out, "out", q.dtype, (T, heads, dim))
-    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    raw = _stream(stream, q)
     if ws is None:
-        size = (T, heads, batch.num_seqs)
-        if size != cache._ws_for:
-            cache.workspace(*size)
-        ws_ptr, ws_bytes = cache._ws_ptr, cache._ws_bytes
+        w = cache._room(stream, raw, (T, heads, batch.num_seqs))
+        ws_ptr, ws_bytes = w.ptr, w.bytes
     else:
         _dense(ws, "ws", torch.uint8, ws.shape)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
+    if out is None:
+        out = _like(q, stream)
+    else:
+        _dense(out, "out", q.dtype, (T, heads, dim))
+    lse = _empty((T, heads), torch.float32, q.device, stream) if return_lse else None
     check(_lib.lib().exl3_paged_attention(
         cache._ref, batch._ref, q.data_ptr(), ts, hs, _ACT[q.dtype], T, heads,
         dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), path, ws_ptr, ws_bytes, _stream(stream, q)),
-        "exl3_paged_attention")
+        None if lse is None else lse.data_ptr(), path, ws_ptr, ws_bytes, raw), "exl3_paged_attention")
     return (out, lse) if return_lse else out
