@@ -310,8 +310,8 @@ exl3_status exl3_test_set_wait_fault(int kernel, int ks, long long budget_cycles
  *   1  a page id outside [0, num_pages): the page's keys count as absent, an
  *      append to it is skipped
  *   2  an inconsistent batch: cu_q not ascending or past T, a length outside
- *      [0, max_pages * page_size], an append before position 0.  A sequence
- *      whose cu_q is inconsistent is left out; a length is clamped
+ *      [0, max_pages * page_size] or past 2^30, an append before position 0.
+ *      A sequence whose cu_q is inconsistent is left out; a length is clamped
  *   4  a bounded wait ran out: outputs are unspecified, those of later calls
  *      too until the caller clears the bit
  */

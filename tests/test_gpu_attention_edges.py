@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_attention import BF, E4, FP, PATHS, check_attention, freqs, setup
+from test_gpu_attention import BF, E4, FP, PATHS, check_attention, freqs, gen, setup
 from trellis_quantized_moe_exl3_gb300 import (PagedBatch, PagedKVCache, _lib, device_status, kv_append,
                                               paged_attention)
 
@@ -300,3 +300,33 @@ def test_append_of_tokens_outside_the_sequence_found():
     # (ascending, the same tokens find their places)
     assert run([0, 3, 3, 5, 12], [3, 0, 32, 7]) == \
         (0, {0: 1, 1: 2, 2: 3, 64 + 30: 4, 64 + 31: 5, **{96 + i: 6 + i for i in range(7)}})
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("c", [([6, 9], [3, 0], 16, 4, 2, 128, BF, BF), ([300, 2, 40], [299, 1, 500], 16, 24, 8, 128, BF, BF),
+                               ([7, 1], [4, 100], 32, 4, 2, 64, BF, E4)], ids=["bf16", "bf16_long", "e4m3"])
+def test_the_widest_window_is_none(c, path):
+    """A window of 2^31 - 1, with tokens that stand before position 0."""
+    cache, step, q = setup(c + (True, 0), pad=0)
+    want = paged_attention(q, cache, batch_of(step), return_lse=True, path=path)
+    for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30 + 1):
+        got = paged_attention(q, cache, batch_of(step), return_lse=True, window=window, path=path)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_lengths_are_held_to_a_billion(path):
+    """A table of 2^31 places of one page, and a length of 2^31 - 1: clamped to
+    2^30 and reported; the window at its end is read where it should be."""
+    g = gen(3)
+    k, v = [torch.randn(1, 4096, 1, 64, generator=g).to(BF).cuda() for _ in range(2)]
+    cache = PagedKVCache(k, v)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.zeros(1, 1 << 19, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 4, 64, generator=g).to(BF).cuda()
+    near = PagedBatch(ints(0, 1), ints(4096), table, 1)
+    want = paged_attention(q, cache, near, window=64, path=path)
+    assert cache.status() == 0
+    got = paged_attention(q, cache, PagedBatch(ints(0, 1), ints(2 ** 31 - 1), table, 1), window=64, path=path)
+    assert cache.status() == 2
+    assert torch.equal(got, want)

@@ -219,7 +219,7 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   p.group = heads / cache->kv_heads;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.causal = causal;
-  p.window = window;
+  p.window = window < kMaxLen ? window : kMaxLen;  // (either sees every earlier key)
   p.bf16 = dt == EXL3_BF16;
   p.e4m3 = cache->dtype == EXL3_E4M3;
   p.dim = cache->head_dim;

@@ -16,6 +16,7 @@ enum : int32_t { kStatusBadPage = 1, kStatusBadBatch = 2 };
 
 constexpr int kMaxSeqs = 65535;
 constexpr int kMaxPageSize = 4096;
+constexpr int kMaxLen = 1 << 30;  // of a sequence: sums of two positions fit 32 bits
 constexpr int kSms = 152;
 constexpr int kRowsCounters = 640;  // parts counters of attn_rows
 
@@ -45,7 +46,8 @@ __device__ __forceinline__ Seq load_seq(const Batch& bt, int b, int32_t* bad) {
     s.n = 0;
     s.q0 = 0;
   }
-  const long long most = (long long)bt.max_pages * bt.page_size;
+  const long long pages = (long long)bt.max_pages * bt.page_size;
+  const long long most = pages < kMaxLen ? pages : kMaxLen;
   if (s.len < 0 || (long long)s.len > most) {
     *bad |= kStatusBadBatch;
     s.len = s.len < 0 ? 0 : (int)most;
