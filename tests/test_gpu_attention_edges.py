@@ -330,3 +330,23 @@ def test_lengths_are_held_to_a_billion(path):
     got = paged_attention(q, cache, PagedBatch(ints(0, 1), ints(2 ** 31 - 1), table, 1), window=64, path=path)
     assert cache.status() == 2
     assert torch.equal(got, want)
+
+
+def test_overlapping_sequences_that_count_past_32_bits():
+    """65535 sequences, every other one of all 2^22 tokens of 8 heads (the rest
+    run backwards): 2^32 units claimed where the rows make 2^17.  The units past
+    those are left out; the first sequence is answered."""
+    T, B = 1 << 22, 65535
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    k, v = [torch.randn(1, 16, 1, 64, generator=gen(8)).to(BF).cuda() for _ in range(2)]
+    cache = PagedKVCache(k, v)
+    q = torch.ones(T, 8, 64, dtype=BF, device="cuda")
+    q[-16:] = torch.randn(16, 8, 64, generator=gen(9)).to(BF).cuda()
+    want = paged_attention(q, cache, PagedBatch(ints(0, T), ints(16), ints([0]), T), path=2)
+    assert cache.status() == 0 and not bool(want[:-16].any()) and bool(want[-16:].any())
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = T
+    lens, table = torch.full((B,), 16, dtype=torch.int32, device="cuda"), torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    got = paged_attention(q, cache, PagedBatch(cu, lens, table, T), path=2)
+    assert cache.status() == 2
+    assert torch.equal(got, want)

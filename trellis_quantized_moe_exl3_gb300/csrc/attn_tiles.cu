@@ -490,8 +490,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnParams p, P
     }
     const long long inc = block_scan(n, &total);
     if (b < B) {
-      pl.seq_unit[b] = (int)(run + inc - n);
-      if (b < kCache) unit_s[b] = (int)(run + inc - n);
+      // (no further than max_unit, whose overlapping sequences could count past
+      // 32 bits: the search below needs ascending numbers)
+      const int first = (int)min(run + inc - n, (long long)max_unit);
+      pl.seq_unit[b] = first;
+      if (b < kCache) unit_s[b] = first;
     }
     run += total;
   }
