@@ -86,12 +86,14 @@ class PagedKVCache:
     handle.  `status()` is the sticky device status of all calls on the handle
     (it synchronises).
 
-    The handle keeps a workspace per stream, grown as needed, so calls on
-    different streams may overlap; `ws` is the current stream's.  Captured calls
-    have one of their own: the largest that earlier calls left, for good, so run
-    a step (or call `workspace()`) once before its capture, which raises a
-    RuntimeError where none is large enough.  The graphs of a handle share it:
-    their replays must not overlap unless ws= keeps them apart."""
+    The handle keeps a workspace per stream (`ws` is the current stream's), so
+    calls on different streams may overlap.  A captured call uses that of the
+    stream it is captured on; torch.cuda.graph's own capture stream gets one
+    that another stream leaves to it for good, so run a step (or call
+    `workspace()`) once before its capture, which raises a RuntimeError where
+    none is large enough.  Replays of a handle's graphs must not overlap one
+    another, nor calls on the stream they were captured on, unless ws= keeps
+    them apart."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         _cuda(k, "k", _CODES)
@@ -113,72 +115,62 @@ class PagedKVCache:
         d.k_scale = k_scale.data_ptr() if k_scale is not None else None
         d.v_scale = v_scale.data_ptr() if v_scale is not None else None
         self._d, self._ref = d, ctypes.byref(d)
-        self._spaces = {}                    # raw stream -> the workspace of its calls
-        self._graph, self._kept = None, []   # captured calls' workspace, and earlier ones
-        if _capturing():
-            self._graph = self._space(_lib.EXL3_ATTENTION_HEAD_BYTES)
-        else:
-            self._spaces[_current_stream(k.get_device())] = self._space(_lib.EXL3_ATTENTION_HEAD_BYTES)
+        self._spaces = {}  # raw stream -> the workspace of its calls
+        self._all = []     # every one so far: a graph may hold an outgrown one
+        self._spaces[_current_stream(k.get_device())] = self._space(_lib.EXL3_ATTENTION_HEAD_BYTES)
 
     def _space(self, n):
         ws = torch.empty(n, dtype=torch.uint8, device=self.k.device)
         ws[:_lib.EXL3_ATTENTION_HEAD_BYTES].zero_()
-        return _Space(ws, torch.cuda.current_stream(ws.device))
+        self._all.append(_Space(ws))
+        return self._all[-1]
 
     def _room(self, stream, raw, size):
         """The workspace of a call of size (tokens, heads, num_seqs), or of one
         that needs the status word only (None), on a stream."""
-        if stream is None:
-            graph = _capturing()
-        else:
+        w = self._spaces.get(raw)
+        n = _lib.EXL3_ATTENTION_HEAD_BYTES if size is None else self.workspace_size(*size)
+        if w is None or w.bytes < n:
             with _on(stream):
-                graph = _capturing()
-        w = self._graph if graph else self._spaces.get(raw)
-        if w is None or (size is not None and size != w.fits):
-            n = _lib.EXL3_ATTENTION_HEAD_BYTES if size is None else self.workspace_size(*size)
-            if w is None or w.bytes < n:
-                w = self._take(n) if graph else self._grow(stream, raw, n)
-            w.fits = size
-        return w
-
-    def _grow(self, stream, raw, n):
-        old = self._spaces.get(raw)
-        with _on(stream):
-            # 1 MiB over: each 256 rows more take tens of bytes more
-            w = self._spaces[raw] = self._space(n + (1 << 20 if n > _lib.EXL3_ATTENTION_HEAD_BYTES else 0))
-            if old is not None:
-                w.ws[:4].copy_(old.ws[:4])
+                if _capturing():
+                    w = self._take(n)
+                else:
+                    # 1 MiB over: each 256 rows more take tens of bytes more
+                    w = self._space(n if size is None else n + (1 << 20))
+            self._spaces[raw] = w
+        w.fits = size
         return w
 
     def _take(self, n):
-        raw = max(self._spaces, key=lambda r: self._spaces[r].bytes, default=None)
-        if raw is None or self._spaces[raw].bytes < n:
+        """A workspace for a capture: no other stream's from now on, unless
+        only those that graphs have taken are large enough."""
+        fit = [(not w.graph, w.bytes, r) for r, w in self._spaces.items() if w.bytes >= n]
+        if not fit:
             raise RuntimeError(f"no workspace of {n} bytes to capture this call with: run it once, or "
                                "call workspace() for its size, before the capture")
-        if self._graph is not None:
-            self._kept.append(self._graph)
-        self._graph = self._spaces.pop(raw)
-        return self._graph
-
-    def _all(self):
-        return [*self._kept, *([self._graph] if self._graph else []), *self._spaces.values()]
+        free, _, raw = max(fit)
+        w = self._spaces.pop(raw) if free else self._spaces[raw]
+        w.graph = True
+        return w
 
     @property
     def ws(self) -> torch.Tensor:
-        return (self._spaces.get(_current_stream(self.k.get_device())) or self._all()[-1]).ws
+        return (self._spaces.get(_current_stream(self.k.get_device())) or self._all[-1]).ws
 
     def status(self, stream=None) -> int:
         """The status bits set so far (0: fine); see exl3.h."""
         torch.cuda.synchronize(self.k.device)
         bits = 0
-        for w in self._all():
+        for w in self._all:
             bits |= device_status(w.ws, stream)
         return bits
 
     def clear_status(self):
-        for w in self._all():
-            with _on(w.stream if w in self._spaces.values() else None):
-                w.ws[:4].zero_()
+        wait = (lambda d: None) if _capturing() else torch.cuda.synchronize
+        wait(self.k.device)  # (the calls of every stream before and after)
+        for w in self._all:
+            w.ws[:4].zero_()
+        wait(self.k.device)
 
     def workspace_size(self, tokens: int, heads: int, num_seqs: int) -> int:
         return int(_lib.lib().exl3_paged_attention_workspace_size(
@@ -190,11 +182,12 @@ class PagedKVCache:
 
 
 class _Space:
-    """A workspace: of the calls on one stream, or of graphs."""
-    __slots__ = ("ws", "ptr", "bytes", "stream", "fits")
+    """A workspace: graph: a capture has taken it; fits: the size of call it was
+    last found to fit."""
+    __slots__ = ("ws", "ptr", "bytes", "graph", "fits")
 
-    def __init__(self, ws, stream):
-        self.ws, self.ptr, self.bytes, self.stream, self.fits = ws, ws.data_ptr(), ws.numel(), stream, None
+    def __init__(self, ws):
+        self.ws, self.ptr, self.bytes, self.graph, self.fits = ws, ws.data_ptr(), ws.numel(), False, None
 
 
 class PagedBatch:
@@ -341,7 +334,8 @@ def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_wei
     raw = _stream(stream, k)
     check(_lib.lib().exl3_kv_append(cache._ref, batch._ref, pq, pk, pv, _ACT[dtype], T,
                                     _rope(inv_freq, interleaved), _positions(positions, T), eps,
-                                    cache._room(stream, raw, None).ptr, raw), "exl3_kv_append")
+                                    (cache._spaces.get(raw) or cache._room(stream, raw, None)).ptr, raw),
+          "exl3_kv_append")
     return q_out
 
 
@@ -366,7 +360,9 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
     T, heads, ts, hs = _act(q, "q", dim)
     raw = _stream(stream, q)
     if ws is None:
-        w = cache._room(stream, raw, (T, heads, batch.num_seqs))
+        w, size = cache._spaces.get(raw), (T, heads, batch.num_seqs)
+        if w is None or w.fits != size:
+            w = cache._room(stream, raw, size)
         ws_ptr, ws_bytes = w.ptr, w.bytes
     else:
         _dense(ws, "ws", torch.uint8, ws.shape)
