@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import _attention_ref as R
 from test_gpu_attention import BF, E4, FP, PATHS, check_attention, freqs, gen, setup
 from trellis_quantized_moe_exl3_gb300 import (PagedBatch, PagedKVCache, _lib, device_status, kv_append,
                                               paged_attention)
@@ -79,6 +80,33 @@ def test_append_with_a_scale_of_zero():
         assert got[0, :4].tolist() == [0, 0, 0, 0] and math.isnan(got[0, 4]) and not got[0, 5:].any()
         assert got[1, :4].tolist() == [0, 2, -4, 448] and math.isnan(got[1, 4])
         assert bool((got[1, 5:] == 1).all())
+
+
+# ------------------------------------------------------------ softmax terms
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype,cdt", [(FP, FP), (BF, BF), (FP, E4)], ids=["fp16", "bf16", "fp16_e4m3"])
+@pytest.mark.parametrize("n,L,D", [(1, 3000, 64), (70, 1500, 128)])
+def test_small_terms_count(n, L, D, dtype, cdt, path):
+    """One key outweighs every other one by about 2^25 and its value is 0: the
+    output is what the others add.  Terms are rounded to 16 bits: half a step
+    of theirs, or in fp16 (below 2^-14) 2^-25, against a largest term that
+    stands at 2^7; so an output is off by at most 2^-32 of the values' sum."""
+    step, pages = R.make_step(gen(1), [n], [L], 16)
+    k = torch.zeros(pages, 16, 1, D, dtype=cdt, device="cuda")
+    v = torch.full_like(k, 64.0, dtype=torch.float32).to(cdt)
+    at = (int(step.table[0, 0]), 0, 0)
+    k[at] = torch.tensor([17.5 if cdt != E4 else 18.0] + [0.0] * (D - 1), device="cuda").to(cdt)
+    v[at] = torch.zeros(D, device="cuda").to(cdt)
+    q = torch.zeros(n, 2, D, dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    batch = PagedBatch(step.cu_q, step.seq_lens, step.table, n)
+    got = paged_attention(q, PagedKVCache(k, v), batch, scale=1.0, path=path).double().cpu()
+    e = math.exp(-float(k[at][0]))
+    others = torch.arange(L - n, L, dtype=torch.float64)[:, None, None]  # keys a token sees but the first
+    ref = 64 * others * e / (1 + others * e)
+    u = R.U[dtype]
+    tol = 2 * u * ref + 1e-4 * ref + 2.0 ** -25 + (64 * others * 2.0 ** -32 if dtype == FP or cdt == E4 else 0)
+    assert bool(((got - ref).abs() <= tol).all()), float(((got - ref).abs() / tol).max())
 
 
 # ------------------------------------------------------------ workspaces and streams

@@ -50,6 +50,13 @@ constexpr float kLn2 = 0.69314718055994531f;
 template <int D_, int NB_, int E8_, int BF_>
 struct Cfg {
   static constexpr int D = D_, NB = NB_, E8 = E8_, BF = BF_;
+  static constexpr int MBF = BF && !E8;             // type of the products
+  // Softmax terms meet V as 16-bit values (an fp32 product would have to be
+  // split in two and take twice the MMAs): bf16 rounds a term by 2^-9 of it at
+  // most; fp16 by 2^-12 while it is above 2^-14, so there the terms are 2^7
+  // times as large (below 2^15 with kRescale), and what is lost of a small one
+  // is below 2^-32 of the largest.  The sum is of the unrounded terms.
+  static constexpr float kLift = MBF ? 0.0f : 7.0f;
   static constexpr int RB = D * (E8 ? 1 : 2);       // bytes of a key row
   static constexpr int CPR = RB / 16;               // 16-byte chunks of it
   // bytes of K (and of V) in a tile: 2 KB at 64 channels let 4 CTAs share an
@@ -324,14 +331,14 @@ __device__ __forceinline__ void store_out4(const AttnParams& p, int token, int h
 
 // Final value of a row: o / l (0 where nothing was seen) and the natural log.
 __device__ __forceinline__ float row_inverse(float l, float vs) { return l > 0.0f || l != l ? vs / l : 0.0f; }
-__device__ __forceinline__ float row_lse(float m, float l) {
-  return l > 0.0f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
+__device__ __forceinline__ float row_lse(float m, float l, float lift) {
+  return l > 0.0f || l != l ? (m + (log2f(l) - lift)) * kLn2 : -INFINITY;
 }
 
 template <class C>
 __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(AttnParams p) {
   constexpr int D = C::D, NB = C::NB, KT = C::KT, MT = C::MT, RT = C::RT;
-  constexpr int MBF = C::BF && !C::E8;  // type of the products
+  constexpr int MBF = C::MBF;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
       for (int nb = 0; nb < NB; nb++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          const float ms = m[nb][e] == -INFINITY ? 0.0f : m[nb][e];
+          const float ms = (m[nb][e] == -INFINITY ? 0.0f : m[nb][e]) - C::kLift;
 #pragma unroll
           for (int t = 0; t < MT; t++)
 #pragma unroll
@@ -744,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[e] *= inv;
         store_out4<C>(p, token, head, d0, acc, C::BF);
-        if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(mm, ll);
+        if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(mm, ll, C::kLift);
       } else {
         *reinterpret_cast<float4*>(part + r * D + d0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         if (d0 == 0) *reinterpret_cast<float2*>(part + RT * D + 2 * r) = make_float2(mm, ll);
@@ -831,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
 #pragma unroll
             for (int e = 0; e < 4; e++) acc[k][e] *= inv;
             store_out4<C>(p, token, head, d0, acc[k], C::BF);
-            if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(sl.x, sl.y);
+            if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(sl.x, sl.y, C::kLift);
           } else {
             float* dst = const_cast<float*>(part_of(from));
             *reinterpret_cast<float4*>(dst + r * D + d0) =

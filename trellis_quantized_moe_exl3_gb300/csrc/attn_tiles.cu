@@ -28,9 +28,11 @@
 // P is handed over in two halves of 64 keys, so that the product starts while
 // the second half's exponentials are taken.
 // A row's O is rescaled only when its maximum has grown by more than 2^8
-// since the last time (P stays below 2^8, in range for both 16-bit types, and
-// the final division removes the common factor), which leaves almost no
-// rescales after a row's first tiles.
+// since the last time (P stays in range for both 16-bit types, and the final
+// division removes the common factor), which leaves almost no rescales after a
+// row's first tiles.  P is 16 bits because that is what the tensor core
+// multiplies: bf16 rounds a term by 2^-9 of it, fp16 by 2^-12; the sum is of
+// the unrounded terms.
 // What a step takes the longest for is not the products (2048 cycles of the
 // tensor core at head_dim 128) but this code around them, and first of all the
 // fetching of it: the MMA warp waited for almost nothing and still took 3000
@@ -74,6 +76,9 @@ template <int D_, int E8_, int BF_>
 struct Cfg {
   static constexpr int D = D_, E8 = E8_, BF = BF_;
   static constexpr int MBF = BF && !E8;                  // type of the products
+  // log2 of a factor of the terms: fp16 holds what is below 2^-14 in fewer
+  // bits, so there they are 2^7 times as large (below 2^15 with kRescale)
+  static constexpr float kLift = MBF ? 0.0f : 7.0f;
   static constexpr int kOp = kTile * D * 2;              // bytes of a 16-bit operand tile
   static constexpr int kRaw = kTile * D;                 // bytes of an E4M3 tile
   // stages of K and of V
@@ -757,8 +762,8 @@ __device__ __noinline__ void add_poison(const Cache c, const int32_t* table, int
 }
 
 __device__ __forceinline__ float row_inverse(float l, float vs) { return l > 0.0f || l != l ? vs / l : 0.0f; }
-__device__ __forceinline__ float row_lse(float m, float l) {
-  return l > 0.0f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
+__device__ __forceinline__ float row_lse(float m, float l, float lift) {
+  return l > 0.0f || l != l ? (m + (log2f(l) - lift)) * kLn2 : -INFINITY;
 }
 
 // Scores of keys that the row does not see (before l0, after h0, in absent
@@ -964,7 +969,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (!whole)
           *reinterpret_cast<float2*>(part + (size_t)kUnitRows * D + 2 * prt) = make_float2(o_m, o_l);
         else if (p.lse)
-          p.lse[at] = row_lse(o_m, o_l);
+          p.lse[at] = row_lse(o_m, o_l, C::kLift);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&u_empty[(nrec - 1) % kUnits]);
@@ -1074,7 +1079,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
         uint32_t pk[32];
         uint64_t sum = 0;
-        const uint64_t c2 = both(c), n2 = both(-(m == -INFINITY ? 0.0f : m));
+        const uint64_t c2 = both(c), n2 = both(C::kLift - (m == -INFINITY ? 0.0f : m));
         take_terms<C::MBF>(s, pk, sum, c2, n2);
         auto hand_over = [&](int half) {
           tmem_st32(s_col + 32 * half, pk);
@@ -1567,7 +1572,7 @@ __global__ void __launch_bounds__(256) attn_tiles_join_kernel(AttnParams p, Plan
     o.x = pack2<C::BF>(acc[0] * inv, acc[1] * inv);
     o.y = pack2<C::BF>(acc[2] * inv, acc[3] * inv);
     *reinterpret_cast<uint2*>(p.out + ((int64_t)token * p.heads + head) * D + d0) = o;
-    if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(mm, ll);
+    if (p.lse && d0 == 0) p.lse[(int64_t)token * p.heads + head] = row_lse(mm, ll, C::kLift);
   }
 }
 
