@@ -438,7 +438,9 @@ size_t exl3_paged_attention_workspace_size(int T, int heads, int kv_heads, int h
  * head_dim 64 or 128, heads a multiple of kv_heads.  Scores, the running
  * maximum and sum and the output are fp32; softmax terms are rounded to the
  * 16-bit type of the products (dt; fp16 with an E4M3 cache) before they meet
- * the values.  Errors: as exl3_kv_append, EXL3_ERR_ARG for scale not finite
+ * the values; bf16 queries meet an E4M3 cache as fp16, times a power of two per
+ * query head that brings its largest channel to 2^14: channels below 2^-31 of
+ * that one lose bits, those below 2^-39 count as 0.  Errors: as exl3_kv_append, EXL3_ERR_ARG for scale not finite
  * and positive, window < 0 or without causal, and EXL3_ERR_WORKSPACE. */
 exl3_status exl3_paged_attention(const exl3_kv_cache *cache, const exl3_kv_batch *batch,
                                  const void *q, int64_t q_token_stride, int64_t q_head_stride,

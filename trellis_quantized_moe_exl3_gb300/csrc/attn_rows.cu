@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
       float f_row = cbase;
       if (C::E8 && C::BF) {
         // bf16 to fp16: 2^s brings the row's largest value to [2^14, 2^15);
-        // values below 2^-38 of it lose bits
+        // values below 2^-31 of it lose bits, those below 2^-39 vanish
         float am = 0.0f;
 #pragma unroll
         for (int i = 0; i < D / 8; i++)

@@ -987,8 +987,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       float c = p.scale_log2 * (C::E8 && p.cache.k_scale ? __ldg(p.cache.k_scale + r.h) : 1.0f);
       if (C::kCvtQ && r.live && j0 < j1) {
         // bf16 queries to fp16, in place, by a power of two per row: 2^s
-        // brings the row's largest value to [2^14, 2^15); values below 2^-38
-        // of it lose bits
+        // brings the row's largest value to [2^14, 2^15); values below 2^-31
+        // of it lose bits, those below 2^-39 vanish
         if (!(ok = wait(&q_raw[t], uses & 1))) break;
         const uint32_t q = sbase + t * C::kOp;
         float am = 0.0f;
