@@ -448,6 +448,18 @@ exl3_status exl3_paged_attention(const exl3_kv_cache *cache, const exl3_kv_batch
                                  int window, void *out, float *lse, int path, void *ws,
                                  size_t ws_bytes, void *stream);
 
+/* Test hook of the bounded waits of exl3_paged_attention's tcgen05 kernel, as
+ * exl3_test_set_wait_fault is of the MoE kernels': in every CTA, barrier number
+ * `barrier` (0 ..; a number past the last has no effect) never completes, so
+ * that the waits on it, where the call has any, run out: after `budget_cycles`
+ * SM clock cycles (1,000,000 .. 1,000,000,000, the default) in the warp that
+ * issues the products, after at most the default in the others.  The call then
+ * sets status bit 4, issues nothing more, drains its copies and products, frees
+ * its TMEM and returns.  barrier = -1 clears the hook.  It stays set for every
+ * later call of the process.  Not thread safe.  Errors: EXL3_ERR_ARG for values
+ * outside these ranges. */
+exl3_status exl3_test_set_attention_wait_fault(int barrier, long long budget_cycles);
+
 const char *exl3_status_string(exl3_status s);
 
 #ifdef __cplusplus

@@ -378,3 +378,33 @@ def test_overlapping_sequences_that_count_past_32_bits():
     got = paged_attention(q, cache, PagedBatch(cu, lens, table, T), path=2)
     assert cache.status() == 2
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------ bounded waits
+@pytest.mark.parametrize("dtype,cdt,D", [(BF, BF, 128), (FP, FP, 64), (BF, E4, 128), (FP, E4, 64)],
+                         ids=["bf16_128", "fp16_64", "e4m3_128", "e4m3_64"])
+def test_attention_waits_run_out(dtype, cdt, D):
+    """Each of the tile kernel's barriers in turn never completes, with a budget
+    of 2,000,000 cycles, about 1 ms (nothing that was issued is held back, so
+    copies and products end by themselves): the call returns, with status bit 4
+    if it waits on that barrier, and once the bit is cleared the next call on
+    the workspace is right."""
+    c = ([700, 300, 1], [9000, 300, 2000], 64, 8, 2, D, dtype, cdt, True, 0)
+    cache, step, q = setup(c, pad=0)
+    batch = batch_of(step)
+    want = paged_attention(q, cache, batch, path=2)
+    assert cache.status() == 0
+    L, seen = _lib.lib(), []
+    for barrier in range(64):
+        assert L.exl3_test_set_attention_wait_fault(barrier, 2_000_000) == 0
+        try:
+            paged_attention(q, cache, batch, path=2)
+            seen.append(cache.status())
+        finally:
+            assert L.exl3_test_set_attention_wait_fault(-1, 0) == 0
+        cache.clear_status()
+        assert torch.equal(paged_attention(q, cache, batch, path=2), want) and cache.status() == 0
+    # k_full, k_empty, v_full, v_empty; queries, scores, outputs, terms; units
+    n = 4 if D == 64 else 2
+    assert set(seen) == {0, 4} and all(seen[i] == 4 for i in range(4 * n)), seen
+    assert seen.count(4) >= 4 * n + 14 and not any(seen[5 * n + 26:]), seen

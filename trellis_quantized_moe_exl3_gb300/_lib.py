@@ -135,6 +135,8 @@ def lib():
     L.exl3_paged_attention_workspace_size.restype = sz
     L.exl3_paged_attention.argtypes = [vp, vp, vp, i64, i64, i, i, i, f, i, i, vp, vp, i, vp, sz, vp]
     L.exl3_paged_attention.restype = i
+    L.exl3_test_set_attention_wait_fault.argtypes = [i, ctypes.c_longlong]
+    L.exl3_test_set_attention_wait_fault.restype = i
     L.exl3_status_string.argtypes = [i]
     L.exl3_status_string.restype = ctypes.c_char_p
     _lib = L

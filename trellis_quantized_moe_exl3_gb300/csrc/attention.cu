@@ -2,6 +2,7 @@
 #include <math.h>
 
 #include "attn.cuh"
+#include "pipeline.cuh"
 
 using namespace exl3;
 
@@ -15,6 +16,13 @@ namespace {
 constexpr int kRowsMost = 16, kRowsMostE4m3 = 32;
 constexpr size_t kHead = EXL3_ATTENTION_HEAD_BYTES;  // status word, counters
 static_assert(256 + kRowsCounters * 4 <= kHead, "counters");
+
+// The bounded waits of attn_tiles (exl3_test_set_attention_wait_fault).
+struct Waits {
+  long long budget = kWaitBudgetCycles;
+  int stuck_barrier = -1;
+};
+Waits g_waits;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool good(const void* p) { return p && aligned16(p); }
@@ -226,6 +234,9 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   p.status = static_cast<int32_t*>(ws);
   p.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
   p.scratch = static_cast<uint8_t*>(ws) + kHead;
+  p.wait_budget = g_waits.budget;
+  p.wait_looks = (uint32_t)(g_waits.budget / 500);  // of up to 1 us, 2000 cycles
+  p.stuck_barrier = g_waits.stuck_barrier;
   // Few rows per sequence and kv head: the cache's bytes bound the step.
   bool tiles = (long long)batch->max_q * p.group > (p.e4m3 ? kRowsMostE4m3 : kRowsMost);
   if (path != EXL3_PATH_AUTO) tiles = path == EXL3_PATH_GEMM;
@@ -234,6 +245,18 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
   if (tiles) err = launch_attn_tiles(p, st);
   if (err == cudaErrorNotSupported) err = launch_attn_rows(p, st);
   return err == cudaSuccess ? EXL3_OK : EXL3_ERR_CUDA;
+}
+
+exl3_status exl3_test_set_attention_wait_fault(int barrier, long long budget_cycles) {
+  if (barrier == -1) {
+    g_waits = Waits{};
+    return EXL3_OK;
+  }
+  if (barrier < 0 || budget_cycles < 1000000 || budget_cycles > kWaitBudgetCycles)
+    return EXL3_ERR_ARG;
+  g_waits.stuck_barrier = barrier;
+  g_waits.budget = budget_cycles;
+  return EXL3_OK;
 }
 
 }  // extern "C"

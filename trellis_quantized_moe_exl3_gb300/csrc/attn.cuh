@@ -102,6 +102,12 @@ struct AttnParams {
   int32_t* status;
   int32_t* counters;  // [kRowsCounters], zero between calls
   void* scratch;
+  // the bounded waits of attn_tiles: the MMA warp's in looks (its status bit
+  // ends the other warps'), the drains' in cycles; the barrier that never
+  // completes (-1: none; a test of the waits)
+  uint32_t wait_looks;
+  int stuck_barrier;
+  long long wait_budget;
 };
 size_t attn_rows_scratch_bytes(int dim);
 cudaError_t launch_attn_rows(const AttnParams& p, cudaStream_t st);

@@ -255,7 +255,6 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, int32_t
 // As wait_warp, written so that the compiler sees the warp stay together (the
 // MMA warp's loops and operands then live in uniform registers) and short: at
 // most `limit` looks of up to 1 us each, after which the limit is 1.
-constexpr uint32_t kLooks = 1u << 21;
 __device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, uint32_t& limit) {
   uint32_t looks = 0;
   do {
@@ -865,6 +864,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       mbar_init(&u_empty[i], 8 + 1 + 1 + (C::E8 ? 4 : 1));
     }
     mbar_init(all_done, 1);
+    if (p.stuck_barrier >= 0 && p.stuck_barrier < C::kBars) {  // a test of the waits
+      asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(k_full + p.stuck_barrier))
+                   : "memory");
+      mbar_init(k_full + p.stuck_barrier, 1 << 16);
+    }
     *poison = 0;
     fence_mbar_init();
   }
@@ -1109,7 +1113,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
     // (no call in this role: a call would cost the operands their uniform
     // registers)
-    uint32_t looks = kLooks;
+    uint32_t looks = p.wait_looks;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return wait_uniform(smem_u32(bar), parity, looks);
     };
@@ -1267,7 +1271,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         j++;
       }
     }
-    if (looks != kLooks && lane == 0) atomicOr(p.status, kStatusTimeout);
+    if (looks != p.wait_looks && lane == 0) atomicOr(p.status, kStatusTimeout);
     commit(all_done);
   } else if (warp == 9) {
     // ------------------------------------------------------------ work, TMA
@@ -1357,7 +1361,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll 1
     for (uint32_t i = n < kBack ? 0 : n - kBack; i < n + (ok ? 0 : 1); i++) {
       const uint32_t st = i % C::kStages, par = (i >> C::kStageBits) & 1;
-      const long long budget = i < n ? kWaitBudgetCycles : 100000;
+      const long long budget = i < n ? p.wait_budget : 100000;
       mbar_drain(C::E8 ? &raw_full[0] : &k_full[st], C::E8 ? i & 1 : par, budget);
       if (i == n) break;
       const bool e = to_edge >> st & 1;
@@ -1423,7 +1427,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
       for (int t = 0; t < 2; t++)
         if (n[t] > 0)
-          mbar_drain(C::kCvtQ ? &q_raw[t] : &q_full[t], (n[t] - 1) & 1, kWaitBudgetCycles);
+          mbar_drain(C::kCvtQ ? &q_raw[t] : &q_full[t], (n[t] - 1) & 1, p.wait_budget);
     }
   } else if (warp == 10) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
@@ -1529,7 +1533,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
-    mbar_drain(all_done, 0, kWaitBudgetCycles);
+    mbar_drain(all_done, 0, p.wait_budget);
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
