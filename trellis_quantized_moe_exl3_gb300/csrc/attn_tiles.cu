@@ -37,7 +37,8 @@
 // tensor core at head_dim 128) but this code around them, and first of all the
 // fetching of it: the MMA warp waited for almost nothing and still took 3000
 // cycles a step (chunks of 512 at 16384 keys, 205 us), 2450 with the steps in
-// the middle of a unit written out from uniform registers (190 us).  So there
+// the middle of a unit written out from uniform registers (190 us; over a whole
+// call, start, unit changes and end included, 2950 to 3030).  So there
 // is one copy of everything (terms against the maximum of the tiles before,
 // which need a second one for the first tile and for rescales, were as fast
 // over long units and 20 % slower over short ones).
