@@ -54,10 +54,11 @@ def _on(stream):
 def _empty(shape, dtype, device, stream):
     """An uninitialised contiguous tensor that the launch stream may write at
     once, for use on the current stream later."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     with _on(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(torch.cuda.current_stream(device))
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -120,8 +121,11 @@ class PagedKVCache:
         self._spaces[_current_stream(k.get_device())] = self._space(_lib.EXL3_ATTENTION_HEAD_BYTES)
 
     def _space(self, n):
-        ws = torch.empty(n, dtype=torch.uint8, device=self.k.device)
-        ws[:_lib.EXL3_ATTENTION_HEAD_BYTES].zero_()
+        if n == _lib.EXL3_ATTENTION_HEAD_BYTES:
+            ws = torch.zeros(n, dtype=torch.uint8, device=self.k.device)
+        else:
+            ws = torch.empty(n, dtype=torch.uint8, device=self.k.device)
+            ws[:_lib.EXL3_ATTENTION_HEAD_BYTES].zero_()
         self._all.append(_Space(ws))
         return self._all[-1]
 
