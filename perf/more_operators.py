@@ -20,7 +20,7 @@ DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 E4M3 = torch.float8_e4m3fn
 EPS = 1e-6
 TOP = 448.0             # the largest E4M3 value
-LEAST, MOST = -64, 64   # exponents of the least and the greatest block scale
+LEAST, MOST = -40, 40   # exponents of the least and the greatest block scale
 
 
 # ------------------------------------------------------------------ the cases
