@@ -53,8 +53,9 @@ typedef enum {
     EXL3_ERR_DEVICE = 6     /* no sm_100-family device / device status set */
 } exl3_status;
 
-/* EXL3_E4M3 is a type of a key/value cache only (exl3_kv_cache). */
-typedef enum { EXL3_F16 = 0, EXL3_BF16 = 1, EXL3_E4M3 = 2 } exl3_dtype;
+/* EXL3_E4M3 is a type of a key/value cache only (exl3_kv_cache), EXL3_F32 one of
+ * probabilities only (exl3_verify_drafts). */
+typedef enum { EXL3_F16 = 0, EXL3_BF16 = 1, EXL3_E4M3 = 2, EXL3_F32 = 3 } exl3_dtype;
 
 /* Kernel path for the expert GEMMs.  AUTO picks the grouped GEMV for
  * decode-sized steps (few tokens per expert) and the tcgen05 grouped GEMM
@@ -314,6 +315,9 @@ exl3_status exl3_test_set_wait_fault(int kernel, int ks, long long budget_cycles
  *      A sequence whose cu_q is inconsistent is left out; a length is clamped
  *   4  a bounded wait ran out: outputs are unspecified, those of later calls
  *      too until the caller clears the bit
+ *   8  a block scale (exl3_kv_scales) that is negative, not finite or above
+ *      2^40: the block's keys of that kv head count as absent, an append to a
+ *      block that holds older tokens behind such a scale is skipped
  */
 
 /* The head of an attention workspace: the status word, and counters that every
@@ -337,6 +341,14 @@ typedef struct {
     const float *v_scale;   /*   value x stands for x * scale (a scale may be 0 or negative);
                                  NULL with the other types */
 } exl3_kv_cache;
+
+/* Block scales of an E4M3 cache: a stored value x of kv head h in page p stands
+ * for x * k[p*page_stride + h] (v for values).  A scale is 0 .. 2^40; one below
+ * 2^-40 counts as 2^-40. */
+typedef struct {
+    float *k, *v;           /* device, [num_pages][kv_heads] */
+    int64_t page_stride;    /* floats, at least kv_heads */
+} exl3_kv_scales;
 
 /* The sequences of one step.  Sequence b has the new tokens cu_q[b] ..
  * cu_q[b+1]-1 of the step (rows of q, k, v, out) and seq_lens[b] tokens in
@@ -411,6 +423,23 @@ exl3_status exl3_kv_append(const exl3_kv_cache *cache, const exl3_kv_batch *batc
                            exl3_dtype dt, int T, const exl3_rope *rope, const int32_t *positions,
                            float eps, int32_t *status, void *stream);
 
+/* As exl3_kv_append, for an E4M3 cache with block scales, which the append
+ * keeps: the scale of a block (page) and kv head is the least power of two
+ * with which 448 covers every value that was appended to the block, 2^-40 ..
+ * 2^40 (larger values saturate).  A block that begins with a new token starts
+ * anew; where new tokens need more than the block's scale covers, its older
+ * tokens (places before the first new one) are brought to the new scale,
+ * exactly but for values below 2^-6 of it.  A scale that covers the new tokens
+ * is left as it is, a power of two or not.  cache->dtype is EXL3_E4M3, its
+ * k_scale and v_scale NULL.  No page may belong to two sequences that append
+ * to it.  Errors: as exl3_kv_append, and EXL3_ERR_ARG for scales NULL,
+ * misaligned or with a stride below kv_heads. */
+exl3_status exl3_kv_append_blocks(const exl3_kv_cache *cache, const exl3_kv_scales *scales,
+                                  const exl3_kv_batch *batch, const exl3_heads *q,
+                                  const exl3_heads *k, const exl3_heads *v, exl3_dtype dt, int T,
+                                  const exl3_rope *rope, const int32_t *positions, float eps,
+                                  int32_t *status, void *stream);
+
 /* Bytes of workspace exl3_paged_attention needs for T new tokens of up to
  * num_seqs sequences. */
 size_t exl3_paged_attention_workspace_size(int T, int heads, int kv_heads, int head_dim,
@@ -448,6 +477,17 @@ exl3_status exl3_paged_attention(const exl3_kv_cache *cache, const exl3_kv_batch
                                  int window, void *out, float *lse, int path, void *ws,
                                  size_t ws_bytes, void *stream);
 
+/* As exl3_paged_attention, over an E4M3 cache with block scales: k_p and v_p are
+ * the stored values times their block's scales.  A value's scale joins the
+ * softmax term (its logarithm the score), so that the 16-bit terms are largest
+ * where a key's share of the output is, however far apart scales lie. */
+exl3_status exl3_paged_attention_blocks(const exl3_kv_cache *cache, const exl3_kv_scales *scales,
+                                        const exl3_kv_batch *batch, const void *q,
+                                        int64_t q_token_stride, int64_t q_head_stride,
+                                        exl3_dtype dt, int T, int heads, float scale, int causal,
+                                        int window, void *out, float *lse, int path, void *ws,
+                                        size_t ws_bytes, void *stream);
+
 /* Test hook of the bounded waits of exl3_paged_attention's tcgen05 kernel, as
  * exl3_test_set_wait_fault is of the MoE kernels': in every CTA, barrier number
  * `barrier` (0 ..; a number past the last has no effect) never completes, so
@@ -459,6 +499,94 @@ exl3_status exl3_paged_attention(const exl3_kv_cache *cache, const exl3_kv_batch
  * later call of the process.  Not thread safe.  Errors: EXL3_ERR_ARG for values
  * outside these ranges. */
 exl3_status exl3_test_set_attention_wait_fault(int barrier, long long budget_cycles);
+
+/* ------------------------------------------------------------------------
+ * Speculative decoding around the above (the pages' counterpart is only the
+ * step that verifies drafts: [p4] Results): which drafts stand, and which pages
+ * a step's tokens go to. */
+
+/* A pool of cache pages and the sequences that hold them, in device memory of
+ * the caller's.  Sequence (row) s has lens[s] tokens, in the pages
+ * table[s][0 .. ceil(lens[s] / page_size) - 1], -1 after them;
+ * free[0 .. *count - 1] are the free pages, taken from the end.  Only the
+ * pool's own calls change these (or the caller, between calls). */
+typedef struct {
+    int num_pages;          /* ids 0 .. num_pages - 1 */
+    int page_size;          /* tokens, as exl3_kv_cache */
+    int max_seqs;           /* rows, 1 .. 65535 */
+    int max_pages;          /* pages of a row; max_pages * page_size <= 2^30 */
+    int32_t *table;         /* [max_seqs][max_pages] */
+    int32_t *lens;          /* [max_seqs] */
+    int32_t *free;          /* [num_pages] */
+    int32_t *count;         /* [1] */
+} exl3_page_pool;
+
+/* Bytes of workspace the pool's calls need for steps of up to num sequences.
+ * The caller zeroes all of it once; its first word is a sticky status:
+ *   1  a request that makes no sense (a row out of range, or named before in
+ *      the same step; a negative count; more tokens to drop than there are):
+ *      the row is left out, too large a drop is clamped
+ *   2  too few free pages
+ *   4  a sequence longer than its row of the table, or rows past max_tokens
+ * It serves one call at a time, like the pool. */
+size_t exl3_pages_workspace_size(int max_seqs, int num);
+
+/* A step begins: sequence i of it is row seqs[i] of the pool and gets
+ * q_lens[i] new tokens, and the pages for them.
+ *   seqs, q_lens  device int32 [num]
+ *   cu_q          device int32 [num + 1]: prefix sums of q_lens (what is
+ *                 negative counts as 0), none above max_tokens
+ *   seq_lens      device int32 [num]: lengths with the new tokens
+ *   block_table   device int32 [num][max_pages]: the row's pages, -1 after them
+ *   positions     device int32 [max_tokens]: of every new token in its sequence
+ *   slots         device int64 [max_tokens]: page * page_size + place of it;
+ *                 positions and slots of rows that are no new token's are -1
+ * cu_q, seq_lens and block_table are what exl3_kv_batch takes.  Sequences are
+ * served in order; one whose pages, with those of all before it, are more than
+ * the free ones gets none, nor do later ones that need any.  A sequence that is
+ * not served keeps its rows but has seq_lens 0 (nothing is appended, and its
+ * tokens see nothing), and the pool's row stays as it was. */
+exl3_status exl3_pages_extend(const exl3_page_pool *pool, int num, const int32_t *seqs,
+                              const int32_t *q_lens, int max_tokens, int32_t *cu_q,
+                              int32_t *seq_lens, int32_t *block_table, int32_t *positions,
+                              int64_t *slots, void *ws, size_t ws_bytes, void *stream);
+
+/* Takes the last drop[i] tokens of row seqs[i] off again (drop NULL: all of
+ * them) and gives back the pages that hold nothing any more.  A step taken
+ * back whole leaves the pool as it was before it. */
+exl3_status exl3_pages_trim(const exl3_page_pool *pool, int num, const int32_t *seqs,
+                            const int32_t *drop, void *ws, size_t ws_bytes, void *stream);
+
+/* Verification of drafted tokens by random numbers that the caller gives.
+ * Sequence b has d = cu_draft[b+1] - cu_draft[b] drafts, draft[cu_draft[b] + j],
+ * and d + 1 rows of the target's probabilities: row cu_draft[b] + b + j of p is
+ * that of the token after j drafts; row cu_draft[b] + j of q is what draft j
+ * was drawn from (q NULL: the drafts are certain).
+ *   draft j is accepted, after all before it, if accept_u * q(x) < p(x);
+ *   after the first refusal the next token is drawn from max(p - q, 0) (p
+ *   without the draft where q is NULL; p itself where nothing is left), after
+ *   the last draft from p: the first token whose cumulative weight is above
+ *   sample_u times the total.
+ * Both are decided exactly: weights are summed in units of 2^-56 (smaller
+ * parts are cut off), so results do not depend on the order of sums.
+ *   p, q      device, rows of vocab probabilities in dt (fp16, bf16 or fp32),
+ *             strides in elements.  NaN and what is negative count as 0, what
+ *             is above 1 as 1; a row sums to less than 256
+ *   draft     device int32 [drafts]; one outside 0 .. vocab - 1 is refused
+ *   accept_u  device fp32 [drafts], in [0, 1)
+ *   sample_u  device fp32 [num_seqs], in [0, 1)
+ *   tokens    device int32 [drafts + num_seqs]: in place cu_draft[b] + b on, the
+ *             accepted drafts, the drawn token (-1 where the row has no
+ *             weight), then -1; -1 behind the last sequence
+ *   accepted, dropped  device int32 [num_seqs]: accepted drafts, and the others
+ * A sequence whose cu_draft does not ascend within 0 .. drafts is left out:
+ * accepted and dropped 0, no tokens.  vocab at most 2^24.  Errors: EXL3_ERR_ARG
+ * (null or misaligned pointers, strides below vocab, bad enum), EXL3_ERR_SHAPE. */
+exl3_status exl3_verify_drafts(const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+                               exl3_dtype dt, int vocab, int num_seqs, int drafts,
+                               const int32_t *cu_draft, const int32_t *draft,
+                               const float *accept_u, const float *sample_u, int32_t *tokens,
+                               int32_t *accepted, int32_t *dropped, void *stream);
 
 const char *exl3_status_string(exl3_status s);
 

@@ -13,6 +13,7 @@ def _api():
 
 
 _ATTENTION = ("PagedKVCache", "PagedBatch", "qk_norm_rope", "kv_append", "paged_attention")
+_SPECULATE = ("PagePool", "PagedStep", "verify_drafts")
 
 
 def __getattr__(name):
@@ -22,6 +23,10 @@ def __getattr__(name):
     if name in _ATTENTION:
         from . import attention
         value = globals()[name] = getattr(attention, name)  # found directly from now on
+        return value
+    if name in _SPECULATE:
+        from . import speculate
+        value = globals()[name] = getattr(speculate, name)
         return value
     if name in ("Layer", "route", "rmsnorm", "device_status"):
         return getattr(_api(), name)

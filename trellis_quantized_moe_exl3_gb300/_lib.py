@@ -17,7 +17,7 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 
 EXL3_OK, EXL3_ERR_ARG, EXL3_ERR_SHAPE, EXL3_ERR_K, EXL3_ERR_WORKSPACE, EXL3_ERR_CUDA, \
     EXL3_ERR_DEVICE = range(7)
-EXL3_F16, EXL3_BF16, EXL3_E4M3 = 0, 1, 2
+EXL3_F16, EXL3_BF16, EXL3_E4M3, EXL3_F32 = 0, 1, 2, 3
 EXL3_PATH_AUTO, EXL3_PATH_GEMV, EXL3_PATH_GEMM = 0, 1, 2
 EXL3_NUM_STAGE_EVENTS = 8
 EXL3_ATTENTION_HEAD_BYTES = 4096
@@ -45,6 +45,10 @@ class KVCache(ctypes.Structure):
     ]
 
 
+class KVScales(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64)]
+
+
 class KVBatch(ctypes.Structure):
     _fields_ = [
         ("num_seqs", ctypes.c_int), ("max_q", ctypes.c_int), ("max_pages", ctypes.c_int),
@@ -65,6 +69,14 @@ class Heads(ctypes.Structure):
 class Rope(ctypes.Structure):
     _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int),
                 ("interleaved", ctypes.c_int)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_seqs", ctypes.c_int),
+        ("max_pages", ctypes.c_int), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+        ("free", ctypes.c_void_p), ("count", ctypes.c_void_p),
+    ]
 
 
 class Exl3Error(RuntimeError):
@@ -135,6 +147,18 @@ def lib():
     L.exl3_paged_attention_workspace_size.restype = sz
     L.exl3_paged_attention.argtypes = [vp, vp, vp, i64, i64, i, i, i, f, i, i, vp, vp, i, vp, sz, vp]
     L.exl3_paged_attention.restype = i
+    L.exl3_kv_append_blocks.argtypes = [vp, *L.exl3_kv_append.argtypes]
+    L.exl3_kv_append_blocks.restype = i
+    L.exl3_paged_attention_blocks.argtypes = [vp, *L.exl3_paged_attention.argtypes]
+    L.exl3_paged_attention_blocks.restype = i
+    L.exl3_pages_workspace_size.argtypes = [i, i]
+    L.exl3_pages_workspace_size.restype = sz
+    L.exl3_pages_extend.argtypes = [vp, i, vp, vp, i, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.exl3_pages_extend.restype = i
+    L.exl3_pages_trim.argtypes = [vp, i, vp, vp, vp, sz, vp]
+    L.exl3_pages_trim.restype = i
+    L.exl3_verify_drafts.argtypes = [vp, i64, vp, i64, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.exl3_verify_drafts.restype = i
     L.exl3_test_set_attention_wait_fault.argtypes = [i, ctypes.c_longlong]
     L.exl3_test_set_attention_wait_fault.restype = i
     L.exl3_status_string.argtypes = [i]

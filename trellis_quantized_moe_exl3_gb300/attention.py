@@ -81,8 +81,11 @@ class PagedKVCache:
     """A paged cache: k and v [pages, page_size, kv_heads, head_dim], fp16, bf16
     or float8_e4m3fn, channels contiguous, the other strides free but alike (a
     permuted view of [pages, kv_heads, page_size, head_dim] works).  k_scale,
-    v_scale: fp32 [kv_heads], E4M3 only; a stored x stands for x * scale (0 and
-    negative scales are fine).
+    v_scale: fp32, E4M3 only; a stored x stands for x * scale.  [kv_heads]: a
+    scale per head, given beforehand (0 and negative ones are fine).  [pages,
+    kv_heads], both: a scale per block (page) and head, which kv_append keeps,
+    a power of two that grows with the block's tokens (zeros to begin with);
+    other programs may write any from 0 to 2^40 (below 2^-40 counts as that).
     page_size is a multiple of 16.  The tensors must stay alive as long as the
     handle.  `status()` is the sticky device status of all calls on the handle
     (it synchronises).
@@ -104,8 +107,17 @@ class PagedKVCache:
                              "same shape and strides")
         if k.numel() and k.stride(3) != 1 and k.shape[3] > 1:
             raise ValueError("the channels of k and v must be contiguous")
+        self.block_scales = k_scale is not None and k_scale.dim() == 2
         for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t is not None:
+            if self.block_scales:
+                if t is None:
+                    raise ValueError("a cache with block scales has both")
+                _cuda(t, n, torch.float32)
+                if k.dtype != torch.float8_e4m3fn or t.shape != (k.shape[0], k.shape[2]) or \
+                        (t.shape[1] > 1 and t.stride(1) != 1) or t.stride() != k_scale.stride():
+                    raise ValueError(f"{n} must be [pages, kv_heads] of an E4M3 cache, with "
+                                     "contiguous rows, k_scale and v_scale alike")
+            elif t is not None:
                 _dense(t, n, torch.float32, (k.shape[2],))
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.kv_heads, self.head_dim, self.dtype = k.shape[2], k.shape[3], k.dtype
@@ -113,8 +125,14 @@ class PagedKVCache:
         d.k, d.v, d.dtype = k.data_ptr(), v.data_ptr(), _CODES[k.dtype]
         d.num_pages, d.page_size, d.kv_heads, d.head_dim = k.shape
         d.page_stride, d.token_stride, d.head_stride = _strides(k)
-        d.k_scale = k_scale.data_ptr() if k_scale is not None else None
-        d.v_scale = v_scale.data_ptr() if v_scale is not None else None
+        self._scales = ()  # a pointer to exl3_kv_scales, where there are block scales
+        if self.block_scales:
+            e = _lib.KVScales(k_scale.data_ptr(), v_scale.data_ptr(),
+                              k_scale.stride(0) if k.shape[0] > 1 else k.shape[2])
+            self._scales = (ctypes.pointer(e),)
+        else:
+            d.k_scale = k_scale.data_ptr() if k_scale is not None else None
+            d.v_scale = v_scale.data_ptr() if v_scale is not None else None
         self._d, self._ref = d, ctypes.byref(d)
         self._spaces = {}  # raw stream -> the workspace of its calls
         self._all = []     # every one so far: a graph may hold an outgrown one
@@ -319,7 +337,9 @@ def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_wei
     """Writes the new tokens' keys (normed and rotated as by qk_norm_rope) and
     values to the cache; with q, returns the normed and rotated queries, from
     the same launch.  positions: those of the rotation (default: the positions
-    in the sequence).  A value past the E4M3 range saturates."""
+    in the sequence).  A value past the E4M3 range saturates.  A cache with
+    block scales keeps them on the way: a block's scale grows until 448 of it
+    covers the new values, its older tokens brought along."""
     dim, dtype = cache.head_dim, k.dtype
     T, H, ts, hs = _act(k, "k", dim)
     Tv, Hv, tv, hv = _act(v, "v", dim)
@@ -336,10 +356,10 @@ def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_wei
         pq = _HEADS.pack(q.data_ptr(), p, _weight(q_weight, "q_weight", dtype, dim), Hq, ts, hs, ots,
                          ohs)
     raw = _stream(stream, k)
-    check(_lib.lib().exl3_kv_append(cache._ref, batch._ref, pq, pk, pv, _ACT[dtype], T,
-                                    _rope(inv_freq, interleaved), _positions(positions, T), eps,
-                                    (cache._spaces.get(raw) or cache._room(stream, raw, None)).ptr, raw),
-          "exl3_kv_append")
+    fn = _lib.lib().exl3_kv_append_blocks if cache._scales else _lib.lib().exl3_kv_append
+    check(fn(cache._ref, *cache._scales, batch._ref, pq, pk, pv, _ACT[dtype], T,
+             _rope(inv_freq, interleaved), _positions(positions, T), eps,
+             (cache._spaces.get(raw) or cache._room(stream, raw, None)).ptr, raw), fn.__name__)
     return q_out
 
 
@@ -376,8 +396,9 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
     else:
         _dense(out, "out", q.dtype, (T, heads, dim))
     lse = _empty((T, heads), torch.float32, q.device, stream) if return_lse else None
-    check(_lib.lib().exl3_paged_attention(
-        cache._ref, batch._ref, q.data_ptr(), ts, hs, _ACT[q.dtype], T, heads,
+    fn = _lib.lib().exl3_paged_attention_blocks if cache._scales else _lib.lib().exl3_paged_attention
+    check(fn(
+        cache._ref, *cache._scales, batch._ref, q.data_ptr(), ts, hs, _ACT[q.dtype], T, heads,
         dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), path, ws_ptr, ws_bytes, raw), "exl3_paged_attention")
+        None if lse is None else lse.data_ptr(), path, ws_ptr, ws_bytes, raw), fn.__name__)
     return (out, lse) if return_lse else out

@@ -42,6 +42,17 @@ exl3_status check_cache(const exl3_kv_cache* c, exl3_dtype dt, int max_dim) {
   return EXL3_OK;
 }
 
+// Block scales of an E4M3 cache (none: s null).
+exl3_status check_scales(const exl3_kv_cache* c, const exl3_kv_scales* s) {
+  if (!s) return EXL3_OK;
+  if (c->dtype != EXL3_E4M3 || c->k_scale || c->v_scale || s->page_stride < c->kv_heads)
+    return EXL3_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(s->k) | reinterpret_cast<uintptr_t>(s->v)) & 3)
+    return EXL3_ERR_ARG;
+  if (c->num_pages > 0 && (!s->k || !s->v)) return EXL3_ERR_ARG;
+  return EXL3_OK;
+}
+
 exl3_status check_batch(const exl3_kv_batch* b) {
   if (!b) return EXL3_ERR_ARG;
   if (b->num_seqs < 0 || b->num_seqs > kMaxSeqs || b->max_pages < 0 || b->max_q < 0 ||
@@ -84,7 +95,7 @@ HeadSet head_set(const exl3_heads* h) {
   return s;
 }
 
-Cache cache_of(const exl3_kv_cache* c) {
+Cache cache_of(const exl3_kv_cache* c, const exl3_kv_scales* s) {
   const int64_t e = c->dtype == EXL3_E4M3 ? 1 : 2;
   Cache o{};
   o.k = static_cast<const uint8_t*>(c->k);
@@ -95,8 +106,9 @@ Cache cache_of(const exl3_kv_cache* c) {
   o.page_bytes = c->page_stride * e;
   o.token_bytes = c->token_stride * e;
   o.head_bytes = c->head_stride * e;
-  o.k_scale = c->k_scale;
-  o.v_scale = c->v_scale;
+  o.k_scale = s ? s->k : c->k_scale;
+  o.v_scale = s ? s->v : c->v_scale;
+  o.scale_stride = s ? s->page_stride : 0;
   return o;
 }
 
@@ -106,6 +118,109 @@ Batch batch_of(const exl3_kv_batch* b, int T, int page_size) {
 }
 
 bool bad_dtype(exl3_dtype dt) { return dt != EXL3_F16 && dt != EXL3_BF16; }
+
+exl3_status kv_append(const exl3_kv_cache* cache, const exl3_kv_scales* scales,
+                      const exl3_kv_batch* batch, const exl3_heads* q, const exl3_heads* k,
+                      const exl3_heads* v, exl3_dtype dt, int T, const exl3_rope* rope,
+                      const int32_t* positions, float eps, int32_t* status, void* stream) {
+  if (!k || !v || !status || bad_dtype(dt) || !(eps >= 0.0f)) return EXL3_ERR_ARG;
+  if (T < 0) return EXL3_ERR_SHAPE;
+  exl3_status e;
+  if ((e = check_cache(cache, dt, 256)) != EXL3_OK) return e;
+  if ((e = check_scales(cache, scales)) != EXL3_OK) return e;
+  if ((e = check_batch(batch)) != EXL3_OK) return e;
+  if (q && (e = check_heads(q, T, 1)) != EXL3_OK) return e;
+  if ((e = check_heads(k, T, 0)) != EXL3_OK) return e;
+  if ((e = check_heads(v, T, 0)) != EXL3_OK) return e;
+  if (k->heads != cache->kv_heads || v->heads != cache->kv_heads) return EXL3_ERR_SHAPE;
+  if ((e = check_rope(rope, cache->head_dim)) != EXL3_OK) return e;
+  if (T == 0 || batch->num_seqs == 0) return EXL3_OK;
+  NormRopeParams p{};
+  if (q) p.set[0] = head_set(q);
+  p.set[1] = head_set(k);
+  p.set[2] = head_set(v);
+  p.set[2].weight = nullptr;
+  p.append = 1;
+  p.bf16 = dt == EXL3_BF16;
+  p.e4m3 = cache->dtype == EXL3_E4M3;
+  p.T = T;
+  p.dim = cache->head_dim;
+  p.inv_dim = 1.0f / (float)p.dim;
+  p.positions = positions;
+  if (rope) {
+    p.inv_freq = rope->inv_freq;
+    p.rot = rope->rotary_dim;
+    p.inter = rope->interleaved;
+  }
+  p.eps = eps;
+  p.cache = cache_of(cache, scales);
+  p.batch = batch_of(batch, T, cache->page_size);
+  p.status = status;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return (scales ? launch_append_blocks(p, st) : launch_norm_rope(p, st)) == cudaSuccess
+             ? EXL3_OK
+             : EXL3_ERR_CUDA;
+}
+
+
+exl3_status attend(const exl3_kv_cache* cache, const exl3_kv_scales* scales,
+                   const exl3_kv_batch* batch, const void* q, int64_t q_token_stride,
+                   int64_t q_head_stride, exl3_dtype dt, int T, int heads, float scale, int causal,
+                   int window, void* out, float* lse, int path, void* ws, size_t ws_bytes,
+                   void* stream) {
+  if (bad_dtype(dt) || !(scale > 0.0f) || !isfinite(scale) || (causal != 0 && causal != 1) ||
+      window < 0 || (window > 0 && !causal) || path < EXL3_PATH_AUTO || path > EXL3_PATH_GEMM)
+    return EXL3_ERR_ARG;
+  if (T < 0 || heads < 1) return EXL3_ERR_SHAPE;
+  exl3_status e;
+  if ((e = check_cache(cache, dt, 128)) != EXL3_OK) return e;
+  if (cache->head_dim != 64 && cache->head_dim != 128) return EXL3_ERR_SHAPE;
+  if (heads % cache->kv_heads) return EXL3_ERR_SHAPE;
+  if ((e = check_scales(cache, scales)) != EXL3_OK) return e;
+  if ((e = check_batch(batch)) != EXL3_OK) return e;
+  if ((long long)T * (heads / cache->kv_heads) > (1ll << 30)) return EXL3_ERR_SHAPE;
+  if (q_token_stride % 8 || q_head_stride % 8 || q_token_stride < 0 || q_head_stride < 0)
+    return EXL3_ERR_ARG;
+  if (T == 0 || batch->num_seqs == 0) return EXL3_OK;
+  if (!good(q) || !out || (reinterpret_cast<uintptr_t>(out) & 31) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3))
+    return EXL3_ERR_ARG;
+  if (!good(ws) || ws_bytes < exl3_paged_attention_workspace_size(T, heads, cache->kv_heads,
+                                                                  cache->head_dim, batch->num_seqs))
+    return EXL3_ERR_WORKSPACE;
+  AttnParams p{};
+  p.cache = cache_of(cache, scales);
+  p.batch = batch_of(batch, T, cache->page_size);
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_ts = q_token_stride;
+  p.q_hs = q_head_stride;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.heads = heads;
+  p.kv_heads = cache->kv_heads;
+  p.group = heads / cache->kv_heads;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.causal = causal;
+  p.window = window < kMaxLen ? window : kMaxLen;  // (either sees every earlier key)
+  p.bf16 = dt == EXL3_BF16;
+  p.e4m3 = cache->dtype == EXL3_E4M3;
+  p.dim = cache->head_dim;
+  p.blocks = scales != nullptr;
+  p.status = static_cast<int32_t*>(ws);
+  p.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
+  p.scratch = static_cast<uint8_t*>(ws) + kHead;
+  p.wait_budget = g_waits.budget;
+  p.wait_looks = (uint32_t)(g_waits.budget / 500);  // of up to 1 us, 2000 cycles
+  p.stuck_barrier = g_waits.stuck_barrier;
+  // Few rows per sequence and kv head: the cache's bytes bound the step.
+  bool tiles = (long long)batch->max_q * p.group > (p.e4m3 ? kRowsMostE4m3 : kRowsMost);
+  if (path != EXL3_PATH_AUTO) tiles = path == EXL3_PATH_GEMM;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t err = cudaErrorNotSupported;  // a cache that cannot be a TMA source
+  if (tiles) err = launch_attn_tiles(p, st);
+  if (err == cudaErrorNotSupported) err = launch_attn_rows(p, st);
+  return err == cudaSuccess ? EXL3_OK : EXL3_ERR_CUDA;
+}
 
 }  // namespace
 
@@ -144,40 +259,16 @@ exl3_status exl3_kv_append(const exl3_kv_cache* cache, const exl3_kv_batch* batc
                            const exl3_heads* q, const exl3_heads* k, const exl3_heads* v,
                            exl3_dtype dt, int T, const exl3_rope* rope, const int32_t* positions,
                            float eps, int32_t* status, void* stream) {
-  if (!k || !v || !status || bad_dtype(dt) || !(eps >= 0.0f)) return EXL3_ERR_ARG;
-  if (T < 0) return EXL3_ERR_SHAPE;
-  exl3_status e;
-  if ((e = check_cache(cache, dt, 256)) != EXL3_OK) return e;
-  if ((e = check_batch(batch)) != EXL3_OK) return e;
-  if (q && (e = check_heads(q, T, 1)) != EXL3_OK) return e;
-  if ((e = check_heads(k, T, 0)) != EXL3_OK) return e;
-  if ((e = check_heads(v, T, 0)) != EXL3_OK) return e;
-  if (k->heads != cache->kv_heads || v->heads != cache->kv_heads) return EXL3_ERR_SHAPE;
-  if ((e = check_rope(rope, cache->head_dim)) != EXL3_OK) return e;
-  if (T == 0 || batch->num_seqs == 0) return EXL3_OK;
-  NormRopeParams p{};
-  if (q) p.set[0] = head_set(q);
-  p.set[1] = head_set(k);
-  p.set[2] = head_set(v);
-  p.set[2].weight = nullptr;
-  p.append = 1;
-  p.bf16 = dt == EXL3_BF16;
-  p.e4m3 = cache->dtype == EXL3_E4M3;
-  p.T = T;
-  p.dim = cache->head_dim;
-  p.inv_dim = 1.0f / (float)p.dim;
-  p.positions = positions;
-  if (rope) {
-    p.inv_freq = rope->inv_freq;
-    p.rot = rope->rotary_dim;
-    p.inter = rope->interleaved;
-  }
-  p.eps = eps;
-  p.cache = cache_of(cache);
-  p.batch = batch_of(batch, T, cache->page_size);
-  p.status = status;
-  return launch_norm_rope(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXL3_OK
-                                                                              : EXL3_ERR_CUDA;
+  return kv_append(cache, nullptr, batch, q, k, v, dt, T, rope, positions, eps, status, stream);
+}
+
+exl3_status exl3_kv_append_blocks(const exl3_kv_cache* cache, const exl3_kv_scales* scales,
+                                  const exl3_kv_batch* batch, const exl3_heads* q,
+                                  const exl3_heads* k, const exl3_heads* v, exl3_dtype dt, int T,
+                                  const exl3_rope* rope, const int32_t* positions, float eps,
+                                  int32_t* status, void* stream) {
+  if (!scales) return EXL3_ERR_ARG;
+  return kv_append(cache, scales, batch, q, k, v, dt, T, rope, positions, eps, status, stream);
 }
 
 size_t exl3_paged_attention_workspace_size(int T, int heads, int kv_heads, int head_dim,
@@ -195,56 +286,19 @@ exl3_status exl3_paged_attention(const exl3_kv_cache* cache, const exl3_kv_batch
                                  exl3_dtype dt, int T, int heads, float scale, int causal,
                                  int window, void* out, float* lse, int path, void* ws,
                                  size_t ws_bytes, void* stream) {
-  if (bad_dtype(dt) || !(scale > 0.0f) || !isfinite(scale) || (causal != 0 && causal != 1) ||
-      window < 0 || (window > 0 && !causal) || path < EXL3_PATH_AUTO || path > EXL3_PATH_GEMM)
-    return EXL3_ERR_ARG;
-  if (T < 0 || heads < 1) return EXL3_ERR_SHAPE;
-  exl3_status e;
-  if ((e = check_cache(cache, dt, 128)) != EXL3_OK) return e;
-  if (cache->head_dim != 64 && cache->head_dim != 128) return EXL3_ERR_SHAPE;
-  if (heads % cache->kv_heads) return EXL3_ERR_SHAPE;
-  if ((e = check_batch(batch)) != EXL3_OK) return e;
-  if ((long long)T * (heads / cache->kv_heads) > (1ll << 30)) return EXL3_ERR_SHAPE;
-  if (q_token_stride % 8 || q_head_stride % 8 || q_token_stride < 0 || q_head_stride < 0)
-    return EXL3_ERR_ARG;
-  if (T == 0 || batch->num_seqs == 0) return EXL3_OK;
-  if (!good(q) || !out || (reinterpret_cast<uintptr_t>(out) & 31) ||
-      (reinterpret_cast<uintptr_t>(lse) & 3))
-    return EXL3_ERR_ARG;
-  if (!good(ws) || ws_bytes < exl3_paged_attention_workspace_size(T, heads, cache->kv_heads,
-                                                                  cache->head_dim, batch->num_seqs))
-    return EXL3_ERR_WORKSPACE;
-  AttnParams p{};
-  p.cache = cache_of(cache);
-  p.batch = batch_of(batch, T, cache->page_size);
-  p.q = static_cast<const uint16_t*>(q);
-  p.q_ts = q_token_stride;
-  p.q_hs = q_head_stride;
-  p.out = static_cast<uint16_t*>(out);
-  p.lse = lse;
-  p.heads = heads;
-  p.kv_heads = cache->kv_heads;
-  p.group = heads / cache->kv_heads;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.causal = causal;
-  p.window = window < kMaxLen ? window : kMaxLen;  // (either sees every earlier key)
-  p.bf16 = dt == EXL3_BF16;
-  p.e4m3 = cache->dtype == EXL3_E4M3;
-  p.dim = cache->head_dim;
-  p.status = static_cast<int32_t*>(ws);
-  p.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
-  p.scratch = static_cast<uint8_t*>(ws) + kHead;
-  p.wait_budget = g_waits.budget;
-  p.wait_looks = (uint32_t)(g_waits.budget / 500);  // of up to 1 us, 2000 cycles
-  p.stuck_barrier = g_waits.stuck_barrier;
-  // Few rows per sequence and kv head: the cache's bytes bound the step.
-  bool tiles = (long long)batch->max_q * p.group > (p.e4m3 ? kRowsMostE4m3 : kRowsMost);
-  if (path != EXL3_PATH_AUTO) tiles = path == EXL3_PATH_GEMM;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t err = cudaErrorNotSupported;  // a cache that cannot be a TMA source
-  if (tiles) err = launch_attn_tiles(p, st);
-  if (err == cudaErrorNotSupported) err = launch_attn_rows(p, st);
-  return err == cudaSuccess ? EXL3_OK : EXL3_ERR_CUDA;
+  return attend(cache, nullptr, batch, q, q_token_stride, q_head_stride, dt, T, heads, scale,
+                causal, window, out, lse, path, ws, ws_bytes, stream);
+}
+
+exl3_status exl3_paged_attention_blocks(const exl3_kv_cache* cache, const exl3_kv_scales* scales,
+                                        const exl3_kv_batch* batch, const void* q,
+                                        int64_t q_token_stride, int64_t q_head_stride,
+                                        exl3_dtype dt, int T, int heads, float scale, int causal,
+                                        int window, void* out, float* lse, int path, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  if (!scales) return EXL3_ERR_ARG;
+  return attend(cache, scales, batch, q, q_token_stride, q_head_stride, dt, T, heads, scale, causal,
+                window, out, lse, path, ws, ws_bytes, stream);
 }
 
 exl3_status exl3_test_set_attention_wait_fault(int barrier, long long budget_cycles) {

@@ -12,7 +12,11 @@
 namespace exl3 {
 
 // Device status bits of these kernels (sticky word).
-enum : int32_t { kStatusBadPage = 1, kStatusBadBatch = 2 };
+enum : int32_t { kStatusBadPage = 1, kStatusBadBatch = 2, kStatusBadScale = 8 };
+// Block scales: what is less counts as the least, what is more is none.  (The
+// range keeps every softmax term that matters within fp32 when a scale's
+// logarithm is added to its scores.)
+constexpr float kLeastScale = 0x1p-40f, kMostScale = 0x1p40f;
 
 constexpr int kMaxSeqs = 65535;
 constexpr int kMaxPageSize = 4096;
@@ -63,6 +67,7 @@ struct Cache {
   int64_t page_bytes, token_bytes, head_bytes;  // strides
   const float* k_scale;
   const float* v_scale;
+  int64_t scale_stride;  // block scales: floats from a page's to the next one's
 };
 
 // ---- norm, rotation, append (norm_rope.cu)
@@ -86,6 +91,8 @@ struct NormRopeParams {
   int32_t* status;
 };
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t st);
+// k and v go to an E4M3 cache with block scales (append_blocks.cu)
+cudaError_t launch_append_blocks(const NormRopeParams& p, cudaStream_t st);
 
 // ---- attention
 struct AttnParams {
@@ -99,6 +106,7 @@ struct AttnParams {
   float scale_log2;  // scale * log2(e)
   int causal, window;
   int bf16, e4m3, dim;
+  int blocks;  // the cache has block scales
   int32_t* status;
   int32_t* counters;  // [kRowsCounters], zero between calls
   void* scratch;

@@ -32,6 +32,12 @@
 // into the score's scale.  Channels of the K product are permuted so that a
 // lane's operands are 16 consecutive bytes; V goes through ldmatrix.trans,
 // where an 8-bit pair of channels travels as one 16-bit element.
+//
+// Block scales (a scale per page and kv head) come with their tiles, two floats
+// per 16 keys.  With S the product of the queries and the stored keys,
+//   x = S scale ks + log2 vs,  w = 2^(x - m),  O += w v,  l += w / vs:
+// the running maximum is that of x, so the 16-bit terms w are largest where a
+// key's share of the output is, whatever the scales of other blocks.
 #include <math.h>
 
 #include "attn.cuh"
@@ -47,9 +53,10 @@ constexpr int kGran = 64;            // keys per granule
 constexpr float kRescale = 8.0f;     // log2 growth of the maximum that rescales O
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <int D_, int NB_, int E8_, int BF_>
+template <int D_, int NB_, int E8_, int BF_, int BS_ = 0>
 struct Cfg {
   static constexpr int D = D_, NB = NB_, E8 = E8_, BF = BF_;
+  static constexpr int BS = BS_;                    // block scales
   static constexpr int MBF = BF && !E8;             // type of the products
   // Softmax terms meet V as 16-bit values (an fp32 product would have to be
   // split in two and take twice the MMAs): bf16 rounds a term by 2^-9 of it at
@@ -73,7 +80,8 @@ struct Cfg {
   static constexpr int OS = D + 4;                  // floats per row of the join buffer
   static constexpr int kJoinBytes = RT * OS * 4;
   static constexpr int kRing = kWarps * (kWarpBytes > kJoinBytes ? kWarpBytes : kJoinBytes);
-  static constexpr int kSmem = kRing + kWarps * RT * 8 + kWarps * kStages * 4 + 64;
+  static constexpr int kScales = kRing + kWarps * RT * 8 + kWarps * kStages * 4 + 16;
+  static constexpr int kSmem = kScales + (BS ? kWarps * kStages * MT * 8 : 0) + 48;
   static constexpr int kCtasPerSm = D == 128 ? 2 : 4;
   static constexpr int kGrid = kSms * kCtasPerSm;
   static constexpr int kFlat = D == 128 ? 40 : 24;  // most parts that are joined in one step
@@ -82,6 +90,10 @@ struct Cfg {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -346,6 +358,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
   const uint32_t ring_s = smem_u32(smem + warp * C::kWarpBytes);
   float2* ml = reinterpret_cast<float2*>(smem + C::kRing);  // [warp][RT]
   uint32_t* absent = reinterpret_cast<uint32_t*>(ml + kWarps * RT) + warp * C::kStages;
+  // block scales of the tiles under way: [stage][16-key group] (k, v)
+  const float2* scales = reinterpret_cast<const float2*>(smem + C::kScales) + warp * C::kStages * MT;
 
   pdl_wait();
   int32_t bad = 0;
@@ -465,6 +479,15 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
           }
         }
         if (lane == 0) absent[ist] = gone;
+        if (C::BS && lane < 2) {
+#pragma unroll
+          for (int j = 0; j < MT; j++) {
+            const bool ok = !(gone >> j & 1);
+            const float* src = lane ? p.cache.v_scale : p.cache.k_scale;
+            cp_async4(smem_u32(scales + ist * MT + j) + lane * 4,
+                      ok ? src + pg[j] * p.cache.scale_stride + h : src, ok ? 4 : 0);
+          }
+        }
 #pragma unroll
         for (int j = 0; j < MT; j++) pg[j] = page_of(i + 1, j);
       }
@@ -479,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
     uint32_t qf[NB][D / 8];
     float cs[NB][2];        // factor of the scores of rows 8 b + 2 c + e, log2 units
     int hi[NB][2], lo[NB][2];
-    const float cbase = p.scale_log2 * (C::E8 && p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f);
+    const float cbase =
+        p.scale_log2 * (C::E8 && !C::BS && p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f);
 #pragma unroll
     for (int nb = 0; nb < NB; nb++) {
       const int r = 8 * nb + g;
@@ -518,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
           qf[nb][i] = pack2<0>(__uint_as_float(qf[nb][i] << 16) * f,
                                __uint_as_float(qf[nb][i] & 0xFFFF0000u) * f);
       }
-      if (C::E8 && !(f_row > 0.0f)) {
+      if (C::E8 && !C::BS && !(f_row > 0.0f)) {
         // a factor that is not positive (a k_scale of 0 or below) would turn
         // the -inf of masked scores: its sign, or its 0, goes to the queries
         const __half2 x = __float2half2_rn(f_row < 0.0f ? -1.0f : f_row == 0.0f ? 0.0f : NAN);
@@ -557,7 +581,26 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
       issue(i + C::kStages - 1);
       const int key0 = key_of(i);
       const uint32_t kd = ring_s + st * C::kStageBytes, vd = kd + C::kHalf;
-      const uint32_t gone = absent[st];
+      uint32_t gone = absent[st];
+      // block scales: the keys', the values' as a logarithm and inverted
+      float ks[MT], lv[MT], iv[MT];
+      bool no_scale = false;
+      if (C::BS) {
+#pragma unroll
+        for (int t = 0; t < MT; t++) {
+          const float2 x = scales[st * MT + t];
+          if (!(x.x >= 0.0f && x.x <= kMostScale && x.y >= 0.0f && x.y <= kMostScale)) {
+            const int key = key0 + 16 * t;
+            if (key < any1 && key + 16 > any0) bad |= kStatusBadScale;
+            gone |= 1u << t;
+            no_scale = true;
+          }
+          const float v = fminf(fmaxf(x.y, kLeastScale), kMostScale);
+          ks[t] = fminf(fmaxf(x.x, kLeastScale), kMostScale);
+          lv[t] = log2f(v);
+          iv[t] = 1.0f / v;
+        }
+      }
       st = st == C::kStages - 1 ? 0 : st + 1;
 
       // ---- scores
@@ -592,6 +635,14 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
           }
         }
       }
+      if (C::BS) {
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+          for (int t = 0; t < MT; t++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) s[nb][t][e] = fmaf(s[nb][t][e], cs[nb][e & 1] * ks[t], lv[t]);
+      }
       if (key0 < all0 || key0 + KT > all1 || gone) {
 #pragma unroll
         for (int nb = 0; nb < NB; nb++)
@@ -618,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
 #pragma unroll
           for (int t = 1; t < MT; t++)
             mx[nb][e] = fmaxf(mx[nb][e], fmaxf(s[nb][t][e], s[nb][t][2 + e]));
-          mx[nb][e] *= cs[nb][e];
+          if (!C::BS) mx[nb][e] *= cs[nb][e];
           grow |= mx[nb][e] > m[nb][e] + kRescale;
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -651,17 +702,19 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
           for (int t = 0; t < MT; t++)
 #pragma unroll
             for (int y = 0; y < 2; y++) {
-              const float v = ex2(fmaf(s[nb][t][2 * y + e], cs[nb][e], -ms));
+              const float v = ex2(C::BS ? s[nb][t][2 * y + e] - ms
+                                        : fmaf(s[nb][t][2 * y + e], cs[nb][e], -ms));
               s[nb][t][2 * y + e] = v;
-              l[nb][e] += v;
+              l[nb][e] = C::BS ? fmaf(v, iv[t], l[nb][e]) : l[nb][e] + v;
             }
         }
       // ---- values
       // a tile with keys that only some rows see: a value there that is not
       // finite would reach the other rows as 0 * inf, so such a tile (looked
-      // for here only) goes key by key
-      if ((max(key0, any0) < all0 || min(key0 + KT, any1) > all1) &&
-          __any_sync(0xffffffffu, not_finite<C>(vd, lane))) {
+      // for here only) goes key by key; so does one with keys behind no scale
+      if (((max(key0, any0) < all0 || min(key0 + KT, any1) > all1) &&
+           __any_sync(0xffffffffu, not_finite<C>(vd, lane))) ||
+          (C::BS && no_scale)) {
         add_seen<C>(o, s, vd, key0, gone, hi, lo, g, c);
         continue;
       }
@@ -721,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
     const bool whole = cnt == sw.n;
     float* part = reinterpret_cast<float*>(p.scratch) +
                   ((size_t)blockIdx.x * 2 + (first_part ? 0 : 1)) * part_floats(RT, D);
-    const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
+    const float vs = C::E8 && !C::BS && p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
     for (int i = threadIdx.x; i < nrows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d0 = (i % (D / 4)) * 4;
       float2 sl[kWarps];
@@ -894,6 +947,8 @@ cudaError_t launch_cfg(const AttnParams& p, cudaStream_t st) {
 
 template <int D, int NB>
 cudaError_t launch_types(const AttnParams& p, cudaStream_t st) {
+  if (p.blocks)
+    return p.bf16 ? launch_cfg<Cfg<D, NB, 1, 1, 1>>(p, st) : launch_cfg<Cfg<D, NB, 1, 0, 1>>(p, st);
   if (p.e4m3)
     return p.bf16 ? launch_cfg<Cfg<D, NB, 1, 1>>(p, st) : launch_cfg<Cfg<D, NB, 1, 0>>(p, st);
   return p.bf16 ? launch_cfg<Cfg<D, NB, 0, 1>>(p, st) : launch_cfg<Cfg<D, NB, 0, 0>>(p, st);

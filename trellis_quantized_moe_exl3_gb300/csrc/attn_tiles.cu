@@ -53,6 +53,14 @@
 // that do not exist are out-of-range coordinates, which TMA fills with zeros.
 // Rows of V that a box brings in beyond the visible range (a page's stale end)
 // are zeroed before they meet P = 0.
+//
+// Block scales (a scale per page and kv head, E4M3) go from the TMA warp, which
+// knows the pages, to the softmax warps in a ring beside that of absent pages,
+// one entry per 16 keys.  With S the product of the queries and the stored keys
+//   x = S scale ks + log2 vs,  w = 2^(x - m),  O += w v,  l += w / vs,
+// so that the 16-bit terms w are largest where a key's share of the output is,
+// whatever the scales of other blocks.  ks > 0: a group's maximum of x is that
+// of S, and a term costs one fma as without block scales.
 #include <cuda.h>
 #include <math.h>
 
@@ -73,9 +81,10 @@ constexpr int kGone = 16;           // ring of absent-page masks (steps)
 constexpr int kUnits = 4;           // ring of published units
 constexpr int kRecInts = 24;
 
-template <int D_, int E8_, int BF_>
+template <int D_, int E8_, int BF_, int BS_ = 0>
 struct Cfg {
   static constexpr int D = D_, E8 = E8_, BF = BF_;
+  static constexpr int BS = BS_;                         // block scales
   static constexpr int MBF = BF && !E8;                  // type of the products
   // log2 of a factor of the terms: fp16 holds what is below 2^-14 in fewer
   // bits, so there they are 2^7 times as large (below 2^15 with kRescale)
@@ -91,7 +100,8 @@ struct Cfg {
   static constexpr int kBars = 5 * kStages + 4 + 15 + 2 * kUnits;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffUnits = kOffMisc + kGone * 4 + 16;
-  static constexpr int kSmem = kOffUnits + kUnits * kRecInts * 4;
+  static constexpr int kOffScales = (kOffUnits + kUnits * kRecInts * 4 + 15) & ~15;
+  static constexpr int kSmem = kOffScales + (BS ? kGone * (kTile / 16) * 16 : 0);
   static constexpr int kCvtQ = E8 && BF;   // queries are brought to fp16
   static constexpr int kThreads = E8 ? 512 : 384;
   // registers of a softmax thread and of the others (their sum over the CTA
@@ -780,6 +790,30 @@ __device__ __forceinline__ void mask_scores(float* s, int h0, int l0, uint32_t g
   }
 }
 
+// As take_terms, for the four groups of 16 keys from g on: c and n of their own,
+// and sums divided by their value scales.
+template <int MBF>
+__device__ __forceinline__ void take_block_terms(const float* s, uint32_t* pk, float& sum, float c,
+                                                 float n, const float4* g) {
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const float4 f = g[k];
+    const uint64_t c2 = both(fmaxf(c * f.x, 0x1p-126f)), n2 = both(n + f.y);
+    uint64_t part[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      float x = s[16 * k + 2 * i], y = s[16 * k + 2 * i + 1];
+      fma2(x, y, c2, n2);
+      x = ex2(x);
+      y = ex2(y);
+      add2(part[i & 1], x, y);
+      pk[8 * k + i] = pack2<MBF>(x, y);
+    }
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(part[0]) : "l"(part[1]));
+    sum = fmaf(sum2(part[0]), f.z, sum);
+  }
+}
+
 // 64 softmax terms 2^(s c + n), their sum, and their 16-bit pairs.
 template <int MBF>
 __device__ __forceinline__ void take_terms(const float* s, uint32_t* pk, uint64_t& sum, uint64_t c,
@@ -835,6 +869,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc) + kGone;
   volatile uint32_t* poison = tmem_slot + 1;     // a V tile held an infinity or a NaN
   Rec* recs = reinterpret_cast<Rec*>(smem + C::kOffUnits);
+  // block scales of 16 keys: of the keys, log2 of the values', its inverse
+  float4* const ring = reinterpret_cast<float4*>(smem + C::kOffScales);  // [kGone][kTile / 16]
 
   // (the same in all lanes, known to the compiler as such)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -928,7 +964,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const bool whole = r.flags & 1, in = row < r.nrows - t * kTile;
       const int tok = o_row / p.group;
       const int64_t at = (int64_t)(r.q0 + tok) * p.heads + r.h * p.group + (o_row - tok * p.group);
-      const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + r.h) : 1.0f;
+      const float vs = C::E8 && !C::BS && p.cache.v_scale ? __ldg(p.cache.v_scale + r.h) : 1.0f;
       const uint64_t inv2 = both(whole ? row_inverse(o_l, vs) : 1.0f);
       const int prt = t * kTile + row;
       float* part = pl.parts + ((size_t)blockIdx.x * 2 + (r.flags >> 1)) * part_floats(D);
@@ -989,7 +1025,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const int pos = r.len - r.n + prow / p.group;
       const int hi = p.causal ? pos : r.len - 1;
       const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-      float c = p.scale_log2 * (C::E8 && p.cache.k_scale ? __ldg(p.cache.k_scale + r.h) : 1.0f);
+      float c = p.scale_log2 *
+                (C::E8 && !C::BS && p.cache.k_scale ? __ldg(p.cache.k_scale + r.h) : 1.0f);
       if (C::kCvtQ && r.live && j0 < j1) {
         // bf16 queries to fp16, in place, by a power of two per row: 2^s
         // brings the row's largest value to [2^14, 2^15); values below 2^-31
@@ -1026,7 +1063,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       // a factor that is not positive (a k_scale of 0 or below) would turn the
       // -inf of masked scores: it is applied before the mask then
       const float pre = c;
-      const bool odd = C::E8 && __any_sync(0xffffffffu, !(c > 0.0f));
+      const bool odd = C::E8 && !C::BS && __any_sync(0xffffffffu, !(c > 0.0f));
       if (odd) c = 1.0f;
       if (owed) {
         put_out();
@@ -1054,14 +1091,31 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
         const bool masked = edge(r, j) || gm;
         if (masked) mask_scores(s, h0, l0, gm);
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        const float4* const f4 = ring + (base + j - r.j0) % kGone * (kTile / 16);
+        float mn = m;
+        if constexpr (C::BS) {
 #pragma unroll
-        for (int i = 4; i + 8 <= kTile; i += 8)
+          for (int g = 0; g < kTile / 16; g++) {
+            const float4 f = f4[g];
+            float mx[2] = {s[16 * g], s[16 * g + 1]};
 #pragma unroll
-          for (int e = 0; e < 4; e++) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
+            for (int i = 2; i + 4 <= 16; i += 4)
 #pragma unroll
-        for (int e = 0; e < 4; e++) mx[e] = fmaxf(mx[e], s[kTile - 4 + e]);
-        const float mn = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c);
+              for (int e = 0; e < 2; e++)
+                mx[e] = max3(mx[e], s[16 * g + i + 2 * e], s[16 * g + i + 2 * e + 1]);
+            const float x = max3(fmaxf(mx[0], mx[1]), s[16 * g + 14], s[16 * g + 15]);
+            mn = fmaxf(mn, fmaf(x, fmaxf(c * f.x, 0x1p-126f), f.y));
+          }
+        } else {
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 4; i + 8 <= kTile; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; e++) mx[e] = max3(mx[e], s[i + 2 * e], s[i + 2 * e + 1]);
+#pragma unroll
+          for (int e = 0; e < 4; e++) mx[e] = fmaxf(mx[e], s[kTile - 4 + e]);
+          mn = fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c);
+        }
         const bool grow = mn > m + kRescale || (m == -INFINITY && mn > m);
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? ex2(m - mn) : 1.0f;
@@ -1084,8 +1138,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
         uint32_t pk[32];
         uint64_t sum = 0;
-        const uint64_t c2 = both(c), n2 = both(C::kLift - (m == -INFINITY ? 0.0f : m));
-        take_terms<C::MBF>(s, pk, sum, c2, n2);
+        const float n = C::kLift - (m == -INFINITY ? 0.0f : m);
+        const uint64_t c2 = both(c), n2 = both(n);
+        float scaled = 0.0f;
+        if (C::BS)
+          take_block_terms<C::MBF>(s, pk, scaled, c, n, f4);
+        else
+          take_terms<C::MBF>(s, pk, sum, c2, n2);
         auto hand_over = [&](int half) {
           tmem_st32(s_col + 32 * half, pk);
           tmem_st_wait();
@@ -1094,8 +1153,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
         };
         hand_over(0);
-        take_terms<C::MBF>(s + 64, pk, sum, c2, n2);
-        l += sum2(sum);
+        if (C::BS)
+          take_block_terms<C::MBF>(s + 64, pk, scaled, c, n, f4 + 4);
+        else
+          take_terms<C::MBF>(s + 64, pk, sum, c2, n2);
+        l += C::BS ? scaled : sum2(sum);
         hand_over(1);
       }
       if (!ok) break;
@@ -1306,11 +1368,36 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (!mine || j >= r.j1 || key >= r.any1 || key + maps.box <= r.any0) return p.cache.num_pages;
         return __ldg(table + (ps_shift >= 0 ? key >> ps_shift : key / ps));
       };
-      int nxt = page_of(r.j0);
+      // block scales of a page (none where there is no page: 0)
+      auto scales_of = [&](int id) {
+        float2 x = make_float2(0.0f, 0.0f);
+        if (C::BS && (unsigned)id < (unsigned)p.cache.num_pages) {
+          x.x = __ldg(p.cache.k_scale + id * p.cache.scale_stride + r.h);
+          x.y = __ldg(p.cache.v_scale + id * p.cache.scale_stride + r.h);
+        }
+        return x;
+      };
+      int nxt = page_of(r.j0), nxt2 = C::BS ? page_of(r.j0 + 1) : 0;
+      float2 snxt = scales_of(nxt);
       for (int j = r.j0; ok && j < r.j1; j++) {
         const int key = (r.first + j) * kTile + bx * maps.box;
-        const int id = nxt;
-        nxt = page_of(j + 1);
+        int id = nxt;
+        float2 sc = snxt;
+        bool no_scale = false;
+        if (C::BS) {
+          nxt = nxt2;
+          snxt = scales_of(nxt);
+          nxt2 = page_of(j + 2);
+          if (!(sc.x >= 0.0f && sc.x <= kMostScale && sc.y >= 0.0f && sc.y <= kMostScale)) {
+            // (such a page is one that is needed: its keys count as absent)
+            no_scale = true;
+            bad |= kStatusBadScale;
+            sc = make_float2(0.0f, 0.0f);
+            id = -1;
+          }
+        } else {
+          nxt = page_of(j + 1);
+        }
         const bool absent = (unsigned)id > (unsigned)p.cache.num_pages ||
                             (id == p.cache.num_pages && mine && key < r.any1 &&
                              key + maps.box > r.any0);
@@ -1318,7 +1405,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         // 16-key groups of absent pages
         uint32_t g = absent ? ((1u << (maps.box / 16)) - 1) << (bx * (maps.box / 16)) : 0u;
         g = __reduce_or_sync(0xffffffffu, g);
-        if (g) bad |= kStatusBadPage;
+        if (absent && !no_scale) bad |= kStatusBadPage;
         const int at = ps_shift >= 0 ? key & (ps - 1) : key % ps;
         const uint32_t st = n % C::kStages, par = (n >> C::kStageBits) & 1;
 #pragma unroll 1
@@ -1335,15 +1422,24 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               edge_par ^= 1u << st;
             }
           }
+          if (C::BS && x == 0) {
+            if (mine) {
+              const float v = fmaxf(sc.y, kLeastScale);
+              const float4 f = make_float4(fmaxf(sc.x, kLeastScale), log2f(v), 1.0f / v, 0.0f);
+              for (int i = 0; i < maps.box / 16; i++)
+                ring[n % kGone * (kTile / 16) + bx * (maps.box / 16) + i] = f;
+            }
+            __syncwarp();
+          }
           if (lane == 0) {
             if (x == 0) gone[n % kGone] = g;
             mbar_arrive_expect_tx(bar, BYTES);
           }
           __syncwarp();
           if (mine) {
-            const uint32_t ring = sbase + (C::E8 ? C::kOffRaw + x * C::kRaw
+            const uint32_t stage = sbase + (C::E8 ? C::kOffRaw + x * C::kRaw
                                                  : (x ? C::kOffV : C::kOffK) + st * C::kOp);
-            const uint32_t dst = ring + half * (kTile * 128) + bx * maps.box * (C::E8 ? D : 128);
+            const uint32_t dst = stage + half * (kTile * 128) + bx * maps.box * (C::E8 ? D : 128);
             const CUtensorMap* m = x == 0 ? &maps.k : &maps.v;
             if (maps.heads_first)
               tma_load_4d(dst, m, half * 64, r.h, at, page, bar);
@@ -1355,6 +1451,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         n++;
       }
     }
+    bad = (int32_t)__reduce_or_sync(0xffffffffu, (uint32_t)bad);
     if (bad && lane == 0) atomicOr(p.status, bad);
     // every box this warp requested has landed before the CTA may exit (after
     // a wait that ran out, a step's K may be under way without its V)
@@ -1553,7 +1650,7 @@ __global__ void __launch_bounds__(256) attn_tiles_join_kernel(AttnParams p, Plan
     const Split u = pl.split[i % splits];
     const int r = i / splits * kRows + threadIdx.x / LR;
     if (r >= u.nrows) continue;
-    const float vs = C::E8 && p.cache.v_scale ? __ldg(p.cache.v_scale + u.head) : 1.0f;
+    const float vs = C::E8 && !C::BS && p.cache.v_scale ? __ldg(p.cache.v_scale + u.head) : 1.0f;
     float mm = -INFINITY, ll = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
     for (int c = u.first; c <= u.last; c++) {
@@ -1674,6 +1771,9 @@ cudaError_t launch_cfg(const AttnParams& p, const Maps& maps, const Plan& pl, in
 template <int D>
 cudaError_t launch_types(const AttnParams& p, const Maps& m, const Plan& pl, int mu,
                          cudaStream_t st) {
+  if (p.blocks)
+    return p.bf16 ? launch_cfg<Cfg<D, 1, 1, 1>>(p, m, pl, mu, st)
+                  : launch_cfg<Cfg<D, 1, 0, 1>>(p, m, pl, mu, st);
   if (p.e4m3)
     return p.bf16 ? launch_cfg<Cfg<D, 1, 1>>(p, m, pl, mu, st)
                   : launch_cfg<Cfg<D, 1, 0>>(p, m, pl, mu, st);

@@ -173,6 +173,13 @@ __device__ __forceinline__ uint32_t e4m3_pack2(float lo, float hi) {
   return f8;
 }
 
+// Two E4M3 bytes (the low half of w) as fp32, exactly.
+__device__ __forceinline__ float2 e4m3_float2(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&r));
+}
+
 // Per-row E4M3 activation operand (the FP8 x FP8 product's activations):
 // s = amax / 448 and q = E4M3_RNE_sat(a / s), both divisions IEEE fp32 (the
 // precision in which the quantised code is decided); an all-zero row has

@@ -1,0 +1,394 @@
+// A pool of cache pages on the GPU: block tables, positions and slots of a
+// step from its sequences' lengths, without the host.
+//
+//   need_b = ceil((L_b + n_b) / P) - ceil(L_b / P), e_b = need_0 + .. + need_(b-1)
+//   k-th new page of b = free[count - 1 - e_b - k]
+//
+// and the way back for tokens that are taken off again, which leaves the stack
+// of free pages as it was before they came.
+//
+// The work is a scan over the sequences and a copy of their table rows; the
+// time is the chain of loads (indices, lengths, pages), so it is one launch: a
+// cluster whose first CTA scans and whose other CTAs then write rows with it.
+#include "attn.cuh"
+#include "common.cuh"
+#include "pipeline.cuh"
+
+namespace exl3 {
+namespace {
+
+constexpr int kThreads = 512, kCtas = 8;
+
+enum : int32_t { kPoolBadRequest = 1, kPoolNoPages = 2, kPoolTooLong = 4 };
+
+// What the first CTA says of a sequence of the step.
+struct Rec {
+  int row;    // of the pool, -1: left out
+  int len;    // tokens before
+  int len2;   // tokens after
+  int first;  // pages of the step's sequences before this one, taken or given back
+};
+
+struct PoolParams {
+  int num_pages, page_size, max_seqs, max_pages;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* free;
+  int32_t* count;
+  int num;  // sequences of the step
+  const int32_t* seqs;
+  const int32_t* n;  // new tokens; tokens to drop (null: all)
+  int max_tokens;
+  int32_t* cu_q;
+  int32_t* seq_lens;
+  int32_t* block_table;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* status;
+  int32_t* owner;  // [max_seqs], zero between calls
+  Rec* rec;        // [num]
+};
+
+__device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
+
+// Inclusive scan of two values over the CTA; *total receives the sums.
+__device__ __forceinline__ longlong2 scan2(longlong2 v, longlong2* total) {
+  __shared__ longlong2 sums[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, v.x, m), y = __shfl_up_sync(0xffffffffu, v.y, m);
+    if (lane >= m) {
+      v.x += x;
+      v.y += y;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = v;
+  __syncthreads();
+  longlong2 t = make_longlong2(0, 0);
+  for (int w = 0; w < kThreads / 32; w++) {
+    if (w == warp) {
+      v.x += t.x;
+      v.y += t.y;
+    }
+    t.x += sums[w].x;
+    t.y += sums[w].y;
+  }
+  *total = t;
+  return v;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// The row of sequence i of the step if it may be used: in range, and the
+// first that names it.
+__device__ __forceinline__ void claim(const PoolParams& p) {
+  for (int i = threadIdx.x; i < p.num; i += kThreads) {
+    const int s = __ldg(p.seqs + i);
+    // (the least i of a row, as the greatest num - i, so that 0 is "none")
+    if (s >= 0 && s < p.max_seqs) atomicMax(p.owner + s, p.num - i);
+  }
+  __threadfence();
+  __syncthreads();
+}
+__device__ __forceinline__ void disclaim(const PoolParams& p) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.num; i += kThreads) {
+    const int s = __ldg(p.seqs + i);
+    if (s >= 0 && s < p.max_seqs) p.owner[s] = 0;
+  }
+}
+__device__ __forceinline__ bool claimed(const PoolParams& p, int i, int s) {
+  return s >= 0 && s < p.max_seqs && __ldcg(p.owner + s) == p.num - i;
+}
+__device__ __forceinline__ int length_of(const PoolParams& p, int s) {
+  return min(max(p.lens[s], 0), (int)min((long long)p.max_pages * p.page_size, (long long)kMaxLen));
+}
+
+__global__ void __launch_bounds__(kThreads) extend_kernel(PoolParams p) {
+  pdl_wait();
+  const int rank = blockIdx.x;
+  const int P = p.page_size;
+  if (rank == 0) {
+    claim(p);
+    const int count = min(max(*p.count, 0), p.num_pages);
+    const long long most = min((long long)p.max_pages * P, (long long)kMaxLen);
+    int32_t bad = 0;
+    longlong2 run = make_longlong2(0, 0), total;
+    int taken = 0;
+    for (int i0 = 0; i0 < p.num; i0 += kThreads) {
+      const int i = i0 + threadIdx.x;
+      int s = -1, len = 0, n = 0;
+      bool ok = false;
+      if (i < p.num) {
+        s = __ldg(p.seqs + i);
+        n = __ldg(p.n + i);
+        ok = claimed(p, i, s) && n >= 0;
+        if (!ok) bad |= kPoolBadRequest;
+        n = max(n, 0);
+        if (ok) {
+          len = length_of(p, s);
+          if (len + (long long)n > most) {
+            ok = false;
+            bad |= kPoolTooLong;
+          }
+        }
+      }
+      // rows first: a sequence whose rows do not exist takes no page
+      const long long need = ok ? pages_of(len + n, P) - pages_of(len, P) : 0;
+      const longlong2 inc = scan2(make_longlong2(n, need), &total);
+      const long long q1 = run.x + inc.x, e = run.y + inc.y - need;
+      if (i < p.num) {
+        if (ok && n > 0 && q1 > p.max_tokens) {
+          ok = false;
+          bad |= kPoolTooLong;
+        }
+        if (ok && need > 0 && e + need > count) {
+          ok = false;
+          bad |= kPoolNoPages;
+        }
+        if (i == 0) p.cu_q[0] = 0;
+        p.cu_q[i + 1] = (int)min(q1, (long long)p.max_tokens);
+        p.seq_lens[i] = ok ? len + n : 0;
+        p.rec[i] = Rec{ok ? s : -1, len, len + n, (int)min(e, (long long)p.num_pages)};
+        if (ok) {
+          p.lens[s] = len + n;
+          if (need > 0) taken = max(taken, (int)(e + need));
+        }
+      }
+      run.x += total.x;
+      run.y += total.y;
+    }
+    if (p.num == 0 && threadIdx.x == 0) p.cu_q[0] = 0;
+    disclaim(p);
+    __shared__ int s_taken;
+    if (threadIdx.x == 0) s_taken = 0;
+    __syncthreads();
+    if (taken) atomicMax(&s_taken, taken);
+    if (bad) atomicOr(p.status, bad);
+    __syncthreads();
+    // (the pages are read from the stack after its count falls: they stay there)
+    if (threadIdx.x == 0) {
+      *p.count = count - s_taken;
+      p.status[1] = count;
+    }
+    __threadfence();
+  }
+  cluster_sync();
+  const int count = __ldcg(p.status + 1);
+  // ---- table rows
+  const int warp = (rank * kThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  constexpr int kWarps = kCtas * kThreads / 32;
+  for (int i = warp; i < p.num; i += kWarps) {
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(p.rec + i));
+    const Rec r{v.x, v.y, v.z, v.w};
+    const int have = r.row < 0 ? 0 : pages_of(r.len, P), want = r.row < 0 ? 0 : pages_of(r.len2, P);
+    int32_t* mine = p.table + (int64_t)max(r.row, 0) * p.max_pages;
+    int32_t* out = p.block_table + (int64_t)i * p.max_pages;
+    for (int k = lane; k < p.max_pages; k += 32) {
+      int id = -1;
+      if (k < have) {
+        id = mine[k];
+      } else if (k < want) {
+        id = p.free[count - 1 - r.first - (k - have)];
+        mine[k] = id;
+      }
+      out[k] = id;
+    }
+  }
+  cluster_sync();  // rows of other warps' sequences
+  // ---- positions and slots
+  for (int t = rank * kThreads + threadIdx.x; t < p.max_tokens; t += kCtas * kThreads) {
+    int lo = 0, hi = p.num;  // the last sequence that begins at or before t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldcg(p.cu_q + mid) <= t)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    int pos = -1;
+    int64_t slot = -1;
+    if (p.num > 0 && t < __ldcg(p.cu_q + lo + 1)) {
+      const int4 v = __ldcg(reinterpret_cast<const int4*>(p.rec + lo));
+      if (v.x >= 0) {
+        pos = v.y + t - __ldcg(p.cu_q + lo);
+        const int id = __ldcg(p.block_table + (int64_t)lo * p.max_pages + pos / P);
+        if (id >= 0) slot = (int64_t)id * P + pos % P;
+      }
+    }
+    p.positions[t] = pos;
+    p.slots[t] = slot;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) trim_kernel(PoolParams p) {
+  pdl_wait();
+  const int rank = blockIdx.x;
+  const int P = p.page_size;
+  if (rank == 0) {
+    claim(p);
+    const int count = min(max(*p.count, 0), p.num_pages);
+    int32_t bad = 0;
+    longlong2 run = make_longlong2(0, 0), total;
+    for (int i0 = 0; i0 < p.num; i0 += kThreads) {
+      const int i = i0 + threadIdx.x;
+      int s = -1, len = 0, n = 0;
+      bool ok = false;
+      if (i < p.num) {
+        s = __ldg(p.seqs + i);
+        ok = claimed(p, i, s);
+        if (ok) {
+          len = length_of(p, s);
+          n = p.n ? __ldg(p.n + i) : len;
+          if (n < 0 || n > len) bad |= kPoolBadRequest;
+          n = min(max(n, 0), len);
+        } else {
+          bad |= kPoolBadRequest;
+        }
+      }
+      const long long back = ok ? pages_of(len, P) - pages_of(len - n, P) : 0;
+      const longlong2 inc = scan2(make_longlong2(0, back), &total);
+      if (i < p.num) {
+        const long long e = run.y + inc.y - back;
+        p.rec[i] = Rec{ok ? s : -1, len, len - n, (int)min(e, (long long)kMaxLen)};
+        if (ok) p.lens[s] = len - n;
+      }
+      run.y += total.y;
+    }
+    disclaim(p);
+    if (run.y > p.num_pages - count) {  // more than there are: the pool was tampered with
+      bad |= kPoolBadRequest;
+      run.y = p.num_pages - count;
+    }
+    if (bad) atomicOr(p.status, bad);
+    if (threadIdx.x == 0) {
+      *p.count = count + (int)run.y;
+      p.status[1] = count + (int)run.y;
+      p.status[2] = count;
+    }
+    __threadfence();
+  }
+  cluster_sync();
+  // the first page of the first sequence goes on top
+  const int top = __ldcg(p.status + 1) - 1, bottom = __ldcg(p.status + 2);
+  const int warp = (rank * kThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  constexpr int kWarps = kCtas * kThreads / 32;
+  for (int i = warp; i < p.num; i += kWarps) {
+    const int4 r = __ldcg(reinterpret_cast<const int4*>(p.rec + i));
+    if (r.x < 0) continue;
+    int32_t* mine = p.table + (int64_t)r.x * p.max_pages;
+    const int keep = pages_of(r.z, P), had = pages_of(r.y, P);
+    for (int k = keep + lane; k < had; k += 32) {
+      const int64_t at = (int64_t)top - r.w - (k - keep);
+      if (at >= bottom) p.free[at] = mine[k];
+      mine[k] = -1;
+    }
+  }
+}
+
+cudaError_t launch(void (*kernel)(PoolParams), const PoolParams& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  note_launches(1);
+  return e;
+}
+
+// workspace: status word and two for the count, the owners, the records
+size_t owners_at() { return 256; }
+size_t records_at(int max_seqs) { return (owners_at() + (size_t)max_seqs * 4 + 255) & ~(size_t)255; }
+
+exl3_status check(const exl3_page_pool* o, int num, const int32_t* seqs, const void* ws,
+                  size_t ws_bytes) {
+  if (!o) return EXL3_ERR_ARG;
+  if (o->num_pages < 0 || o->page_size < 16 || o->page_size > kMaxPageSize || o->page_size % 16 ||
+      o->max_seqs < 1 || o->max_seqs > kMaxSeqs || o->max_pages < 1 || num < 0 || num > kMaxSeqs ||
+      (long long)o->max_pages * o->page_size > kMaxLen)
+    return EXL3_ERR_SHAPE;
+  if (!o->table || !o->lens || !o->count || (o->num_pages > 0 && !o->free) || (num > 0 && !seqs))
+    return EXL3_ERR_ARG;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) ||
+      ws_bytes < exl3_pages_workspace_size(o->max_seqs, num))
+    return EXL3_ERR_WORKSPACE;
+  return EXL3_OK;
+}
+
+PoolParams params_of(const exl3_page_pool* o, int num, const int32_t* seqs, const int32_t* n,
+                     void* ws) {
+  PoolParams p{};
+  p.num_pages = o->num_pages;
+  p.page_size = o->page_size;
+  p.max_seqs = o->max_seqs;
+  p.max_pages = o->max_pages;
+  p.table = o->table;
+  p.lens = o->lens;
+  p.free = o->free;
+  p.count = o->count;
+  p.num = num;
+  p.seqs = seqs;
+  p.n = n;
+  p.status = static_cast<int32_t*>(ws);
+  p.owner = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + owners_at());
+  p.rec = reinterpret_cast<Rec*>(static_cast<uint8_t*>(ws) + records_at(o->max_seqs));
+  return p;
+}
+
+}  // namespace
+}  // namespace exl3
+
+using namespace exl3;
+
+extern "C" {
+
+size_t exl3_pages_workspace_size(int max_seqs, int num) {
+  if (max_seqs < 1 || max_seqs > kMaxSeqs || num < 0 || num > kMaxSeqs) return 0;
+  return records_at(max_seqs) + (size_t)num * sizeof(Rec);
+}
+
+exl3_status exl3_pages_extend(const exl3_page_pool* pool, int num, const int32_t* seqs,
+                              const int32_t* q_lens, int max_tokens, int32_t* cu_q,
+                              int32_t* seq_lens, int32_t* block_table, int32_t* positions,
+                              int64_t* slots, void* ws, size_t ws_bytes, void* stream) {
+  const exl3_status e = check(pool, num, seqs, ws, ws_bytes);
+  if (e != EXL3_OK) return e;
+  if (max_tokens < 0 || max_tokens > (1 << 30)) return EXL3_ERR_SHAPE;
+  if (!cu_q || (num > 0 && (!q_lens || !seq_lens || !block_table)) ||
+      (max_tokens > 0 && (!positions || !slots)) || (reinterpret_cast<uintptr_t>(slots) & 7))
+    return EXL3_ERR_ARG;
+  PoolParams p = params_of(pool, num, seqs, q_lens, ws);
+  p.max_tokens = max_tokens;
+  p.cu_q = cu_q;
+  p.seq_lens = seq_lens;
+  p.block_table = block_table;
+  p.positions = positions;
+  p.slots = slots;
+  return launch(extend_kernel, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXL3_OK
+                                                                                    : EXL3_ERR_CUDA;
+}
+
+exl3_status exl3_pages_trim(const exl3_page_pool* pool, int num, const int32_t* seqs,
+                            const int32_t* drop, void* ws, size_t ws_bytes, void* stream) {
+  const exl3_status e = check(pool, num, seqs, ws, ws_bytes);
+  if (e != EXL3_OK) return e;
+  if (num == 0) return EXL3_OK;
+  const PoolParams p = params_of(pool, num, seqs, drop, ws);
+  return launch(trim_kernel, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXL3_OK
+                                                                                  : EXL3_ERR_CUDA;
+}
+
+}  // extern "C"

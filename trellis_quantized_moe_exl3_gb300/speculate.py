@@ -1,0 +1,212 @@
+"""Speculative decoding around the paged cache: Python API over the C ABI.
+
+    pool = PagePool(num_pages, page_size, max_seqs, max_pages)   # pages of the cache, on the GPU
+    step = pool.extend(seqs, q_lens, max_q, max_tokens)          # a PagedBatch with its pages
+    q = kv_append(cache, step, ...); out = paged_attention(q, cache, step)
+    tokens, accepted, dropped = verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=q_probs)
+    pool.trim(seqs, dropped)                                     # refused drafts leave the cache
+
+Nothing of it is read on the host, so a whole step can be captured in a CUDA
+graph.  Every call is one kernel on the current stream (or on stream=, which the
+inputs must then be ready on).
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import check
+from .api import device_status
+from .attention import PagedBatch, _capturing, _cuda, _dense, _empty, _stream
+
+_PROBS = {torch.float16: _lib.EXL3_F16, torch.bfloat16: _lib.EXL3_BF16,
+          torch.float32: _lib.EXL3_F32}
+
+
+class PagedStep(PagedBatch):
+    """A step as PagePool.extend lays it out: a PagedBatch (cu_q, seq_lens,
+    block_table) with positions [max_tokens] int32 and slots [max_tokens] int64
+    (page * page_size + place) of its new tokens, -1 in rows that are none's."""
+
+    def __init__(self, buf, num, max_q, max_tokens, max_pages):
+        self._buf, self._max_pages, self.max_tokens = buf, max_pages, max_tokens
+        self.num_seqs, self.max_q = num, int(max_q)
+        self._at = a = _places(num, max_tokens)
+        p = buf.data_ptr()
+        d = _lib.KVBatch()
+        d.num_seqs, d.max_q, d.max_pages, d.table_stride = num, self.max_q, max_pages, max_pages
+        d.cu_q, d.seq_lens, d.block_table = p + 4 * a[1], p + 4 * a[2], p + 4 * a[3]
+        self._d, self._ref = d, ctypes.byref(d)
+
+    @property
+    def slots(self):
+        return self._buf[:2 * self.max_tokens].view(torch.int64)
+
+    @property
+    def positions(self):
+        return self._buf[self._at[0]:self._at[0] + self.max_tokens]
+
+    @property
+    def cu_q(self):
+        return self._buf[self._at[1]:self._at[1] + self.num_seqs + 1]
+
+    @property
+    def seq_lens(self):
+        return self._buf[self._at[2]:self._at[2] + self.num_seqs]
+
+    @property
+    def block_table(self):
+        return self._buf[self._at[3]:].view(self.num_seqs, self._max_pages)
+
+
+def _places(num, max_tokens):
+    """Where positions, cu_q, seq_lens and block_table begin in a step's buffer
+    (32-bit words; slots come first, the table last and aligned)."""
+    cu = 3 * max_tokens
+    return 2 * max_tokens, cu, cu + num + 1, (cu + 2 * num + 1 + 3) & ~3
+
+
+class PagePool:
+    """The pages of a cache and the sequences that hold them, on the GPU: `table`
+    [max_seqs, max_pages], `lens` [max_seqs], `free` [num_pages] and `count` [1],
+    int32.  A sequence is a row of the table; free[0 .. count - 1] are the free
+    pages, taken from the end.  Between calls a program may write these tensors
+    (a restored state); `status()` is the sticky device status (exl3.h; it
+    synchronises).  A pool's calls follow one another: it serves one stream at a
+    time."""
+
+    def __init__(self, num_pages: int, page_size: int, max_seqs: int, max_pages: int, device=None):
+        if num_pages < 0 or max_seqs < 1 or max_pages < 1:
+            raise ValueError("a pool has pages, rows and columns")
+        device = torch.device("cuda") if device is None else torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("a pool lives on a CUDA device")
+
+        def full(x, *shape):
+            return torch.full(shape, x, dtype=torch.int32, device=device)
+
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.max_seqs, self.max_pages = int(max_seqs), int(max_pages)
+        self.table, self.lens = full(-1, max_seqs, max_pages), full(0, max_seqs)
+        self.free = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.count = full(num_pages, 1)
+        n = _lib.lib().exl3_pages_workspace_size(self.max_seqs, self.max_seqs)
+        if n == 0:
+            raise ValueError(f"max_seqs {max_seqs} is out of range")
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=device)
+        d = _lib.PagePool()
+        d.num_pages, d.page_size, d.max_seqs, d.max_pages = num_pages, page_size, max_seqs, max_pages
+        d.table, d.lens = self.table.data_ptr(), self.lens.data_ptr()
+        d.free, d.count = self.free.data_ptr() or None, self.count.data_ptr()
+        self._d, self._ref = d, ctypes.byref(d)
+        self._ws, self._ws_bytes = self.ws.data_ptr(), n
+
+    def _seqs(self, seqs):
+        if seqs.dtype != torch.int32 or seqs.dim() != 1 or not seqs.is_cuda or \
+                not seqs.is_contiguous() or seqs.shape[0] > self.max_seqs:
+            _cuda(seqs, "seqs", torch.int32)
+            raise ValueError(f"seqs must be a contiguous tensor of at most {self.max_seqs} rows")
+        return seqs.shape[0]
+
+    def extend(self, seqs, q_lens, max_q: int, max_tokens: int, stream=None) -> PagedStep:
+        """Begins a step: row seqs[i] of the pool gets q_lens[i] new tokens and the
+        pages for them (int32 [sequences]).  max_tokens: rows of the step's token
+        tensors, at least the sum of q_lens; max_q: as PagedBatch's.  A sequence
+        for which there are no pages left keeps its rows, but has length 0 in the
+        step and stays as it was in the pool."""
+        n = self._seqs(seqs)
+        if q_lens.dtype != torch.int32 or q_lens.shape != (n,) or not q_lens.is_cuda or \
+                not q_lens.is_contiguous():
+            _dense(q_lens, "q_lens", torch.int32, (n,))
+        if max_tokens < 0:
+            raise ValueError("max_tokens must not be negative")
+        a = _places(n, max_tokens)
+        buf = _empty((a[3] + n * self.max_pages,), torch.int32, seqs.device, stream)
+        step = PagedStep(buf, n, max_q, max_tokens, self.max_pages)
+        p, d = buf.data_ptr(), step._d
+        check(_lib.lib().exl3_pages_extend(
+            self._ref, n, seqs.data_ptr(), q_lens.data_ptr(), max_tokens, d.cu_q, d.seq_lens,
+            d.block_table, p + 4 * a[0], p, self._ws, self._ws_bytes, _stream(stream, seqs)),
+            "exl3_pages_extend")
+        return step
+
+    def trim(self, seqs, drop=None, stream=None):
+        """Takes the last drop[i] tokens (None: all) of row seqs[i] off and gives
+        back the pages that hold nothing any more."""
+        n = self._seqs(seqs)
+        if drop is not None and (drop.dtype != torch.int32 or drop.shape != (n,) or
+                                 not drop.is_cuda or not drop.is_contiguous()):
+            _dense(drop, "drop", torch.int32, (n,))
+        check(_lib.lib().exl3_pages_trim(self._ref, n, seqs.data_ptr(),
+                                         drop.data_ptr() if drop is not None else None, self._ws,
+                                         self._ws_bytes, _stream(stream, seqs)), "exl3_pages_trim")
+
+    def status(self, stream=None) -> int:
+        """The status bits set so far (0: fine); see exl3.h."""
+        torch.cuda.synchronize(self.ws.device)
+        return device_status(self.ws, stream)
+
+    def clear_status(self):
+        wait = (lambda d: None) if _capturing() else torch.cuda.synchronize
+        wait(self.ws.device)
+        self.ws[:4].zero_()
+        wait(self.ws.device)
+
+
+def _rows(x, name, rows, vocab=None):
+    """Checks a [rows, vocab] tensor of probabilities; its row stride."""
+    if x.dtype not in _PROBS or not x.is_cuda:
+        _cuda(x, name, tuple(_PROBS))
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 2 or shape[0] != rows or (vocab is not None and shape[1] != vocab) or \
+            (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be [{rows}, {vocab or 'vocab'}] with contiguous rows, not "
+                         f"{tuple(shape)}")
+    return stride[0] if rows > 1 else shape[1]
+
+
+def _vector(x, name, dtype, n):
+    if x.dtype != dtype or x.shape != (n,) or not x.is_cuda or not x.is_contiguous():
+        _dense(x, name, dtype, (n,))
+    return x.data_ptr()
+
+
+def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None):
+    """Which drafted tokens stand, and the token after them.
+
+    Sequence b has the drafts draft[cu_draft[b] .. cu_draft[b+1] - 1] (int32;
+    cu_draft int32 [sequences + 1], read on the device).  p [drafts + sequences,
+    vocab]: the target's probabilities, fp32, fp16 or bf16, one row more per
+    sequence than drafts: row cu_draft[b] + b + j is that of the token after j
+    drafts.  q [drafts, vocab]: the probabilities that the drafts were drawn from
+    (None: they are certain).  accept_u [drafts], sample_u [sequences]: fp32
+    random numbers in [0, 1).
+
+    Draft x is accepted, after all before it, if accept_u * q(x) < p(x).  After
+    the first refusal a token is drawn from max(p - q, 0), after the last draft
+    from p: the first whose cumulative weight is above sample_u of the total
+    (both exactly, whatever the size of the vocabulary).
+
+    Returns int32 (tokens [drafts + sequences], accepted [sequences], dropped
+    [sequences]): from place cu_draft[b] + b on, the accepted drafts, the drawn
+    token, then -1; accepted drafts, and the others (what PagePool.trim takes)."""
+    D, B = draft.shape[0], sample_u.shape[0]
+    ps = _rows(p, "p", D + B)
+    vocab, qp, qs = p.shape[1], None, 0
+    if q is not None:
+        qs = _rows(q, "q", D, vocab)
+        if q.dtype != p.dtype:
+            raise ValueError("p and q must have the same dtype")
+        qp = q.data_ptr() if D else None
+    dev = p.device
+    tokens = _empty((D + B,), torch.int32, dev, stream)
+    accepted, dropped = _empty((B,), torch.int32, dev, stream), _empty((B,), torch.int32, dev, stream)
+    check(_lib.lib().exl3_verify_drafts(
+        p.data_ptr(), ps, qp, qs, _PROBS[p.dtype], vocab, B, D,
+        _vector(cu_draft, "cu_draft", torch.int32, B + 1), _vector(draft, "draft", torch.int32, D),
+        _vector(accept_u, "accept_u", torch.float32, D),
+        _vector(sample_u, "sample_u", torch.float32, B), tokens.data_ptr(), accepted.data_ptr(),
+        dropped.data_ptr(), _stream(stream, p)), "exl3_verify_drafts")
+    return tokens, accepted, dropped
