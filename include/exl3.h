@@ -567,11 +567,11 @@ exl3_status exl3_pages_trim(const exl3_page_pool *pool, int num, const int32_t *
  *   without the draft where q is NULL; p itself where nothing is left), after
  *   the last draft from p: the first token whose cumulative weight is above
  *   sample_u times the total.
- * Both are decided exactly: weights are summed in units of 2^-56 (smaller
- * parts are cut off), so results do not depend on the order of sums.
+ * Both are decided exactly: probabilities are rounded to units of 2^-46 and
+ * summed as whole numbers, so results do not depend on the order of sums.
  *   p, q      device, rows of vocab probabilities in dt (fp16, bf16 or fp32),
  *             strides in elements.  NaN and what is negative count as 0, what
- *             is above 1 as 1; a row sums to less than 256
+ *             is above 1 as 1; a row sums to less than 2^16
  *   draft     device int32 [drafts]; one outside 0 .. vocab - 1 is refused
  *   accept_u  device fp32 [drafts], in [0, 1)
  *   sample_u  device fp32 [num_seqs], in [0, 1)

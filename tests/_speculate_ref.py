@@ -80,10 +80,10 @@ class Pool:
 
 # ------------------------------------------------------------ verification
 def fixed(x):
-    """Probabilities in units of 2^-56, cut off (exact: a product by a power of two)."""
+    """Probabilities rounded to units of 2^-46 (exact up to it: a product by a power of two)."""
     x = x.double().cpu().numpy()
     x = np.where(x > 0, np.minimum(x, 1.0), 0.0)
-    return (x * 2.0 ** 56).astype(np.uint64)
+    return np.rint(x * 2.0 ** 46).astype(np.uint64)
 
 
 def verify(p, draft, cu, accept_u, sample_u, q):

@@ -7,9 +7,10 @@
 // and the way back for tokens that are taken off again, which leaves the stack
 // of free pages as it was before they came.
 //
-// The work is a scan over the sequences and a copy of their table rows; the
-// time is the chain of loads (indices, lengths, pages), so it is one launch: a
-// cluster whose first CTA scans and whose other CTAs then write rows with it.
+// A scan over the sequences, then a copy of their table rows.  Small steps are a
+// chain of loads (indices, lengths, pages): one launch, a cluster whose first CTA
+// scans and whose CTAs then write rows with it.  Where the rows are many, eight
+// SMs are too few to write them: the scan and the rows are two launches.
 #include "attn.cuh"
 #include "common.cuh"
 #include "pipeline.cuh"
@@ -18,6 +19,11 @@ namespace exl3 {
 namespace {
 
 constexpr int kThreads = 512, kCtas = 8;
+// Words a step writes up to which it is one launch: a step and its way back, us in
+// one / two launches of extend, 8 sequences of 128 pages 9.7 / 9.9, 256 of 2048
+// 18.4 / 12.2.
+constexpr long long kFused = 65536;
+constexpr int kOwners = 8192;  // rows of a pool whose claims fit shared memory
 
 enum : int32_t { kPoolBadRequest = 1, kPoolNoPages = 2, kPoolTooLong = 4 };
 
@@ -84,125 +90,174 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 
-// The row of sequence i of the step if it may be used: in range, and the
-// first that names it.
-__device__ __forceinline__ void claim(const PoolParams& p) {
-  for (int i = threadIdx.x; i < p.num; i += kThreads) {
-    const int s = __ldg(p.seqs + i);
-    // (the least i of a row, as the greatest num - i, so that 0 is "none")
-    if (s >= 0 && s < p.max_seqs) atomicMax(p.owner + s, p.num - i);
+// Claims: sequence i of the step may use its row if the row exists and no earlier
+// one names it.  A row's owner is the greatest num - i (0: none).
+struct Claims {
+  int32_t* owner;
+  int num, max_seqs;
+  __device__ Claims(const PoolParams& p, int32_t* shared) : num(p.num), max_seqs(p.max_seqs) {
+    owner = max_seqs <= kOwners ? shared : p.owner;
+    if (owner == shared) {
+      for (int s = threadIdx.x; s < max_seqs; s += kThreads) owner[s] = 0;
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < num; i += kThreads) {
+      const int s = __ldg(p.seqs + i);
+      if (s >= 0 && s < max_seqs) atomicMax(owner + s, num - i);
+    }
+    __threadfence_block();
+    __syncthreads();
   }
-  __threadfence();
-  __syncthreads();
-}
-__device__ __forceinline__ void disclaim(const PoolParams& p) {
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.num; i += kThreads) {
-    const int s = __ldg(p.seqs + i);
-    if (s >= 0 && s < p.max_seqs) p.owner[s] = 0;
+  __device__ bool holds(int i, int s) const {
+    return s >= 0 && s < max_seqs && *static_cast<volatile int32_t*>(owner + s) == num - i;
   }
-}
-__device__ __forceinline__ bool claimed(const PoolParams& p, int i, int s) {
-  return s >= 0 && s < p.max_seqs && __ldcg(p.owner + s) == p.num - i;
-}
+  // (the workspace's are left at zero)
+  __device__ void end(const PoolParams& p) const {
+    if (owner != p.owner) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < num; i += kThreads) {
+      const int s = __ldg(p.seqs + i);
+      if (s >= 0 && s < max_seqs) owner[s] = 0;
+    }
+  }
+};
 __device__ __forceinline__ int length_of(const PoolParams& p, int s) {
   return min(max(p.lens[s], 0), (int)min((long long)p.max_pages * p.page_size, (long long)kMaxLen));
 }
+__device__ __forceinline__ Rec load_rec(const PoolParams& p, int i) {
+  const int4 v = __ldcg(reinterpret_cast<const int4*>(p.rec + i));
+  return Rec{v.x, v.y, v.z, v.w};
+}
 
-__global__ void __launch_bounds__(kThreads) extend_kernel(PoolParams p) {
-  pdl_wait();
-  const int rank = blockIdx.x;
+// The scan (one CTA): lengths, records, the pool's new state.
+__device__ __forceinline__ void plan_extend(const PoolParams& p, int32_t* shared) {
   const int P = p.page_size;
-  if (rank == 0) {
-    claim(p);
-    const int count = min(max(*p.count, 0), p.num_pages);
-    const long long most = min((long long)p.max_pages * P, (long long)kMaxLen);
-    int32_t bad = 0;
-    longlong2 run = make_longlong2(0, 0), total;
-    int taken = 0;
-    for (int i0 = 0; i0 < p.num; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      int s = -1, len = 0, n = 0;
-      bool ok = false;
-      if (i < p.num) {
-        s = __ldg(p.seqs + i);
-        n = __ldg(p.n + i);
-        ok = claimed(p, i, s) && n >= 0;
-        if (!ok) bad |= kPoolBadRequest;
-        n = max(n, 0);
-        if (ok) {
-          len = length_of(p, s);
-          if (len + (long long)n > most) {
-            ok = false;
-            bad |= kPoolTooLong;
-          }
-        }
-      }
-      // rows first: a sequence whose rows do not exist takes no page
-      const long long need = ok ? pages_of(len + n, P) - pages_of(len, P) : 0;
-      const longlong2 inc = scan2(make_longlong2(n, need), &total);
-      const long long q1 = run.x + inc.x, e = run.y + inc.y - need;
-      if (i < p.num) {
-        if (ok && n > 0 && q1 > p.max_tokens) {
+  const int count = min(max(*p.count, 0), p.num_pages);
+  const long long most = min((long long)p.max_pages * P, (long long)kMaxLen);
+  const Claims claims(p, shared);
+  int32_t bad = 0;
+  longlong2 run = make_longlong2(0, 0), total;
+  int taken = 0;
+  for (int i0 = 0; i0 < p.num; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    int s = -1, len = 0, n = 0;
+    bool ok = false;
+    if (i < p.num) {
+      s = __ldg(p.seqs + i);
+      n = __ldg(p.n + i);
+      ok = claims.holds(i, s) && n >= 0;
+      if (!ok) bad |= kPoolBadRequest;
+      n = max(n, 0);
+      if (ok) {
+        len = length_of(p, s);
+        if (len + (long long)n > most) {
           ok = false;
           bad |= kPoolTooLong;
         }
-        if (ok && need > 0 && e + need > count) {
-          ok = false;
-          bad |= kPoolNoPages;
-        }
-        if (i == 0) p.cu_q[0] = 0;
-        p.cu_q[i + 1] = (int)min(q1, (long long)p.max_tokens);
-        p.seq_lens[i] = ok ? len + n : 0;
-        p.rec[i] = Rec{ok ? s : -1, len, len + n, (int)min(e, (long long)p.num_pages)};
-        if (ok) {
-          p.lens[s] = len + n;
-          if (need > 0) taken = max(taken, (int)(e + need));
-        }
       }
-      run.x += total.x;
-      run.y += total.y;
     }
-    if (p.num == 0 && threadIdx.x == 0) p.cu_q[0] = 0;
-    disclaim(p);
-    __shared__ int s_taken;
-    if (threadIdx.x == 0) s_taken = 0;
-    __syncthreads();
-    if (taken) atomicMax(&s_taken, taken);
-    if (bad) atomicOr(p.status, bad);
-    __syncthreads();
-    // (the pages are read from the stack after its count falls: they stay there)
-    if (threadIdx.x == 0) {
-      *p.count = count - s_taken;
-      p.status[1] = count;
+    const long long need = ok ? pages_of(len + n, P) - pages_of(len, P) : 0;
+    const longlong2 inc = scan2(make_longlong2(n, need), &total);
+    const long long q1 = run.x + inc.x, e = run.y + inc.y - need;
+    if (i < p.num) {
+      if (ok && n > 0 && q1 > p.max_tokens) {
+        ok = false;
+        bad |= kPoolTooLong;
+      }
+      if (ok && need > 0 && e + need > count) {
+        ok = false;
+        bad |= kPoolNoPages;
+      }
+      p.cu_q[i + 1] = (int)min(q1, (long long)p.max_tokens);
+      p.seq_lens[i] = ok ? len + n : 0;
+      p.rec[i] = Rec{ok ? s : -1, len, len + n, (int)min(e, (long long)p.num_pages)};
+      if (ok) {
+        p.lens[s] = len + n;
+        if (need > 0) taken = max(taken, (int)(e + need));
+      }
     }
-    __threadfence();
+    run.x += total.x;
+    run.y += total.y;
   }
-  cluster_sync();
-  const int count = __ldcg(p.status + 1);
-  // ---- table rows
-  const int warp = (rank * kThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  constexpr int kWarps = kCtas * kThreads / 32;
-  for (int i = warp; i < p.num; i += kWarps) {
-    const int4 v = __ldcg(reinterpret_cast<const int4*>(p.rec + i));
-    const Rec r{v.x, v.y, v.z, v.w};
+  __shared__ int s_taken, s_bad;
+  if (threadIdx.x == 0) s_taken = s_bad = 0;
+  __syncthreads();
+  if (taken) atomicMax(&s_taken, taken);
+  if (bad) atomicOr(&s_bad, bad);
+  claims.end(p);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p.cu_q[0] = 0;
+    // (the pages are read from the stack after its count falls: they stay there)
+    *p.count = count - s_taken;
+    p.status[1] = count;
+    if (s_bad) atomicOr(p.status, s_bad);
+  }
+}
+
+// Table rows, positions and slots, by `threads` threads of which this is `me`.
+template <int VEC>
+__device__ __forceinline__ void fill_rows(const PoolParams& p, int count, int me, int threads) {
+  constexpr int U = 4, kItem = 32 * U * VEC;  // entries that a warp writes at a time
+  const int P = p.page_size, lane = me & 31;
+  const long long per_row = (p.max_pages + kItem - 1) / kItem, items = per_row * p.num;
+  for (long long it = me >> 5; it < items; it += threads >> 5) {
+    const int i = (int)(it / per_row), k0 = (int)(it % per_row) * kItem + lane * VEC;
+    const Rec r = load_rec(p, i);
     const int have = r.row < 0 ? 0 : pages_of(r.len, P), want = r.row < 0 ? 0 : pages_of(r.len2, P);
     int32_t* mine = p.table + (int64_t)max(r.row, 0) * p.max_pages;
     int32_t* out = p.block_table + (int64_t)i * p.max_pages;
-    for (int k = lane; k < p.max_pages; k += 32) {
-      int id = -1;
-      if (k < have) {
-        id = mine[k];
-      } else if (k < want) {
-        id = p.free[count - 1 - r.first - (k - have)];
-        mine[k] = id;
+    int id[U][VEC];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int k = k0 + u * 32 * VEC;
+#pragma unroll
+      for (int v = 0; v < VEC; v++) id[u][v] = -1;
+      if (k < have && k < p.max_pages) {
+        if (VEC == 4) {
+          const int4 w = *reinterpret_cast<const int4*>(mine + k);
+          id[u][0] = w.x;
+          id[u][VEC > 1 ? 1 : 0] = w.y;
+          id[u][VEC > 1 ? 2 : 0] = w.z;
+          id[u][VEC > 1 ? 3 : 0] = w.w;
+        } else {
+          id[u][0] = mine[k];
+        }
       }
-      out[k] = id;
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int k = k0 + u * 32 * VEC;
+      if (k + VEC > have && k < want) {
+#pragma unroll
+        for (int v = 0; v < VEC; v++)
+          if (k + v >= have && k + v < want) {
+            id[u][v] = p.free[count - 1 - r.first - (k + v - have)];
+            mine[k + v] = id[u][v];
+          }
+      }
+#pragma unroll
+      for (int v = 0; v < VEC; v++)
+        if (k + v >= want) id[u][v] = -1;
+      if (k < p.max_pages) {
+        if (VEC == 4)
+          *reinterpret_cast<int4*>(out + k) =
+              make_int4(id[u][0], id[u][VEC > 1 ? 1 : 0], id[u][VEC > 1 ? 2 : 0], id[u][VEC > 1 ? 3 : 0]);
+        else
+          out[k] = id[u][0];
+      }
     }
   }
-  cluster_sync();  // rows of other warps' sequences
-  // ---- positions and slots
-  for (int t = rank * kThreads + threadIdx.x; t < p.max_tokens; t += kCtas * kThreads) {
+}
+__device__ __forceinline__ void fill(const PoolParams& p, int me, int threads) {
+  const int P = p.page_size, count = __ldcg(p.status + 1);
+  // 16 bytes at a time where rows begin on 16 bytes
+  if (p.max_pages % 4 == 0 &&
+      ((reinterpret_cast<uintptr_t>(p.table) | reinterpret_cast<uintptr_t>(p.block_table)) & 15) == 0)
+    fill_rows<4>(p, count, me, threads);
+  else
+    fill_rows<1>(p, count, me, threads);
+  for (int t = me; t < p.max_tokens; t += threads) {
     int lo = 0, hi = p.num;  // the last sequence that begins at or before t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -214,10 +269,12 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(PoolParams p) {
     int pos = -1;
     int64_t slot = -1;
     if (p.num > 0 && t < __ldcg(p.cu_q + lo + 1)) {
-      const int4 v = __ldcg(reinterpret_cast<const int4*>(p.rec + lo));
-      if (v.x >= 0) {
-        pos = v.y + t - __ldcg(p.cu_q + lo);
-        const int id = __ldcg(p.block_table + (int64_t)lo * p.max_pages + pos / P);
+      const Rec r = load_rec(p, lo);
+      if (r.row >= 0) {
+        pos = r.len + t - __ldcg(p.cu_q + lo);
+        const int k = pos / P, have = pages_of(r.len, P);
+        const int id = k < have ? p.table[(int64_t)r.row * p.max_pages + k]
+                                : p.free[count - 1 - r.first - (k - have)];
         if (id >= 0) slot = (int64_t)id * P + pos % P;
       }
     }
@@ -226,12 +283,36 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(PoolParams p) {
   }
 }
 
+// One cluster: the scan, then the rows.
+__global__ void __launch_bounds__(kThreads) extend_kernel(PoolParams p) {
+  __shared__ int32_t owners[kOwners];
+  pdl_wait();
+  if (blockIdx.x == 0) {
+    plan_extend(p, owners);
+    __threadfence();
+  }
+  cluster_sync();
+  fill(p, blockIdx.x * kThreads + threadIdx.x, kCtas * kThreads);
+}
+// The same in two launches.
+__global__ void __launch_bounds__(kThreads) extend_plan_kernel(PoolParams p) {
+  __shared__ int32_t owners[kOwners];
+  pdl_wait();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  plan_extend(p, owners);
+}
+__global__ void __launch_bounds__(kThreads) extend_fill_kernel(PoolParams p) {
+  pdl_wait();
+  fill(p, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
+}
+
 __global__ void __launch_bounds__(kThreads) trim_kernel(PoolParams p) {
+  __shared__ int32_t owners[kOwners];
   pdl_wait();
   const int rank = blockIdx.x;
   const int P = p.page_size;
   if (rank == 0) {
-    claim(p);
+    const Claims claims(p, owners);
     const int count = min(max(*p.count, 0), p.num_pages);
     int32_t bad = 0;
     longlong2 run = make_longlong2(0, 0), total;
@@ -241,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(PoolParams p) {
       bool ok = false;
       if (i < p.num) {
         s = __ldg(p.seqs + i);
-        ok = claimed(p, i, s);
+        ok = claims.holds(i, s);
         if (ok) {
           len = length_of(p, s);
           n = p.n ? __ldg(p.n + i) : len;
@@ -260,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(PoolParams p) {
       }
       run.y += total.y;
     }
-    disclaim(p);
+    claims.end(p);
     if (run.y > p.num_pages - count) {  // more than there are: the pool was tampered with
       bad |= kPoolBadRequest;
       run.y = p.num_pages - count;
@@ -377,8 +458,16 @@ exl3_status exl3_pages_extend(const exl3_page_pool* pool, int num, const int32_t
   p.block_table = block_table;
   p.positions = positions;
   p.slots = slots;
-  return launch(extend_kernel, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXL3_OK
-                                                                                    : EXL3_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  if ((long long)num * pool->max_pages + 3ll * max_tokens <= kFused) {
+    err = launch(extend_kernel, p, st);
+  } else {
+    err = launch_pdl(extend_plan_kernel, dim3(1), dim3(kThreads), 0, st, p);
+    if (err == cudaSuccess) err = launch_pdl(extend_fill_kernel, dim3(2 * kSms), dim3(kThreads), 0, st, p);
+    note_launches(2);
+  }
+  return err == cudaSuccess ? EXL3_OK : EXL3_ERR_CUDA;
 }
 
 exl3_status exl3_pages_trim(const exl3_page_pool* pool, int num, const int32_t* seqs,

@@ -6,10 +6,10 @@
 // cumulative weight exceeds sample_u times the total.
 //
 // Both decisions are exact.  u q is a product of two 24-bit values, formed in
-// 64 bits; weights are summed as 64-bit integers in units of 2^-56 (what is
-// above 2^-32 is held whole, a row of 2^18 tokens loses at most 2^-38), so the
-// order of a sum does not matter, and no border between two tokens moves with
-// the split of a row over threads.
+// 64 bits; weights are summed as 64-bit integers in units of 2^-46, so the order
+// of a sum does not matter, and no border between two tokens moves with the split
+// of a row over threads.  (What is above 2^-22 is held whole; over a row of 2^17
+// tokens the roundings of the others come to about 2^-38 of it.)
 //
 // One row of p (and of q) per sequence is all that has to be read: memory
 // bounds large batches, the chain of loads (bounds, drafts, their
@@ -23,8 +23,12 @@
 namespace exl3 {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kUnroll = 8;  // loads of a row in flight per thread
+constexpr int kThreads = 256, kWarps = kThreads / 32, kPerSm = 1024 / kThreads;
+// of a cluster, one cluster per sequence.  64 pairs of rows of 131072 fp32 (floor 10
+// us): 16.9 us; 16 CTAs of 128 threads as fast, 16 of 256 and 8 of 128 slower
+constexpr int kCtas = 8;
+constexpr int kGroups = 8;  // parts of a warp's run whose sums are kept
+constexpr int kUnroll = 4;  // 16-byte loads of p (and of q) in flight per thread
 
 struct VerifyParams {
   const void* p;
@@ -46,37 +50,188 @@ __device__ __forceinline__ float value(const void* x, int64_t i) {
   return load_act(x, DT == EXL3_BF16, (size_t)i);
 }
 
-// A probability in units of 2^-56; NaN and what is negative count as 0.
-__device__ __forceinline__ unsigned long long fixed(float x) {
-  return x > 0.0f ? __float2ull_rz(fminf(x, 1.0f) * 0x1p56f) : 0ull;
+// A probability x rounded to units of 2^-46, h 2^23 + l, as the low bits of two
+// floats: each a sum with a power of two (and a half, for signed ones) that leaves
+// a step of 1; what the first leaves over is exact.  NaN and what is negative
+// count as 0.  (Conversions to integers issue at an eighth of the rate.)
+struct Limbs {
+  uint32_t h, l;
+};
+constexpr float kH = 0x1p23f, kL = 0x1.8p23f;
+__device__ __forceinline__ Limbs limbs(float x) {
+  const float y = __saturatef(x);
+  const float h = fmaf(y, 0x1p23f, kH);
+  const float r = fmaf(y, 0x1p23f, -(h - kH));
+  return Limbs{__float_as_uint(h), __float_as_uint(fmaf(r, 0x1p23f, kL))};
 }
 
-__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+__device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
 }
 
-// The weights of one row: p, or max(p - q, 0), or p without one token.
+// The weights of one row: p, or max(p - q, 0), or p without one token.  Chunks
+// are the 16-byte pieces of p's memory: token v is element v + shift of them.
 template <int DT>
 struct Row {
-  const void* p;
-  const void* q;
-  int64_t p0, q0;
-  int skip;  // -1: none
-  __device__ __forceinline__ unsigned long long at(int v) const {
-    unsigned long long w = fixed(value<DT>(p, p0 + v));
-    if (q) {
-      const unsigned long long x = fixed(value<DT>(q, q0 + v));
-      w = w > x ? w - x : 0;
+  static constexpr int kSize = DT == EXL3_F32 ? 4 : 2, VEC = 16 / kSize;
+  const uint8_t* p;  // the first chunk
+  const uint8_t* q;  // the same tokens of q, or null
+  int shift, vocab;
+  int skip;          // a token without weight, -1: none
+  int inner0, inner_n;  // the chunks that are the row's whole
+  bool q_aligned;
+  struct Chunk {
+    uint4 p, q;
+  };
+  // element i of a chunk's 16 bytes
+  static __device__ __forceinline__ float element(const uint4& w, int i) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    if (DT == EXL3_F32) return __uint_as_float(x[i]);
+    if (DT == EXL3_BF16)
+      return __uint_as_float(i & 1 ? x[i >> 1] & 0xFFFF0000u : x[i >> 1] << 16);
+    return __half2float(__ushort_as_half((unsigned short)(x[i >> 1] >> (16 * (i & 1)))));
+  }
+  // the elements [lo, hi) of 16 bytes that need not be aligned, 0 for the others
+  static __device__ __forceinline__ uint4 pieces(const uint8_t* at, int lo, int hi) {
+    uint32_t x[4] = {};
+#pragma unroll
+    for (int i = 0; i < VEC; i++)
+      if (i >= lo && i < hi) {
+        if (DT == EXL3_F32)
+          x[i] = __ldg(reinterpret_cast<const uint32_t*>(at) + i);
+        else
+          x[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(at) + i) << (16 * (i & 1));
+      }
+    return make_uint4(x[0], x[1], x[2], x[3]);
+  }
+  template <bool Q>
+  __device__ __forceinline__ Chunk load(int c, int end) const {
+    Chunk x;
+    x.p = x.q = make_uint4(0, 0, 0, 0);
+    if (c >= end) return x;
+    const int64_t at = (int64_t)c * 16;
+    const bool inner = (unsigned)(c - inner0) < (unsigned)inner_n;
+    const int lo = inner ? 0 : shift - c * VEC, hi = inner ? VEC : lo + vocab;
+    if (inner)
+      x.p = __ldg(reinterpret_cast<const uint4*>(p + at));
+    else
+      x.p = pieces(p + at, lo, hi);
+    if (Q) {
+      if (inner && q_aligned)
+        x.q = __ldg(reinterpret_cast<const uint4*>(q + at));
+      else
+        x.q = pieces(q + at, lo, hi);
     }
-    return v == skip ? 0 : w;
+    return x;
+  }
+  // adds the weight of element i of chunk c, limb by limb
+  template <bool Q>
+  __device__ __forceinline__ void add(const Chunk& x, int c, int i, Limbs& sum) const {
+    const float a = element(x.p, i);
+    const Limbs w = limbs(a);
+    Limbs minus{__float_as_uint(kH), __float_as_uint(kL)};
+    bool some = c * VEC + i != skip + shift;
+    if (Q) {
+      const float b = element(x.q, i);
+      minus = limbs(b);
+      some = __saturatef(a) > __saturatef(b);
+    }
+    if (some) {
+      sum.h += w.h - minus.h;
+      sum.l += w.l - minus.l;
+    }
+  }
+  static __device__ __forceinline__ long long whole(const Limbs& x) {
+    return ((long long)(int)x.h << 23) + (int)x.l;
+  }
+  // the weight of a chunk
+  template <bool Q>
+  __device__ __forceinline__ long long weigh(const Chunk& x, int c) const {
+    Limbs sum{0, 0};
+#pragma unroll
+    for (int i = 0; i < VEC; i++) add<Q>(x, c, i, sum);
+    return whole(sum);
+  }
+  // the sums of a warp's groups of `per` loads by lane, to `sums`, and of all
+  // `loads` of them
+  template <bool Q>
+  __device__ __forceinline__ long long sum(int c0, int loads, int per, int end, int lane,
+                                           long long (*sums)[32]) const {
+    long long all = 0, s = 0;
+    int left = per, g = 0;
+    // the loads whose chunks are all the row's whole, and aligned
+    const int lo = c0 < inner0 ? 1 : 0;
+    const int hi = Q && !q_aligned ? 0 : (min(inner0 + inner_n, end) - c0) / 32;
+    const uint8_t* pl = p + (int64_t)(c0 + lane) * 16;
+    const int64_t to_q = q - p;
+#pragma unroll 1
+    for (int it = 0; it < loads; it += kUnroll, pl += kUnroll * 512) {
+      Chunk x[kUnroll];
+      if (it >= lo && it + kUnroll <= hi) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++) {
+          x[u].p = __ldg(reinterpret_cast<const uint4*>(pl + u * 512));
+          if (Q) x[u].q = __ldg(reinterpret_cast<const uint4*>(pl + to_q + u * 512));
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++)  // (nothing past the run: `end` is its end)
+          x[u] = load<Q>(c0 + (it + u) * 32 + lane, end);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; u++) {
+        s += weigh<Q>(x[u], c0 + (it + u) * 32 + lane);
+        if (--left == 0) {
+          if (g < kGroups) sums[g][lane] = s;
+          g++;
+          all += s;
+          s = 0;
+          left = per;
+        }
+      }
+    }
+    if (g < kGroups) sums[g][lane] = s;
+    return all + s;
+  }
+  // the first token of the chunks c0 .. whose cumulative weight is above want
+  // (less than what they weigh), in every lane that finds it; -1 in the others
+  template <bool Q>
+  __device__ __forceinline__ int find(int c0, int per, int end, int lane, long long want) const {
+#pragma unroll 1
+    for (int it = 0; it < per; it++) {
+      const int c = c0 + it * 32 + lane;
+      const Chunk x = load<Q>(c, end);
+      const long long mine = weigh<Q>(x, c);
+      long long inc = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+        if (lane >= m) inc += o;
+      }
+      if (__any_sync(0xffffffffu, inc > want)) {
+        if (!(inc > want && inc - mine <= want)) return -1;
+        long long s = inc - mine;
+        int v = -1;
+#pragma unroll
+        for (int i = 0; i < VEC; i++) {
+          Limbs w{0, 0};
+          add<Q>(x, c, i, w);
+          s += whole(w);
+          if (v < 0 && s > want) v = c * VEC + i - shift;
+        }
+        return v;
+      }
+      want -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return -1;
   }
 };
 
-__device__ __forceinline__ unsigned long long load_remote(unsigned long long* at, int rank) {
+__device__ __forceinline__ long long load_remote(long long* at, int rank) {
   uint32_t a;
-  unsigned long long v;
+  long long v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
@@ -86,13 +241,39 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 
+// The token of a row that weighs `all` (`before` of it in the CTAs before this
+// one): the first v with a cumulative weight above u * all.  The one warp whose
+// run holds it writes it to place `at`.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) verify_kernel(VerifyParams p, int ctas) {
-  __shared__ unsigned long long total[2];         // of this CTA, by pass
-  __shared__ unsigned long long warp_total[kWarps];
+__device__ __forceinline__ void draw(const VerifyParams& p, const Row<DT>& row, int at, int b,
+                                     int first, int per, int last, long long all, long long before,
+                                     const long long* warp_total, const long long (*sums)[32]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float u = fminf(fmaxf(__ldg(p.sample_u + b), 0.0f), 1.0f - 0x1p-24f);
+  long long want =
+      (long long)__umul64hi(__float2ull_rz(u * 0x1p64f), (unsigned long long)all) - before;
+  for (int w = 0; w < warp; w++) want -= warp_total[w];
+  if (want < 0 || want >= warp_total[warp]) return;
+  int g = 0;
+  for (; g < kGroups - 1; g++) {
+    const long long t = warp_sum(sums[g][lane]);
+    if (want < t) break;
+    want -= t;
+  }
+  const int c = first + g * per * 32;
+  const int v = row.q ? row.template find<true>(c, per, last, lane, want)
+                      : row.template find<false>(c, per, last, lane, want);
+  if (v >= 0) p.tokens[at] = v;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyParams p) {
+  __shared__ long long total[2];  // of this CTA, by pass
+  __shared__ long long warp_total[kWarps];
+  __shared__ long long sums[kWarps][kGroups][32];
   __shared__ int s_accepted;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  const int b = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;
   pdl_wait();
   const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
   const bool good = c0 >= 0 && c1 >= c0 && c1 <= p.drafts;
@@ -140,33 +321,48 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyParams p, int ct
   }
   if (!good) return;  // (the whole cluster: it waits for no one)
 
-  // ---- the row's weights: this CTA's piece, a run of it per warp
+  // ---- the row's weights: a run of chunks per warp
   Row<DT> row;
-  row.p = p.p;
-  row.p0 = (int64_t)(c0 + a + b) * p.p_stride;
-  row.q = a < d ? p.q : nullptr;
-  row.q0 = (int64_t)(c0 + a) * p.q_stride;
+  row.vocab = p.vocab;
   row.skip = a < d && !p.q ? __ldg(p.draft + c0 + a) : -1;
-  const int run = ((p.vocab + ctas * kWarps - 1) / (ctas * kWarps) + 31) & ~31;
-  const int v0 = min((rank * kWarps + warp) * run, p.vocab), v1 = min(v0 + run, p.vocab);
-  unsigned long long all = 0, before = 0;
+  row.p = static_cast<const uint8_t*>(p.p) + (int64_t)(c0 + a + b) * p.p_stride * row.kSize;
+  row.shift = (int)(reinterpret_cast<uintptr_t>(row.p) & 15) / row.kSize;
+  row.p -= row.shift * row.kSize;
+  row.q = nullptr;
+  row.q_aligned = false;
+  if (a < d && p.q) {
+    row.q = static_cast<const uint8_t*>(p.q) + (int64_t)(c0 + a) * p.q_stride * row.kSize -
+            row.shift * row.kSize;
+    row.q_aligned = (reinterpret_cast<uintptr_t>(row.q) & 15) == 0;
+  }
+  const int end = (row.shift + p.vocab + row.VEC - 1) / row.VEC;  // chunks
+  row.inner0 = row.shift > 0;
+  row.inner_n = max((row.shift + p.vocab) / row.VEC - row.inner0, 0);
+  // `per` of a run's loads are a group (short rows have fewer groups)
+  constexpr int kAll = kCtas * kWarps;
+  const int loads = (end + kAll * 32 - 1) / (kAll * 32);
+  const int per = (loads + kGroups - 1) / kGroups;
+  const int run = loads * 32;
+  const int first = (rank * kWarps + warp) * run, last = min(first + run, end);
+  long long all = 0, before = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; pass++) {
-    unsigned long long sum = 0;
-#pragma unroll kUnroll
-    for (int v = v0 + lane; v < v1; v += 32) sum += row.at(v);
-    sum = warp_sum(sum);
+    const long long sum =
+        warp_sum(row.q ? row.template sum<true>(first, loads, per, last, lane, sums[warp])
+                       : row.template sum<false>(first, loads, per, last, lane, sums[warp]));
     if (lane == 0) warp_total[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-      unsigned long long t = 0;
+      long long t = 0;
+#pragma unroll
       for (int w = 0; w < kWarps; w++) t += warp_total[w];
       total[pass] = t;
     }
     cluster_sync();
     all = before = 0;
-    for (int r = 0; r < ctas; r++) {
-      const unsigned long long t = load_remote(&total[pass], r);
+#pragma unroll
+    for (int r = 0; r < kCtas; r++) {
+      const long long t = load_remote(&total[pass], r);
       if (r < rank) before += t;
       all += t;
     }
@@ -175,47 +371,28 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyParams p, int ct
     row.q = nullptr;
     row.skip = -1;
   }
-  // no CTA leaves while another may read its sums
-  cluster_sync();
-
-  // ---- the token: the first v with a cumulative weight above u * all
-  const float u = fminf(fmaxf(__ldg(p.sample_u + b), 0.0f), 1.0f - 0x1p-24f);
-  const unsigned long long want = __umul64hi(__float2ull_rz(u * 0x1p64f), all);
-  if (all == 0) return;
-  for (int w = 0; w < warp; w++) before += warp_total[w];
-  if (want < before || want - before >= warp_total[warp]) return;
-  for (int v = v0; v < v1; v += 32) {
-    unsigned long long inc = v + lane < v1 ? row.at(v + lane) : 0;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const unsigned long long o = __shfl_up_sync(0xffffffffu, inc, m);
-      if (lane >= m) inc += o;
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, before + inc > want);
-    if (m) {
-      if (lane == 0) p.tokens[c0 + b + a] = v + __ffs(m) - 1;
-      return;
-    }
-    before += __shfl_sync(0xffffffffu, inc, 31);
-  }
+  // (no CTA leaves while another may read its sums: waited for at the end)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (all > 0) draw(p, row, c0 + b + a, b, first, per, last, all, before, warp_total, sums[warp]);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int DT>
 cudaError_t launch(const VerifyParams& p, cudaStream_t st) {
-  constexpr int ctas = 8;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.num_seqs * ctas);
+  cfg.gridDim = dim3((unsigned)p.num_seqs * kCtas);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = kCtas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<DT>, p, ctas);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<DT>, p);
   note_launches(1);
   return e;
 }

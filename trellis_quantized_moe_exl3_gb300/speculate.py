@@ -25,47 +25,26 @@ _PROBS = {torch.float16: _lib.EXL3_F16, torch.bfloat16: _lib.EXL3_BF16,
           torch.float32: _lib.EXL3_F32}
 
 
+def _outputs(stream, device, *of):
+    """New tensors of the shapes and types `of`.  (A tensor each: views of one
+    take longer to make than their memory.)"""
+    if stream is None:
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in of]
+    return [_empty(shape, dtype, device, stream) for shape, dtype in of]
+
+
 class PagedStep(PagedBatch):
     """A step as PagePool.extend lays it out: a PagedBatch (cu_q, seq_lens,
     block_table) with positions [max_tokens] int32 and slots [max_tokens] int64
     (page * page_size + place) of its new tokens, -1 in rows that are none's."""
 
-    def __init__(self, buf, num, max_q, max_tokens, max_pages):
-        self._buf, self._max_pages, self.max_tokens = buf, max_pages, max_tokens
-        self.num_seqs, self.max_q = num, int(max_q)
-        self._at = a = _places(num, max_tokens)
-        p = buf.data_ptr()
-        d = _lib.KVBatch()
-        d.num_seqs, d.max_q, d.max_pages, d.table_stride = num, self.max_q, max_pages, max_pages
-        d.cu_q, d.seq_lens, d.block_table = p + 4 * a[1], p + 4 * a[2], p + 4 * a[3]
-        self._d, self._ref = d, ctypes.byref(d)
-
-    @property
-    def slots(self):
-        return self._buf[:2 * self.max_tokens].view(torch.int64)
-
-    @property
-    def positions(self):
-        return self._buf[self._at[0]:self._at[0] + self.max_tokens]
-
-    @property
-    def cu_q(self):
-        return self._buf[self._at[1]:self._at[1] + self.num_seqs + 1]
-
-    @property
-    def seq_lens(self):
-        return self._buf[self._at[2]:self._at[2] + self.num_seqs]
-
-    @property
-    def block_table(self):
-        return self._buf[self._at[3]:].view(self.num_seqs, self._max_pages)
-
-
-def _places(num, max_tokens):
-    """Where positions, cu_q, seq_lens and block_table begin in a step's buffer
-    (32-bit words; slots come first, the table last and aligned)."""
-    cu = 3 * max_tokens
-    return 2 * max_tokens, cu, cu + num + 1, (cu + 2 * num + 1 + 3) & ~3
+    def __init__(self, cu_q, seq_lens, block_table, positions, slots, max_q):
+        self.cu_q, self.seq_lens, self.block_table = cu_q, seq_lens, block_table
+        self.positions, self.slots = positions, slots
+        self.num_seqs, self.max_q = block_table.shape[0], max_q
+        self._d = d = _lib.KVBatch(self.num_seqs, max_q, block_table.shape[1], block_table.shape[1],
+                                   cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr())
+        self._ref = ctypes.byref(d)
 
 
 class PagePool:
@@ -122,14 +101,16 @@ class PagePool:
             _dense(q_lens, "q_lens", torch.int32, (n,))
         if max_tokens < 0:
             raise ValueError("max_tokens must not be negative")
-        a = _places(n, max_tokens)
-        buf = _empty((a[3] + n * self.max_pages,), torch.int32, seqs.device, stream)
-        step = PagedStep(buf, n, max_q, max_tokens, self.max_pages)
-        p, d = buf.data_ptr(), step._d
+        cu_q, seq_lens, table, positions, slots = _outputs(
+            stream, seqs.device, ((n + 1,), torch.int32), ((n,), torch.int32),
+            ((n, self.max_pages), torch.int32), ((max_tokens,), torch.int32),
+            ((max_tokens,), torch.int64))
+        step = PagedStep(cu_q, seq_lens, table, positions, slots, int(max_q))
+        d = step._d
         check(_lib.lib().exl3_pages_extend(
             self._ref, n, seqs.data_ptr(), q_lens.data_ptr(), max_tokens, d.cu_q, d.seq_lens,
-            d.block_table, p + 4 * a[0], p, self._ws, self._ws_bytes, _stream(stream, seqs)),
-            "exl3_pages_extend")
+            d.block_table, positions.data_ptr(), slots.data_ptr(), self._ws, self._ws_bytes,
+            _stream(stream, seqs)), "exl3_pages_extend")
         return step
 
     def trim(self, seqs, drop=None, stream=None):
@@ -200,13 +181,12 @@ def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None):
         if q.dtype != p.dtype:
             raise ValueError("p and q must have the same dtype")
         qp = q.data_ptr() if D else None
-    dev = p.device
-    tokens = _empty((D + B,), torch.int32, dev, stream)
-    accepted, dropped = _empty((B,), torch.int32, dev, stream), _empty((B,), torch.int32, dev, stream)
-    check(_lib.lib().exl3_verify_drafts(
-        p.data_ptr(), ps, qp, qs, _PROBS[p.dtype], vocab, B, D,
-        _vector(cu_draft, "cu_draft", torch.int32, B + 1), _vector(draft, "draft", torch.int32, D),
-        _vector(accept_u, "accept_u", torch.float32, D),
-        _vector(sample_u, "sample_u", torch.float32, B), tokens.data_ptr(), accepted.data_ptr(),
-        dropped.data_ptr(), _stream(stream, p)), "exl3_verify_drafts")
+    args = (p.data_ptr(), ps, qp, qs, _PROBS[p.dtype], vocab, B, D,
+            _vector(cu_draft, "cu_draft", torch.int32, B + 1),
+            _vector(draft, "draft", torch.int32, D), _vector(accept_u, "accept_u", torch.float32, D),
+            _vector(sample_u, "sample_u", torch.float32, B))
+    tokens, accepted, dropped = _outputs(stream, p.device, ((D + B,), torch.int32),
+                                         ((B,), torch.int32), ((B,), torch.int32))
+    check(_lib.lib().exl3_verify_drafts(*args, tokens.data_ptr(), accepted.data_ptr(),
+                                        dropped.data_ptr(), _stream(stream, p)), "exl3_verify_drafts")
     return tokens, accepted, dropped
