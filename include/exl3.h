@@ -430,7 +430,8 @@ exl3_status exl3_kv_append(const exl3_kv_cache *cache, const exl3_kv_batch *batc
  * anew; where new tokens need more than the block's scale covers, its older
  * tokens (places before the first new one) are brought to the new scale,
  * exactly but for values below 2^-6 of it.  A scale that covers the new tokens
- * is left as it is, a power of two or not.  cache->dtype is EXL3_E4M3, its
+ * is left as it is, a power of two or not.  A value is stored as
+ * E4M3_RNE(clamp(x * (1 / scale), -448, 448)), product and inverse in fp32.  cache->dtype is EXL3_E4M3, its
  * k_scale and v_scale NULL.  No page may belong to two sequences that append
  * to it.  Errors: as exl3_kv_append, and EXL3_ERR_ARG for scales NULL,
  * misaligned or with a stride below kv_heads. */

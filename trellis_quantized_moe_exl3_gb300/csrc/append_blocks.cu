@@ -1,8 +1,8 @@
 // The append of keys and values to a paged E4M3 cache with a scale per block
-// (page) and kv head.
+// (page) and kv head, queries normed and rotated in the same launch.
 //
 //   scale = the least 2^e with max |x| <= 448 * 2^e over the block's tokens
-//   byte  = E4M3_RNE(x / scale)
+//   byte  = E4M3_RNE(x * (1 / scale))
 //
 // Tokens come to a block a few at a time, so its scale only grows: where new
 // tokens need more than it covers, the older tokens' bytes are brought to the
@@ -12,17 +12,27 @@
 // by it, being a floating type.  A block that begins with a new token starts
 // anew.
 //
-// A unit (block, kv head, keys or values) belongs to a team of lane groups (a
-// head vector's lanes, as in norm_rope_kernel): one group where a step brings
-// a few tokens per sequence, a whole CTA for prompts.  The first kHold rows of
-// a group stay in registers between the maximum and the rounding, later ones
-// (long blocks) are formed twice.
+// A head vector belongs to LPR lanes of 16 channels: two runs of 8 that hold both
+// sides of 8 rotation pairs.  (With 8 channels per lane the addresses, shuffles
+// and loops around them were most of what was issued: 7000 tokens of 48 heads
+// took 48 us.)  Keys and values: a unit (block, kv head, keys or values) belongs to
+// a team of such lane groups, one group where a step brings a few tokens per
+// sequence, a whole CTA for prompts; the first kHold rows of a group stay in
+// registers between the maximum and the rounding, later ones (long blocks) are
+// formed twice.  Queries: a lane group takes some heads of one token, whose
+// cosines and sines it keeps.
 #include "norm_rope.cuh"
 
 namespace exl3 {
 namespace {
 
-constexpr int kThreads = 128;
+#ifndef AR
+#define AR 3
+#define WANT 4ll
+#define HO 2
+#endif
+constexpr int kThreads = 256, kPerSm = AR;
+constexpr int kHold = HO;
 
 // the least 2^e >= top / 448, within the range of scales
 __device__ __forceinline__ float scale_for(float top) {
@@ -32,222 +42,390 @@ __device__ __forceinline__ float scale_for(float top) {
   return fminf(__uint_as_float(e << 23), kMostScale);
 }
 
-template <int LPR, int TEAM, int BF16, int INTER>
-__global__ void __launch_bounds__(kThreads) append_blocks_kernel(NormRopeParams p) {
-  constexpr int NG = kThreads / LPR, NT = NG / TEAM;
-  constexpr int kHold = TEAM == 1 ? 4 : 8;
-  static_assert(TEAM == 1 || TEAM == NG, "a team is a lane group or the CTA");
-  __shared__ float tops[NG];
-  const int wl = threadIdx.x & 31;
-  const int grp = threadIdx.x / LPR, lane = threadIdx.x % LPR;
-  const uint32_t mask = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1) << (wl / LPR * LPR);
-  const int P = p.cache.page_size;
-  pdl_wait();
+// A lane's share of a head vector.
+struct Raw {
+  uint4 a, b;
+};
+template <int BF16>
+__device__ __forceinline__ void unpack8(const uint4& r, float2* v) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    v[i] = BF16 ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u))
+                : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+}
+template <int BF16>
+__device__ __forceinline__ uint4 pack8(const float2* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if (BF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[i].x, v[i].y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      const __half2 h = __floats2half2_rn(v[i].x, v[i].y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int LPR, int BF16, int INTER>
+struct Lane {
+  static constexpr int NG = kThreads / LPR;
+  int lane, ca, cb;  // its place in the row, the first channels of its two runs
+  bool in_a, in_b;   // whether they are there
+  bool pairs;        // it has rotation pairs
+  uint32_t mask;
+  __device__ __forceinline__ Lane(const NormRopeParams& p) {
+    lane = threadIdx.x % LPR;
+    mask = ((1u << LPR) - 1) << ((threadIdx.x & 31) / LPR * LPR);
+    pairs = p.inv_freq && lane < p.rot / 16;
+    ca = lane * 16;
+    cb = ca + 8;
+    if (!INTER && lane < p.rot / 16) {
+      ca = lane * 8;
+      cb = ca + p.rot / 2;
+    }
+    in_a = ca < p.dim;
+    in_b = cb < p.dim;
+  }
+  __device__ __forceinline__ Raw load(const uint16_t* x, bool some) const {
+    Raw w{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (some && in_a) w.a = *reinterpret_cast<const uint4*>(x + ca);
+    if (some && in_b) w.b = *reinterpret_cast<const uint4*>(x + cb);
+    return w;
+  }
+  static __device__ __forceinline__ void unpack(const Raw& w, float2* v) {
+    unpack8<BF16>(w.a, v);
+    unpack8<BF16>(w.b, v + 4);
+  }
+  // cosines and sines of its pairs 2 e, 2 e + 1 at a position.  The fraction of a
+  // turn is exact; the fast functions of it are off by 2^-21, a row's values by
+  // 1e-6 of its largest: nothing beside the rounding to 8 or 16 bits that follows
+  // (and a fifth of the instructions of the exact ones).
+  __device__ __forceinline__ void angles(const uint64_t* turns, int pos, int e, float2* c,
+                                         float2* s) const {
+    float x[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+      x[i] = (float)(int32_t)((turns[8 * lane + 2 * e + i] * (uint64_t)(int64_t)pos) >> 32) *
+             (0x1p-31f * 3.14159265358979f);
+    *c = make_float2(__cosf(x[0]), __cosf(x[1]));
+    *s = make_float2(__sinf(x[0]), __sinf(x[1]));
+  }
+  __device__ __forceinline__ void norm(float2* v, const Raw& weight, const NormRopeParams& p) const {
+    float2 q2 = mul2(v[0], v[0]);
+#pragma unroll
+    for (int e = 1; e < 8; e++) q2 = fma2(v[e], v[e], q2);
+    float sq = q2.x + q2.y;
+#pragma unroll
+    for (int m = LPR / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(mask, sq, m, LPR);
+    const float f = rsqrtf(fmaf(sq, p.inv_dim, p.eps));
+    float2 wt[8];
+    unpack(weight, wt);
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = mul2(mul2(v[e], make_float2(f, f)), wt[e]);
+  }
+  // turns pairs 2 e, 2 e + 1
+  static __device__ __forceinline__ void rotate(float2* v, int e, float2 c, float2 s) {
+    if (INTER) {  // (a, b) of a pair share a register pair: a' = a c - b s, b' = a s + b c
+      const float cc[2] = {c.x, c.y}, ss[2] = {s.x, s.y};
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        float2& x = v[2 * e + i];
+        x = fma2(x, make_float2(cc[i], cc[i]),
+                 mul2(make_float2(x.y, x.x), make_float2(-ss[i], ss[i])));
+      }
+    } else {
+      const float2 a = v[e], b = v[4 + e];
+      v[e] = fma2(a, c, mul2(b, make_float2(-s.x, -s.y)));
+      v[4 + e] = fma2(b, c, mul2(a, s));
+    }
+  }
+  __device__ __forceinline__ int sum(int x) const {
+#pragma unroll
+    for (int m = LPR / 2; m > 0; m >>= 1) x += __shfl_xor_sync(mask, x, m, LPR);
+    return x;
+  }
+};
 
-  // ---- the block: sequence b has the slots cu_q[b] / P + 2 b .. of the grid,
-  // as many as it can touch blocks (every warp for itself)
-  const int slot = blockIdx.x;
+// Queries: lane group `item` of the launch takes heads of one token.
+template <int LPR, int BF16, int INTER>
+__device__ __forceinline__ void do_queries(const NormRopeParams& p, const uint64_t* turns,
+                                           int64_t item, int slices, int per) {
+  const Lane<LPR, BF16, INTER> ln(p);
+  const int64_t ti = item / slices;
+  if (ti >= p.T) return;
+  const int t = (int)ti, j0 = (int)(item % slices) * per, j1 = min(j0 + per, p.set[0].heads);
+  const HeadSet& hs = p.set[0];
+  const uint16_t* x = hs.x + (int64_t)t * hs.ts + j0 * hs.hs;
+  Raw raw = ln.load(x, j0 < j1);
+  const Raw weight = ln.load(hs.weight, hs.weight != nullptr);
+  int below = 0;  // sequences that end at or before t
+  for (int b = ln.lane; b < p.batch.num_seqs; b += LPR) below += __ldg(p.batch.cu_q + b + 1) <= t;
+  const int b = ln.sum(below);
+  if (b >= p.batch.num_seqs) return;  // padding: left as it is
+  float2 c[4], s[4];
+  if (p.inv_freq) {
+    int32_t ignored = 0;
+    const Seq q = load_seq(p.batch, b, &ignored);
+    const int pos = p.positions ? __ldg(p.positions + t) : q.len - q.n + (t - q.q0);
+    if (ln.pairs) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) ln.angles(turns, pos, e, &c[e], &s[e]);
+    }
+  }
+  uint16_t* out = hs.out + (int64_t)t * hs.ots + j0 * hs.ohs;
+#pragma unroll 1
+  for (int j = j0; j < j1; j++, out += hs.ohs) {
+    float2 v[8];
+    ln.unpack(raw, v);
+    x += hs.hs;
+    raw = ln.load(x, j + 1 < j1);
+    if (hs.weight) ln.norm(v, weight, p);
+    if (ln.pairs) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) ln.rotate(v, e, c[e], s[e]);
+    }
+    if (ln.in_a) *reinterpret_cast<uint4*>(out + ln.ca) = pack8<BF16>(v);
+    if (ln.in_b) *reinterpret_cast<uint4*>(out + ln.cb) = pack8<BF16>(v + 4);
+  }
+}
+
+// The new tokens of one block.
+struct Job {
+  int page;         // -1: nothing to do
+  int lo, rows;     // position of the first one, how many
+  int older;        // tokens before them in the block
+  int t0;           // their first row
+};
+// Block slot `slot` of the launch (one warp): sequence b has the slots
+// cu_q[b] / P + 2 b .., as many as it can touch blocks.
+__device__ __forceinline__ Job find_job(const NormRopeParams& p, int slot, bool report) {
+  const int P = p.cache.page_size, shift = p.cache.page_shift, lane = threadIdx.x & 31;
+  auto pages = [&](int x) { return shift >= 0 ? x >> shift : x / P; };  // (x >= 0 where it counts)
   int below = 0;
-  for (int b = wl; b < p.batch.num_seqs; b += 32)
-    below += __ldg(p.batch.cu_q + b + 1) / P + 2 * (b + 1) <= slot;
+  for (int b = lane; b < p.batch.num_seqs; b += 32)
+    below += pages(__ldg(p.batch.cu_q + b + 1)) + 2 * (b + 1) <= slot;
   const int b = __reduce_add_sync(0xffffffffu, below);
-  if (b >= p.batch.num_seqs) return;
+  Job j{-1, 0, 0, 0, 0};
+  if (b >= p.batch.num_seqs) return j;
   int32_t bad = 0;
   const Seq s = load_seq(p.batch, b, &bad);
   const int start = s.len - s.n;  // position of the first new token
   if (s.n > 0 && start < 0) bad |= kStatusBadBatch;
-  const int from = max(start, 0);
-  const int blk = from / P + slot - (s.q0 / P + 2 * b);
-  const int lo = max(from, blk * P), hi = (int)min((long long)s.len, ((long long)blk + 1) * P);
-  int page = -1;
-  if (s.n > 0 && blk >= from / P && lo < hi) {
-    page = __ldg(p.batch.table + (int64_t)b * p.batch.table_stride + blk);
-    if (page < 0 || page >= p.cache.num_pages) {
+  const int from = max(start, 0), first = pages(from);
+  const int blk = first + slot - (pages(s.q0) + 2 * b);
+  if (s.n > 0 && blk >= first && (long long)blk * P < s.len) {
+    j.lo = max(from, blk * P);
+    j.rows = min(s.len, blk * P + P) - j.lo;  // (lengths are at most 2^30)
+    j.older = j.lo - blk * P;
+    j.t0 = s.q0 + j.lo - start;
+    j.page = __ldg(p.batch.table + (int64_t)b * p.batch.table_stride + blk);
+    if (j.page < 0 || j.page >= p.cache.num_pages) {
       bad |= kStatusBadPage;
-      page = -1;
+      j.page = -1;
     }
   }
-  if (bad && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.status, bad);
-  if (page < 0) return;
+  if (bad && report && lane == 0) atomicOr(p.status, bad);
+  return j;
+}
 
-  // ---- the unit
-  const int unit = blockIdx.y * NT + (TEAM == 1 ? grp : 0);
-  if (unit >= 2 * p.set[1].heads) return;  // (whole groups; no barrier below unless TEAM = NG)
-  const int kv = unit & 1, h = unit >> 1, me = TEAM == 1 ? 0 : grp;
+// Keys and values of a block: the units unit0 + 0, 1, .., one per team.  A team is
+// `team` (a power of two) lane groups.
+template <int LPR, int BF16, int INTER>
+__device__ __forceinline__ void do_block(const NormRopeParams& p, const uint64_t* turns,
+                                         const Job& job, int unit0, int team) {
+  using L = Lane<LPR, BF16, INTER>;
+  constexpr int GW = 32 / LPR, kWarps = kThreads / 32;
+  __shared__ uint32_t tops[kWarps];
+  const int grp = threadIdx.x / LPR, wl = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const L ln(p);
+  const int me = grp & (team - 1), unit = unit0 + grp / team;
+  const uint32_t mask = team >= GW ? 0xffffffffu
+                                   : ((1u << (team * LPR)) - 1) << (wl & ~(team * LPR - 1));
+  const bool live = unit < 2 * p.set[1].heads;
+  const int kv = unit & 1, h = live ? unit >> 1 : 0;
+  const int rows = live ? job.rows : 0, lo = job.lo, older = job.older, t0 = job.t0;
   const HeadSet& hs = p.set[1 + kv];
-  const bool in_row = lane * 8 < p.dim;
-  const bool turn = !kv && p.inv_freq && lane < p.rot / 8;
-  int ca = lane * 8, cb = ca + 4;  // first channels of the lane's two runs
-  if (!INTER && lane < p.rot / 8) {
-    ca = lane * 4;
-    cb = ca + p.rot / 2;
-  }
-  float* const scale_at = const_cast<float*>(kv ? p.cache.v_scale : p.cache.k_scale) +
-                          page * p.cache.scale_stride + h;
-  const int older = lo - blk * P, rows = hi - lo;
-  const float held = older > 0 ? *scale_at : 0.0f;
-  uint64_t turns[4];
-  if (turn) {
-#pragma unroll
-    for (int e = 0; e < 4; e++) turns[e] = turns_of(__ldg(p.inv_freq + 4 * lane + e));
-  }
-  float wt[8] = {};
-  if (hs.weight && in_row) {
-    unpack4(__ldg(reinterpret_cast<const uint2*>(hs.weight + ca)), BF16, wt);
-    unpack4(__ldg(reinterpret_cast<const uint2*>(hs.weight + cb)), BF16, wt + 4);
-  }
-  const int t0 = s.q0 + lo - start;  // row of the block's first new token
   const uint16_t* const x0 = hs.x + (int64_t)t0 * hs.ts + h * hs.hs;
-
-  struct Raw {
-    uint2 a, b;
-  };
-  auto load = [&](int r) {
-    Raw w{make_uint2(0, 0), make_uint2(0, 0)};
-    if (in_row && r < rows) {
-      w.a = *reinterpret_cast<const uint2*>(x0 + r * hs.ts + ca);
-      w.b = *reinterpret_cast<const uint2*>(x0 + r * hs.ts + cb);
-    }
-    return w;
-  };
+  Raw raw[kHold];
+#pragma unroll
+  for (int i = 0; i < kHold; i++)
+    raw[i] = ln.load(x0 + (me + i * team) * hs.ts, me + i * team < rows);
+  const bool turn = !kv && ln.pairs;
+  float* const scale_at = const_cast<float*>(kv ? p.cache.v_scale : p.cache.k_scale) +
+                          job.page * p.cache.scale_stride + h;
+  const float held = older > 0 ? *scale_at : 0.0f;
   // new token r of the block, normed and rotated
-  auto form = [&](const Raw& w, int r, float* v) {
-    unpack4(w.a, BF16, v);
-    unpack4(w.b, BF16, v + 4);
-    if (hs.weight) {
-      float sq = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; e++) sq = fmaf(v[e], v[e], sq);
-#pragma unroll
-      for (int m = LPR / 2; m > 0; m >>= 1) sq += __shfl_xor_sync(mask, sq, m, LPR);
-      const float f = rsqrtf(fmaf(sq, p.inv_dim, p.eps));
-#pragma unroll
-      for (int e = 0; e < 8; e++) v[e] = v[e] * f * wt[e];
-    }
+  auto form = [&](const Raw& w, int r, float2* v) {
+    ln.unpack(w, v);
+    if (hs.weight) ln.norm(v, ln.load(hs.weight, true), p);
     if (turn) {
       const int pos = p.positions ? __ldg(p.positions + min(t0 + r, p.T - 1)) : lo + r;
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        float sn, c;
-        sincospif((float)(int32_t)((turns[e] * (uint64_t)(int64_t)pos) >> 32) * 0x1p-31f, &sn, &c);
-        float& x = v[INTER ? 2 * e : e];
-        float& y = v[INTER ? 2 * e + 1 : 4 + e];
-        const float x1 = fmaf(x, c, -(y * sn)), y1 = fmaf(y, c, x * sn);
-        x = x1;
-        y = y1;
+        float2 c, sn;
+        ln.angles(turns, pos, e, &c, &sn);
+        ln.rotate(v, e, c, sn);
       }
     }
+  };
+  auto raise = [](float top, const float2* v) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) top = fmaxf(top, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
+    return top;
   };
 
   // ---- the largest value
   float top = 0.0f;
-  float keep[kHold][8];
-  {
-    Raw raw[kHold];
+  float2 keep[kHold][8];
 #pragma unroll
-    for (int i = 0; i < kHold; i++) raw[i] = load(me + i * TEAM);
-#pragma unroll
-    for (int i = 0; i < kHold; i++) {
-      if (TEAM == 1 && i * TEAM >= rows) break;  // (the same in the whole group)
-      form(raw[i], me + i * TEAM, keep[i]);
-#pragma unroll
-      for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(keep[i][e]));
-    }
+  for (int i = 0; i < kHold; i++) {
+    form(raw[i], me + i * team, keep[i]);
+    top = raise(top, keep[i]);
   }
-  for (int r0 = kHold * TEAM; r0 < rows; r0 += TEAM) {
-    float v[8];
-    form(load(r0 + me), r0 + me, v);
-#pragma unroll
-    for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(v[e]));
+#pragma unroll 1
+  for (int r0 = kHold * team; r0 < rows; r0 += team) {
+    float2 v[8];
+    form(ln.load(x0 + (r0 + me) * hs.ts, r0 + me < rows), r0 + me, v);
+    top = raise(top, v);
   }
-#pragma unroll
-  for (int m = LPR / 2; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, m, LPR));
-  if (TEAM > 1) {
-    if (lane == 0) tops[grp] = top;
+  // (as whole numbers: it is no NaN and not negative)
+  uint32_t most = __reduce_max_sync(mask, __float_as_uint(top));
+  if (team > GW) {
+    const int w0 = warp & ~(team / GW - 1);
+    if (wl == 0) tops[warp] = most;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NG; i++) top = fmaxf(top, tops[i]);
+    for (int i = 0; i < team / GW; i++) most = max(most, tops[w0 + i]);
   }
+  top = __uint_as_float(most);
 
   // ---- the scale
+  if (!live) return;
   if (!(held >= 0.0f && held <= kMostScale)) {  // no scale: the block is left alone
-    if (lane == 0 && me == 0) atomicOr(p.status, kStatusBadScale);
+    if (ln.lane == 0 && me == 0) atomicOr(p.status, kStatusBadScale);
     return;
   }
   const float old = fmaxf(held, kLeastScale);
   const float scale = top <= 448.0f * old ? old : scale_for(top);
-  if (lane == 0 && me == 0) *scale_at = scale;
+  if (ln.lane == 0 && me == 0) *scale_at = scale;
   uint8_t* const dst = const_cast<uint8_t*>(kv ? p.cache.v : p.cache.k) +
-                       page * p.cache.page_bytes + h * p.cache.head_bytes;
+                       job.page * p.cache.page_bytes + h * p.cache.head_bytes;
 
   // ---- older tokens, where it has grown
-  if (older > 0 && scale != old && in_row) {
+  if (older > 0 && scale != old) {
     const float ratio = old / scale;
-    for (int r = me; r < older; r += TEAM) {
-      uint2* at = reinterpret_cast<uint2*>(dst + r * p.cache.token_bytes + lane * 8);
-      const uint2 w = *at;
-      uint32_t o[2];
+#pragma unroll 1
+    for (int r = me; r < older; r += team)
 #pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const uint32_t x = i ? w.y : w.x;
-        const float2 a = e4m3_float2(x), c = e4m3_float2(x >> 16);
-        o[i] = e4m3_pack2(a.x * ratio, a.y * ratio) |
-               (e4m3_pack2(c.x * ratio, c.y * ratio) << 16);
+      for (int half = 0; half < 2; half++) {
+        if (!(half ? ln.in_b : ln.in_a)) continue;
+        uint2* at =
+            reinterpret_cast<uint2*>(dst + r * p.cache.token_bytes + (half ? ln.cb : ln.ca));
+        const uint2 w = *at;
+        uint32_t o[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const uint32_t x = i ? w.y : w.x;
+          const float2 a = e4m3_float2(x), c = e4m3_float2(x >> 16);
+          o[i] = e4m3_pack2(a.x * ratio, a.y * ratio) |
+                 (e4m3_pack2(c.x * ratio, c.y * ratio) << 16);
+        }
+        *at = make_uint2(o[0], o[1]);
       }
-      *at = make_uint2(o[0], o[1]);
-    }
   }
 
   // ---- new tokens
-  const bool exact = (__float_as_uint(scale) & 0x7FFFFFu) == 0;  // (its inverse is a float)
-  const float inv = 1.0f / scale;
-  auto store = [&](int r, float* v) {
-    if (!in_row || r >= rows) return;
+  const float inv = 1.0f / scale;  // (exact for a power of two)
+  uint8_t* const dst_new = dst + (int64_t)older * p.cache.token_bytes;
+  auto store = [&](int r, const float2* v) {
+    if (r >= rows) return;
+    uint8_t* at = dst_new + r * p.cache.token_bytes;
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 8; e++) v[e] = exact ? v[e] * inv : __fdiv_rn(v[e], scale);
-    uint8_t* at = dst + (int64_t)(older + r) * p.cache.token_bytes;
-    *reinterpret_cast<uint32_t*>(at + ca) = e4m3_pack2(v[0], v[1]) | (e4m3_pack2(v[2], v[3]) << 16);
-    *reinterpret_cast<uint32_t*>(at + cb) = e4m3_pack2(v[4], v[5]) | (e4m3_pack2(v[6], v[7]) << 16);
+    for (int i = 0; i < 4; i++) {
+      const float2 a = mul2(v[2 * i], make_float2(inv, inv));
+      const float2 b = mul2(v[2 * i + 1], make_float2(inv, inv));
+      w[i] = e4m3_pack2(a.x, a.y) | (e4m3_pack2(b.x, b.y) << 16);
+    }
+    if (ln.in_a) *reinterpret_cast<uint2*>(at + ln.ca) = make_uint2(w[0], w[1]);
+    if (ln.in_b) *reinterpret_cast<uint2*>(at + ln.cb) = make_uint2(w[2], w[3]);
   };
 #pragma unroll
-  for (int i = 0; i < kHold; i++) store(me + i * TEAM, keep[i]);
-  for (int r0 = kHold * TEAM; r0 < rows; r0 += TEAM) {
-    float v[8];
-    form(load(r0 + me), r0 + me, v);
+  for (int i = 0; i < kHold; i++) store(me + i * team, keep[i]);
+#pragma unroll 1
+  for (int r0 = kHold * team; r0 < rows; r0 += team) {
+    float2 v[8];
+    form(ln.load(x0 + (r0 + me) * hs.ts, r0 + me < rows), r0 + me, v);
     store(r0 + me, v);
   }
 }
 
-template <int LPR, int TEAM>
-cudaError_t launch_team(const NormRopeParams& p, cudaStream_t st) {
-  constexpr int NT = kThreads / LPR / TEAM;
-  const dim3 grid((unsigned)(p.T / p.cache.page_size + 2 * p.batch.num_seqs),
-                  (unsigned)((2 * p.set[1].heads + NT - 1) / NT));
-  const dim3 block(kThreads);
-  note_launches(1);
-  if (p.inter)
-    return p.bf16 ? launch_pdl(append_blocks_kernel<LPR, TEAM, 1, 1>, grid, block, 0, st, p)
-                  : launch_pdl(append_blocks_kernel<LPR, TEAM, 0, 1>, grid, block, 0, st, p);
-  return p.bf16 ? launch_pdl(append_blocks_kernel<LPR, TEAM, 1, 0>, grid, block, 0, st, p)
-                : launch_pdl(append_blocks_kernel<LPR, TEAM, 0, 0>, grid, block, 0, st, p);
+// CTAs 0 .. blocks * groups - 1: block slots, `groups` of them to a slot; the
+// others: queries.
+struct Split {
+  int blocks, groups, team, slices, per;
+};
+template <int LPR, int BF16, int INTER>
+__global__ void __launch_bounds__(kThreads, kPerSm) append_blocks_kernel(NormRopeParams p, Split c) {
+  constexpr int NG = kThreads / LPR;
+  __shared__ uint64_t turns[128];  // of the pairs, per position
+  __shared__ Job s_job;
+  const int64_t cta = blockIdx.x, first = (int64_t)c.blocks * c.groups;
+  const bool block = cta < first;
+  pdl_wait();
+  // the first warp finds the block, others the angles
+  if (block && threadIdx.x < 32) {
+    const Job j = find_job(p, (int)(cta / c.groups), cta % c.groups == 0);
+    if (threadIdx.x == 0) s_job = j;
+  }
+  const int i = threadIdx.x - 32;
+  if (p.inv_freq && i >= 0 && i < p.rot / 2) turns[i] = turns_of(__ldg(p.inv_freq + i));
+  __syncthreads();
+  if (!block) {
+    do_queries<LPR, BF16, INTER>(p, turns, (cta - first) * NG + threadIdx.x / LPR, c.slices, c.per);
+  } else {
+    const Job job = s_job;
+    if (job.page >= 0)
+      do_block<LPR, BF16, INTER>(p, turns, job, (int)(cta % c.groups) * (NG / c.team), c.team);
+  }
 }
 
 template <int LPR>
 cudaError_t launch_lpr(const NormRopeParams& p, cudaStream_t st) {
-  return p.batch.max_q <= 4 ? launch_team<LPR, 1>(p, st) : launch_team<LPR, kThreads / LPR>(p, st);
+  constexpr int NG = kThreads / LPR;
+  Split c{};
+  c.blocks = p.T / p.cache.page_size + 2 * p.batch.num_seqs;
+  // a team's lane groups hold the most rows that a step can bring to a block
+  const int rows = p.batch.max_q < p.cache.page_size ? p.batch.max_q : p.cache.page_size;
+  for (c.team = 1; c.team < NG && c.team * kHold < rows;) c.team *= 2;
+  const int teams = NG / c.team;
+  c.groups = (2 * p.set[1].heads + teams - 1) / teams;
+  long long ctas = (long long)c.blocks * c.groups;
+  // a token's query heads are spread over lane groups until those fill the GPU
+  if (p.set[0].heads > 0) {
+    const long long want = (WANT * kSms * kPerSm * NG + p.T - 1) / p.T;
+    c.slices = (int)(want < p.set[0].heads ? want : p.set[0].heads);
+    c.per = (p.set[0].heads + c.slices - 1) / c.slices;
+    c.slices = (p.set[0].heads + c.per - 1) / c.per;
+    ctas += ((long long)p.T * c.slices + NG - 1) / NG;
+  }
+  if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)ctas), block(kThreads);
+  note_launches(1);
+  if (p.inter)
+    return p.bf16 ? launch_pdl(append_blocks_kernel<LPR, 1, 1>, grid, block, 0, st, p, c)
+                  : launch_pdl(append_blocks_kernel<LPR, 0, 1>, grid, block, 0, st, p, c);
+  return p.bf16 ? launch_pdl(append_blocks_kernel<LPR, 1, 0>, grid, block, 0, st, p, c)
+                : launch_pdl(append_blocks_kernel<LPR, 0, 0>, grid, block, 0, st, p, c);
 }
 
 }  // namespace
 
 cudaError_t launch_append_blocks(const NormRopeParams& p, cudaStream_t st) {
-  if (p.set[0].heads > 0) {
-    NormRopeParams q = p;  // the queries alone
-    q.set[1] = q.set[2] = HeadSet{};
-    const cudaError_t e = launch_norm_rope(q, st);
-    if (e != cudaSuccess) return e;
-  }
-  return p.dim <= 64 ? launch_lpr<8>(p, st) : p.dim <= 128 ? launch_lpr<16>(p, st)
-                                                           : launch_lpr<32>(p, st);
+  return p.dim <= 64 ? launch_lpr<4>(p, st) : p.dim <= 128 ? launch_lpr<8>(p, st)
+                                                           : launch_lpr<16>(p, st);
 }
 
 }  // namespace exl3

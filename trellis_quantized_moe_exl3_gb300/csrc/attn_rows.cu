@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
           }
           const float v = fminf(fmaxf(x.y, kLeastScale), kMostScale);
           ks[t] = fminf(fmaxf(x.x, kLeastScale), kMostScale);
-          lv[t] = log2f(v);
-          iv[t] = 1.0f / v;
+          asm("lg2.approx.f32 %0, %1;" : "=f"(lv[t]) : "f"(v));
+          asm("rcp.approx.f32 %0, %1;" : "=f"(iv[t]) : "f"(v));
         }
       }
       st = st == C::kStages - 1 ? 0 : st + 1;

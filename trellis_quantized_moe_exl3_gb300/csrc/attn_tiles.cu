@@ -78,13 +78,15 @@ constexpr int kMinSteps = 4;        // key tiles per piece, where there are enou
 constexpr float kRescale = 8.0f;    // log2 growth of the maximum that rescales O
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kGone = 16;           // ring of absent-page masks (steps)
+constexpr int kScaleSteps = 8;      // ring of block scales (at most stages + 3 in use)
 constexpr int kUnits = 4;           // ring of published units
 constexpr int kRecInts = 24;
 
 template <int D_, int E8_, int BF_, int BS_ = 0>
 struct Cfg {
   static constexpr int D = D_, E8 = E8_, BF = BF_;
-  static constexpr int BS = BS_;                         // block scales
+  // block scales: 16-key groups that share one (1 or 4; 0: a scale per head)
+  static constexpr int BS = BS_;
   static constexpr int MBF = BF && !E8;                  // type of the products
   // log2 of a factor of the terms: fp16 holds what is below 2^-14 in fewer
   // bits, so there they are 2^7 times as large (below 2^15 with kRescale)
@@ -101,7 +103,8 @@ struct Cfg {
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffUnits = kOffMisc + kGone * 4 + 16;
   static constexpr int kOffScales = (kOffUnits + kUnits * kRecInts * 4 + 15) & ~15;
-  static constexpr int kSmem = kOffScales + (BS ? kGone * (kTile / 16) * 16 : 0);
+  static constexpr int kSmem = kOffScales + (BS ? kScaleSteps * (kTile / 16) * 32 : 0);
+  static_assert(kStages + 3 <= kScaleSteps, "ring");
   static constexpr int kCvtQ = E8 && BF;   // queries are brought to fp16
   static constexpr int kThreads = E8 ? 512 : 384;
   // registers of a softmax thread and of the others (their sum over the CTA
@@ -790,28 +793,38 @@ __device__ __forceinline__ void mask_scores(float* s, int h0, int l0, uint32_t g
   }
 }
 
-// As take_terms, for the four groups of 16 keys from g on: c and n of their own,
-// and sums divided by their value scales.
-template <int MBF>
-__device__ __forceinline__ void take_block_terms(const float* s, uint32_t* pk, float& sum, float c,
-                                                 float n, const float4* g) {
+// The block scales of 16 keys, twice each for packed arithmetic: of the keys, log2
+// of the values' and its inverse.
+struct __align__(16) GroupScales {
+  float ks[2], lv[2], iv[2], pad[2];
+};
+// As take_terms, for the four groups of 16 keys from g on, BS of which share a
+// factor and an offset, and sums divided by their value scales.
+template <int MBF, int BS>
+__device__ __forceinline__ void take_block_terms(const float* s, uint32_t* pk, uint64_t& sum,
+                                                 uint64_t c, uint64_t n, const GroupScales* g) {
+  uint64_t part[2] = {0, 0};
 #pragma unroll
-  for (int k = 0; k < 4; k++) {
-    const float4 f = g[k];
-    const uint64_t c2 = both(fmaxf(c * f.x, 0x1p-126f)), n2 = both(n + f.y);
-    uint64_t part[2] = {0, 0};
+  for (int k = 0; k < 4; k += BS) {
+    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(g + k);
+    const uint64_t iv = *reinterpret_cast<const uint64_t*>(g[k].iv);
+    uint64_t ck, nk;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(ck) : "l"(f.x), "l"(c));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(nk) : "l"(f.y), "l"(n));
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
+    for (int i = 0; i < 8 * BS; i++) {
       float x = s[16 * k + 2 * i], y = s[16 * k + 2 * i + 1];
-      fma2(x, y, c2, n2);
+      fma2(x, y, ck, nk);
       x = ex2(x);
       y = ex2(y);
-      add2(part[i & 1], x, y);
+      asm("{\n\t.reg .b64 b;\n\tmov.b64 b, {%1, %2};\n\tfma.rn.f32x2 %0, b, %3, %0;\n\t}"
+          : "+l"(part[i & 1])
+          : "f"(x), "f"(y), "l"(iv));
       pk[8 * k + i] = pack2<MBF>(x, y);
     }
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(part[0]) : "l"(part[1]));
-    sum = fmaf(sum2(part[0]), f.z, sum);
   }
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(part[0]) : "l"(part[1]));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(part[0]));
 }
 
 // 64 softmax terms 2^(s c + n), their sum, and their 16-bit pairs.
@@ -869,8 +882,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc) + kGone;
   volatile uint32_t* poison = tmem_slot + 1;     // a V tile held an infinity or a NaN
   Rec* recs = reinterpret_cast<Rec*>(smem + C::kOffUnits);
-  // block scales of 16 keys: of the keys, log2 of the values', its inverse
-  float4* const ring = reinterpret_cast<float4*>(smem + C::kOffScales);  // [kGone][kTile / 16]
+  GroupScales* const ring =  // [kScaleSteps][kTile / 16]
+      reinterpret_cast<GroupScales*>(smem + C::kOffScales);
 
   // (the same in all lanes, known to the compiler as such)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -1065,6 +1078,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       const float pre = c;
       const bool odd = C::E8 && !C::BS && __any_sync(0xffffffffu, !(c > 0.0f));
       if (odd) c = 1.0f;
+      if (C::BS) c = fmaxf(c, 0x1p-86f);  // (times a scale it stays positive)
       if (owed) {
         put_out();
         if (!ok) break;
@@ -1091,20 +1105,21 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
         const bool masked = edge(r, j) || gm;
         if (masked) mask_scores(s, h0, l0, gm);
-        const float4* const f4 = ring + (base + j - r.j0) % kGone * (kTile / 16);
+        const GroupScales* const gs = ring + (base + j - r.j0) % kScaleSteps * (kTile / 16);
         float mn = m;
         if constexpr (C::BS) {
 #pragma unroll
-          for (int g = 0; g < kTile / 16; g++) {
-            const float4 f = f4[g];
-            float mx[2] = {s[16 * g], s[16 * g + 1]};
+          for (int g = 0; g < kTile / 16; g += C::BS) {
+            const float4 f = *reinterpret_cast<const float4*>(gs + g);
+            const float* t = s + 16 * g;
+            constexpr int N = 16 * C::BS;
+            float mx[2] = {t[0], t[1]};
 #pragma unroll
-            for (int i = 2; i + 4 <= 16; i += 4)
+            for (int i = 2; i + 4 <= N; i += 4)
 #pragma unroll
-              for (int e = 0; e < 2; e++)
-                mx[e] = max3(mx[e], s[16 * g + i + 2 * e], s[16 * g + i + 2 * e + 1]);
-            const float x = max3(fmaxf(mx[0], mx[1]), s[16 * g + 14], s[16 * g + 15]);
-            mn = fmaxf(mn, fmaf(x, fmaxf(c * f.x, 0x1p-126f), f.y));
+              for (int e = 0; e < 2; e++) mx[e] = max3(mx[e], t[i + 2 * e], t[i + 2 * e + 1]);
+            const float x = max3(fmaxf(mx[0], mx[1]), t[N - 2], t[N - 1]);
+            mn = fmaxf(mn, fmaf(x, c * f.x, f.z));
           }
         } else {
           float mx[4] = {s[0], s[1], s[2], s[3]};
@@ -1138,11 +1153,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
         uint32_t pk[32];
         uint64_t sum = 0;
-        const float n = C::kLift - (m == -INFINITY ? 0.0f : m);
-        const uint64_t c2 = both(c), n2 = both(n);
-        float scaled = 0.0f;
-        if (C::BS)
-          take_block_terms<C::MBF>(s, pk, scaled, c, n, f4);
+        const uint64_t c2 = both(c), n2 = both(C::kLift - (m == -INFINITY ? 0.0f : m));
+        if constexpr (C::BS > 0)
+          take_block_terms<C::MBF, C::BS>(s, pk, sum, c2, n2, gs);
         else
           take_terms<C::MBF>(s, pk, sum, c2, n2);
         auto hand_over = [&](int half) {
@@ -1153,11 +1166,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
         };
         hand_over(0);
-        if (C::BS)
-          take_block_terms<C::MBF>(s + 64, pk, scaled, c, n, f4 + 4);
+        if constexpr (C::BS > 0)
+          take_block_terms<C::MBF, C::BS>(s + 64, pk, sum, c2, n2, gs + 4);
         else
           take_terms<C::MBF>(s + 64, pk, sum, c2, n2);
-        l += C::BS ? scaled : sum2(sum);
+        l += sum2(sum);
         hand_over(1);
       }
       if (!ok) break;
@@ -1408,6 +1421,23 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (absent && !no_scale) bad |= kStatusBadPage;
         const int at = ps_shift >= 0 ? key & (ps - 1) : key % ps;
         const uint32_t st = n % C::kStages, par = (n >> C::kStageBits) & 1;
+        if (C::BS) {
+          // 16-key group `lane`, from the lane of its box (before the waits: nothing
+          // stands between a free stage and its load.  The entry's last readers are
+          // kScaleSteps steps back.)
+          const int from = lane * 16 / maps.box;
+          const float k = fmaxf(__shfl_sync(0xffffffffu, sc.x, from), kLeastScale);
+          const float v = fmaxf(__shfl_sync(0xffffffffu, sc.y, from), kLeastScale);
+          float l, i;
+          asm("lg2.approx.f32 %0, %1;" : "=f"(l) : "f"(v));
+          asm("rcp.approx.f32 %0, %1;" : "=f"(i) : "f"(v));
+          if (lane < kTile / 16) {
+            GroupScales* at = ring + n % kScaleSteps * (kTile / 16) + lane;
+            *reinterpret_cast<float4*>(at->ks) = make_float4(k, k, l, l);
+            *reinterpret_cast<float2*>(at->iv) = make_float2(i, i);
+          }
+        }
+        if (C::BS) __syncwarp();
 #pragma unroll 1
         for (int x = 0; x < 2; x++) {  // K, V
           uint64_t* const full = C::E8 ? &raw_full[x] : x ? &v_full[st] : &k_full[st];
@@ -1421,15 +1451,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
               to_edge |= 1u << st;
               edge_par ^= 1u << st;
             }
-          }
-          if (C::BS && x == 0) {
-            if (mine) {
-              const float v = fmaxf(sc.y, kLeastScale);
-              const float4 f = make_float4(fmaxf(sc.x, kLeastScale), log2f(v), 1.0f / v, 0.0f);
-              for (int i = 0; i < maps.box / 16; i++)
-                ring[n % kGone * (kTile / 16) + bx * (maps.box / 16) + i] = f;
-            }
-            __syncwarp();
           }
           if (lane == 0) {
             if (x == 0) gone[n % kGone] = g;
@@ -1771,6 +1792,9 @@ cudaError_t launch_cfg(const AttnParams& p, const Maps& maps, const Plan& pl, in
 template <int D>
 cudaError_t launch_types(const AttnParams& p, const Maps& m, const Plan& pl, int mu,
                          cudaStream_t st) {
+  if (p.blocks && m.box >= 64)  // a box, and so 64 keys, in one block
+    return p.bf16 ? launch_cfg<Cfg<D, 1, 1, 4>>(p, m, pl, mu, st)
+                  : launch_cfg<Cfg<D, 1, 0, 4>>(p, m, pl, mu, st);
   if (p.blocks)
     return p.bf16 ? launch_cfg<Cfg<D, 1, 1, 1>>(p, m, pl, mu, st)
                   : launch_cfg<Cfg<D, 1, 0, 1>>(p, m, pl, mu, st);
