@@ -74,7 +74,12 @@ struct Cfg {
   static constexpr int MT = KT / 16;                // 16-key groups (one page each)
   static constexpr int RPI = 32 / CPR;              // rows per copy instruction
   static constexpr int RT = 8 * NB;                 // rows of a unit
-  static constexpr int kStages = 3;
+  // (block scales: us of 64 sequences of 500 .. 8000 keys of 128 channels, and of four
+  // tokens over 16 of 1000 .. 6000 keys of 64: 110 and 29.8 with the CTAs and stages
+  // of the others, 103 and 28.6 with these; units of 16 rows at 128 channels, whose
+  // registers do not let a third CTA in, stay as they are)
+  static constexpr bool kThree = BS && (D == 64 || NB == 1);
+  static constexpr int kStages = kThree && D == 128 ? 2 : 3;
   static constexpr int kStageBytes = 2 * kHalf;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int OS = D + 4;                  // floats per row of the join buffer
@@ -82,7 +87,7 @@ struct Cfg {
   static constexpr int kRing = kWarps * (kWarpBytes > kJoinBytes ? kWarpBytes : kJoinBytes);
   static constexpr int kScales = kRing + kWarps * RT * 8 + kWarps * kStages * 4 + 16;
   static constexpr int kSmem = kScales + (BS ? kWarps * kStages * MT * 8 : 0) + 48;
-  static constexpr int kCtasPerSm = D == 128 ? 2 : 4;
+  static constexpr int kCtasPerSm = kThree ? 3 : D == 128 ? 2 : 4;
   static constexpr int kGrid = kSms * kCtasPerSm;
   static constexpr int kFlat = D == 128 ? 40 : 24;  // most parts that are joined in one step
 };
