@@ -53,10 +53,11 @@ constexpr int kGran = 64;            // keys per granule
 constexpr float kRescale = 8.0f;     // log2 growth of the maximum that rescales O
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <int D_, int NB_, int E8_, int BF_, int BS_ = 0>
+template <int D_, int NB_, int E8_, int BF_, int BS_ = 0, int CUT_ = 0>
 struct Cfg {
   static constexpr int D = D_, NB = NB_, E8 = E8_, BF = BF_;
   static constexpr int BS = BS_;                    // block scales
+  static constexpr int CUT = CUT_;                  // the line by cut_warp
   static constexpr int MBF = BF && !E8;             // type of the products
   // Softmax terms meet V as 16-bit values (an fp32 product would have to be
   // split in two and take twice the MMAs): bf16 rounds a term by 2^-9 of it at
@@ -89,6 +90,9 @@ struct Cfg {
   static constexpr int kSmem = kScales + (BS ? kWarps * kStages * MT * 8 : 0) + 48;
   static constexpr int kCtasPerSm = kThree ? 3 : D == 128 ? 2 : 4;
   static constexpr int kGrid = kSms * kCtasPerSm;
+  // how many granules a cut at units' borders may have its pieces longer than an
+  // equal one's (cut_warp)
+  static constexpr int kExtra = 24;
   static constexpr int kFlat = D == 128 ? 40 : 24;  // most parts that are joined in one step
 };
 
@@ -329,6 +333,85 @@ __device__ __forceinline__ int piece_with(long long total, int pieces, long long
   return (int)(((x + 1) * pieces + total - 1) / total) - 1;
 }
 
+// This CTA's piece [pos, end) of the line, in sequence b, which begins at base.
+// np > 0: the line is cut at units' borders, the unit's np pieces are those of the
+// CTAs from c0 on.  np = 0: it is cut into `pieces` equal ones.
+struct Cut {
+  long long pos, end, base, total;
+  int b, pieces, c0, np;
+};
+// The cut of up to 32 sequences (block scales), by a warp, a lane per sequence.
+//
+// An equal cut has most CTAs work on the ends of two units, each with a chain of
+// loads and a join of its own (5 us).  Few units are therefore cut one by one, unit
+// n long into ceil(n / g) equal pieces with g = total / (grid - units) rounded up,
+// so that there are at most `grid` of them, unless that makes the longest one
+// much longer than an equal cut's.
+template <class C>
+__device__ __forceinline__ Cut cut_warp(const AttnParams& p, int32_t* bad) {
+  const int lane = threadIdx.x & 31;
+  const bool live = lane < p.batch.num_seqs;
+  SeqWork s{};
+  if (live) s = seq_work(p, C::RT, lane, bad);
+  const int u = live ? s.rc * p.kv_heads : 0;
+  long long inc = s.w;
+  int units = u;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+    if (lane >= m) inc += o;
+  }
+  units = __reduce_add_sync(0xffffffffu, min(units, C::kGrid));
+  Cut c{};
+  c.total = __shfl_sync(0xffffffffu, inc, 31);
+  const long long base = inc - s.w;
+  const long long room = C::kGrid - units;
+  long long g = 0;
+  if (units <= C::kGrid / 2) {
+    g = (c.total + room - 1) / room;
+    if (g * units > (long long)C::kExtra * C::kGrid) g = 0;
+  }
+  if (g > 0) {
+    // us of one token, one sequence of 16 granules, pieces of 1 / 2 / 4 / 8: 9.4 / 9.4
+    // / 10.3 / 12.1; of 62, 1 / 2 / 4 / 8: 13.0 / 11.7 / 11.0 / 12.2; of 8, 1 / 8: 9.1
+    // / 7.5 (64 channels); no more parts than are joined in one step
+    const int least = s.n <= 8 ? 8 : max(s.n < 48 ? 2 : 4, (s.n + C::kFlat - 1) / C::kFlat);
+    g = max(g, (long long)least);
+    const int k = live ? (int)((s.n + g - 1) / g) : 0, mine = u * k;
+    int end = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, end, m);
+      if (lane >= m) end += o;
+    }
+    const int x = (int)blockIdx.x - (end - mine);
+    const uint32_t who = __ballot_sync(0xffffffffu, x >= 0 && x < mine);
+    if (!who) return c;
+    const int from = __ffs(who) - 1;
+    if (x >= 0 && x < mine) {
+      const int unit = x / k, i = x - unit * k;
+      const long long u0 = base + (long long)unit * s.n;
+      c.pos = u0 + (long long)s.n * i / k;
+      c.end = u0 + (long long)s.n * (i + 1) / k;
+      c.c0 = (int)blockIdx.x - i;
+      c.np = k;
+    }
+    c.pos = __shfl_sync(0xffffffffu, c.pos, from);
+    c.end = __shfl_sync(0xffffffffu, c.end, from);
+    c.c0 = __shfl_sync(0xffffffffu, c.c0, from);
+    c.np = __shfl_sync(0xffffffffu, c.np, from);
+    c.b = from;
+  } else {
+    c.pieces = pieces_of<C>(c.total);
+    if ((int)blockIdx.x >= c.pieces) return c;
+    c.pos = piece_start(c.total, c.pieces, blockIdx.x);
+    c.end = piece_start(c.total, c.pieces, blockIdx.x + 1);
+    c.b = __ffs(__ballot_sync(0xffffffffu, c.pos >= base && c.pos < inc)) - 1;
+  }
+  c.base = __shfl_sync(0xffffffffu, base, c.b);
+  return c;
+}
+
 // scratch: [kGrid][2] parts of RT rows: fp32 O rows, then (m, l) pairs
 __host__ __device__ constexpr size_t part_floats(int rt, int d) { return (size_t)rt * (d + 2); }
 
@@ -368,21 +451,37 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
 
   pdl_wait();
   int32_t bad = 0;
-  Place place;
-  const long long total = scan_line(
-      p, RT,
-      [&](long long t) {
-        const int n = pieces_of<C>(t);
-        return (int)blockIdx.x < n ? piece_start(t, n, blockIdx.x) : -1LL;
-      },
-      &place, &bad);
+  __shared__ Cut s_cut;  // (what only joins and unit changes need stays there)
+  Cut cut{};
+  if (C::CUT) {
+    cut = cut_warp<C>(p, &bad);
+  } else {
+    Place place;
+    cut.total = scan_line(
+        p, RT,
+        [&](long long t) {
+          const int n = pieces_of<C>(t);
+          return (int)blockIdx.x < n ? piece_start(t, n, blockIdx.x) : -1LL;
+        },
+        &place, &bad);
+    cut.pieces = pieces_of<C>(cut.total);
+    if ((int)blockIdx.x < cut.pieces) {
+      cut.pos = piece_start(cut.total, cut.pieces, blockIdx.x);
+      cut.end = piece_start(cut.total, cut.pieces, blockIdx.x + 1);
+      cut.b = place.b;
+      cut.base = place.base;
+    }
+  }
   if (bad && blockIdx.x == 0) atomicOr(p.status, bad);
-  const int pieces = pieces_of<C>(total);
-  if ((int)blockIdx.x >= pieces) return;
-  long long pos = piece_start(total, pieces, blockIdx.x);
-  const long long end = piece_start(total, pieces, blockIdx.x + 1);
-  int b = place.b;
-  long long base = place.base;
+  if (cut.pos >= cut.end) return;
+  if (C::CUT) {
+    if (threadIdx.x == 0) s_cut = cut;
+    __syncthreads();
+  }
+  const Cut& rest = C::CUT ? s_cut : cut;
+  long long pos = cut.pos;
+  int b = cut.b;
+  long long base = cut.base;
   bool first_part = true;
   int done = 0;  // granules of the piece so far
 
@@ -393,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
   const int64_t lane_off = lrow * tb + lch * 16;
   const int64_t it_off = C::RPI * tb;
 
-  while (pos < end && b < p.batch.num_seqs) {
+  while (pos < rest.end && b < p.batch.num_seqs) {
     const SeqWork sw = seq_work(p, RT, b, &bad);
     if (pos >= base + sw.w) {
       base += sw.w;
@@ -402,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
     }
     const int u = (int)((pos - base) / sw.n), g0 = (int)((pos - base) % sw.n);
     const long long u0 = base + (long long)u * sw.n;  // the unit's place on the line
-    const int cnt = (int)min((long long)(sw.n - g0), end - pos);
+    const int cnt = (int)min((long long)(sw.n - g0), rest.end - pos);
     const int h = u / sw.rc, rc = u % sw.rc;
     pos += cnt;
 
@@ -424,9 +523,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
     // now if all pieces had begun at multiples of their length: pieces of a
     // sequence's other heads then read the same tokens at about the same time,
     // neighbours in memory.
-    int turn;
-    {
-      const float len = (float)total / pieces, e = (float)done;
+    int turn = warp;
+    if (rest.np == 0) {
+      const float len = (float)rest.total / rest.pieces, e = (float)done;
       const int x0 = (int)(ceilf((g0 - e) / len) * len + e) - g0;
       turn = x0 * (kGran / KT);
       if (x0 < 0 || turn >= ntile) turn = 0;
@@ -823,15 +922,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
       // 8000 keys (2 units of 125 parts of 16 x 128): 33.5 us with one step,
       // 20.2 with two; but 38 parts of 4 rows 15.6 and 17.0, and units of 19
       // parts of 16 x 64 18.0 and 25.0.
-      const int c0 = piece_with(total, pieces, u0), c1 = piece_with(total, pieces, u0 + sw.n - 1);
+      const long long total = rest.total;
+      const int pieces = rest.pieces, c0 = rest.np ? rest.c0 : piece_with(total, pieces, u0);
       const float* parts = reinterpret_cast<const float*>(p.scratch);
       // piece c0 holds the unit's first part as its second, unless the unit
       // starts the piece; every other piece as its first
-      const size_t slot0 = (size_t)c0 * 2 + (piece_start(total, pieces, c0) < u0 ? 1 : 0);
+      const size_t slot0 =
+          (size_t)c0 * 2 + (rest.np == 0 && piece_start(total, pieces, c0) < u0 ? 1 : 0);
       auto part_of = [&](int i) {
         return parts + (i == 0 ? slot0 : (size_t)(c0 + i) * 2) * part_floats(RT, D);
       };
-      const int np = c1 - c0 + 1;
+      const int np = rest.np ? rest.np : piece_with(total, pieces, u0 + sw.n - 1) - c0 + 1;
       const int per = np <= C::kFlat ? np : (int)ceilf(sqrtf((float)np));  // parts of a group
       const int ng = (np + per - 1) / per;
       const int lead = ((int)blockIdx.x - c0) / per * per;  // first part of this one's group
@@ -952,6 +1053,11 @@ cudaError_t launch_cfg(const AttnParams& p, cudaStream_t st) {
 
 template <int D, int NB>
 cudaError_t launch_types(const AttnParams& p, cudaStream_t st) {
+  // (a kernel of its own for the cut of few sequences: in one, the loop over the
+  // tiles was 3 % slower for the registers that were left to it)
+  if (p.blocks && p.batch.num_seqs <= 32)
+    return p.bf16 ? launch_cfg<Cfg<D, NB, 1, 1, 1, 1>>(p, st)
+                  : launch_cfg<Cfg<D, NB, 1, 0, 1, 1>>(p, st);
   if (p.blocks)
     return p.bf16 ? launch_cfg<Cfg<D, NB, 1, 1, 1>>(p, st) : launch_cfg<Cfg<D, NB, 1, 0, 1>>(p, st);
   if (p.e4m3)
