@@ -1,9 +1,13 @@
 """One decoder layer served: ragged prompts in chunks, then single tokens from a CUDA graph.
 
     python examples/serve_block.py [--experts 32] [--seqs 8] [--prompt 700] [--steps 64] [--e4m3]
+                                   [--blocks] [--drafts 4]
 
-Synthetic weights; prints the tokens per second of both phases and the layer's
-device status."""
+The cache's pages come from a pool on the GPU.  --e4m3: an 8-bit cache with a
+scale per head, --blocks: with one per page and head.  --drafts N: then steps of
+N drafted tokens each, verified and taken back where they are refused, from a
+graph as well.  Synthetic weights; prints the tokens per second of every phase
+and the layer's device status."""
 import argparse
 import os
 import sys
@@ -13,7 +17,8 @@ import numpy as np
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from trellis_quantized_moe_exl3_gb300 import DecoderBlock, Layer, PagedBatch, PagedKVCache, synth  # noqa: E402
+from trellis_quantized_moe_exl3_gb300 import (DecoderBlock, Layer, PagedKVCache, PagePool,  # noqa: E402
+                                               synth, verify_drafts)
 
 
 def build_block(spec, heads, kv_heads, dim, top_k, seed=0):
@@ -42,22 +47,27 @@ def main():
     ap.add_argument("--prompt", type=int, default=700)
     ap.add_argument("--chunk", type=int, default=256)
     ap.add_argument("--steps", type=int, default=64)
-    ap.add_argument("--e4m3", action="store_true", help="8-bit cache")
+    ap.add_argument("--e4m3", action="store_true", help="8-bit cache, a scale per head")
+    ap.add_argument("--blocks", action="store_true", help="8-bit cache, a scale per page and head")
+    ap.add_argument("--drafts", type=int, default=0, help="drafted tokens per step of a last phase")
     a = ap.parse_args()
     heads, kv_heads, dim, page = 32, 8, 128, 64
     spec = synth.LayerSpec(seed=2, num_experts=a.experts)
     block = build_block(spec, heads, kv_heads, dim, top_k=min(8, a.experts))
     prompts = [max(1, a.prompt - 37 * b) for b in range(a.seqs)]
-    per = -(-(max(prompts) + a.steps + 8) // page)
-    table = torch.randperm(a.seqs * per, device="cuda").int().view(a.seqs, per)
-    kv = [torch.zeros(a.seqs * per, page, kv_heads, dim, device="cuda",
-                      dtype=torch.float8_e4m3fn if a.e4m3 else torch.bfloat16) for _ in range(2)]
-    scale = [torch.full((kv_heads,), 0.05, device="cuda") if a.e4m3 else None for _ in range(2)]
-    cache = PagedKVCache(*kv, *scale)
+    # (a token per step, then a token and its drafts at most)
+    per = -(-(max(prompts) + (a.steps + 8) * (2 + a.drafts if a.drafts else 1)) // page)
+    pages = a.seqs * per
+    eight = a.e4m3 or a.blocks
+    kv = [torch.zeros(pages, page, kv_heads, dim, device="cuda",
+                      dtype=torch.float8_e4m3fn if eight else torch.bfloat16) for _ in range(2)]
+    scale = [torch.zeros(pages, kv_heads, device="cuda") if a.blocks else
+             torch.full((kv_heads,), 0.05, device="cuda") if eight else None for _ in range(2)]
+    cache, pool = PagedKVCache(*kv, *scale), PagePool(pages, page, a.seqs, per)
+    seqs = torch.arange(a.seqs, dtype=torch.int32, device="cuda")
 
-    def batch_of(new, total):
-        cu = torch.tensor(np.cumsum([0] + new), dtype=torch.int32, device="cuda")
-        return PagedBatch(cu, torch.tensor(total, dtype=torch.int32, device="cuda"), table, max(new))
+    def extend(new):
+        return pool.extend(seqs, torch.tensor(new, dtype=torch.int32, device="cuda"), max(new), sum(new))
 
     # prompts, a chunk of each sequence at a time
     done, t0, out = [0] * a.seqs, time.perf_counter(), None
@@ -65,19 +75,25 @@ def main():
         new = [min(a.chunk, p - d) for d, p in zip(done, prompts)]
         done = [d + n for d, n in zip(done, new)]
         x = torch.randn(sum(new), spec.hidden, device="cuda").bfloat16()
-        out = block(x, cache, batch_of(new, done))
+        out = block(x, cache, extend(new))
     torch.cuda.synchronize()
     print(f"prompts: {sum(prompts)} tokens, {sum(prompts) / (time.perf_counter() - t0):.0f} tokens/s "
           f"(first calls included), output norm {float(out.float().norm()):.3e}")
 
-    # single tokens: one captured step whose lengths advance on the device
-    batch = batch_of([1] * a.seqs, done)
+    # single tokens: one captured step that takes its pages from the pool
+    one = torch.ones(a.seqs, dtype=torch.int32, device="cuda")
     x = torch.randn(a.seqs, spec.hidden, device="cuda").bfloat16()
+    y, dt = timed(lambda: block(x, cache, pool.extend(seqs, one, 1, a.seqs)), a.steps)
+    print(f"decode: {a.steps} steps of {a.seqs} sequences, {dt / a.steps * 1e6:.1f} us per step, "
+          f"{a.steps * a.seqs / dt:.0f} tokens/s, lengths now {pool.lens.tolist()}, "
+          f"output norm {float(y.float().norm()):.3e}")
+    if a.drafts:
+        speculate(block, cache, pool, seqs, spec.hidden, a.drafts, a.steps)
+    print("device status", cache.status() | pool.status())
 
-    def step():
-        batch.seq_lens.add_(1)
-        return block(x, cache, batch)
 
+def timed(step, steps):
+    """The last result of a step that is captured and replayed, and the seconds taken."""
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -88,14 +104,45 @@ def main():
         y = step()
     torch.cuda.synchronize()
     t0 = time.perf_counter()
-    for _ in range(a.steps):
+    for _ in range(steps):
         graph.replay()
     torch.cuda.synchronize()
-    dt = time.perf_counter() - t0
-    print(f"decode: {a.steps} steps of {a.seqs} sequences, {dt / a.steps * 1e6:.1f} us per step, "
-          f"{a.steps * a.seqs / dt:.0f} tokens/s, lengths now {batch.seq_lens.tolist()}, "
-          f"output norm {float(y.float().norm()):.3e}")
-    print("device status", cache.status())
+    return y, time.perf_counter() - t0
+
+
+def speculate(block, cache, pool, seqs, hidden, drafts, steps, vocab=1000):
+    """Steps of a token and its drafts: pages, the block, the target's probabilities,
+    verification, and refused drafts out of the cache again.  The drafting model
+    here says that every token is as likely as any other."""
+    n, rows = len(seqs), drafts + 1
+    embed = torch.randn(vocab, hidden, device="cuda").bfloat16()
+    head = (torch.randn(hidden, vocab, device="cuda") * hidden ** -0.5).bfloat16()
+    q_lens = torch.full((n,), rows, dtype=torch.int32, device="cuda")
+    cu_draft = torch.arange(0, n * drafts + 1, drafts, dtype=torch.int32, device="cuda")
+    q = torch.full((n * drafts, vocab), 1.0 / vocab, device="cuda")
+    last = torch.zeros(n, dtype=torch.int64, device="cuda")
+    made = torch.zeros(1, dtype=torch.int64, device="cuda")
+
+    def step():
+        draft = torch.randint(0, vocab, (n, drafts), device="cuda")
+        x = embed[torch.cat([last[:, None], draft], 1).flatten()]
+        y = block(x, cache, pool.extend(seqs, q_lens, rows, n * rows))
+        y = y.float()
+        p = ((y / y.norm(dim=-1, keepdim=True)) @ head.float()).softmax(-1)
+        tokens, accepted, dropped = verify_drafts(
+            p, draft.int().flatten(), cu_draft, torch.rand(n * drafts, device="cuda"),
+            torch.rand(n, device="cuda"), q=q)
+        pool.trim(seqs, dropped)
+        last.copy_(tokens.view(n, rows).gather(1, accepted.long()[:, None])[:, 0])
+        made.add_((accepted + 1).sum())
+        return accepted
+
+    made.zero_()
+    accepted, dt = timed(step, steps)
+    made = int(made)
+    print(f"drafts: {steps} steps of {n} x {drafts}, {dt / steps * 1e6:.1f} us per step, "
+          f"{made / (steps + 1):.1f} tokens per step, lengths now {pool.lens.tolist()}, "
+          f"last token {int(last[0])}")
 
 
 if __name__ == "__main__":

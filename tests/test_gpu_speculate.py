@@ -252,3 +252,86 @@ def test_verify_no_sequences():
     e = torch.zeros(0, device="cuda")
     t, a, d = verify_drafts(torch.zeros(0, 10, device="cuda"), ints([]), ints([0]), e, e)
     assert t.shape == (0,) and a.shape == (0,) and d.shape == (0,)
+
+
+# ------------------------------------------------------------ a step of all of them
+@pytest.mark.parametrize("captured", [False, True])
+def test_speculative_steps_over_a_block_scaled_cache(captured):
+    """Pages, append, attention, verification and the way back, step after step:
+    lengths follow what was accepted, every token's attention is that of the cache
+    as it is then, and refused drafts leave no page behind."""
+    import _attention_ref as A
+    from trellis_quantized_moe_exl3_gb300 import PagedKVCache, kv_append, paged_attention
+    n, drafts, heads, hk, d, page, vocab = 5, 3, 8, 2, 64, 16, 97
+    g = gen(77)
+    cache = PagedKVCache(*[torch.zeros(60, page, hk, d, dtype=R.E4M3, device="cuda") for _ in range(2)],
+                         *[torch.zeros(60, hk, device="cuda") for _ in range(2)])
+    pool, ref = PagePool(60, page, 9, 12), R.Pool(60, page, 9, 12)
+    rows_of = [4, 0, 8, 2, 7]
+    seqs, rows = ints(rows_of), drafts + 1
+    T = n * rows
+    table = torch.randn(vocab, heads + 2 * hk, d, generator=g).to(BF).cuda()
+    head = (torch.randn(heads * d, vocab, generator=g) * 0.3).cuda()
+    f = (500000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)).cuda()
+    tokens_in = torch.zeros(n, rows, dtype=torch.int64, device="cuda")
+    au, su = torch.zeros(n * drafts, device="cuda"), torch.zeros(n, device="cuda")
+    cu = ints([b * drafts for b in range(n + 1)])
+    q_probs = torch.full((n * drafts, vocab), 1.0 / vocab, device="cuda")
+    q_lens = ints([rows] * n)
+
+    def step():
+        qkv = table[tokens_in.flatten()]
+        s = pool.extend(seqs, q_lens, rows, T)
+        q = kv_append(cache, s, qkv[:, heads:heads + hk], qkv[:, heads + hk:], inv_freq=f,
+                      q=qkv[:, :heads])
+        out = paged_attention(q, cache, s)
+        p = (out.view(T, -1).float() @ head).softmax(-1)
+        t, accepted, dropped = verify_drafts(p, tokens_in[:, 1:].int().flatten(), cu, au, su, q=q_probs)
+        return s, q, out, p, t, accepted, dropped
+
+    def whole():
+        got = step()
+        pool.trim(seqs, got[-1])
+        return got
+
+    # prompts of odd lengths first
+    start = [17, 3, 40, 16, 1]
+    s = pool.extend(seqs, ints(start), max(start), sum(start))
+    ref.extend(rows_of, start, sum(start))
+    kv = table[torch.randint(0, vocab, (sum(start),), generator=g).cuda()]
+    kv_append(cache, s, kv[:, heads:heads + hk], kv[:, heads + hk:], inv_freq=f)
+    cache.workspace(T, heads, n)
+    graph = None
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = whole()
+    total = 0
+    for k in range(6):
+        tokens_in.copy_(torch.randint(0, vocab, (n, rows), generator=g))
+        au.copy_(torch.rand(n * drafts, generator=g) * 0.7)
+        su.copy_(torch.rand(n, generator=g))
+        if captured:
+            graph.replay()
+        else:
+            got = whole()
+        s, q, out, p, t, accepted, dropped = got
+        cu_r, lens, tab, pos, slots = ref.extend(rows_of, [rows] * n, T)
+        assert s.cu_q.tolist() == cu_r and s.seq_lens.tolist() == lens
+        assert s.block_table.tolist() == tab and s.slots.tolist() == slots and s.positions.tolist() == pos
+        want = R.verify(p.cpu(), tokens_in[:, 1:].flatten().cpu(), cu.tolist(), au.cpu(), su.cpu(),
+                        q_probs.cpu())
+        assert t.tolist() == want[0] and accepted.tolist() == want[1] and dropped.tolist() == want[2]
+        # (nothing is appended between the attention and this look: the cache still holds the step)
+        o, mag, _ = R.attention(q, R.values(cache.k, cache.k_scale), R.values(cache.v, cache.v_scale),
+                                torch.tensor(tab), [rows] * n, lens, page, d ** -0.5, True, 0)
+        tol = A.U[BF] * (o.abs() + mag) + 1e-4 * mag + 2.0 ** -25
+        assert bool(((out.double().cpu() - o).abs() <= tol).all())
+        ref.trim(rows_of, want[2])
+        same_state(pool, ref)
+        total += sum(want[1])
+    assert total > 0 and cache.status() == 0
+    pool.trim(seqs)
+    ref.trim(rows_of)
+    same_state(pool, ref)
+    assert int(pool.count) == 60
