@@ -26,13 +26,8 @@
 namespace exl3 {
 namespace {
 
-#ifndef AR
-#define AR 3
-#define WANT 4ll
-#define HO 2
-#endif
-constexpr int kThreads = 256, kPerSm = AR;
-constexpr int kHold = HO;
+// three CTAs of 80 registers on an SM (7000 tokens 40.9 us; four of 64 44.6, two 47)
+constexpr int kThreads = 256, kPerSm = 3;
 
 // the least 2^e >= top / 448, within the range of scales
 __device__ __forceinline__ float scale_for(float top) {
@@ -233,7 +228,7 @@ __device__ __forceinline__ Job find_job(const NormRopeParams& p, int slot, bool 
 
 // Keys and values of a block: the units unit0 + 0, 1, .., one per team.  A team is
 // `team` (a power of two) lane groups.
-template <int LPR, int BF16, int INTER>
+template <int LPR, int kHold, int BF16, int INTER>
 __device__ __forceinline__ void do_block(const NormRopeParams& p, const uint64_t* turns,
                                          const Job& job, int unit0, int team) {
   using L = Lane<LPR, BF16, INTER>;
@@ -273,7 +268,8 @@ __device__ __forceinline__ void do_block(const NormRopeParams& p, const uint64_t
   };
   auto raise = [](float top, const float2* v) {
 #pragma unroll
-    for (int e = 0; e < 8; e++) top = fmaxf(top, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
+    for (int e = 0; e < 8; e++)  // (a NaN counts for nothing)
+      asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(fabsf(v[e].x)), "f"(fabsf(v[e].y)));
     return top;
   };
 
@@ -297,7 +293,7 @@ __device__ __forceinline__ void do_block(const NormRopeParams& p, const uint64_t
     const int w0 = warp & ~(team / GW - 1);
     if (wl == 0) tops[warp] = most;
     __syncthreads();
-    for (int i = 0; i < team / GW; i++) most = max(most, tops[w0 + i]);
+    most = __reduce_max_sync(0xffffffffu, tops[w0 + (wl & (team / GW - 1))]);
   }
   top = __uint_as_float(most);
 
@@ -362,16 +358,17 @@ __device__ __forceinline__ void do_block(const NormRopeParams& p, const uint64_t
   }
 }
 
-// CTAs 0 .. blocks * groups - 1: block slots, `groups` of them to a slot; the
-// others: queries.
+// `blocks` block slots of `groups` CTAs each; the other CTAs: queries, `slices`
+// lane groups to a token, `per` heads to a lane group.
 struct Split {
   int blocks, groups, team, slices, per;
 };
-template <int LPR, int BF16, int INTER>
+template <int LPR, int kHold, int BF16, int INTER>
 __global__ void __launch_bounds__(kThreads, kPerSm) append_blocks_kernel(NormRopeParams p, Split c) {
   constexpr int NG = kThreads / LPR;
   __shared__ uint64_t turns[128];  // of the pairs, per position
   __shared__ Job s_job;
+  // (keys and values first; in turn with the queries they took as long)
   const int64_t cta = blockIdx.x, first = (int64_t)c.blocks * c.groups;
   const bool block = cta < first;
   pdl_wait();
@@ -388,12 +385,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) append_blocks_kernel(NormRop
   } else {
     const Job job = s_job;
     if (job.page >= 0)
-      do_block<LPR, BF16, INTER>(p, turns, job, (int)(cta % c.groups) * (NG / c.team), c.team);
+      do_block<LPR, kHold, BF16, INTER>(p, turns, job, (int)(cta % c.groups) * (NG / c.team), c.team);
   }
 }
 
-template <int LPR>
-cudaError_t launch_lpr(const NormRopeParams& p, cudaStream_t st) {
+template <int LPR, int kHold>
+cudaError_t launch_hold(const NormRopeParams& p, cudaStream_t st) {
   constexpr int NG = kThreads / LPR;
   Split c{};
   c.blocks = p.T / p.cache.page_size + 2 * p.batch.num_seqs;
@@ -405,7 +402,7 @@ cudaError_t launch_lpr(const NormRopeParams& p, cudaStream_t st) {
   long long ctas = (long long)c.blocks * c.groups;
   // a token's query heads are spread over lane groups until those fill the GPU
   if (p.set[0].heads > 0) {
-    const long long want = (WANT * kSms * kPerSm * NG + p.T - 1) / p.T;
+    const long long want = (4ll * kSms * kPerSm * NG + p.T - 1) / p.T;
     c.slices = (int)(want < p.set[0].heads ? want : p.set[0].heads);
     c.per = (p.set[0].heads + c.slices - 1) / c.slices;
     c.slices = (p.set[0].heads + c.per - 1) / c.per;
@@ -415,10 +412,18 @@ cudaError_t launch_lpr(const NormRopeParams& p, cudaStream_t st) {
   const dim3 grid((unsigned)ctas), block(kThreads);
   note_launches(1);
   if (p.inter)
-    return p.bf16 ? launch_pdl(append_blocks_kernel<LPR, 1, 1>, grid, block, 0, st, p, c)
-                  : launch_pdl(append_blocks_kernel<LPR, 0, 1>, grid, block, 0, st, p, c);
-  return p.bf16 ? launch_pdl(append_blocks_kernel<LPR, 1, 0>, grid, block, 0, st, p, c)
-                : launch_pdl(append_blocks_kernel<LPR, 0, 0>, grid, block, 0, st, p, c);
+    return p.bf16 ? launch_pdl(append_blocks_kernel<LPR, kHold, 1, 1>, grid, block, 0, st, p, c)
+                  : launch_pdl(append_blocks_kernel<LPR, kHold, 0, 1>, grid, block, 0, st, p, c);
+  return p.bf16 ? launch_pdl(append_blocks_kernel<LPR, kHold, 1, 0>, grid, block, 0, st, p, c)
+                : launch_pdl(append_blocks_kernel<LPR, kHold, 0, 0>, grid, block, 0, st, p, c);
+}
+
+template <int LPR>
+cudaError_t launch_lpr(const NormRopeParams& p, cudaStream_t st) {
+  // one row per lane group keeps a step of a few tokens short (64 of one token 3.8 us,
+  // with two 4.4), two keep a block of 64 tokens in registers (7000 tokens 40.9 us,
+  // with one, formed twice, 43.4)
+  return p.batch.max_q <= 8 ? launch_hold<LPR, 1>(p, st) : launch_hold<LPR, 2>(p, st);
 }
 
 }  // namespace
