@@ -413,3 +413,94 @@ def test_attention_blocks_results_do_not_depend_on_timing():
     for _ in range(3):
         got = paged_attention(q, cache, batch_of(step), return_lse=True)
         assert all(torch.equal(a[:3], b[:3]) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------ how a line is cut, streams, graphs
+@pytest.mark.parametrize("qs,lens,H,Hk,D", [
+    ([1] * 32, [(i * 97) % 1500 + 1 for i in range(32)], 8, 2, 128),     # as many as a warp cuts
+    ([1] * 33, [(i * 97) % 1500 + 1 for i in range(33)], 8, 2, 128),     # one more
+    ([0] * 31 + [1], [50] * 31 + [5000], 4, 1, 64),                      # one of them has new tokens
+    ([1, 1, 1, 1], [1, 512, 513, 9000], 8, 8, 64),                       # whole units beside cut ones
+    ([70, 3, 1], [90, 2000, 30000], 16, 2, 64),                          # several chunks of rows
+    ([2, 2], [70000, 3], 2, 2, 128),                                     # parts joined in two steps
+    ([1] * 20, [8000 - 390 * i for i in range(20)], 16, 8, 128),         # too long to be cut one by one
+    ([300], [300], 8, 1, 64),                                            # more units than half the grid
+])
+def test_attention_blocks_cuts(qs, lens, H, Hk, D):
+    c = (qs, lens, 64, H, Hk, D, BF, True, 0)
+    cache, step, q = setup(c)
+    first = check(cache, step, q, c, 1)
+    for _ in range(2):  # the counters are back at zero, and the result is the same
+        again = paged_attention(q, cache, batch_of(step), scale=D ** -0.5, return_lse=True, path=1)
+        assert all(torch.equal(a[:sum(qs)], b[:sum(qs)]) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_attention_blocks_without_a_scale_beside_nan(path):
+    """A NaN that some rows see sends tiles through the careful way: blocks without
+    a scale stay absent there too."""
+    c = CASES[12]
+    cache, step, q = setup(c)
+    absent = torch.zeros(cache.k.shape[0], c[4], dtype=torch.bool)
+    b, L = 1, c[1][1]                                   # 333 new tokens of 700
+    nan_at, bad_blk = L - 100, (L - 150) // c[2]
+    pg, bad_pg = int(step.table[b, nan_at // c[2]]), int(step.table[b, bad_blk])
+    for h in range(c[4]):
+        cache.v.view(torch.uint8)[pg, nan_at % c[2], h, 7] = 0x7F
+        cache.v.view(torch.uint8)[bad_pg, 5, h, 9] = 0x7F
+        cache.v_scale[bad_pg, h] = -2.0
+        absent[bad_pg, h] = True
+    check(cache, step, q, c, path, absent, status=8)
+
+
+def test_block_scales_on_other_streams_and_in_graphs():
+    """Append and attention on a stream of their own (stream= and a current one),
+    and two captured graphs of one handle replayed in turn."""
+    g = gen(21)
+    qs, lens, page = [1, 5, 40], [30, 5, 333], 16
+    step, pages = A.make_step(g, qs, lens, page)
+    T = sum(qs)
+    qkv, f = torch.randn(T, 12, 64, generator=g).to(BF).cuda(), freqs(64)
+
+    def fresh():
+        cache = blank(pages, page, 2, 64)
+        for x, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+            x.copy_((torch.randn(x.shape, generator=gen(5)) * 50).to(E4))
+            s.fill_(2.0 ** -6)
+        return cache
+
+    def run(cache, stream=None):
+        q = kv_append(cache, batch_of(step), qkv[:, 8:10], qkv[:, 10:], q=qkv[:, :8], inv_freq=f,
+                      stream=stream)
+        return paged_attention(q, cache, batch_of(step), stream=stream)
+
+    cache = fresh()
+    want = run(cache)
+    state = [u8(cache.k), u8(cache.v), cache.k_scale.clone(), cache.v_scale.clone()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for how in ("stream=", "current"):
+        cache = fresh()
+        torch.cuda.synchronize()
+        if how == "stream=":
+            got = run(cache, side)
+        else:
+            with torch.cuda.stream(side):
+                got = run(cache)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and cache.status() == 0
+        for a, b in zip(state, [u8(cache.k), u8(cache.v), cache.k_scale, cache.v_scale]):
+            assert torch.equal(a, b)
+    cache = fresh()
+    run(cache)
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run(cache)
+        graphs.append((graph, out))
+    for graph, out in graphs + graphs:
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+    assert cache.status() == 0

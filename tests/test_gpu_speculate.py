@@ -335,3 +335,25 @@ def test_speculative_steps_over_a_block_scaled_cache(captured):
     ref.trim(rows_of)
     same_state(pool, ref)
     assert int(pool.count) == 60
+
+
+def test_verify_drafts_of_no_sequence_and_padding():
+    """Rows that belong to no sequence give -1, also where there is none at all."""
+    p = torch.rand(7, 33, device="cuda")
+    e = torch.zeros(0, device="cuda")
+    t, a, d = verify_drafts(p, ints([1] * 7), ints([0]), torch.rand(7, device="cuda"), e)
+    assert t.tolist() == [-1] * 7 and a.shape == d.shape == (0,)
+
+
+def test_pool_on_another_stream():
+    side = torch.cuda.Stream()
+    seqs, q = ints([1, 0]), ints([20, 3])
+    torch.cuda.synchronize()
+    pool = PagePool(9, 16, 2, 4)
+    step = pool.extend(seqs, q, 20, 23, stream=side)
+    pool.trim(seqs, ints([7, 0]), stream=None)  # (ints waits for the device)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        pool.trim(seqs, q)
+    assert step.cu_q.tolist() == [0, 20, 23] and pool.lens.tolist() == [0, 0]
+    assert int(pool.count) == 9 and pool.status() == 1      # (7 of the 20 were gone already)

@@ -299,7 +299,7 @@ __device__ __forceinline__ void do_block(const NormRopeParams& p, const uint64_t
 
   // ---- the scale
   if (!live) return;
-  if (!(held >= 0.0f && held <= kMostScale)) {  // no scale: the block is left alone
+  if (!good_scale(held)) {  // no scale: the block is left alone
     if (ln.lane == 0 && me == 0) atomicOr(p.status, kStatusBadScale);
     return;
   }

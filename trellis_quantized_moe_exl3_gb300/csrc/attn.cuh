@@ -17,6 +17,7 @@ enum : int32_t { kStatusBadPage = 1, kStatusBadBatch = 2, kStatusBadScale = 8 };
 // range keeps every softmax term that matters within fp32 when a scale's
 // logarithm is added to its scores.)
 constexpr float kLeastScale = 0x1p-40f, kMostScale = 0x1p40f;
+__device__ __forceinline__ bool good_scale(float x) { return x >= 0.0f && x <= kMostScale; }
 
 constexpr int kMaxSeqs = 65535;
 constexpr int kMaxPageSize = 4096;

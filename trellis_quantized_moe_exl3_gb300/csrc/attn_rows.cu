@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
 #pragma unroll
         for (int t = 0; t < MT; t++) {
           const float2 x = scales[st * MT + t];
-          if (!(x.x >= 0.0f && x.x <= kMostScale && x.y >= 0.0f && x.y <= kMostScale)) {
+          if (!good_scale(x.x) || !good_scale(x.y)) {
             const int key = key0 + 16 * t;
             if (key < any1 && key + 16 > any0) bad |= kStatusBadScale;
             gone |= 1u << t;

@@ -756,6 +756,10 @@ __device__ __noinline__ void add_poison(const Cache c, const int32_t* table, int
     for (int key = max(k0, lo); key <= min(k0 + kTile - 1, hi); key++) {
       const int page = __ldg(table + key / c.page_size);
       if (page < 0 || page >= c.num_pages) continue;
+      if (C::BS) {  // a block without a scale counts as absent
+        const int64_t at = page * c.scale_stride + h;
+        if (!good_scale(c.k_scale[at]) || !good_scale(c.v_scale[at])) continue;
+      }
       const uint8_t* v = c.v + page * c.page_bytes + (int64_t)(key % c.page_size) * c.token_bytes +
                          h * c.head_bytes;
       for (int d = 0; d < C::D; d++) {
@@ -1401,7 +1405,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           nxt = nxt2;
           snxt = scales_of(nxt);
           nxt2 = page_of(j + 2);
-          if (!(sc.x >= 0.0f && sc.x <= kMostScale && sc.y >= 0.0f && sc.y <= kMostScale)) {
+          if (!good_scale(sc.x) || !good_scale(sc.y)) {
             // (such a page is one that is needed: its keys count as absent)
             no_scale = true;
             bad |= kStatusBadScale;

@@ -413,7 +413,14 @@ extern "C" exl3_status exl3_verify_drafts(const void* p, int64_t p_stride, const
       drafts > (1 << 30))
     return EXL3_ERR_SHAPE;
   if (p_stride < vocab || (q && q_stride < vocab)) return EXL3_ERR_ARG;
-  if (num_seqs == 0) return EXL3_OK;
+  if (num_seqs == 0) {
+    if (drafts == 0) return EXL3_OK;
+    if (!tokens) return EXL3_ERR_ARG;
+    return cudaMemsetAsync(tokens, 0xFF, (size_t)drafts * 4, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? EXL3_OK
+               : EXL3_ERR_CUDA;
+  }
   const uintptr_t size = dt == EXL3_F32 ? 4 : 2;
   if (!p || reinterpret_cast<uintptr_t>(p) % size || reinterpret_cast<uintptr_t>(q) % size ||
       !cu_draft || !sample_u || !tokens || !accepted || !dropped ||

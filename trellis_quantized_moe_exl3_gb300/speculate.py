@@ -13,6 +13,7 @@ inputs must then be ready on).
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -25,12 +26,10 @@ _PROBS = {torch.float16: _lib.EXL3_F16, torch.bfloat16: _lib.EXL3_BF16,
           torch.float32: _lib.EXL3_F32}
 
 
-def _outputs(stream, device, *of):
-    """New tensors of the shapes and types `of`.  (A tensor each: views of one
-    take longer to make than their memory.)"""
-    if stream is None:
-        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in of]
-    return [_empty(shape, dtype, device, stream) for shape, dtype in of]
+# exl3_kv_batch as C lays it out, packed bytes for the call's own cost
+_BATCH = struct.Struct("@iiiqQQQ")
+assert _BATCH.size == ctypes.sizeof(_lib.KVBatch)
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
 class PagedStep(PagedBatch):
@@ -41,10 +40,10 @@ class PagedStep(PagedBatch):
     def __init__(self, cu_q, seq_lens, block_table, positions, slots, max_q):
         self.cu_q, self.seq_lens, self.block_table = cu_q, seq_lens, block_table
         self.positions, self.slots = positions, slots
-        self.num_seqs, self.max_q = block_table.shape[0], max_q
-        self._d = d = _lib.KVBatch(self.num_seqs, max_q, block_table.shape[1], block_table.shape[1],
-                                   cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr())
-        self._ref = ctypes.byref(d)
+        n, m = block_table.shape
+        self.num_seqs, self.max_q = n, max_q
+        self._ref = _BATCH.pack(n, max_q, m, m, cu_q.data_ptr(), seq_lens.data_ptr(),
+                                block_table.data_ptr())
 
 
 class PagePool:
@@ -81,13 +80,17 @@ class PagePool:
         d.free, d.count = self.free.data_ptr() or None, self.count.data_ptr()
         self._d, self._ref = d, ctypes.byref(d)
         self._ws, self._ws_bytes = self.ws.data_ptr(), n
+        if not _capturing():  # calls on other streams find it made
+            torch.cuda.current_stream(device).synchronize()
+        self._extend, self._trim = _lib.lib().exl3_pages_extend, _lib.lib().exl3_pages_trim
 
     def _seqs(self, seqs):
-        if seqs.dtype != torch.int32 or seqs.dim() != 1 or not seqs.is_cuda or \
-                not seqs.is_contiguous() or seqs.shape[0] > self.max_seqs:
-            _cuda(seqs, "seqs", torch.int32)
+        shape = seqs.shape
+        if seqs.dtype != _I32 or len(shape) != 1 or not seqs.is_cuda or not seqs.is_contiguous() or \
+                shape[0] > self.max_seqs:
+            _cuda(seqs, "seqs", _I32)
             raise ValueError(f"seqs must be a contiguous tensor of at most {self.max_seqs} rows")
-        return seqs.shape[0]
+        return shape[0]
 
     def extend(self, seqs, q_lens, max_q: int, max_tokens: int, stream=None) -> PagedStep:
         """Begins a step: row seqs[i] of the pool gets q_lens[i] new tokens and the
@@ -96,22 +99,29 @@ class PagePool:
         for which there are no pages left keeps its rows, but has length 0 in the
         step and stays as it was in the pool."""
         n = self._seqs(seqs)
-        if q_lens.dtype != torch.int32 or q_lens.shape != (n,) or not q_lens.is_cuda or \
+        if q_lens.dtype != _I32 or q_lens.shape != (n,) or not q_lens.is_cuda or \
                 not q_lens.is_contiguous():
             _dense(q_lens, "q_lens", torch.int32, (n,))
         if max_tokens < 0:
             raise ValueError("max_tokens must not be negative")
-        cu_q, seq_lens, table, positions, slots = _outputs(
-            stream, seqs.device, ((n + 1,), torch.int32), ((n,), torch.int32),
-            ((n, self.max_pages), torch.int32), ((max_tokens,), torch.int32),
-            ((max_tokens,), torch.int64))
-        step = PagedStep(cu_q, seq_lens, table, positions, slots, int(max_q))
-        d = step._d
-        check(_lib.lib().exl3_pages_extend(
-            self._ref, n, seqs.data_ptr(), q_lens.data_ptr(), max_tokens, d.cu_q, d.seq_lens,
-            d.block_table, positions.data_ptr(), slots.data_ptr(), self._ws, self._ws_bytes,
-            _stream(stream, seqs)), "exl3_pages_extend")
-        return step
+        dev = seqs.device
+        # (a tensor each: views of one take longer to make than their memory)
+        if stream is None:
+            cu_q = torch.empty(n + 1, dtype=_I32, device=dev)
+            seq_lens = torch.empty(n, dtype=_I32, device=dev)
+            table = torch.empty((n, self.max_pages), dtype=_I32, device=dev)
+            positions = torch.empty(max_tokens, dtype=_I32, device=dev)
+            slots = torch.empty(max_tokens, dtype=_I64, device=dev)
+        else:
+            cu_q, seq_lens = _empty(n + 1, _I32, dev, stream), _empty(n, _I32, dev, stream)
+            table = _empty((n, self.max_pages), _I32, dev, stream)
+            positions = _empty(max_tokens, _I32, dev, stream)
+            slots = _empty(max_tokens, _I64, dev, stream)
+        check(self._extend(
+            self._ref, n, seqs.data_ptr(), q_lens.data_ptr(), max_tokens, cu_q.data_ptr(),
+            seq_lens.data_ptr(), table.data_ptr(), positions.data_ptr(), slots.data_ptr(), self._ws,
+            self._ws_bytes, _stream(stream, seqs)), "exl3_pages_extend")
+        return PagedStep(cu_q, seq_lens, table, positions, slots, int(max_q))
 
     def trim(self, seqs, drop=None, stream=None):
         """Takes the last drop[i] tokens (None: all) of row seqs[i] off and gives
@@ -120,9 +130,8 @@ class PagePool:
         if drop is not None and (drop.dtype != torch.int32 or drop.shape != (n,) or
                                  not drop.is_cuda or not drop.is_contiguous()):
             _dense(drop, "drop", torch.int32, (n,))
-        check(_lib.lib().exl3_pages_trim(self._ref, n, seqs.data_ptr(),
-                                         drop.data_ptr() if drop is not None else None, self._ws,
-                                         self._ws_bytes, _stream(stream, seqs)), "exl3_pages_trim")
+        check(self._trim(self._ref, n, seqs.data_ptr(), drop.data_ptr() if drop is not None else None,
+                         self._ws, self._ws_bytes, _stream(stream, seqs)), "exl3_pages_trim")
 
     def status(self, stream=None) -> int:
         """The status bits set so far (0: fine); see exl3.h."""
@@ -149,7 +158,7 @@ def _rows(x, name, rows, vocab=None):
 
 
 def _vector(x, name, dtype, n):
-    if x.dtype != dtype or x.shape != (n,) or not x.is_cuda or not x.is_contiguous():
+    if x.dtype != dtype or x.shape != (n,) or not (x.is_cuda and x.is_contiguous()):
         _dense(x, name, dtype, (n,))
     return x.data_ptr()
 
@@ -174,19 +183,23 @@ def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None):
     [sequences]): from place cu_draft[b] + b on, the accepted drafts, the drawn
     token, then -1; accepted drafts, and the others (what PagePool.trim takes)."""
     D, B = draft.shape[0], sample_u.shape[0]
-    ps = _rows(p, "p", D + B)
-    vocab, qp, qs = p.shape[1], None, 0
+    ps, qp, qs, dtype = _rows(p, "p", D + B), None, 0, p.dtype
+    vocab = p.shape[1]
     if q is not None:
         qs = _rows(q, "q", D, vocab)
-        if q.dtype != p.dtype:
+        if q.dtype != dtype:
             raise ValueError("p and q must have the same dtype")
         qp = q.data_ptr() if D else None
-    args = (p.data_ptr(), ps, qp, qs, _PROBS[p.dtype], vocab, B, D,
-            _vector(cu_draft, "cu_draft", torch.int32, B + 1),
-            _vector(draft, "draft", torch.int32, D), _vector(accept_u, "accept_u", torch.float32, D),
-            _vector(sample_u, "sample_u", torch.float32, B))
-    tokens, accepted, dropped = _outputs(stream, p.device, ((D + B,), torch.int32),
-                                         ((B,), torch.int32), ((B,), torch.int32))
-    check(_lib.lib().exl3_verify_drafts(*args, tokens.data_ptr(), accepted.data_ptr(),
-                                        dropped.data_ptr(), _stream(stream, p)), "exl3_verify_drafts")
+    cu, dr = _vector(cu_draft, "cu_draft", _I32, B + 1), _vector(draft, "draft", _I32, D)
+    au, su = _vector(accept_u, "accept_u", _F32, D), _vector(sample_u, "sample_u", _F32, B)
+    dev = p.device
+    if stream is None:
+        tokens = torch.empty(D + B, dtype=_I32, device=dev)
+        accepted = torch.empty(B, dtype=_I32, device=dev)
+        dropped = torch.empty(B, dtype=_I32, device=dev)
+    else:
+        tokens, accepted, dropped = (_empty(x, _I32, dev, stream) for x in (D + B, B, B))
+    check(_lib.lib().exl3_verify_drafts(
+        p.data_ptr(), ps, qp, qs, _PROBS[dtype], vocab, B, D, cu, dr, au, su, tokens.data_ptr(),
+        accepted.data_ptr(), dropped.data_ptr(), _stream(stream, p)), "exl3_verify_drafts")
     return tokens, accepted, dropped
