@@ -10,7 +10,7 @@ import ctypes
 import os
 import re
 
-from .build import LIB_PATH
+from .build import LIB_PATH, NATIVE_PATH
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                       "exl3.h")
@@ -174,3 +174,22 @@ def status_string(s: int) -> str:
 def check(status: int, what: str):
     if status != EXL3_OK:
         raise Exl3Error(status, what)
+
+
+_native = None
+
+
+def native():
+    """_native.so: calls of the smallest operators on torch tensors, over the same
+    library (csrc/binding.cpp)."""
+    global _native
+    if _native is None:
+        lib()
+        if not os.path.exists(NATIVE_PATH):
+            raise ImportError(f"{NATIVE_PATH} is missing: build it with "
+                              "trellis_quantized_moe_exl3_gb300.build.build()")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location(__package__ + "._native", NATIVE_PATH)
+        _native = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_native)
+    return _native

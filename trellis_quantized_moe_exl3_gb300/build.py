@@ -1,4 +1,6 @@
-"""Build the CUDA library libexl3_gb300.so in-tree with nvcc (sm_103a only).
+"""Build the CUDA library libexl3_gb300.so in-tree with nvcc (sm_103a only), and
+_native.so, the Python calls of its smallest operators, with g++ against the
+installed torch.
 
 Every translation unit compiles in parallel; the link uses the static CUDA
 runtime so the library has no runtime search-path dependency.
@@ -10,11 +12,13 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libexl3_gb300.so")
+NATIVE_PATH = os.path.join(OUT_DIR, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]
@@ -36,6 +40,22 @@ def _stale(obj: str, src: str, headers) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(f) > t for f in [src] + headers)
+
+
+def _native_commands(tmp: str):
+    """Compile and link lines of _native.so."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    obj = os.path.join(OUT_DIR, "binding.o") + f".tmp{os.getpid()}"
+    inc = [os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return obj, ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+                 *[f"-I{i}" for i in inc], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj], \
+        ["g++", "-shared", obj, "-o", tmp, f"-L{OUT_DIR}", "-lexl3_gb300",
+         f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+         "-Wl,-rpath,$ORIGIN"]
 
 
 def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
@@ -66,14 +86,26 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         os.replace(cmd[-1], obj)
         return out
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    binding = os.path.join(CSRC, "binding.cpp")
+    native = native_obj = None
+    if force or jobs or _stale(NATIVE_PATH, binding, headers) or not os.path.exists(LIB_PATH):
+        native = NATIVE_PATH + f".tmp{os.getpid()}"
+        native_obj, compile_cmd, link_cmd = _native_commands(native)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        also = ex.submit(run, compile_cmd) if native else None
         for out in ex.map(compile_one, jobs):
             if verbose and out.strip():
                 print(out)
+        if also:
+            also.result()
     if force or jobs or not os.path.exists(LIB_PATH):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"])
         os.replace(tmp, LIB_PATH)
+    if native:
+        run(link_cmd)
+        os.remove(native_obj)
+        os.replace(native, NATIVE_PATH)
     return LIB_PATH
 
 

@@ -1,0 +1,226 @@
+// Python calls of the operators whose kernels take a few microseconds
+// (speculate.py), on torch tensors: checks, output tensors, the C ABI.  Written
+// against the interpreter and torch's C++ side because through ctypes and torch's
+// Python side a call's own cost was two to three times its kernel's (verification
+// 16 us around 5, a step of the pool 23 around 10).
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/exl3.h"
+
+namespace {
+
+PyObject* g_error;  // _lib.Exl3Error
+
+// Thrown where a Python exception has been set.
+struct Raised {};
+
+[[noreturn]] void raise(PyObject* type, const char* format, const char* name, const char* more = "") {
+  PyErr_Format(type, format, name, more);
+  throw Raised{};
+}
+
+const at::Tensor& tensor(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) raise(PyExc_TypeError, "%s must be a tensor", name);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_cuda()) raise(PyExc_ValueError, "%s must be a CUDA tensor", name);
+  return t;
+}
+// A contiguous vector of n values (n < 0: any number).
+const at::Tensor& vector(PyObject* o, const char* name, at::ScalarType type, int64_t n) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != type)
+    raise(PyExc_TypeError, "%s has another dtype than %s", name, c10::toString(type));
+  if (t.dim() != 1 || (n >= 0 && t.size(0) != n))
+    raise(PyExc_ValueError, "%s has the wrong shape", name);
+  if (!t.is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", name);
+  return t;
+}
+int64_t whole(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+template <class T>
+T* address(PyObject* o) {
+  void* p = PyLong_AsVoidPtr(o);
+  if (!p && PyErr_Occurred()) throw Raised{};
+  return static_cast<T*>(p);
+}
+
+// The stream of a call: stream= (an object with a cuda_stream) or the device's
+// current one.  Outputs are made on it, and are for use on the current one later.
+struct Stream {
+  c10::cuda::CUDAStream current, launch;
+  bool other;
+  Stream(PyObject* given, const at::Tensor& t)
+      : current(c10::cuda::getCurrentCUDAStream(t.get_device())), launch(current), other(false) {
+    if (given == Py_None) return;
+    PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
+    if (!raw) throw Raised{};
+    const auto s = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(raw));
+    Py_DECREF(raw);
+    if (PyErr_Occurred()) throw Raised{};
+    launch = c10::cuda::getStreamFromExternal(s, t.get_device());
+    other = s != current.stream();
+  }
+  at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+    const auto options = at::TensorOptions().dtype(type).device(launch.device());
+    if (!other) return at::empty(shape, options);
+    c10::cuda::CUDAStreamGuard guard(launch);
+    at::Tensor t = at::empty(shape, options);
+    t.record_stream(current);
+    return t;
+  }
+};
+
+void check(exl3_status s, const char* what) {
+  if (s == EXL3_OK) return;
+  if (PyObject* e = PyObject_CallFunction(g_error, "is", (int)s, what)) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+  throw Raised{};
+}
+
+PyObject* tuple(std::initializer_list<at::Tensor> of) {
+  PyObject* r = PyTuple_New((Py_ssize_t)of.size());
+  if (!r) throw Raised{};
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : of) PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t));
+  return r;
+}
+
+// [rows, vocab] probabilities (vocab < 0: any): the row stride.
+int64_t rows_of(const at::Tensor& x, const char* name, int64_t rows, int64_t vocab) {
+  if (x.scalar_type() != at::kFloat && x.scalar_type() != at::kHalf &&
+      x.scalar_type() != at::kBFloat16)
+    raise(PyExc_TypeError, "%s must be fp32, fp16 or bf16", name);
+  if (x.dim() != 2 || x.size(0) != rows || (vocab >= 0 && x.size(1) != vocab) ||
+      (x.stride(1) != 1 && x.size(1) > 1))
+    raise(PyExc_ValueError, "%s must be [rows, vocab] with contiguous rows: a row per draft (q), and "
+                            "one more per sequence (p)", name);
+  return rows > 1 ? x.stride(0) : x.size(1);
+}
+
+// (p, draft, cu_draft, accept_u, sample_u, q, stream)
+PyObject* verify_drafts(PyObject* const* a) {
+  const at::Tensor& draft = vector(a[1], "draft", at::kInt, -1);
+  const at::Tensor& su = vector(a[4], "sample_u", at::kFloat, -1);
+  const int64_t D = draft.size(0), B = su.size(0);
+  const at::Tensor& p = tensor(a[0], "p");
+  const int64_t ps = rows_of(p, "p", D + B, -1), vocab = p.size(1);
+  const void* q = nullptr;
+  int64_t qs = 0;
+  if (a[5] != Py_None) {
+    const at::Tensor& t = tensor(a[5], "q");
+    qs = rows_of(t, "q", D, vocab);
+    if (t.scalar_type() != p.scalar_type())
+      raise(PyExc_ValueError, "%s must have the same dtype", "p and q");
+    if (D > 0) q = t.data_ptr();
+  }
+  const at::Tensor& cu = vector(a[2], "cu_draft", at::kInt, B + 1);
+  const at::Tensor& au = vector(a[3], "accept_u", at::kFloat, D);
+  if (D > INT32_MAX || B > INT32_MAX || vocab > INT32_MAX)
+    raise(PyExc_ValueError, "%s has too many rows or columns", "p");
+  const Stream st(a[6], p);
+  at::Tensor tokens = st.empty({D + B}, at::kInt), accepted = st.empty({B}, at::kInt),
+             dropped = st.empty({B}, at::kInt);
+  const exl3_dtype dt = p.scalar_type() == at::kFloat  ? EXL3_F32
+                        : p.scalar_type() == at::kHalf ? EXL3_F16
+                                                       : EXL3_BF16;
+  check(exl3_verify_drafts(p.data_ptr(), ps, q, qs, dt, (int)vocab, (int)B, (int)D,
+                           static_cast<const int32_t*>(cu.data_ptr()),
+                           static_cast<const int32_t*>(draft.data_ptr()),
+                           static_cast<const float*>(au.data_ptr()),
+                           static_cast<const float*>(su.data_ptr()),
+                           static_cast<int32_t*>(tokens.data_ptr()),
+                           static_cast<int32_t*>(accepted.data_ptr()),
+                           static_cast<int32_t*>(dropped.data_ptr()), st.launch.stream()),
+        "exl3_verify_drafts");
+  return tuple({tokens, accepted, dropped});
+}
+
+const at::Tensor& rows_named(PyObject* o, const exl3_page_pool* pool) {
+  const at::Tensor& seqs = vector(o, "seqs", at::kInt, -1);
+  if (seqs.size(0) > pool->max_seqs) raise(PyExc_ValueError, "%s names more rows than the pool has", "seqs");
+  return seqs;
+}
+
+// (pool, ws, ws_bytes, seqs, q_lens, max_tokens, stream), the first three as numbers
+PyObject* pages_extend(PyObject* const* a) {
+  const auto* pool = address<exl3_page_pool>(a[0]);
+  const at::Tensor& seqs = rows_named(a[3], pool);
+  const int64_t n = seqs.size(0), tokens = whole(a[5]);
+  const at::Tensor& q = vector(a[4], "q_lens", at::kInt, n);
+  if (tokens < 0 || tokens > INT32_MAX)
+    raise(PyExc_ValueError, "%s must not be negative", "max_tokens");
+  const Stream st(a[6], seqs);
+  // (a tensor each: views of one take longer to make than their memory)
+  at::Tensor cu = st.empty({n + 1}, at::kInt), lens = st.empty({n}, at::kInt),
+             table = st.empty({n, pool->max_pages}, at::kInt), pos = st.empty({tokens}, at::kInt),
+             slots = st.empty({tokens}, at::kLong);
+  check(exl3_pages_extend(pool, (int)n, static_cast<const int32_t*>(seqs.data_ptr()),
+                          static_cast<const int32_t*>(q.data_ptr()), (int)tokens,
+                          static_cast<int32_t*>(cu.data_ptr()),
+                          static_cast<int32_t*>(lens.data_ptr()),
+                          static_cast<int32_t*>(table.data_ptr()),
+                          static_cast<int32_t*>(pos.data_ptr()),
+                          static_cast<int64_t*>(slots.data_ptr()), address<void>(a[1]),
+                          (size_t)whole(a[2]), st.launch.stream()),
+        "exl3_pages_extend");
+  return tuple({cu, lens, table, pos, slots});
+}
+
+// (pool, ws, ws_bytes, seqs, drop, stream)
+PyObject* pages_trim(PyObject* const* a) {
+  const auto* pool = address<exl3_page_pool>(a[0]);
+  const at::Tensor& seqs = rows_named(a[3], pool);
+  const int32_t* drop = nullptr;
+  if (a[4] != Py_None)
+    drop = static_cast<const int32_t*>(vector(a[4], "drop", at::kInt, seqs.size(0)).data_ptr());
+  const Stream st(a[5], seqs);
+  check(exl3_pages_trim(pool, (int)seqs.size(0), static_cast<const int32_t*>(seqs.data_ptr()), drop,
+                        address<void>(a[1]), (size_t)whole(a[2]), st.launch.stream()),
+        "exl3_pages_trim");
+  Py_RETURN_NONE;
+}
+
+template <PyObject* (*F)(PyObject* const*), int N>
+PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "%d arguments, not %zd", N, n);
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const Raised&) {
+  } catch (const std::exception& e) {  // torch's own (no memory)
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+template <PyObject* (*F)(PyObject* const*), int N>
+PyMethodDef method(const char* name) {
+  return PyMethodDef{name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<F, N>)),
+                     METH_FASTCALL, nullptr};
+}
+
+PyMethodDef g_methods[] = {method<verify_drafts, 7>("verify_drafts"),
+                           method<pages_extend, 7>("pages_extend"),
+                           method<pages_trim, 6>("pages_trim"),
+                           {nullptr, nullptr, 0, nullptr}};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods,
+                        nullptr,               nullptr,   nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__native() {
+  PyObject* lib = PyImport_ImportModule("trellis_quantized_moe_exl3_gb300._lib");
+  if (!lib) return nullptr;
+  g_error = PyObject_GetAttrString(lib, "Exl3Error");
+  Py_DECREF(lib);
+  return g_error ? PyModule_Create(&g_module) : nullptr;
+}

@@ -18,18 +18,12 @@ import struct
 import torch
 
 from . import _lib
-from ._lib import check
 from .api import device_status
-from .attention import PagedBatch, _capturing, _cuda, _dense, _empty, _stream
-
-_PROBS = {torch.float16: _lib.EXL3_F16, torch.bfloat16: _lib.EXL3_BF16,
-          torch.float32: _lib.EXL3_F32}
-
+from .attention import PagedBatch, _capturing
 
 # exl3_kv_batch as C lays it out, packed bytes for the call's own cost
 _BATCH = struct.Struct("@iiiqQQQ")
 assert _BATCH.size == ctypes.sizeof(_lib.KVBatch)
-_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
 class PagedStep(PagedBatch):
@@ -78,19 +72,11 @@ class PagePool:
         d.num_pages, d.page_size, d.max_seqs, d.max_pages = num_pages, page_size, max_seqs, max_pages
         d.table, d.lens = self.table.data_ptr(), self.lens.data_ptr()
         d.free, d.count = self.free.data_ptr() or None, self.count.data_ptr()
-        self._d, self._ref = d, ctypes.byref(d)
+        self._d, self._at = d, ctypes.addressof(d)
         self._ws, self._ws_bytes = self.ws.data_ptr(), n
         if not _capturing():  # calls on other streams find it made
             torch.cuda.current_stream(device).synchronize()
-        self._extend, self._trim = _lib.lib().exl3_pages_extend, _lib.lib().exl3_pages_trim
-
-    def _seqs(self, seqs):
-        shape = seqs.shape
-        if seqs.dtype != _I32 or len(shape) != 1 or not seqs.is_cuda or not seqs.is_contiguous() or \
-                shape[0] > self.max_seqs:
-            _cuda(seqs, "seqs", _I32)
-            raise ValueError(f"seqs must be a contiguous tensor of at most {self.max_seqs} rows")
-        return shape[0]
+        self._native = _lib.native()
 
     def extend(self, seqs, q_lens, max_q: int, max_tokens: int, stream=None) -> PagedStep:
         """Begins a step: row seqs[i] of the pool gets q_lens[i] new tokens and the
@@ -98,40 +84,13 @@ class PagePool:
         tensors, at least the sum of q_lens; max_q: as PagedBatch's.  A sequence
         for which there are no pages left keeps its rows, but has length 0 in the
         step and stays as it was in the pool."""
-        n = self._seqs(seqs)
-        if q_lens.dtype != _I32 or q_lens.shape != (n,) or not q_lens.is_cuda or \
-                not q_lens.is_contiguous():
-            _dense(q_lens, "q_lens", torch.int32, (n,))
-        if max_tokens < 0:
-            raise ValueError("max_tokens must not be negative")
-        dev = seqs.device
-        # (a tensor each: views of one take longer to make than their memory)
-        if stream is None:
-            cu_q = torch.empty(n + 1, dtype=_I32, device=dev)
-            seq_lens = torch.empty(n, dtype=_I32, device=dev)
-            table = torch.empty((n, self.max_pages), dtype=_I32, device=dev)
-            positions = torch.empty(max_tokens, dtype=_I32, device=dev)
-            slots = torch.empty(max_tokens, dtype=_I64, device=dev)
-        else:
-            cu_q, seq_lens = _empty(n + 1, _I32, dev, stream), _empty(n, _I32, dev, stream)
-            table = _empty((n, self.max_pages), _I32, dev, stream)
-            positions = _empty(max_tokens, _I32, dev, stream)
-            slots = _empty(max_tokens, _I64, dev, stream)
-        check(self._extend(
-            self._ref, n, seqs.data_ptr(), q_lens.data_ptr(), max_tokens, cu_q.data_ptr(),
-            seq_lens.data_ptr(), table.data_ptr(), positions.data_ptr(), slots.data_ptr(), self._ws,
-            self._ws_bytes, _stream(stream, seqs)), "exl3_pages_extend")
-        return PagedStep(cu_q, seq_lens, table, positions, slots, int(max_q))
+        return PagedStep(*self._native.pages_extend(self._at, self._ws, self._ws_bytes, seqs, q_lens,
+                                                    max_tokens, stream), int(max_q))
 
     def trim(self, seqs, drop=None, stream=None):
         """Takes the last drop[i] tokens (None: all) of row seqs[i] off and gives
         back the pages that hold nothing any more."""
-        n = self._seqs(seqs)
-        if drop is not None and (drop.dtype != torch.int32 or drop.shape != (n,) or
-                                 not drop.is_cuda or not drop.is_contiguous()):
-            _dense(drop, "drop", torch.int32, (n,))
-        check(self._trim(self._ref, n, seqs.data_ptr(), drop.data_ptr() if drop is not None else None,
-                         self._ws, self._ws_bytes, _stream(stream, seqs)), "exl3_pages_trim")
+        self._native.pages_trim(self._at, self._ws, self._ws_bytes, seqs, drop, stream)
 
     def status(self, stream=None) -> int:
         """The status bits set so far (0: fine); see exl3.h."""
@@ -143,24 +102,6 @@ class PagePool:
         wait(self.ws.device)
         self.ws[:4].zero_()
         wait(self.ws.device)
-
-
-def _rows(x, name, rows, vocab=None):
-    """Checks a [rows, vocab] tensor of probabilities; its row stride."""
-    if x.dtype not in _PROBS or not x.is_cuda:
-        _cuda(x, name, tuple(_PROBS))
-    shape, stride = x.shape, x.stride()
-    if len(shape) != 2 or shape[0] != rows or (vocab is not None and shape[1] != vocab) or \
-            (stride[1] != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be [{rows}, {vocab or 'vocab'}] with contiguous rows, not "
-                         f"{tuple(shape)}")
-    return stride[0] if rows > 1 else shape[1]
-
-
-def _vector(x, name, dtype, n):
-    if x.dtype != dtype or x.shape != (n,) or not (x.is_cuda and x.is_contiguous()):
-        _dense(x, name, dtype, (n,))
-    return x.data_ptr()
 
 
 def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None):
@@ -182,24 +123,4 @@ def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None):
     Returns int32 (tokens [drafts + sequences], accepted [sequences], dropped
     [sequences]): from place cu_draft[b] + b on, the accepted drafts, the drawn
     token, then -1; accepted drafts, and the others (what PagePool.trim takes)."""
-    D, B = draft.shape[0], sample_u.shape[0]
-    ps, qp, qs, dtype = _rows(p, "p", D + B), None, 0, p.dtype
-    vocab = p.shape[1]
-    if q is not None:
-        qs = _rows(q, "q", D, vocab)
-        if q.dtype != dtype:
-            raise ValueError("p and q must have the same dtype")
-        qp = q.data_ptr() if D else None
-    cu, dr = _vector(cu_draft, "cu_draft", _I32, B + 1), _vector(draft, "draft", _I32, D)
-    au, su = _vector(accept_u, "accept_u", _F32, D), _vector(sample_u, "sample_u", _F32, B)
-    dev = p.device
-    if stream is None:
-        tokens = torch.empty(D + B, dtype=_I32, device=dev)
-        accepted = torch.empty(B, dtype=_I32, device=dev)
-        dropped = torch.empty(B, dtype=_I32, device=dev)
-    else:
-        tokens, accepted, dropped = (_empty(x, _I32, dev, stream) for x in (D + B, B, B))
-    check(_lib.lib().exl3_verify_drafts(
-        p.data_ptr(), ps, qp, qs, _PROBS[dtype], vocab, B, D, cu, dr, au, su, tokens.data_ptr(),
-        accepted.data_ptr(), dropped.data_ptr(), _stream(stream, p)), "exl3_verify_drafts")
-    return tokens, accepted, dropped
+    return _lib.native().verify_drafts(p, draft, cu_draft, accept_u, sample_u, q, stream)
