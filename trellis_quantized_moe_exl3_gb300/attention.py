@@ -125,15 +125,15 @@ class PagedKVCache:
         d.k, d.v, d.dtype = k.data_ptr(), v.data_ptr(), _CODES[k.dtype]
         d.num_pages, d.page_size, d.kv_heads, d.head_dim = k.shape
         d.page_stride, d.token_stride, d.head_stride = _strides(k)
-        self._scales = ()  # a pointer to exl3_kv_scales, where there are block scales
+        self._scales, self._scales_at = None, 0  # exl3_kv_scales, where there are block scales
         if self.block_scales:
-            e = _lib.KVScales(k_scale.data_ptr(), v_scale.data_ptr(),
-                              k_scale.stride(0) if k.shape[0] > 1 else k.shape[2])
-            self._scales = (ctypes.pointer(e),)
+            self._scales = _lib.KVScales(k_scale.data_ptr(), v_scale.data_ptr(),
+                                         k_scale.stride(0) if k.shape[0] > 1 else k.shape[2])
+            self._scales_at = ctypes.addressof(self._scales)
         else:
             d.k_scale = k_scale.data_ptr() if k_scale is not None else None
             d.v_scale = v_scale.data_ptr() if v_scale is not None else None
-        self._d, self._ref = d, ctypes.byref(d)
+        self._d, self._ref, self._at = d, ctypes.byref(d), ctypes.addressof(d)
         self._spaces = {}  # raw stream -> the workspace of its calls
         self._all = []     # every one so far: a graph may hold an outgrown one
         self._spaces[_current_stream(k.get_device())] = self._space(_lib.EXL3_ATTENTION_HEAD_BYTES)
@@ -236,7 +236,7 @@ class PagedBatch:
         d.table_stride = block_table.stride(0)
         d.cu_q, d.seq_lens = cu_q.data_ptr(), seq_lens.data_ptr()
         d.block_table = block_table.data_ptr()
-        self._d, self._ref = d, ctypes.byref(d)
+        self._d, self._ref, self._at = d, ctypes.byref(d), ctypes.addressof(d)
 
 
 def _strides(t):
@@ -340,27 +340,12 @@ def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_wei
     in the sequence).  A value past the E4M3 range saturates.  A cache with
     block scales keeps them on the way: a block's scale grows until 448 of it
     covers the new values, its older tokens brought along."""
-    dim, dtype = cache.head_dim, k.dtype
-    T, H, ts, hs = _act(k, "k", dim)
-    Tv, Hv, tv, hv = _act(v, "v", dim)
-    if v.dtype != dtype or Tv != T or H != cache.kv_heads or Hv != H:
-        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one dtype")
-    pk = _HEADS.pack(k.data_ptr(), 0, _weight(k_weight, "k_weight", dtype, dim), H, ts, hs, 0, 0)
-    pv = _HEADS.pack(v.data_ptr(), 0, 0, H, tv, hv, 0, 0)
-    pq = None
-    if q is not None:
-        Tq, Hq, ts, hs = _act(q, "q", dim)
-        if Tq != T or q.dtype != dtype:
-            raise ValueError("q and k must have the same dtype and tokens")
-        q_out, p, ots, ohs = _out(q_out, q, T, Hq, dim, "q_out", stream)
-        pq = _HEADS.pack(q.data_ptr(), p, _weight(q_weight, "q_weight", dtype, dim), Hq, ts, hs, ots,
-                         ohs)
+    if not k.is_cuda:
+        _cuda(k, "k", _ACT)
     raw = _stream(stream, k)
-    fn = _lib.lib().exl3_kv_append_blocks if cache._scales else _lib.lib().exl3_kv_append
-    check(fn(cache._ref, *cache._scales, batch._ref, pq, pk, pv, _ACT[dtype], T,
-             _rope(inv_freq, interleaved), _positions(positions, T), eps,
-             (cache._spaces.get(raw) or cache._room(stream, raw, None)).ptr, raw), fn.__name__)
-    return q_out
+    w = cache._spaces.get(raw) or cache._room(stream, raw, None)
+    return _lib.native().kv_append(cache._at, cache._scales_at, batch._at, k, v, inv_freq, k_weight, q,
+                                   q_weight, q_out, positions, eps, interleaved, w.ptr, stream)
 
 
 def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causal: bool = True,
@@ -381,24 +366,16 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
     if not q.is_cuda:
         _cuda(q, "q", _ACT)
     dim = cache.head_dim
-    T, heads, ts, hs = _act(q, "q", dim)
-    raw = _stream(stream, q)
     if ws is None:
-        w, size = cache._spaces.get(raw), (T, heads, batch.num_seqs)
+        raw = _stream(stream, q)
+        w, size = cache._spaces.get(raw), (*q.shape[:2], batch.num_seqs)
         if w is None or w.fits != size:
+            _act(q, "q", dim)
             w = cache._room(stream, raw, size)
         ws_ptr, ws_bytes = w.ptr, w.bytes
     else:
         _dense(ws, "ws", torch.uint8, ws.shape)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
-    if out is None:
-        out = _like(q, stream)
-    else:
-        _dense(out, "out", q.dtype, (T, heads, dim))
-    lse = _empty((T, heads), torch.float32, q.device, stream) if return_lse else None
-    fn = _lib.lib().exl3_paged_attention_blocks if cache._scales else _lib.lib().exl3_paged_attention
-    check(fn(
-        cache._ref, *cache._scales, batch._ref, q.data_ptr(), ts, hs, _ACT[q.dtype], T, heads,
-        dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), path, ws_ptr, ws_bytes, raw), fn.__name__)
-    return (out, lse) if return_lse else out
+    return _lib.native().paged_attention(cache._at, cache._scales_at, batch._at, q,
+                                         dim ** -0.5 if scale is None else scale, causal, window, out,
+                                         return_lse, path, ws_ptr, ws_bytes, stream)

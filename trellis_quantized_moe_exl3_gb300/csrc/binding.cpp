@@ -1,8 +1,9 @@
 // Python calls of the operators whose kernels take a few microseconds
-// (speculate.py), on torch tensors: checks, output tensors, the C ABI.  Written
-// against the interpreter and torch's C++ side because through ctypes and torch's
-// Python side a call's own cost was two to three times its kernel's (verification
-// 16 us around 5, a step of the pool 23 around 10).
+// (speculate.py; append and attention of attention.py), on torch tensors: checks,
+// output tensors, the C ABI.  Written against the interpreter and torch's C++ side
+// because through ctypes and torch's Python side a call's own cost was two to three
+// times its kernel's (verification 16 us around 5, a step of the pool 23 around 10,
+// the append of 64 tokens 15 around 4).
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -188,6 +189,147 @@ PyObject* pages_trim(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
+// ---- append and attention
+bool activation(const at::Tensor& t) {
+  return t.scalar_type() == at::kHalf || t.scalar_type() == at::kBFloat16;
+}
+exl3_dtype code_of(const at::Tensor& t) {
+  return t.scalar_type() == at::kHalf ? EXL3_F16 : EXL3_BF16;
+}
+// [tokens, heads, dim] activations with contiguous channels; the strides of a token
+// and a head (0 where a dimension of one leaves them open).
+const at::Tensor& heads_of(PyObject* o, const char* name, int64_t dim, int64_t* ts, int64_t* hs) {
+  const at::Tensor& t = tensor(o, name);
+  if (!activation(t)) raise(PyExc_TypeError, "%s must be fp16 or bf16", name);
+  if (t.dim() != 3 || t.size(2) != dim || (t.stride(2) != 1 && t.numel() > 0))
+    raise(PyExc_ValueError, "%s must be [tokens, heads, head_dim] with contiguous channels", name);
+  if (t.size(0) > INT32_MAX || t.size(1) > INT32_MAX)
+    raise(PyExc_ValueError, "%s has too many rows", name);
+  *ts = t.size(0) == 1 ? 0 : t.stride(0);
+  *hs = t.size(1) == 1 ? 0 : t.stride(1);
+  return t;
+}
+const void* weight_of(PyObject* o, const char* name, at::ScalarType type, int64_t dim) {
+  return o == Py_None ? nullptr : vector(o, name, type, dim).data_ptr();
+}
+// exl3_kv_batch: packed bytes or the address of one
+const exl3_kv_batch* batch_of(PyObject* o) {
+  return PyBytes_Check(o) ? reinterpret_cast<const exl3_kv_batch*>(PyBytes_AS_STRING(o))
+                          : address<const exl3_kv_batch>(o);
+}
+
+// (cache, scales, batch, k, v, inv_freq, k_weight, q, q_weight, q_out, positions, eps,
+//  interleaved, status, stream); cache, scales, batch and status as numbers
+PyObject* kv_append(PyObject* const* a) {
+  const auto* cache = address<const exl3_kv_cache>(a[0]);
+  const auto* scales = address<const exl3_kv_scales>(a[1]);
+  const int64_t dim = cache->head_dim;
+  exl3_heads k{}, v{}, q{};
+  const at::Tensor& kt = heads_of(a[3], "k", dim, &k.token_stride, &k.head_stride);
+  const at::Tensor& vt = heads_of(a[4], "v", dim, &v.token_stride, &v.head_stride);
+  const int64_t T = kt.size(0);
+  if (vt.scalar_type() != kt.scalar_type() || vt.size(0) != T || kt.size(1) != cache->kv_heads ||
+      vt.size(1) != kt.size(1))
+    raise(PyExc_ValueError, "%s must be [tokens, kv_heads, head_dim] of one dtype", "k and v");
+  k.x = kt.data_ptr();
+  v.x = vt.data_ptr();
+  k.heads = v.heads = (int)kt.size(1);
+  k.weight = weight_of(a[6], "k_weight", kt.scalar_type(), dim);
+  const Stream st(a[14], kt);
+  at::Tensor out;
+  if (a[7] != Py_None) {
+    const at::Tensor& qt = heads_of(a[7], "q", dim, &q.token_stride, &q.head_stride);
+    if (qt.scalar_type() != kt.scalar_type() || qt.size(0) != T)
+      raise(PyExc_ValueError, "%s must have the same dtype and tokens", "q and k");
+    q.x = qt.data_ptr();
+    q.heads = (int)qt.size(1);
+    q.weight = weight_of(a[8], "q_weight", qt.scalar_type(), dim);
+    if (a[9] == Py_None) {
+      out = st.empty(qt.sizes(), qt.scalar_type());
+      q.out_token_stride = qt.size(1) * dim;
+      q.out_head_stride = dim;
+    } else {
+      out = heads_of(a[9], "q_out", dim, &q.out_token_stride, &q.out_head_stride);
+      if (out.scalar_type() != qt.scalar_type() || out.sizes() != qt.sizes())
+        raise(PyExc_ValueError, "%s must have q's shape and dtype", "q_out");
+    }
+    q.out = out.data_ptr();
+  }
+  exl3_rope rope{};
+  if (a[5] != Py_None) {
+    const at::Tensor& f = vector(a[5], "inv_freq", at::kDouble, -1);
+    if (f.size(0) > INT32_MAX / 2) raise(PyExc_ValueError, "%s is too long", "inv_freq");
+    rope.inv_freq = static_cast<const double*>(f.data_ptr());
+    rope.rotary_dim = 2 * (int)f.size(0);
+    rope.interleaved = PyObject_IsTrue(a[12]);
+  }
+  const int32_t* positions =
+      a[10] == Py_None ? nullptr
+                       : static_cast<const int32_t*>(vector(a[10], "positions", at::kInt, T).data_ptr());
+  const double eps = PyFloat_AsDouble(a[11]);
+  if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
+  const exl3_heads* qp = a[7] != Py_None ? &q : nullptr;
+  const exl3_rope* rp = rope.inv_freq || a[5] != Py_None ? &rope : nullptr;
+  if (scales)
+    check(exl3_kv_append_blocks(cache, scales, batch_of(a[2]), qp, &k, &v, code_of(kt), (int)T, rp,
+                                positions, (float)eps, address<int32_t>(a[13]), st.launch.stream()),
+          "exl3_kv_append_blocks");
+  else
+    check(exl3_kv_append(cache, batch_of(a[2]), qp, &k, &v, code_of(kt), (int)T, rp, positions,
+                         (float)eps, address<int32_t>(a[13]), st.launch.stream()),
+          "exl3_kv_append");
+  if (!out.defined()) {  // (no q: what was given as its place comes back)
+    Py_INCREF(a[9]);
+    return a[9];
+  }
+  return THPVariable_Wrap(out);
+}
+
+// (cache, scales, batch, q, scale, causal, window, out, return_lse, path, ws, ws_bytes,
+//  stream); cache, scales, batch and ws as numbers
+PyObject* paged_attention(PyObject* const* a) {
+  const auto* cache = address<const exl3_kv_cache>(a[0]);
+  const auto* scales = address<const exl3_kv_scales>(a[1]);
+  const int64_t dim = cache->head_dim;
+  int64_t ts, hs;
+  const at::Tensor& q = heads_of(a[3], "q", dim, &ts, &hs);
+  const double scale = PyFloat_AsDouble(a[4]);
+  if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
+  const int64_t window = whole(a[6]), path = whole(a[9]);
+  const bool with_lse = PyObject_IsTrue(a[8]);
+  if (window < INT32_MIN || window > INT32_MAX || path < INT32_MIN || path > INT32_MAX)
+    raise(PyExc_ValueError, "%s out of range", "window or path");
+  const Stream st(a[12], q);
+  at::Tensor out;
+  if (a[7] == Py_None) {
+    out = st.empty(q.sizes(), q.scalar_type());
+  } else {
+    out = tensor(a[7], "out");
+    if (out.scalar_type() != q.scalar_type()) raise(PyExc_TypeError, "%s must have q's dtype", "out");
+    if (out.sizes() != q.sizes()) raise(PyExc_ValueError, "%s must have q's shape", "out");
+    if (!out.is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", "out");
+  }
+  at::Tensor lse;
+  if (with_lse) lse = st.empty({q.size(0), q.size(1)}, at::kFloat);
+  float* l = with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
+  void* const ws = address<void>(a[10]);
+  const size_t bytes = (size_t)whole(a[11]);
+  const int causal = PyObject_IsTrue(a[5]);
+  if (scales)
+    check(exl3_paged_attention_blocks(cache, scales, batch_of(a[2]), q.data_ptr(), ts, hs, code_of(q),
+                                      (int)q.size(0), (int)q.size(1), (float)scale, causal,
+                                      (int)window, out.data_ptr(), l, (int)path, ws, bytes,
+                                      st.launch.stream()),
+          "exl3_paged_attention_blocks");
+  else
+    check(exl3_paged_attention(cache, batch_of(a[2]), q.data_ptr(), ts, hs, code_of(q),
+                               (int)q.size(0), (int)q.size(1), (float)scale, causal, (int)window,
+                               out.data_ptr(), l, (int)path, ws, bytes, st.launch.stream()),
+          "exl3_paged_attention");
+  if (with_lse) return tuple({out, lse});
+  return THPVariable_Wrap(out);
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
@@ -211,6 +353,8 @@ PyMethodDef method(const char* name) {
 PyMethodDef g_methods[] = {method<verify_drafts, 7>("verify_drafts"),
                            method<pages_extend, 7>("pages_extend"),
                            method<pages_trim, 6>("pages_trim"),
+                           method<kv_append, 15>("kv_append"),
+                           method<paged_attention, 13>("paged_attention"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods,
                         nullptr,               nullptr,   nullptr, nullptr};

@@ -36,8 +36,8 @@ class PagedStep(PagedBatch):
         self.positions, self.slots = positions, slots
         n, m = block_table.shape
         self.num_seqs, self.max_q = n, max_q
-        self._ref = _BATCH.pack(n, max_q, m, m, cu_q.data_ptr(), seq_lens.data_ptr(),
-                                block_table.data_ptr())
+        self._at = self._ref = _BATCH.pack(n, max_q, m, m, cu_q.data_ptr(), seq_lens.data_ptr(),
+                                           block_table.data_ptr())
 
 
 class PagePool:
