@@ -365,18 +365,20 @@ __device__ __forceinline__ Cut cut_warp(const AttnParams& p, int32_t* bad) {
   Cut c{};
   c.total = __shfl_sync(0xffffffffu, inc, 31);
   const long long base = inc - s.w;
-  const long long room = C::kGrid - units;
-  long long g = 0;
-  if (units <= C::kGrid / 2) {
-    g = (c.total + room - 1) / room;
-    if (g * units > (long long)C::kExtra * C::kGrid) g = 0;
+  // (in 32 bits: four 64-bit divisions in a row took 0.6 us)
+  const unsigned total = (unsigned)c.total, room = C::kGrid - units;
+  unsigned g = 0;
+  if (units <= C::kGrid / 2 && c.total < (1ll << 31)) {
+    g = (total + room - 1) / room;
+    if (g > (unsigned)(C::kExtra * C::kGrid)) g = 0;
+    if (g * units > (unsigned)(C::kExtra * C::kGrid)) g = 0;
   }
   if (g > 0) {
     // us of one token, one sequence of 16 granules, pieces of 1 / 2 / 4 / 8: 9.4 / 9.4
     // / 10.3 / 12.1; of 62, 1 / 2 / 4 / 8: 13.0 / 11.7 / 11.0 / 12.2; of 8, 1 / 8: 9.1
     // / 7.5 (64 channels); no more parts than are joined in one step
     const int least = s.n <= 8 ? 8 : max(s.n < 48 ? 2 : 4, (s.n + C::kFlat - 1) / C::kFlat);
-    g = max(g, (long long)least);
+    g = max(g, (unsigned)least);
     const int k = live ? (int)((s.n + g - 1) / g) : 0, mine = u * k;
     int end = mine;
 #pragma unroll
@@ -391,8 +393,10 @@ __device__ __forceinline__ Cut cut_warp(const AttnParams& p, int32_t* bad) {
     if (x >= 0 && x < mine) {
       const int unit = x / k, i = x - unit * k;
       const long long u0 = base + (long long)unit * s.n;
-      c.pos = u0 + (long long)s.n * i / k;
-      c.end = u0 + (long long)s.n * (i + 1) / k;
+      // (n / k of them each, one more for the first n % k)
+      const int each = s.n / k, more = s.n - each * k;
+      c.pos = u0 + each * i + min(i, more);
+      c.end = c.pos + each + (i < more);
       c.c0 = (int)blockIdx.x - i;
       c.np = k;
     }
@@ -499,7 +503,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtasPerSm) attn_rows_kernel(Attn
       b++;
       continue;
     }
-    const int u = (int)((pos - base) / sw.n), g0 = (int)((pos - base) % sw.n);
+    const unsigned long long at = pos - base;
+    const int u = at >> 32 ? (int)(at / sw.n) : (int)((unsigned)at / (unsigned)sw.n);
+    const int g0 = (int)(at - (unsigned long long)u * sw.n);
     const long long u0 = base + (long long)u * sw.n;  // the unit's place on the line
     const int cnt = (int)min((long long)(sw.n - g0), rest.end - pos);
     const int h = u / sw.rc, rc = u % sw.rc;

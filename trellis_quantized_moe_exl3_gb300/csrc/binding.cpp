@@ -5,6 +5,7 @@
 // times its kernel's (verification 16 us around 5, a step of the pool 23 around 10,
 // the append of 64 tokens 15 around 4).
 #include <ATen/ops/empty.h>
+#include <array>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -67,6 +68,29 @@ struct Stream {
     launch = c10::cuda::getStreamFromExternal(s, t.get_device());
     other = s != current.stream();
   }
+  // Tensors of 32-bit words (the first of 64-bit ones where asked) side by side in
+  // one allocation: each one's own costs as much as the rest of a small call.
+  template <int N>
+  std::array<at::Tensor, N> words(const at::IntArrayRef (&shapes)[N], bool first64 = false) const {
+    int64_t at[N], n = 0;
+    for (int i = 0; i < N; i++) {
+      at[i] = n;
+      int64_t size = 1;
+      for (const int64_t d : shapes[i]) size *= d;
+      n += ((first64 && i == 0 ? 2 * size : size) + 3) & ~(int64_t)3;  // 16 bytes aligned
+    }
+    const at::Tensor all = empty({n}, at::kInt);
+    std::array<at::Tensor, N> r;
+    for (int i = 0; i < N; i++) {
+      const bool wide = first64 && i == 0;
+      r[i] = at::detail::make_tensor<c10::TensorImpl>(
+          c10::Storage(all.storage()), all.key_set(),
+          caffe2::TypeMeta::fromScalarType(wide ? at::kLong : at::kInt));
+      r[i].unsafeGetTensorImpl()->set_sizes_contiguous(shapes[i]);
+      r[i].unsafeGetTensorImpl()->set_storage_offset(wide ? at[i] / 2 : at[i]);
+    }
+    return r;
+  }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
     const auto options = at::TensorOptions().dtype(type).device(launch.device());
     if (!other) return at::empty(shape, options);
@@ -127,8 +151,7 @@ PyObject* verify_drafts(PyObject* const* a) {
   if (D > INT32_MAX || B > INT32_MAX || vocab > INT32_MAX)
     raise(PyExc_ValueError, "%s has too many rows or columns", "p");
   const Stream st(a[6], p);
-  at::Tensor tokens = st.empty({D + B}, at::kInt), accepted = st.empty({B}, at::kInt),
-             dropped = st.empty({B}, at::kInt);
+  const auto [tokens, accepted, dropped] = st.words<3>({{D + B}, {B}, {B}});
   const exl3_dtype dt = p.scalar_type() == at::kFloat  ? EXL3_F32
                         : p.scalar_type() == at::kHalf ? EXL3_F16
                                                        : EXL3_BF16;
@@ -159,10 +182,8 @@ PyObject* pages_extend(PyObject* const* a) {
   if (tokens < 0 || tokens > INT32_MAX)
     raise(PyExc_ValueError, "%s must not be negative", "max_tokens");
   const Stream st(a[6], seqs);
-  // (a tensor each: views of one take longer to make than their memory)
-  at::Tensor cu = st.empty({n + 1}, at::kInt), lens = st.empty({n}, at::kInt),
-             table = st.empty({n, pool->max_pages}, at::kInt), pos = st.empty({tokens}, at::kInt),
-             slots = st.empty({tokens}, at::kLong);
+  const auto [slots, pos, cu, lens, table] =
+      st.words<5>({{tokens}, {tokens}, {n + 1}, {n}, {n, pool->max_pages}}, true);
   check(exl3_pages_extend(pool, (int)n, static_cast<const int32_t*>(seqs.data_ptr()),
                           static_cast<const int32_t*>(q.data_ptr()), (int)tokens,
                           static_cast<int32_t*>(cu.data_ptr()),

@@ -36,7 +36,7 @@ struct Rec {
 };
 
 struct PoolParams {
-  int num_pages, page_size, max_seqs, max_pages;
+  int num_pages, page_size, page_shift, max_seqs, max_pages;
   int32_t* table;
   int32_t* lens;
   int32_t* free;
@@ -55,7 +55,12 @@ struct PoolParams {
   Rec* rec;        // [num]
 };
 
-__device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
+// (a page size is a multiple of 16, most often a power of two)
+struct Page {
+  int size, shift;  // shift: log2 of the size, -1 if it is no power of two
+  __device__ int of(int pos) const { return shift >= 0 ? pos >> shift : pos / size; }
+};
+__device__ __forceinline__ int pages_of(int len, Page page) { return page.of(len + page.size - 1); }
 
 // Inclusive scan of two values over the CTA; *total receives the sums.
 __device__ __forceinline__ longlong2 scan2(longlong2 v, longlong2* total) {
@@ -72,16 +77,23 @@ __device__ __forceinline__ longlong2 scan2(longlong2 v, longlong2* total) {
   __syncthreads();
   if (lane == 31) sums[warp] = v;
   __syncthreads();
-  longlong2 t = make_longlong2(0, 0);
-  for (int w = 0; w < kThreads / 32; w++) {
-    if (w == warp) {
-      v.x += t.x;
-      v.y += t.y;
+  longlong2 t = lane < kThreads / 32 ? sums[lane] : make_longlong2(0, 0);
+#pragma unroll
+  for (int m = 1; m < kThreads / 32; m <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, t.x, m), y = __shfl_up_sync(0xffffffffu, t.y, m);
+    if (lane >= m) {
+      t.x += x;
+      t.y += y;
     }
-    t.x += sums[w].x;
-    t.y += sums[w].y;
   }
-  *total = t;
+  const int last = kThreads / 32 - 1;
+  *total = make_longlong2(__shfl_sync(0xffffffffu, t.x, last), __shfl_sync(0xffffffffu, t.y, last));
+  const long long x = __shfl_sync(0xffffffffu, t.x, max(warp - 1, 0));
+  const long long y = __shfl_sync(0xffffffffu, t.y, max(warp - 1, 0));
+  if (warp > 0) {
+    v.x += x;
+    v.y += y;
+  }
   return v;
 }
 
@@ -131,9 +143,9 @@ __device__ __forceinline__ Rec load_rec(const PoolParams& p, int i) {
 
 // The scan (one CTA): lengths, records, the pool's new state.
 __device__ __forceinline__ void plan_extend(const PoolParams& p, int32_t* shared) {
-  const int P = p.page_size;
+  const Page P{p.page_size, p.page_shift};
   const int count = min(max(*p.count, 0), p.num_pages);
-  const long long most = min((long long)p.max_pages * P, (long long)kMaxLen);
+  const long long most = min((long long)p.max_pages * P.size, (long long)kMaxLen);
   const Claims claims(p, shared);
   int32_t bad = 0;
   longlong2 run = make_longlong2(0, 0), total;
@@ -199,7 +211,8 @@ __device__ __forceinline__ void plan_extend(const PoolParams& p, int32_t* shared
 template <int VEC>
 __device__ __forceinline__ void fill_rows(const PoolParams& p, int count, int me, int threads) {
   constexpr int U = 4, kItem = 32 * U * VEC;  // entries that a warp writes at a time
-  const int P = p.page_size, lane = me & 31;
+  const Page P{p.page_size, p.page_shift};
+  const int lane = me & 31;
   const long long per_row = (p.max_pages + kItem - 1) / kItem, items = per_row * p.num;
   for (long long it = me >> 5; it < items; it += threads >> 5) {
     const int i = (int)(it / per_row), k0 = (int)(it % per_row) * kItem + lane * VEC;
@@ -250,7 +263,8 @@ __device__ __forceinline__ void fill_rows(const PoolParams& p, int count, int me
   }
 }
 __device__ __forceinline__ void fill(const PoolParams& p, int me, int threads) {
-  const int P = p.page_size, count = __ldcg(p.status + 1);
+  const Page P{p.page_size, p.page_shift};
+  const int count = __ldcg(p.status + 1);
   // 16 bytes at a time where rows begin on 16 bytes
   if (p.max_pages % 4 == 0 &&
       ((reinterpret_cast<uintptr_t>(p.table) | reinterpret_cast<uintptr_t>(p.block_table)) & 15) == 0)
@@ -272,10 +286,10 @@ __device__ __forceinline__ void fill(const PoolParams& p, int me, int threads) {
       const Rec r = load_rec(p, lo);
       if (r.row >= 0) {
         pos = r.len + t - __ldcg(p.cu_q + lo);
-        const int k = pos / P, have = pages_of(r.len, P);
+        const int k = P.of(pos), have = pages_of(r.len, P);
         const int id = k < have ? p.table[(int64_t)r.row * p.max_pages + k]
                                 : p.free[count - 1 - r.first - (k - have)];
-        if (id >= 0) slot = (int64_t)id * P + pos % P;
+        if (id >= 0) slot = (int64_t)id * P.size + (pos - k * P.size);
       }
     }
     p.positions[t] = pos;
@@ -310,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(PoolParams p) {
   __shared__ int32_t owners[kOwners];
   pdl_wait();
   const int rank = blockIdx.x;
-  const int P = p.page_size;
+  const Page P{p.page_size, p.page_shift};
   if (rank == 0) {
     const Claims claims(p, owners);
     const int count = min(max(*p.count, 0), p.num_pages);
@@ -414,6 +428,7 @@ PoolParams params_of(const exl3_page_pool* o, int num, const int32_t* seqs, cons
   PoolParams p{};
   p.num_pages = o->num_pages;
   p.page_size = o->page_size;
+  p.page_shift = o->page_size & (o->page_size - 1) ? -1 : __builtin_ctz(o->page_size);
   p.max_seqs = o->max_seqs;
   p.max_pages = o->max_pages;
   p.table = o->table;
