@@ -110,11 +110,13 @@ void check(exl3_status s, const char* what) {
   throw Raised{};
 }
 
-PyObject* tuple(std::initializer_list<at::Tensor> of) {
-  PyObject* r = PyTuple_New((Py_ssize_t)of.size());
+// The tensors, and after them `last` (whose reference it takes) if there is one.
+PyObject* tuple(std::initializer_list<at::Tensor> of, PyObject* last = nullptr) {
+  PyObject* r = PyTuple_New((Py_ssize_t)of.size() + (last != nullptr));
   if (!r) throw Raised{};
   Py_ssize_t i = 0;
   for (const at::Tensor& t : of) PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t));
+  if (last) PyTuple_SET_ITEM(r, i, last);
   return r;
 }
 
@@ -173,15 +175,17 @@ const at::Tensor& rows_named(PyObject* o, const exl3_page_pool* pool) {
   return seqs;
 }
 
-// (pool, ws, ws_bytes, seqs, q_lens, max_tokens, stream), the first three as numbers
+// (pool, ws, ws_bytes, seqs, q_lens, max_tokens, max_q, stream), the first three as
+// numbers; the step's tensors and its exl3_kv_batch as bytes
 PyObject* pages_extend(PyObject* const* a) {
   const auto* pool = address<exl3_page_pool>(a[0]);
   const at::Tensor& seqs = rows_named(a[3], pool);
-  const int64_t n = seqs.size(0), tokens = whole(a[5]);
+  const int64_t n = seqs.size(0), tokens = whole(a[5]), max_q = whole(a[6]);
   const at::Tensor& q = vector(a[4], "q_lens", at::kInt, n);
   if (tokens < 0 || tokens > INT32_MAX)
     raise(PyExc_ValueError, "%s must not be negative", "max_tokens");
-  const Stream st(a[6], seqs);
+  if (max_q < 0 || max_q > INT32_MAX) raise(PyExc_ValueError, "%s must not be negative", "max_q");
+  const Stream st(a[7], seqs);
   const auto [slots, pos, cu, lens, table] =
       st.words<5>({{tokens}, {tokens}, {n + 1}, {n}, {n, pool->max_pages}}, true);
   check(exl3_pages_extend(pool, (int)n, static_cast<const int32_t*>(seqs.data_ptr()),
@@ -193,7 +197,16 @@ PyObject* pages_extend(PyObject* const* a) {
                           static_cast<int64_t*>(slots.data_ptr()), address<void>(a[1]),
                           (size_t)whole(a[2]), st.launch.stream()),
         "exl3_pages_extend");
-  return tuple({cu, lens, table, pos, slots});
+  exl3_kv_batch batch{};
+  batch.num_seqs = (int)n;
+  batch.max_q = (int)max_q;
+  batch.max_pages = pool->max_pages;
+  batch.table_stride = pool->max_pages;
+  batch.cu_q = static_cast<const int32_t*>(cu.data_ptr());
+  batch.seq_lens = static_cast<const int32_t*>(lens.data_ptr());
+  batch.block_table = static_cast<const int32_t*>(table.data_ptr());
+  return tuple({cu, lens, table, pos, slots},
+               PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&batch), sizeof batch));
 }
 
 // (pool, ws, ws_bytes, seqs, drop, stream)
@@ -372,7 +385,7 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<verify_drafts, 7>("verify_drafts"),
-                           method<pages_extend, 7>("pages_extend"),
+                           method<pages_extend, 8>("pages_extend"),
                            method<pages_trim, 6>("pages_trim"),
                            method<kv_append, 15>("kv_append"),
                            method<paged_attention, 13>("paged_attention"),

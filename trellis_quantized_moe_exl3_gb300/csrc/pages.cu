@@ -146,6 +146,8 @@ __device__ __forceinline__ void plan_extend(const PoolParams& p, int32_t* shared
   const Page P{p.page_size, p.page_shift};
   const int count = min(max(*p.count, 0), p.num_pages);
   const long long most = min((long long)p.max_pages * P.size, (long long)kMaxLen);
+  __shared__ int s_taken, s_bad;
+  if (threadIdx.x == 0) s_taken = s_bad = 0;
   const Claims claims(p, shared);
   int32_t bad = 0;
   longlong2 run = make_longlong2(0, 0), total;
@@ -191,9 +193,6 @@ __device__ __forceinline__ void plan_extend(const PoolParams& p, int32_t* shared
     run.x += total.x;
     run.y += total.y;
   }
-  __shared__ int s_taken, s_bad;
-  if (threadIdx.x == 0) s_taken = s_bad = 0;
-  __syncthreads();
   if (taken) atomicMax(&s_taken, taken);
   if (bad) atomicOr(&s_bad, bad);
   claims.end(p);
@@ -271,29 +270,46 @@ __device__ __forceinline__ void fill(const PoolParams& p, int me, int threads) {
     fill_rows<4>(p, count, me, threads);
   else
     fill_rows<1>(p, count, me, threads);
-  for (int t = me; t < p.max_tokens; t += threads) {
-    int lo = 0, hi = p.num;  // the last sequence that begins at or before t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldcg(p.cu_q + mid) <= t)
-        lo = mid;
-      else
-        hi = mid;
-    }
+  // place j of sequence i, in row t
+  auto put = [&](int t, int j, const Rec& r) {
     int pos = -1;
     int64_t slot = -1;
-    if (p.num > 0 && t < __ldcg(p.cu_q + lo + 1)) {
-      const Rec r = load_rec(p, lo);
-      if (r.row >= 0) {
-        pos = r.len + t - __ldcg(p.cu_q + lo);
-        const int k = P.of(pos), have = pages_of(r.len, P);
-        const int id = k < have ? p.table[(int64_t)r.row * p.max_pages + k]
-                                : p.free[count - 1 - r.first - (k - have)];
-        if (id >= 0) slot = (int64_t)id * P.size + (pos - k * P.size);
-      }
+    if (r.row >= 0) {
+      pos = r.len + j;
+      const int k = P.of(pos), have = pages_of(r.len, P);
+      const int id = k < have ? p.table[(int64_t)r.row * p.max_pages + k]
+                              : p.free[count - 1 - r.first - (k - have)];
+      if (id >= 0) slot = (int64_t)id * P.size + (pos - k * P.size);
     }
     p.positions[t] = pos;
     p.slots[t] = slot;
+  };
+  // (from the last warps on, while the first ones write table rows)
+  const int from = threads - 1 - me;
+  int all = p.num > 0 ? __ldcg(p.cu_q + p.num) : 0;  // rows that are some sequence's
+  if (p.max_tokens <= 64 * p.num) {
+    // few tokens each: a warp per sequence
+    for (int i = from >> 5; i < p.num; i += threads >> 5) {
+      const Rec r = load_rec(p, i);
+      const int t0 = __ldcg(p.cu_q + i), n = __ldcg(p.cu_q + i + 1) - t0;
+      for (int j = from & 31; j < n; j += 32) put(t0 + j, j, r);
+    }
+  } else {
+    for (int t = from; t < all; t += threads) {
+      int lo = 0, hi = p.num;  // the last sequence that begins at or before t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldcg(p.cu_q + mid) <= t)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      put(t, t - __ldcg(p.cu_q + lo), load_rec(p, lo));
+    }
+  }
+  for (int t = all + from; t < p.max_tokens; t += threads) {
+    p.positions[t] = -1;
+    p.slots[t] = -1;
   }
 }
 
@@ -301,11 +317,8 @@ __device__ __forceinline__ void fill(const PoolParams& p, int me, int threads) {
 __global__ void __launch_bounds__(kThreads) extend_kernel(PoolParams p) {
   __shared__ int32_t owners[kOwners];
   pdl_wait();
-  if (blockIdx.x == 0) {
-    plan_extend(p, owners);
-    __threadfence();
-  }
-  cluster_sync();
+  if (blockIdx.x == 0) plan_extend(p, owners);
+  cluster_sync();  // (releases what the first CTA wrote to the others)
   fill(p, blockIdx.x * kThreads + threadIdx.x, kCtas * kThreads);
 }
 // The same in two launches.
@@ -366,7 +379,6 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(PoolParams p) {
       p.status[1] = count + (int)run.y;
       p.status[2] = count;
     }
-    __threadfence();
   }
   cluster_sync();
   // the first page of the first sequence goes on top

@@ -13,7 +13,6 @@ inputs must then be ready on).
 from __future__ import annotations
 
 import ctypes
-import struct
 
 import torch
 
@@ -21,23 +20,17 @@ from . import _lib
 from .api import device_status
 from .attention import PagedBatch, _capturing
 
-# exl3_kv_batch as C lays it out, packed bytes for the call's own cost
-_BATCH = struct.Struct("@iiiqQQQ")
-assert _BATCH.size == ctypes.sizeof(_lib.KVBatch)
-
 
 class PagedStep(PagedBatch):
     """A step as PagePool.extend lays it out: a PagedBatch (cu_q, seq_lens,
     block_table) with positions [max_tokens] int32 and slots [max_tokens] int64
     (page * page_size + place) of its new tokens, -1 in rows that are none's."""
 
-    def __init__(self, cu_q, seq_lens, block_table, positions, slots, max_q):
+    def __init__(self, max_q, cu_q, seq_lens, block_table, positions, slots, batch):
         self.cu_q, self.seq_lens, self.block_table = cu_q, seq_lens, block_table
         self.positions, self.slots = positions, slots
-        n, m = block_table.shape
-        self.num_seqs, self.max_q = n, max_q
-        self._at = self._ref = _BATCH.pack(n, max_q, m, m, cu_q.data_ptr(), seq_lens.data_ptr(),
-                                           block_table.data_ptr())
+        self.num_seqs, self.max_q = len(seq_lens), max_q
+        self._at = self._ref = batch  # exl3_kv_batch, its bytes
 
 
 class PagePool:
@@ -84,8 +77,8 @@ class PagePool:
         tensors, at least the sum of q_lens; max_q: as PagedBatch's.  A sequence
         for which there are no pages left keeps its rows, but has length 0 in the
         step and stays as it was in the pool."""
-        return PagedStep(*self._native.pages_extend(self._at, self._ws, self._ws_bytes, seqs, q_lens,
-                                                    max_tokens, stream), int(max_q))
+        return PagedStep(max_q, *self._native.pages_extend(self._at, self._ws, self._ws_bytes, seqs,
+                                                           q_lens, max_tokens, max_q, stream))
 
     def trim(self, seqs, drop=None, stream=None):
         """Takes the last drop[i] tokens (None: all) of row seqs[i] off and gives
