@@ -66,7 +66,6 @@ __device__ __forceinline__ uint4 pack8(const float2* v) {
 }
 template <int LPR, int BF16, int INTER>
 struct Lane {
-  static constexpr int NG = kThreads / LPR;
   int lane, ca, cb;  // its place in the row, the first channels of its two runs
   bool in_a, in_b;   // whether they are there
   bool pairs;        // it has rotation pairs
@@ -189,24 +188,37 @@ __device__ __forceinline__ void do_queries(const NormRopeParams& p, const uint64
 
 // The new tokens of one block.
 struct Job {
-  int page;         // -1: nothing to do
-  int lo, rows;     // position of the first one, how many
+  int rows;         // how many; 0: nothing to do
+  int lo;           // position of the first one
   int older;        // tokens before them in the block
   int t0;           // their first row
+  int64_t entry;    // of the block table, the block's page
 };
 // Block slot `slot` of the launch (one warp): sequence b has the slots
-// cu_q[b] / P + 2 b .., as many as it can touch blocks.
+// cu_q[b] / P + 2 b .., as many as it can touch blocks.  The page is not looked
+// up here: its load and the rows' go out together.
 __device__ __forceinline__ Job find_job(const NormRopeParams& p, int slot, bool report) {
   const int P = p.cache.page_size, shift = p.cache.page_shift, lane = threadIdx.x & 31;
   auto pages = [&](int x) { return shift >= 0 ? x >> shift : x / P; };  // (x >= 0 where it counts)
+  int32_t bad = 0;
+  Seq mine{};  // of sequence `lane`, loaded beside the bounds
+  const int few = p.batch.num_seqs <= 32;
+  if (few && lane < p.batch.num_seqs) mine = load_seq(p.batch, lane, &bad);
   int below = 0;
   for (int b = lane; b < p.batch.num_seqs; b += 32)
     below += pages(__ldg(p.batch.cu_q + b + 1)) + 2 * (b + 1) <= slot;
   const int b = __reduce_add_sync(0xffffffffu, below);
-  Job j{-1, 0, 0, 0, 0};
+  Job j{};
   if (b >= p.batch.num_seqs) return j;
-  int32_t bad = 0;
-  const Seq s = load_seq(p.batch, b, &bad);
+  Seq s;
+  if (few) {
+    s.q0 = __shfl_sync(0xffffffffu, mine.q0, b);
+    s.n = __shfl_sync(0xffffffffu, mine.n, b);
+    s.len = __shfl_sync(0xffffffffu, mine.len, b);
+    bad = __shfl_sync(0xffffffffu, bad, b);
+  } else {
+    s = load_seq(p.batch, b, &bad);
+  }
   const int start = s.len - s.n;  // position of the first new token
   if (s.n > 0 && start < 0) bad |= kStatusBadBatch;
   const int from = max(start, 0), first = pages(from);
@@ -216,11 +228,7 @@ __device__ __forceinline__ Job find_job(const NormRopeParams& p, int slot, bool 
     j.rows = min(s.len, blk * P + P) - j.lo;  // (lengths are at most 2^30)
     j.older = j.lo - blk * P;
     j.t0 = s.q0 + j.lo - start;
-    j.page = __ldg(p.batch.table + (int64_t)b * p.batch.table_stride + blk);
-    if (j.page < 0 || j.page >= p.cache.num_pages) {
-      bad |= kStatusBadPage;
-      j.page = -1;
-    }
+    j.entry = (int64_t)b * p.batch.table_stride + blk;
   }
   if (bad && report && lane == 0) atomicOr(p.status, bad);
   return j;
@@ -230,7 +238,7 @@ __device__ __forceinline__ Job find_job(const NormRopeParams& p, int slot, bool 
 // `team` (a power of two) lane groups.
 template <int LPR, int kHold, int BF16, int INTER>
 __device__ __forceinline__ void do_block(const NormRopeParams& p, const uint64_t* turns,
-                                         const Job& job, int unit0, int team) {
+                                         const Job& job, int unit0, int team, bool report) {
   using L = Lane<LPR, BF16, INTER>;
   constexpr int GW = 32 / LPR, kWarps = kThreads / 32;
   __shared__ uint32_t tops[kWarps];
@@ -248,9 +256,14 @@ __device__ __forceinline__ void do_block(const NormRopeParams& p, const uint64_t
 #pragma unroll
   for (int i = 0; i < kHold; i++)
     raw[i] = ln.load(x0 + (me + i * team) * hs.ts, me + i * team < rows);
+  const int page = __ldg(p.batch.table + job.entry);
+  if (page < 0 || page >= p.cache.num_pages) {  // (the whole CTA)
+    if (report && threadIdx.x == 0) atomicOr(p.status, kStatusBadPage);
+    return;
+  }
   const bool turn = !kv && ln.pairs;
   float* const scale_at = const_cast<float*>(kv ? p.cache.v_scale : p.cache.k_scale) +
-                          job.page * p.cache.scale_stride + h;
+                          page * p.cache.scale_stride + h;
   const float held = older > 0 ? *scale_at : 0.0f;
   // new token r of the block, normed and rotated
   auto form = [&](const Raw& w, int r, float2* v) {
@@ -307,7 +320,7 @@ __device__ __forceinline__ void do_block(const NormRopeParams& p, const uint64_t
   const float scale = top <= 448.0f * old ? old : scale_for(top);
   if (ln.lane == 0 && me == 0) *scale_at = scale;
   uint8_t* const dst = const_cast<uint8_t*>(kv ? p.cache.v : p.cache.k) +
-                       job.page * p.cache.page_bytes + h * p.cache.head_bytes;
+                       page * p.cache.page_bytes + h * p.cache.head_bytes;
 
   // ---- older tokens, where it has grown
   if (older > 0 && scale != old) {
@@ -384,8 +397,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) append_blocks_kernel(NormRop
     do_queries<LPR, BF16, INTER>(p, turns, (cta - first) * NG + threadIdx.x / LPR, c.slices, c.per);
   } else {
     const Job job = s_job;
-    if (job.page >= 0)
-      do_block<LPR, kHold, BF16, INTER>(p, turns, job, (int)(cta % c.groups) * (NG / c.team), c.team);
+    if (job.rows > 0)
+      do_block<LPR, kHold, BF16, INTER>(p, turns, job, (int)(cta % c.groups) * (NG / c.team), c.team,
+                                        cta % c.groups == 0);
   }
 }
 
