@@ -378,8 +378,23 @@ __device__ __forceinline__ Cut cut_warp(const AttnParams& p, int32_t* bad) {
     // / 10.3 / 12.1; of 62, 1 / 2 / 4 / 8: 13.0 / 11.7 / 11.0 / 12.2; of 8, 1 / 8: 9.1
     // / 7.5 (64 channels); no more parts than are joined in one step
     const int least = s.n <= 8 ? 8 : max(s.n < 48 ? 2 : 4, (s.n + C::kFlat - 1) / C::kFlat);
-    g = max(g, (unsigned)least);
-    const int k = live ? (int)((s.n + g - 1) / g) : 0, mine = u * k;
+    auto pieces_at = [&](unsigned x) {
+      x = max(x, (unsigned)least);
+      return live ? (int)((s.n + x - 1) / x) : 0;
+    };
+    // the shortest longest piece that `grid` CTAs allow, by halves: units of many
+    // lengths leave room (four tokens over 16 sequences of 1003 .. 6001 keys, 27.8 us
+    // with the bound, 26.4 with what is found below it)
+    unsigned lo = (total + C::kGrid - 1) / C::kGrid;
+#pragma unroll 1
+    for (int i = 0; i < 5 && lo < g; i++) {
+      const unsigned mid = (lo + g) / 2;
+      if (__reduce_add_sync(0xffffffffu, u * pieces_at(mid)) <= C::kGrid)
+        g = mid;
+      else
+        lo = mid + 1;
+    }
+    const int k = pieces_at(g), mine = u * k;
     int end = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
