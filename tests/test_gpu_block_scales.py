@@ -504,3 +504,21 @@ def test_block_scales_on_other_streams_and_in_graphs():
         graph.replay()
         assert torch.equal(out, want)
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("page,D", [(16, 128), (64, 64), (256, 128)])
+def test_append_blocks_whatever_max_q_says(page, D):
+    """max_q only picks how many lanes share a block: the bytes are the same."""
+    g = gen(page)
+    qs, lens = [40, 1, 300], [55, 70, 333]
+    step, pages = A.make_step(g, qs, lens, page)
+    k, v = (torch.randn(sum(qs), 2, D, generator=g).to(FP).cuda() for _ in range(2))
+    w = (1 + 0.1 * torch.randn(D, generator=g)).to(FP).cuda()
+    want = None
+    for hint in (300, 0, 1, 2, 9, 33, 1 << 20):
+        cache = blank(pages, page, 2, D)
+        kv_append(cache, PagedBatch(step.cu_q, step.seq_lens, step.table, hint), k, v, inv_freq=freqs(D),
+                  k_weight=w)
+        got = [u8(cache.k), u8(cache.v), cache.k_scale, cache.v_scale]
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and cache.status() == 0

@@ -121,6 +121,41 @@ def test_pages_of_many_sequences():
         step_both(pool, ref, seqs, q, sum(q) + 3)
 
 
+def test_pages_of_a_pool_with_many_rows():
+    """Claims of more rows than fit shared memory, rows named twice among them."""
+    n = 700
+    pool, ref = PagePool(2500, 16, 9000, 4), R.Pool(2500, 16, 9000, 4)
+    g = np.random.default_rng(4)
+    seqs = g.permutation(9000)[:n].tolist()
+    seqs[300], seqs[650], seqs[651] = seqs[2], 9000, seqs[2]
+    for top in (20, 5):
+        q = g.integers(0, top, n).tolist()
+        step_both(pool, ref, seqs, q, sum(q))
+        drop = [min(1, x) for x in q]
+        for i in (300, 650, 651):
+            drop[i] = 0
+        pool.trim(ints(seqs), ints(drop))
+        ref.trim(seqs, drop)
+        same_state(pool, ref)
+
+
+def test_pages_of_a_pool_that_makes_no_sense():
+    """Whatever a program has written to the pool, its calls stay inside it."""
+    g = gen(1)
+    for count, lens, table in ((10 ** 6, 5, 0), (-7, 1 << 30, 99), (4, -5, -1), (1 << 31 - 1, 1 << 30, 1 << 30)):
+        pool = PagePool(6, 16, 3, 4)
+        pool.count.fill_(min(count, (1 << 31) - 1))
+        pool.lens.fill_(lens)
+        pool.table.fill_(table)
+        pool.free.copy_(torch.randint(-1 << 31, 1 << 31, (6,), generator=g).int())
+        for _ in range(3):
+            step = pool.extend(ints([0, 1, 2]), ints([30, 1, 0]), 30, 31)
+            pool.trim(ints([2, 1, 0]), ints([5, 70, 1]))
+            pool.trim(ints([1]))
+            assert 0 <= int(pool.count) <= 6
+            assert bool((step.seq_lens >= 0).all()) and bool((step.seq_lens <= 64).all())
+
+
 def test_pages_no_sequences_and_captured_steps():
     pool = PagePool(64, 16, 4, 9)
     step = pool.extend(ints([]), ints([]), 1, 3)
@@ -172,7 +207,7 @@ def run_both(p, draft, cu, au, su, q):
     ([3, 0, 7, 1], 50001, BF, False, 0), ([5] * 30, 777, FP, True, 2), ([2] * 9, 8191, F32, False, 3),
     ([40, 1, 70], 301, F32, True, 0),                    # more drafts than a warp's lanes
     ([0, 0, 0], 33, BF, True, 0), ([3, 2], 131072, F32, True, 0), ([2, 3], 199999, BF, True, 0),
-    ([1] * 200, 64, F32, True, 0),
+    ([1] * 200, 64, F32, True, 0), ([1, 2], 1000003, F32, True, 0), ([1], 300001, FP, True, 1),
 ])
 @pytest.mark.parametrize("sharp", [0.5, 4.0])
 def test_verify(ds, vocab, dtype, given, pad, sharp):
