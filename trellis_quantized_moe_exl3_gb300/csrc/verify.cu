@@ -25,9 +25,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kPerSm = 1024 / kThreads;
 // of a cluster, one cluster per sequence.  64 pairs of rows of 131072 fp32 (floor 10
-// us): 16.9 us; 16 CTAs of 128 threads as fast, 16 of 256 and 8 of 128 slower
+// us): 16.5 us; 16 CTAs of 128 threads as fast, 16 of 256 and 8 of 128 slower
 constexpr int kCtas = 8;
-constexpr int kGroups = 8;  // parts of a warp's run whose sums are kept
+constexpr int kGroups = 8;  // parts of a warp's run whose sums are kept (draw: four lanes each)
 constexpr int kUnroll = 4;  // 16-byte loads of p (and of q) in flight per thread
 
 struct VerifyParams {
@@ -192,7 +192,7 @@ struct Row {
         }
       }
     }
-    if (g < kGroups) sums[g][lane] = s;
+    for (int x = g; x < kGroups; x++) sums[x][lane] = x == g ? s : 0;
     return all + s;
   }
   // the first token of the chunks c0 .. whose cumulative weight is above want
@@ -252,14 +252,24 @@ __device__ __forceinline__ void draw(const VerifyParams& p, const Row<DT>& row, 
   const float u = fminf(fmaxf(__ldg(p.sample_u + b), 0.0f), 1.0f - 0x1p-24f);
   long long want =
       (long long)__umul64hi(__float2ull_rz(u * 0x1p64f), (unsigned long long)all) - before;
-  for (int w = 0; w < warp; w++) want -= warp_total[w];
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) want -= w < warp ? warp_total[w] : 0;
   if (want < 0 || want >= warp_total[warp]) return;
-  int g = 0;
-  for (; g < kGroups - 1; g++) {
-    const long long t = warp_sum(sums[g][lane]);
-    if (want < t) break;
-    want -= t;
+  // the group: four lanes sum one, then the sums before it (one after the other,
+  // each over the warp, they took 1 us)
+  long long mine = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) mine += sums[lane >> 2][(lane & 3) + 4 * i];
+  mine += __shfl_xor_sync(0xffffffffu, mine, 1);
+  mine += __shfl_xor_sync(0xffffffffu, mine, 2);
+  long long inc = mine;
+#pragma unroll
+  for (int m = 4; m < 32; m <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+    if (lane >= m) inc += o;
   }
+  const int g = (__ffs(__ballot_sync(0xffffffffu, inc > want)) - 1) >> 2;
+  want -= __shfl_sync(0xffffffffu, inc - mine, 4 * g);
   const int c = first + g * per * 32;
   const int v = row.q ? row.template find<true>(c, per, last, lane, want)
                       : row.template find<false>(c, per, last, lane, want);
@@ -279,13 +289,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyParams p
   const bool good = c0 >= 0 && c1 >= c0 && c1 <= p.drafts;
   const int d = good ? c1 - c0 : 0;
   // ---- the first refusal (every CTA for itself)
+  const bool few = d < 32;  // (the drafts then stay in the lanes of the first warp)
   if (warp == 0) {
-    int a = d;
+    int a = d, x = 0;
     for (int j0 = 0; j0 < d; j0 += 32) {
       const int j = j0 + lane;
       bool no = false;
       if (j < d) {
-        const int x = __ldg(p.draft + c0 + j);
+        x = __ldg(p.draft + c0 + j);
         no = true;
         if (x >= 0 && x < p.vocab) {
           const double u = __ldg(p.accept_u + c0 + j);
@@ -301,13 +312,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyParams p
       }
     }
     if (lane == 0) s_accepted = a;
+    if (rank == 0 && good && few && lane <= d) p.tokens[c0 + b + lane] = lane < a ? x : -1;
   }
   __syncthreads();
   const int a = s_accepted;
   if (rank == 0) {
     // accepted drafts, then -1 (the drawn token's place too, until it is known);
     // rows that belong to no sequence as well
-    if (good)
+    if (good && !few)
       for (int j = threadIdx.x; j <= d; j += kThreads)
         p.tokens[c0 + b + j] = j < a ? __ldg(p.draft + c0 + j) : -1;
     if (b == p.num_seqs - 1 && good)

@@ -7,8 +7,8 @@
     pool.trim(seqs, dropped)                                     # refused drafts leave the cache
 
 Nothing of it is read on the host, so a whole step can be captured in a CUDA
-graph.  Every call is one kernel on the current stream (or on stream=, which the
-inputs must then be ready on).
+graph.  Every call is one or two kernels on the current stream (or on stream=,
+which the inputs must then be ready on).
 """
 from __future__ import annotations
 
