@@ -392,3 +392,52 @@ def test_pool_on_another_stream():
         pool.trim(seqs, q)
     assert step.cu_q.tolist() == [0, 20, 23] and pool.lens.tolist() == [0, 0]
     assert int(pool.count) == 9 and pool.status() == 1      # (7 of the 20 were gone already)
+
+
+def test_tensors_of_another_device_are_refused():
+    """Before anything is launched.  (The handles say that they live elsewhere: there
+    may be one device only.)"""
+    from trellis_quantized_moe_exl3_gb300 import PagedBatch, PagedKVCache, kv_append, paged_attention
+    pool = PagePool(9, 16, 2, 4)
+    seqs, q = ints([1, 0]), ints([20, 3])
+    here = pool._device
+    assert here == torch.cuda.current_device()
+    pool._device = here + 1
+    with pytest.raises(ValueError, match="another device"):
+        pool.extend(seqs, q, 20, 23)
+    with pytest.raises(ValueError, match="another device"):
+        pool.trim(seqs)
+    pool._device = here
+    step = pool.extend(seqs, q, 20, 23)
+    t = torch.zeros(9, 16, 1, 64, device="cuda").to(torch.float8_e4m3fn)
+    s = torch.zeros(9, 1, device="cuda")
+    cache = PagedKVCache(t, t.clone(), s, s.clone())
+    x = torch.randn(23, 1, 64, device="cuda").to(BF)
+    for both in (False, True):  # the batch beside the cache, then the tensors beside both
+        cache._device = here + 1
+        step._device = here + both
+        with pytest.raises(ValueError, match="another device"):
+            kv_append(cache, step, x, x)
+        with pytest.raises(ValueError, match="another device"):
+            paged_attention(x, cache, step)
+    cache._device = step._device = here
+    kv_append(cache, step, x, x)
+    assert bool((paged_attention(x, cache, step) != 0).any())
+    assert cache.status() == pool.status() == 0 and pool.lens.tolist() == [3, 20]
+    with pytest.raises(ValueError, match="CUDA"):
+        pool.extend(seqs, q.cpu(), 20, 23)
+    with pytest.raises(ValueError, match="one device"):
+        PagedBatch(step.cu_q.cpu().cuda(), step.seq_lens, _Elsewhere(step.block_table), 20)
+
+
+class _Elsewhere:
+    """A tensor that says it is on the next device."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.t.get_device() + 1

@@ -77,6 +77,19 @@ def _dense(t, name, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _one_device(**tensors):
+    """The index of the device that all of them (but None) are on."""
+    of = {n: t.get_device() for n, t in tensors.items() if t is not None}
+    if len(set(of.values())) != 1:
+        raise ValueError(f"{', '.join(of)} must be on one device")
+    return next(iter(of.values()))
+
+
+def _beside(cache, batch):
+    if batch._device != cache._device:
+        raise ValueError("the batch is on another device than the cache")
+
+
 class PagedKVCache:
     """A paged cache: k and v [pages, page_size, kv_heads, head_dim], fp16, bf16
     or float8_e4m3fn, channels contiguous, the other strides free but alike (a
@@ -119,6 +132,7 @@ class PagedKVCache:
                                      "contiguous rows, k_scale and v_scale alike")
             elif t is not None:
                 _dense(t, n, torch.float32, (k.shape[2],))
+        self._device = _one_device(k=k, v=v, k_scale=k_scale, v_scale=v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.kv_heads, self.head_dim, self.dtype = k.shape[2], k.shape[3], k.dtype
         d = _lib.KVCache()
@@ -229,6 +243,7 @@ class PagedBatch:
         if block_table.dim() != 2 or block_table.shape[0] != n or \
                 (block_table.shape[1] > 1 and block_table.stride(1) != 1):
             raise ValueError("block_table must be [sequences, pages] with contiguous rows")
+        self._device = _one_device(cu_q=cu_q, seq_lens=seq_lens, block_table=block_table)
         self.cu_q, self.seq_lens, self.block_table = cu_q, seq_lens, block_table
         self.num_seqs, self.max_q = n, int(max_q)
         d = _lib.KVBatch()
@@ -342,10 +357,12 @@ def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_wei
     covers the new values, its older tokens brought along."""
     if not k.is_cuda:
         _cuda(k, "k", _ACT)
+    _beside(cache, batch)
     raw = _stream(stream, k)
     w = cache._spaces.get(raw) or cache._room(stream, raw, None)
     return _lib.native().kv_append(cache._at, cache._scales_at, batch._at, k, v, inv_freq, k_weight, q,
-                                   q_weight, q_out, positions, eps, interleaved, w.ptr, stream)
+                                   q_weight, q_out, positions, eps, interleaved, w.ptr, stream,
+                                   cache._device)
 
 
 def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causal: bool = True,
@@ -365,6 +382,7 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
     (device_status(ws))."""
     if not q.is_cuda:
         _cuda(q, "q", _ACT)
+    _beside(cache, batch)
     dim = cache.head_dim
     if ws is None:
         raw = _stream(stream, q)
@@ -375,7 +393,8 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
         ws_ptr, ws_bytes = w.ptr, w.bytes
     else:
         _dense(ws, "ws", torch.uint8, ws.shape)
+        _one_device(cache=cache.k, ws=ws)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     return _lib.native().paged_attention(cache._at, cache._scales_at, batch._at, q,
                                          dim ** -0.5 if scale is None else scale, causal, window, out,
-                                         return_lse, path, ws_ptr, ws_bytes, stream)
+                                         return_lse, path, ws_ptr, ws_bytes, stream, cache._device)

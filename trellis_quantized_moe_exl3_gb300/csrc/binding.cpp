@@ -24,10 +24,16 @@ struct Raised {};
   throw Raised{};
 }
 
+// The device of a call: its cache's or pool's, else its first tensor's (-1: none yet).
+thread_local int t_device;
+
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) raise(PyExc_TypeError, "%s must be a tensor", name);
   const at::Tensor& t = THPVariable_Unpack(o);
   if (!t.is_cuda()) raise(PyExc_ValueError, "%s must be a CUDA tensor", name);
+  if (t_device < 0) t_device = t.get_device();
+  if (t.get_device() != t_device)
+    raise(PyExc_ValueError, "%s is on another device than the rest of the call", name);
   return t;
 }
 // A contiguous vector of n values (n < 0: any number).
@@ -54,11 +60,15 @@ T* address(PyObject* o) {
 
 // The stream of a call: stream= (an object with a cuda_stream) or the device's
 // current one.  Outputs are made on it, and are for use on the current one later.
+// The tensors' device is the current one as long as it lives: a raw default stream
+// is the current device's, whichever that is.
 struct Stream {
+  c10::cuda::OptionalCUDAGuard device;
   c10::cuda::CUDAStream current, launch;
   bool other;
   Stream(PyObject* given, const at::Tensor& t)
       : current(c10::cuda::getCurrentCUDAStream(t.get_device())), launch(current), other(false) {
+    if (c10::cuda::current_device() != t.get_device()) device.set_index(t.get_device());
     if (given == Py_None) return;
     PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
     if (!raw) throw Raised{};
@@ -175,9 +185,10 @@ const at::Tensor& rows_named(PyObject* o, const exl3_page_pool* pool) {
   return seqs;
 }
 
-// (pool, ws, ws_bytes, seqs, q_lens, max_tokens, max_q, stream), the first three as
-// numbers; the step's tensors and its exl3_kv_batch as bytes
+// (pool, ws, ws_bytes, seqs, q_lens, max_tokens, max_q, stream, device), the first
+// three as numbers; the step's tensors and its exl3_kv_batch as bytes
 PyObject* pages_extend(PyObject* const* a) {
+  t_device = (int)whole(a[8]);
   const auto* pool = address<exl3_page_pool>(a[0]);
   const at::Tensor& seqs = rows_named(a[3], pool);
   const int64_t n = seqs.size(0), tokens = whole(a[5]), max_q = whole(a[6]);
@@ -209,8 +220,9 @@ PyObject* pages_extend(PyObject* const* a) {
                PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&batch), sizeof batch));
 }
 
-// (pool, ws, ws_bytes, seqs, drop, stream)
+// (pool, ws, ws_bytes, seqs, drop, stream, device)
 PyObject* pages_trim(PyObject* const* a) {
+  t_device = (int)whole(a[6]);
   const auto* pool = address<exl3_page_pool>(a[0]);
   const at::Tensor& seqs = rows_named(a[3], pool);
   const int32_t* drop = nullptr;
@@ -253,8 +265,9 @@ const exl3_kv_batch* batch_of(PyObject* o) {
 }
 
 // (cache, scales, batch, k, v, inv_freq, k_weight, q, q_weight, q_out, positions, eps,
-//  interleaved, status, stream); cache, scales, batch and status as numbers
+//  interleaved, status, stream, device); cache, scales, batch and status as numbers
 PyObject* kv_append(PyObject* const* a) {
+  t_device = (int)whole(a[15]);
   const auto* cache = address<const exl3_kv_cache>(a[0]);
   const auto* scales = address<const exl3_kv_scales>(a[1]);
   const int64_t dim = cache->head_dim;
@@ -320,8 +333,9 @@ PyObject* kv_append(PyObject* const* a) {
 }
 
 // (cache, scales, batch, q, scale, causal, window, out, return_lse, path, ws, ws_bytes,
-//  stream); cache, scales, batch and ws as numbers
+//  stream, device); cache, scales, batch and ws as numbers
 PyObject* paged_attention(PyObject* const* a) {
+  t_device = (int)whole(a[13]);
   const auto* cache = address<const exl3_kv_cache>(a[0]);
   const auto* scales = address<const exl3_kv_scales>(a[1]);
   const int64_t dim = cache->head_dim;
@@ -370,6 +384,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "%d arguments, not %zd", N, n);
     return nullptr;
   }
+  t_device = -1;
   try {
     return F(args);
   } catch (const Raised&) {
@@ -385,10 +400,10 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<verify_drafts, 7>("verify_drafts"),
-                           method<pages_extend, 8>("pages_extend"),
-                           method<pages_trim, 6>("pages_trim"),
-                           method<kv_append, 15>("kv_append"),
-                           method<paged_attention, 13>("paged_attention"),
+                           method<pages_extend, 9>("pages_extend"),
+                           method<pages_trim, 7>("pages_trim"),
+                           method<kv_append, 16>("kv_append"),
+                           method<paged_attention, 14>("paged_attention"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods,
                         nullptr,               nullptr,   nullptr, nullptr};

@@ -26,10 +26,10 @@ class PagedStep(PagedBatch):
     block_table) with positions [max_tokens] int32 and slots [max_tokens] int64
     (page * page_size + place) of its new tokens, -1 in rows that are none's."""
 
-    def __init__(self, max_q, cu_q, seq_lens, block_table, positions, slots, batch):
+    def __init__(self, device, max_q, cu_q, seq_lens, block_table, positions, slots, batch):
         self.cu_q, self.seq_lens, self.block_table = cu_q, seq_lens, block_table
         self.positions, self.slots = positions, slots
-        self.num_seqs, self.max_q = len(seq_lens), max_q
+        self.num_seqs, self.max_q, self._device = len(seq_lens), max_q, device
         self._at = self._ref = batch  # exl3_kv_batch, its bytes
 
 
@@ -66,7 +66,7 @@ class PagePool:
         d.table, d.lens = self.table.data_ptr(), self.lens.data_ptr()
         d.free, d.count = self.free.data_ptr() or None, self.count.data_ptr()
         self._d, self._at = d, ctypes.addressof(d)
-        self._ws, self._ws_bytes = self.ws.data_ptr(), n
+        self._ws, self._ws_bytes, self._device = self.ws.data_ptr(), n, self.ws.get_device()
         if not _capturing():  # calls on other streams find it made
             torch.cuda.current_stream(device).synchronize()
         self._native = _lib.native()
@@ -77,13 +77,13 @@ class PagePool:
         tensors, at least the sum of q_lens; max_q: as PagedBatch's.  A sequence
         for which there are no pages left keeps its rows, but has length 0 in the
         step and stays as it was in the pool."""
-        return PagedStep(max_q, *self._native.pages_extend(self._at, self._ws, self._ws_bytes, seqs,
-                                                           q_lens, max_tokens, max_q, stream))
+        return PagedStep(self._device, max_q, *self._native.pages_extend(
+            self._at, self._ws, self._ws_bytes, seqs, q_lens, max_tokens, max_q, stream, self._device))
 
     def trim(self, seqs, drop=None, stream=None):
         """Takes the last drop[i] tokens (None: all) of row seqs[i] off and gives
         back the pages that hold nothing any more."""
-        self._native.pages_trim(self._at, self._ws, self._ws_bytes, seqs, drop, stream)
+        self._native.pages_trim(self._at, self._ws, self._ws_bytes, seqs, drop, stream, self._device)
 
     def status(self, stream=None) -> int:
         """The status bits set so far (0: fine); see exl3.h."""
