@@ -126,12 +126,12 @@ def speculate(block, cache, pool, seqs, hidden, drafts, steps, vocab=1000):
     def step():
         draft = torch.randint(0, vocab, (n, drafts), device="cuda")
         x = embed[torch.cat([last[:, None], draft], 1).flatten()]
-        y = block(x, cache, pool.extend(seqs, q_lens, rows, n * rows))
-        y = y.float()
+        at = pool.extend(seqs, q_lens, rows, n * rows)
+        y = block(x, cache, at).float()
         p = ((y / y.norm(dim=-1, keepdim=True)) @ head.float()).softmax(-1)
         tokens, accepted, dropped = verify_drafts(
             p, draft.int().flatten(), cu_draft, torch.rand(n * drafts, device="cuda"),
-            torch.rand(n, device="cuda"), q=q)
+            torch.rand(n, device="cuda"), q=q, step=at)
         pool.trim(seqs, dropped)
         last.copy_(tokens.view(n, rows).gather(1, accepted.long()[:, None])[:, 0])
         made.add_((accepted + 1).sum())

@@ -554,9 +554,18 @@ exl3_status exl3_pages_extend(const exl3_page_pool *pool, int num, const int32_t
 
 /* Takes the last drop[i] tokens of row seqs[i] off again (drop NULL: all of
  * them) and gives back the pages that hold nothing any more.  A step taken
- * back whole leaves the pool as it was before it. */
+ * back whole leaves the pool as it was before it, if all its sequences were
+ * served: one that was not got no tokens, and would lose older ones. */
 exl3_status exl3_pages_trim(const exl3_page_pool *pool, int num, const int32_t *seqs,
                             const int32_t *drop, void *ws, size_t ws_bytes, void *stream);
+
+/* The same after a step whose seq_lens are step_lens (device int32 [num], what
+ * exl3_pages_extend wrote for the same seqs; NULL: exl3_pages_trim): a sequence
+ * with length 0 there was not served, and its row is left alone.  A step taken
+ * back whole leaves the pool as it was, whatever was served. */
+exl3_status exl3_pages_trim_step(const exl3_page_pool *pool, int num, const int32_t *seqs,
+                                 const int32_t *drop, const int32_t *step_lens, void *ws,
+                                 size_t ws_bytes, void *stream);
 
 /* Verification of drafted tokens by random numbers that the caller gives.
  * Sequence b has d = cu_draft[b+1] - cu_draft[b] drafts, draft[cu_draft[b] + j],
@@ -588,6 +597,18 @@ exl3_status exl3_verify_drafts(const void *p, int64_t p_stride, const void *q, i
                                const int32_t *cu_draft, const int32_t *draft,
                                const float *accept_u, const float *sample_u, int32_t *tokens,
                                int32_t *accepted, int32_t *dropped, void *stream);
+
+/* The same for the sequences of a step whose seq_lens are step_lens (device
+ * int32 [num_seqs], what exl3_pages_extend wrote; NULL: exl3_verify_drafts): one
+ * with length 0 there was not served, so its rows of p are those of no token.
+ * It gets tokens -1, accepted and dropped 0: nothing came that could be taken
+ * off its row of the pool. */
+exl3_status exl3_verify_drafts_step(const void *p, int64_t p_stride, const void *q, int64_t q_stride,
+                                    exl3_dtype dt, int vocab, int num_seqs, int drafts,
+                                    const int32_t *cu_draft, const int32_t *draft,
+                                    const float *accept_u, const float *sample_u,
+                                    const int32_t *step_lens, int32_t *tokens, int32_t *accepted,
+                                    int32_t *dropped, void *stream);
 
 const char *exl3_status_string(exl3_status s);
 

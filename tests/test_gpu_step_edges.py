@@ -1,0 +1,128 @@
+"""What a speculative step does where its calls meet: sequences without pages,
+bounds that make no sense, odd probabilities, tensors that are freed or saved."""
+import math
+
+import pytest
+import torch
+
+import _speculate_ref as R
+from trellis_quantized_moe_exl3_gb300 import PagedKVCache, PagePool, kv_append, paged_attention, verify_drafts
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def state(pool):
+    return [t.clone() for t in (pool.table, pool.lens, pool.free, pool.count)]
+
+
+# ------------------------------------------------------------ sequences that a step does not serve
+@pytest.mark.parametrize("captured", [False, True])
+def test_sequences_without_pages_keep_their_tokens(captured):
+    """The whole loop with a pool that runs out: a sequence that gets no pages gets no
+    token and no counts, and its row, length and pages stay as they were."""
+    page, rows, cols, hk, d, drafts, vocab = 16, 4, 4, 1, 64, 3, 50
+    start, pages = [15, 14, 16, 3], 6              # four pages taken, two left
+    need = drafts + 1
+    g = gen(1)
+    cache = PagedKVCache(*[torch.zeros(pages, page, hk, d, dtype=R.E4M3, device="cuda") for _ in range(2)],
+                         *[torch.zeros(pages, hk, device="cuda") for _ in range(2)])
+    pool, ref = PagePool(pages, page, rows, cols), R.Pool(pages, page, rows, cols)
+    seqs, n, T = [0, 1, 2, 3], 4, 4 * need
+    kv = torch.randn(sum(start), 2 * hk, d, generator=g).to(BF).cuda()
+    kv_append(cache, pool.extend(ints(seqs), ints(start), 16, sum(start)), kv[:, :hk], kv[:, hk:])
+    ref.extend(seqs, start, sum(start))
+    x = torch.randn(T, 3 * hk, d, generator=g).to(BF).cuda()
+    p = torch.rand(T, vocab, generator=g).cuda()
+    p /= p.sum(-1, keepdim=True)
+    q = torch.full((n * drafts, vocab), 1.0 / vocab, device="cuda")
+    draft = torch.randint(0, vocab, (n * drafts,), generator=g).int().cuda()
+    cu = ints([drafts * b for b in range(n + 1)])
+    au, su = torch.rand(n * drafts, generator=g).cuda(), torch.rand(n, generator=g).cuda()
+    seqs_d, q_lens = ints(seqs), ints([need] * n)
+
+    def whole():
+        s = pool.extend(seqs_d, q_lens, need, T)
+        kv_append(cache, s, x[:, :hk], x[:, hk:2 * hk])
+        out = paged_attention(x[:, 2 * hk:], cache, s)
+        got = verify_drafts(p, draft, cu, au, su, q=q, step=s)
+        pool.trim(seqs_d, got[2])
+        return s, out, got
+
+    cache.workspace(T, 1, n)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            s, out, got = whole()
+    unserved = 0
+    for _ in range(3):
+        before = state(pool)
+        _, lens, table, _, _ = ref.extend(seqs, [need] * n, T)
+        if captured:
+            graph.replay()
+        else:
+            s, out, got = whole()
+        assert s.seq_lens.tolist() == lens and s.block_table.tolist() == table
+        want = R.verify(p.cpu(), draft.cpu(), cu.tolist(), au.cpu(), su.cpu(), q.cpu())
+        for b in range(n):
+            at = need * b
+            if lens[b]:
+                assert got[0][at:at + need].tolist() == want[0][at:at + need]
+                assert int(got[1][b]) == want[1][b] and int(got[2][b]) == want[2][b]
+            else:
+                unserved += 1
+                assert got[0][at:at + need].tolist() == [-1] * need
+                assert int(got[1][b]) == int(got[2][b]) == 0
+                assert bool((out[at:at + need] == 0).all())
+                assert torch.equal(pool.table[b], before[0][b]) and int(pool.lens[b]) == int(before[1][b])
+        ref.trim(seqs, [want[2][b] if lens[b] else 0 for b in range(n)])
+        table, lens, free = ref.state()
+        assert pool.table.tolist() == table and pool.lens.tolist() == lens
+        assert pool.free[:len(free)].tolist() == free and int(pool.count) == len(free)
+    assert unserved and pool.status() == 2
+
+
+@pytest.mark.parametrize("q,seqs,max_tokens,pages", [
+    ([3, 4, 5], [0, 1, 2], 12, 20),             # all of them served
+    ([5, 40, 1, 16], [0, 1, 2, 3], 70, 7),      # too few pages for the second and the last
+    ([3, 4, 5], [0, 7, 1], 12, 20),             # row 7 of 4
+    ([3, 4, 5, 6], [2, 0, 2, 2], 18, 20),       # the same row three times
+    ([49, 3], [1, 0], 60, 20),                  # past its row of the table
+    ([5, 5, 0, 5], [0, 1, 2, 3], 9, 20),        # past max_tokens
+])
+def test_a_step_taken_back_whole_whatever_was_served(q, seqs, max_tokens, pages):
+    pool = PagePool(pages, 16, 4, 3)
+    pool.extend(ints([0, 1, 2, 3]), ints([16, 2, 15, 9]), 16, 42)
+    assert pool.status() == 0
+    before = state(pool)
+    step = pool.extend(ints(seqs), ints(q), max(q), max_tokens)
+    pool.trim(ints(seqs), ints(q), step=step)
+    # (a refused sequence's request is a request that makes no sense to trim as well)
+    for b, now in zip(before, state(pool)):
+        assert torch.equal(b, now)
+    # rows that were served are released, the others keep what they have
+    step = pool.extend(ints(seqs), ints(q), max(q), max_tokens)
+    served = {s for s, n in zip(seqs, step.seq_lens.tolist()) if n}
+    pool.trim(ints(seqs), step=step)
+    want = [0 if s in served else n for s, n in enumerate([16, 2, 15, 9])]
+    assert pool.lens.tolist() == want
+    assert int(pool.count) == pages - sum(-(-n // 16) for n in want)
+
+
+def test_steps_of_another_size_are_refused():
+    pool = PagePool(9, 16, 4, 3)
+    step = pool.extend(ints([0, 1]), ints([3, 3]), 3, 6)
+    with pytest.raises(ValueError, match="seq_lens"):
+        pool.trim(ints([0]), ints([1]), step=step)
+    p, z = torch.full((3, 9), 1 / 9, device="cuda"), torch.zeros(2, device="cuda")
+    with pytest.raises(ValueError, match="seq_lens"):
+        verify_drafts(p, ints([1, 2]), ints([0, 2]), z, z[:1], step=step)

@@ -159,6 +159,10 @@ def lib():
     L.exl3_pages_trim.restype = i
     L.exl3_verify_drafts.argtypes = [vp, i64, vp, i64, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp]
     L.exl3_verify_drafts.restype = i
+    L.exl3_pages_trim_step.argtypes = [vp, i, vp, vp, vp, vp, sz, vp]
+    L.exl3_pages_trim_step.restype = i
+    L.exl3_verify_drafts_step.argtypes = [vp, i64, vp, i64, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.exl3_verify_drafts_step.restype = i
     L.exl3_test_set_attention_wait_fault.argtypes = [i, ctypes.c_longlong]
     L.exl3_test_set_attention_wait_fault.restype = i
     L.exl3_status_string.argtypes = [i]

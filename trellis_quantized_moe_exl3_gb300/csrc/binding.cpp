@@ -46,6 +46,11 @@ const at::Tensor& vector(PyObject* o, const char* name, at::ScalarType type, int
   if (!t.is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", name);
   return t;
 }
+// The lengths of a step's n sequences, or none.
+const int32_t* lens_of(PyObject* o, int64_t n) {
+  return o == Py_None ? nullptr
+                      : static_cast<const int32_t*>(vector(o, "step.seq_lens", at::kInt, n).data_ptr());
+}
 int64_t whole(PyObject* o) {
   const int64_t v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw Raised{};
@@ -142,7 +147,7 @@ int64_t rows_of(const at::Tensor& x, const char* name, int64_t rows, int64_t voc
   return rows > 1 ? x.stride(0) : x.size(1);
 }
 
-// (p, draft, cu_draft, accept_u, sample_u, q, stream)
+// (p, draft, cu_draft, accept_u, sample_u, q, stream, the step's seq_lens)
 PyObject* verify_drafts(PyObject* const* a) {
   const at::Tensor& draft = vector(a[1], "draft", at::kInt, -1);
   const at::Tensor& su = vector(a[4], "sample_u", at::kFloat, -1);
@@ -160,6 +165,7 @@ PyObject* verify_drafts(PyObject* const* a) {
   }
   const at::Tensor& cu = vector(a[2], "cu_draft", at::kInt, B + 1);
   const at::Tensor& au = vector(a[3], "accept_u", at::kFloat, D);
+  const int32_t* lens = lens_of(a[7], B);
   if (D > INT32_MAX || B > INT32_MAX || vocab > INT32_MAX)
     raise(PyExc_ValueError, "%s has too many rows or columns", "p");
   const Stream st(a[6], p);
@@ -167,14 +173,14 @@ PyObject* verify_drafts(PyObject* const* a) {
   const exl3_dtype dt = p.scalar_type() == at::kFloat  ? EXL3_F32
                         : p.scalar_type() == at::kHalf ? EXL3_F16
                                                        : EXL3_BF16;
-  check(exl3_verify_drafts(p.data_ptr(), ps, q, qs, dt, (int)vocab, (int)B, (int)D,
-                           static_cast<const int32_t*>(cu.data_ptr()),
-                           static_cast<const int32_t*>(draft.data_ptr()),
-                           static_cast<const float*>(au.data_ptr()),
-                           static_cast<const float*>(su.data_ptr()),
-                           static_cast<int32_t*>(tokens.data_ptr()),
-                           static_cast<int32_t*>(accepted.data_ptr()),
-                           static_cast<int32_t*>(dropped.data_ptr()), st.launch.stream()),
+  check(exl3_verify_drafts_step(p.data_ptr(), ps, q, qs, dt, (int)vocab, (int)B, (int)D,
+                                static_cast<const int32_t*>(cu.data_ptr()),
+                                static_cast<const int32_t*>(draft.data_ptr()),
+                                static_cast<const float*>(au.data_ptr()),
+                                static_cast<const float*>(su.data_ptr()), lens,
+                                static_cast<int32_t*>(tokens.data_ptr()),
+                                static_cast<int32_t*>(accepted.data_ptr()),
+                                static_cast<int32_t*>(dropped.data_ptr()), st.launch.stream()),
         "exl3_verify_drafts");
   return tuple({tokens, accepted, dropped});
 }
@@ -220,7 +226,7 @@ PyObject* pages_extend(PyObject* const* a) {
                PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&batch), sizeof batch));
 }
 
-// (pool, ws, ws_bytes, seqs, drop, stream, device)
+// (pool, ws, ws_bytes, seqs, drop, stream, device, the step's seq_lens)
 PyObject* pages_trim(PyObject* const* a) {
   t_device = (int)whole(a[6]);
   const auto* pool = address<exl3_page_pool>(a[0]);
@@ -228,9 +234,10 @@ PyObject* pages_trim(PyObject* const* a) {
   const int32_t* drop = nullptr;
   if (a[4] != Py_None)
     drop = static_cast<const int32_t*>(vector(a[4], "drop", at::kInt, seqs.size(0)).data_ptr());
+  const int32_t* lens = lens_of(a[7], seqs.size(0));
   const Stream st(a[5], seqs);
-  check(exl3_pages_trim(pool, (int)seqs.size(0), static_cast<const int32_t*>(seqs.data_ptr()), drop,
-                        address<void>(a[1]), (size_t)whole(a[2]), st.launch.stream()),
+  check(exl3_pages_trim_step(pool, (int)seqs.size(0), static_cast<const int32_t*>(seqs.data_ptr()),
+                             drop, lens, address<void>(a[1]), (size_t)whole(a[2]), st.launch.stream()),
         "exl3_pages_trim");
   Py_RETURN_NONE;
 }
@@ -399,9 +406,9 @@ PyMethodDef method(const char* name) {
                      METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<verify_drafts, 7>("verify_drafts"),
+PyMethodDef g_methods[] = {method<verify_drafts, 8>("verify_drafts"),
                            method<pages_extend, 9>("pages_extend"),
-                           method<pages_trim, 7>("pages_trim"),
+                           method<pages_trim, 8>("pages_trim"),
                            method<kv_append, 16>("kv_append"),
                            method<paged_attention, 14>("paged_attention"),
                            {nullptr, nullptr, 0, nullptr}};

@@ -44,6 +44,7 @@ struct PoolParams {
   int num;  // sequences of the step
   const int32_t* seqs;
   const int32_t* n;  // new tokens; tokens to drop (null: all)
+  const int32_t* step_lens;  // trim: 0 for sequences that the step did not serve (null: all served)
   int max_tokens;
   int32_t* cu_q;
   int32_t* seq_lens;
@@ -350,7 +351,9 @@ __global__ void __launch_bounds__(kThreads) trim_kernel(PoolParams p) {
       if (i < p.num) {
         s = __ldg(p.seqs + i);
         ok = claims.holds(i, s);
-        if (ok) {
+        if (ok && p.step_lens && __ldg(p.step_lens + i) <= 0) {
+          ok = false;  // it got no tokens: what its row holds is older
+        } else if (ok) {
           len = length_of(p, s);
           n = p.n ? __ldg(p.n + i) : len;
           if (n < 0 || n > len) bad |= kPoolBadRequest;
@@ -497,14 +500,21 @@ exl3_status exl3_pages_extend(const exl3_page_pool* pool, int num, const int32_t
   return err == cudaSuccess ? EXL3_OK : EXL3_ERR_CUDA;
 }
 
-exl3_status exl3_pages_trim(const exl3_page_pool* pool, int num, const int32_t* seqs,
-                            const int32_t* drop, void* ws, size_t ws_bytes, void* stream) {
+exl3_status exl3_pages_trim_step(const exl3_page_pool* pool, int num, const int32_t* seqs,
+                                 const int32_t* drop, const int32_t* step_lens, void* ws,
+                                 size_t ws_bytes, void* stream) {
   const exl3_status e = check(pool, num, seqs, ws, ws_bytes);
   if (e != EXL3_OK) return e;
   if (num == 0) return EXL3_OK;
-  const PoolParams p = params_of(pool, num, seqs, drop, ws);
+  PoolParams p = params_of(pool, num, seqs, drop, ws);
+  p.step_lens = step_lens;
   return launch(trim_kernel, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EXL3_OK
                                                                                   : EXL3_ERR_CUDA;
+}
+
+exl3_status exl3_pages_trim(const exl3_page_pool* pool, int num, const int32_t* seqs,
+                            const int32_t* drop, void* ws, size_t ws_bytes, void* stream) {
+  return exl3_pages_trim_step(pool, num, seqs, drop, nullptr, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

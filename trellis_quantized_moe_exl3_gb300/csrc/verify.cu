@@ -42,6 +42,7 @@ struct VerifyParams {
   int32_t* tokens;
   int32_t* accepted;
   int32_t* dropped;
+  const int32_t* step_lens;  // 0: the step did not serve the sequence (null: all served)
 };
 
 template <int DT>
@@ -287,6 +288,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyParams p
   pdl_wait();
   const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
   const bool good = c0 >= 0 && c1 >= c0 && c1 <= p.drafts;
+  if (good && p.step_lens && __ldg(p.step_lens + b) <= 0) {
+    // its rows of p are those of no token: nothing is drawn, nothing came that
+    // could be dropped (the whole cluster)
+    if (rank == 0) {
+      for (int64_t j = (int64_t)c0 + b + threadIdx.x;
+           j <= (b == p.num_seqs - 1 ? (int64_t)p.drafts + b : (int64_t)c1 + b); j += kThreads)
+        p.tokens[j] = -1;
+      if (threadIdx.x == 0) p.accepted[b] = p.dropped[b] = 0;
+    }
+    return;
+  }
   const int d = good ? c1 - c0 : 0;
   // ---- the first refusal (every CTA for itself)
   const bool few = d < 32;  // (the drafts then stay in the lanes of the first warp)
@@ -414,12 +426,14 @@ cudaError_t launch(const VerifyParams& p, cudaStream_t st) {
 
 using namespace exl3;
 
-extern "C" exl3_status exl3_verify_drafts(const void* p, int64_t p_stride, const void* q,
-                                          int64_t q_stride, exl3_dtype dt, int vocab, int num_seqs,
-                                          int drafts, const int32_t* cu_draft, const int32_t* draft,
-                                          const float* accept_u, const float* sample_u,
-                                          int32_t* tokens, int32_t* accepted, int32_t* dropped,
-                                          void* stream) {
+extern "C" {
+
+exl3_status exl3_verify_drafts_step(const void* p, int64_t p_stride, const void* q, int64_t q_stride,
+                                    exl3_dtype dt, int vocab, int num_seqs, int drafts,
+                                    const int32_t* cu_draft, const int32_t* draft,
+                                    const float* accept_u, const float* sample_u,
+                                    const int32_t* step_lens, int32_t* tokens, int32_t* accepted,
+                                    int32_t* dropped, void* stream) {
   if (dt != EXL3_F16 && dt != EXL3_BF16 && dt != EXL3_F32) return EXL3_ERR_ARG;
   if (vocab < 1 || vocab > (1 << 24) || num_seqs < 0 || num_seqs > kMaxSeqs || drafts < 0 ||
       drafts > (1 << 30))
@@ -438,11 +452,22 @@ extern "C" exl3_status exl3_verify_drafts(const void* p, int64_t p_stride, const
       !cu_draft || !sample_u || !tokens || !accepted || !dropped ||
       (drafts > 0 && (!draft || !accept_u)))
     return EXL3_ERR_ARG;
-  const VerifyParams a{p,        q,     p_stride, q_stride, vocab,  num_seqs, drafts,
-                       cu_draft, draft, accept_u, sample_u, tokens, accepted, dropped};
+  const VerifyParams a{p,     q,        p_stride, q_stride, vocab,    num_seqs, drafts,   cu_draft,
+                       draft, accept_u, sample_u, tokens,   accepted, dropped,  step_lens};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dt == EXL3_F32    ? launch<EXL3_F32>(a, st)
                         : dt == EXL3_BF16 ? launch<EXL3_BF16>(a, st)
                                           : launch<EXL3_F16>(a, st);
   return e == cudaSuccess ? EXL3_OK : EXL3_ERR_CUDA;
 }
+
+exl3_status exl3_verify_drafts(const void* p, int64_t p_stride, const void* q, int64_t q_stride,
+                               exl3_dtype dt, int vocab, int num_seqs, int drafts,
+                               const int32_t* cu_draft, const int32_t* draft, const float* accept_u,
+                               const float* sample_u, int32_t* tokens, int32_t* accepted,
+                               int32_t* dropped, void* stream) {
+  return exl3_verify_drafts_step(p, p_stride, q, q_stride, dt, vocab, num_seqs, drafts, cu_draft,
+                                 draft, accept_u, sample_u, nullptr, tokens, accepted, dropped, stream);
+}
+
+}  // extern "C"

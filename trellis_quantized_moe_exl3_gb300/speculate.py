@@ -3,7 +3,8 @@
     pool = PagePool(num_pages, page_size, max_seqs, max_pages)   # pages of the cache, on the GPU
     step = pool.extend(seqs, q_lens, max_q, max_tokens)          # a PagedBatch with its pages
     q = kv_append(cache, step, ...); out = paged_attention(q, cache, step)
-    tokens, accepted, dropped = verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=q_probs)
+    tokens, accepted, dropped = verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=q_probs,
+                                              step=step)
     pool.trim(seqs, dropped)                                     # refused drafts leave the cache
 
 Nothing of it is read on the host, so a whole step can be captured in a CUDA
@@ -80,10 +81,14 @@ class PagePool:
         return PagedStep(self._device, max_q, *self._native.pages_extend(
             self._at, self._ws, self._ws_bytes, seqs, q_lens, max_tokens, max_q, stream, self._device))
 
-    def trim(self, seqs, drop=None, stream=None):
+    def trim(self, seqs, drop=None, stream=None, step=None):
         """Takes the last drop[i] tokens (None: all) of row seqs[i] off and gives
-        back the pages that hold nothing any more."""
-        self._native.pages_trim(self._at, self._ws, self._ws_bytes, seqs, drop, stream, self._device)
+        back the pages that hold nothing any more.  step: the step of the same
+        seqs that these tokens are of (extend's); rows that it did not serve got
+        none, and are left alone.  Without it a drop of tokens that never came
+        takes older ones."""
+        self._native.pages_trim(self._at, self._ws, self._ws_bytes, seqs, drop, stream, self._device,
+                                None if step is None else step.seq_lens)
 
     def status(self, stream=None) -> int:
         """The status bits set so far (0: fine); see exl3.h."""
@@ -97,7 +102,7 @@ class PagePool:
         wait(self.ws.device)
 
 
-def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None):
+def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None, step=None):
     """Which drafted tokens stand, and the token after them.
 
     Sequence b has the drafts draft[cu_draft[b] .. cu_draft[b+1] - 1] (int32;
@@ -115,5 +120,10 @@ def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None):
 
     Returns int32 (tokens [drafts + sequences], accepted [sequences], dropped
     [sequences]): from place cu_draft[b] + b on, the accepted drafts, the drawn
-    token, then -1; accepted drafts, and the others (what PagePool.trim takes)."""
-    return _lib.native().verify_drafts(p, draft, cu_draft, accept_u, sample_u, q, stream)
+    token, then -1; accepted drafts, and the others (what PagePool.trim takes).
+
+    step: the step (PagePool.extend's) that p was computed for.  A sequence that
+    it did not serve, for want of pages, has seen nothing: it gets tokens -1, and
+    0 of both counts, so that trim takes nothing off its row."""
+    return _lib.native().verify_drafts(p, draft, cu_draft, accept_u, sample_u, q, stream,
+                                       None if step is None else step.seq_lens)
