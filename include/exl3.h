@@ -587,11 +587,13 @@ exl3_status exl3_pages_trim_step(const exl3_page_pool *pool, int num, const int3
  *   sample_u  device fp32 [num_seqs], in [0, 1)
  *   tokens    device int32 [drafts + num_seqs]: in place cu_draft[b] + b on, the
  *             accepted drafts, the drawn token (-1 where the row has no
- *             weight), then -1; -1 behind the last sequence
+ *             weight), then -1; -1 in places of no sequence (before the first
+ *             one, behind the last, of one that is left out)
  *   accepted, dropped  device int32 [num_seqs]: accepted drafts, and the others
- * A sequence whose cu_draft does not ascend within 0 .. drafts is left out:
- * accepted and dropped 0, no tokens.  vocab at most 2^24.  Errors: EXL3_ERR_ARG
- * (null or misaligned pointers, strides below vocab, bad enum), EXL3_ERR_SHAPE. */
+ * A sequence whose cu_draft does not ascend within 0 .. drafts, or leaves
+ * cu_draft[0] .. cu_draft[num_seqs] (as far as these are in that range), is left
+ * out: accepted and dropped 0, tokens -1 (a place that such bounds give to two
+ * sequences holds what either has there).  vocab at most 2^24.  Errors: EXL3_ERR_ARG (null or misaligned pointers, strides below vocab, bad enum), EXL3_ERR_SHAPE. */
 exl3_status exl3_verify_drafts(const void *p, int64_t p_stride, const void *q, int64_t q_stride,
                                exl3_dtype dt, int vocab, int num_seqs, int drafts,
                                const int32_t *cu_draft, const int32_t *draft,

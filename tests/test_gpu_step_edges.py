@@ -126,3 +126,53 @@ def test_steps_of_another_size_are_refused():
     p, z = torch.full((3, 9), 1 / 9, device="cuda"), torch.zeros(2, device="cuda")
     with pytest.raises(ValueError, match="seq_lens"):
         verify_drafts(p, ints([1, 2]), ints([0, 2]), z, z[:1], step=step)
+
+
+# ------------------------------------------------------------ verification: bounds that make no sense
+def verify_into_garbage(p, draft, cu, au, su, q):
+    """verify_drafts with its outputs in memory that has held something else."""
+    B, D = len(su), len(draft)
+    n = sum((x + 3) // 4 * 4 for x in (D + B, B, B))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        held = [torch.full((n,), 0x5EED, dtype=torch.int32, device="cuda") for _ in range(8)]
+        del held
+    got = verify_drafts(p.cuda(), draft.cuda(), ints(cu), au.cuda(), su.cuda(), q=q.cuda())
+    return [x.tolist() for x in got]
+
+
+@pytest.mark.parametrize("D,cu", [
+    (6, [0, 2, 4, 6]), (6, [1, 3, 5]), (6, [0, 3]), (6, [2, 2, 2]),          # rows before and behind
+    (6, [0, 2, 9, 6]), (6, [-1, 2, 4, 6]), (6, [0, 2, 4, 7]), (6, [0, 2, -5, 6]),
+    (6, [0, 2, 4, -1]), (6, [9, 2, 4, 6]), (6, [5, 0]), (6, [0, 6, 2]), (6, [9, 9, 9]), (6, [-3, -2, -1]),
+    (6, [0, 1 << 30, 1 << 30, 6]), (6, [-(1 << 31), (1 << 31) - 1, 3, 6]), (0, [0, 5, 0]), (0, [0]),
+    (6, [0, 4, 2, 6]), (100, [0, 50, 40, 90]), (100, [0, 1000, 10, 70]),
+])
+def test_every_token_is_written(D, cu):
+    """Places of no sequence and of those left out hold -1, whatever was there."""
+    B, vocab = len(cu) - 1, 40
+    g = gen(D + B)
+    p = torch.rand(D + B, vocab, generator=g)
+    p /= p.sum(-1, keepdim=True).clamp(min=1e-9)
+    q = torch.full((D, vocab), 1.0 / vocab)
+    draft = torch.randint(0, vocab, (D,), generator=g).int()
+    au, su = torch.rand(D, generator=g), torch.rand(B, generator=g)
+    tokens, accepted, dropped = verify_into_garbage(p, draft, cu, au, su, q)
+    lo, hi = cu[0] if 0 <= cu[0] <= D else 0, cu[-1] if 0 <= cu[-1] <= D else D
+    want = [{-1} for _ in range(D + B)]
+    claimed = [[] for _ in range(D + B)]
+    for b in range(B):
+        c0, c1 = cu[b], cu[b + 1]
+        if lo <= c0 <= c1 <= hi:
+            t, a, d = R.verify(p[b:], draft, [c0, c1], au, su[b:], q)
+            assert accepted[b] == a[0] and dropped[b] == d[0]
+            for j, x in enumerate(t):
+                claimed[c0 + b + j].append(x)
+        else:
+            assert accepted[b] == dropped[b] == 0
+    # (a place that bounds up and down give to two of them: either's)
+    twice = any(x > y for x, y in zip(cu, cu[1:]))
+    for j, x in enumerate(claimed):
+        if x:
+            want[j] = set(x) | ({-1} if twice else set())
+    assert all(t in w for t, w in zip(tokens, want)), (tokens, want)

@@ -287,19 +287,33 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyParams p
   const int b = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;
   pdl_wait();
   const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
-  const bool good = c0 >= 0 && c1 >= c0 && c1 <= p.drafts;
-  if (good && p.step_lens && __ldg(p.step_lens + b) <= 0) {
-    // its rows of p are those of no token: nothing is drawn, nothing came that
-    // could be dropped (the whole cluster)
+  // the drafts that belong to sequences (a bound out of range says nothing)
+  int lo = __ldg(p.cu), hi = __ldg(p.cu + p.num_seqs);
+  if (lo < 0 || lo > p.drafts) lo = 0;
+  if (hi < 0 || hi > p.drafts) hi = p.drafts;
+  const bool good = c0 >= lo && c1 >= c0 && c1 <= hi;
+  auto none = [&](int64_t from, int64_t to) {  // places of no token
+    for (int64_t j = from + threadIdx.x; j < to; j += kThreads) p.tokens[j] = -1;
+  };
+  if (rank == 0) {
+    if (b == 0) none(0, lo);
+    if (b == p.num_seqs - 1) none((int64_t)hi + p.num_seqs, (int64_t)p.drafts + p.num_seqs);
+  }
+  // Left out: bounds that do not ascend, or a sequence that the step did not
+  // serve, whose rows of p are those of no token: nothing is drawn, nothing came
+  // that could be dropped.  (The bounds, held to lo .. hi, lead from the first
+  // place to the last in steps up and down, and every place lies in a step up: of
+  // a sequence that writes its own, or of one that is left out.)
+  if (!good || (p.step_lens && __ldg(p.step_lens + b) <= 0)) {
     if (rank == 0) {
-      for (int64_t j = (int64_t)c0 + b + threadIdx.x;
-           j <= (b == p.num_seqs - 1 ? (int64_t)p.drafts + b : (int64_t)c1 + b); j += kThreads)
-        p.tokens[j] = -1;
+      const int from = b == 0 ? lo : min(max(c0, lo), hi);
+      const int to = b == p.num_seqs - 1 ? hi : min(max(c1, lo), hi);
+      none((int64_t)from + b, (int64_t)to + b + 1);
       if (threadIdx.x == 0) p.accepted[b] = p.dropped[b] = 0;
     }
-    return;
+    return;  // (the whole cluster: it waits for no one)
   }
-  const int d = good ? c1 - c0 : 0;
+  const int d = c1 - c0;
   // ---- the first refusal (every CTA for itself)
   const bool few = d < 32;  // (the drafts then stay in the lanes of the first warp)
   if (warp == 0) {
@@ -324,26 +338,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyParams p
       }
     }
     if (lane == 0) s_accepted = a;
-    if (rank == 0 && good && few && lane <= d) p.tokens[c0 + b + lane] = lane < a ? x : -1;
+    if (rank == 0 && few && lane <= d) p.tokens[c0 + b + lane] = lane < a ? x : -1;
   }
   __syncthreads();
   const int a = s_accepted;
   if (rank == 0) {
-    // accepted drafts, then -1 (the drawn token's place too, until it is known);
-    // rows that belong to no sequence as well
-    if (good && !few)
+    // accepted drafts, then -1 (the drawn token's place too, until it is known)
+    if (!few)
       for (int j = threadIdx.x; j <= d; j += kThreads)
         p.tokens[c0 + b + j] = j < a ? __ldg(p.draft + c0 + j) : -1;
-    if (b == p.num_seqs - 1 && good)
-      for (int64_t j = (int64_t)c1 + b + 1 + threadIdx.x; j < (int64_t)p.drafts + p.num_seqs;
-           j += kThreads)
-        p.tokens[j] = -1;
     if (threadIdx.x == 0) {
       p.accepted[b] = a;
       p.dropped[b] = d - a;
     }
   }
-  if (!good) return;  // (the whole cluster: it waits for no one)
 
   // ---- the row's weights: a run of chunks per warp
   Row<DT> row;
