@@ -176,3 +176,39 @@ def test_every_token_is_written(D, cu):
         if x:
             want[j] = set(x) | ({-1} if twice else set())
     assert all(t in w for t, w in zip(tokens, want)), (tokens, want)
+
+
+# ------------------------------------------------------------ verification: odd probabilities
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, BF])
+@pytest.mark.parametrize("u", [0.0, 0.25, 0.75])
+def test_acceptance_holds_probabilities_to_0_and_1(dtype, u):
+    """NaN and what is negative count as 0, what is above 1 as 1, in the decision on a
+    draft as in the weights of the token that follows."""
+    values = [math.nan, -math.inf, -2.0, -0.0, 0.0, 0.125, 0.5, 1.0, 2.0, 1000.0, math.inf]
+    pairs = [(a, b) for a in values for b in values]
+    n, vocab = len(pairs), 5
+    p = torch.zeros(2 * n, vocab)
+    p[0::2, 1], p[1::2, 4] = 0.25, 1.0
+    q = torch.zeros(n, vocab)
+    for i, (a, b) in enumerate(pairs):
+        p[2 * i, 3], q[i, 3] = a, b
+
+    def held(x):
+        return min(max(x, 0.0), 1.0) if x == x else 0.0
+
+    p, q = p.to(dtype), q.to(dtype)
+    draft = torch.full((n,), 3, dtype=torch.int32)
+    t, accepted, dropped = verify_drafts(p.cuda(), draft.cuda(), ints(list(range(n + 1))),
+                                         torch.full((n,), u, device="cuda"),
+                                         torch.full((n,), 0.5, device="cuda"), q=q.cuda())
+    t = t.view(n, 2).tolist()
+    for i, (a, b) in enumerate(pairs):
+        stands = u * held(b) < held(a)
+        # refused: of token 1 (0.25) and token 3 (what is left of it), the one at half of the sum
+        rest = max(held(a) - held(b), 0.0)
+        want = [3, 4] if stands else [1 if 0.5 * (0.25 + rest) < 0.25 else 3, -1]
+        assert t[i] == want and int(accepted[i]) == stands and int(dropped[i]) == 1 - stands, (a, b, t[i])
+    # without q a draft is certain: refused only where it has no probability, or u is past it
+    t, accepted, _ = verify_drafts(p.cuda(), draft.cuda(), ints(list(range(n + 1))),
+                                   torch.full((n,), u, device="cuda"), torch.full((n,), 0.5, device="cuda"))
+    assert accepted.tolist() == [int(u < held(a)) for a, _ in pairs]

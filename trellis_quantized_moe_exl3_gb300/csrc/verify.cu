@@ -326,8 +326,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyParams p
         no = true;
         if (x >= 0 && x < p.vocab) {
           const double u = __ldg(p.accept_u + c0 + j);
-          const float pp = value<DT>(p.p, (int64_t)(c0 + j + b) * p.p_stride + x);
-          const float qq = p.q ? value<DT>(p.q, (int64_t)(c0 + j) * p.q_stride + x) : 1.0f;
+          // (held to 0 .. 1, NaN as 0, as the weights are)
+          const float pp = __saturatef(value<DT>(p.p, (int64_t)(c0 + j + b) * p.p_stride + x));
+          const float qq =
+              p.q ? __saturatef(value<DT>(p.q, (int64_t)(c0 + j) * p.q_stride + x)) : 1.0f;
           no = !(u * (double)qq < (double)pp);
         }
       }
