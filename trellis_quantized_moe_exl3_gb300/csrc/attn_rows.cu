@@ -91,8 +91,8 @@ struct Cfg {
   static constexpr int kCtasPerSm = kThree ? 3 : D == 128 ? 2 : 4;
   static constexpr int kGrid = kSms * kCtasPerSm;
   // how many granules a cut at units' borders may have its pieces longer than an
-  // equal one's (cut_warp)
-  static constexpr int kExtra = 24;
+  // equal one's (cut_warp), and how many for a join in one step
+  static constexpr int kExtra = 24, kExtraFlat = 6;
   static constexpr int kFlat = D == 128 ? 40 : 24;  // most parts that are joined in one step
 };
 
@@ -345,8 +345,8 @@ struct Cut {
 // An equal cut has most CTAs work on the ends of two units, each with a chain of
 // loads and a join of its own (5 us).  Few units are therefore cut one by one, unit
 // n long into ceil(n / g) equal pieces with g = total / (grid - units) rounded up,
-// so that there are at most `grid` of them, unless that makes the longest one
-// much longer than an equal cut's.
+// so that there are at most `grid` of them, unless that, or the most parts that
+// one join takes, makes the longest one much longer than an equal cut's.
 template <class C>
 __device__ __forceinline__ Cut cut_warp(const AttnParams& p, int32_t* bad) {
   const int lane = threadIdx.x & 31;
@@ -373,11 +373,18 @@ __device__ __forceinline__ Cut cut_warp(const AttnParams& p, int32_t* bad) {
     if (g > (unsigned)(C::kExtra * C::kGrid)) g = 0;
     if (g * units > (unsigned)(C::kExtra * C::kGrid)) g = 0;
   }
+  // no more parts than are joined in one step, unless that keeps most CTAs idle: a
+  // line of a few long units is cut as a whole then.  us of one token, one sequence,
+  // at most kFlat parts / an equal cut: 64 channels, 1 kv head, 16000 keys 20.5 /
+  // 18.4, 250000 82 / 29; 8 kv heads, 32000 26.6 / 26.6, 250000 90 / 72; 128 channels,
+  // 2 kv heads, 8000 16.4 / 18.4, 32000 24.6 / 24.5, 250000 68 / 45
+  const int flat = u > 0 ? (s.n + C::kFlat - 1) / C::kFlat : 0;
+  if (__reduce_max_sync(0xffffffffu, (unsigned)flat) > g + C::kExtraFlat) g = 0;
   if (g > 0) {
     // us of one token, one sequence of 16 granules, pieces of 1 / 2 / 4 / 8: 9.4 / 9.4
     // / 10.3 / 12.1; of 62, 1 / 2 / 4 / 8: 13.0 / 11.7 / 11.0 / 12.2; of 8, 1 / 8: 9.1
-    // / 7.5 (64 channels); no more parts than are joined in one step
-    const int least = s.n <= 8 ? 8 : max(s.n < 48 ? 2 : 4, (s.n + C::kFlat - 1) / C::kFlat);
+    // / 7.5 (64 channels)
+    const int least = s.n <= 8 ? 8 : max(s.n < 48 ? 2 : 4, flat);
     auto pieces_at = [&](unsigned x) {
       x = max(x, (unsigned)least);
       return live ? (int)((s.n + x - 1) / x) : 0;
