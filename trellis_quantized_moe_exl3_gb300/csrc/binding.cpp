@@ -125,6 +125,17 @@ void check(exl3_status s, const char* what) {
   throw Raised{};
 }
 
+// Runs f, which touches nothing of Python's, while other Python threads may run:
+// an allocation may wait for the GPU, a launch for room in a full queue.
+template <class F>
+auto unlocked(F f) {
+  struct Lock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return f();
+}
+
 // The tensors, and after them `last` (whose reference it takes) if there is one.
 PyObject* tuple(std::initializer_list<at::Tensor> of, PyObject* last = nullptr) {
   PyObject* r = PyTuple_New((Py_ssize_t)of.size() + (last != nullptr));
@@ -169,20 +180,23 @@ PyObject* verify_drafts(PyObject* const* a) {
   if (D > INT32_MAX || B > INT32_MAX || vocab > INT32_MAX)
     raise(PyExc_ValueError, "%s has too many rows or columns", "p");
   const Stream st(a[6], p);
-  const auto [tokens, accepted, dropped] = st.words<3>({{D + B}, {B}, {B}});
   const exl3_dtype dt = p.scalar_type() == at::kFloat  ? EXL3_F32
                         : p.scalar_type() == at::kHalf ? EXL3_F16
                                                        : EXL3_BF16;
-  check(exl3_verify_drafts_step(p.data_ptr(), ps, q, qs, dt, (int)vocab, (int)B, (int)D,
-                                static_cast<const int32_t*>(cu.data_ptr()),
-                                static_cast<const int32_t*>(draft.data_ptr()),
-                                static_cast<const float*>(au.data_ptr()),
-                                static_cast<const float*>(su.data_ptr()), lens,
-                                static_cast<int32_t*>(tokens.data_ptr()),
-                                static_cast<int32_t*>(accepted.data_ptr()),
-                                static_cast<int32_t*>(dropped.data_ptr()), st.launch.stream()),
-        "exl3_verify_drafts");
-  return tuple({tokens, accepted, dropped});
+  std::array<at::Tensor, 3> out;  // tokens, accepted, dropped
+  const exl3_status s = unlocked([&] {
+    out = st.words<3>({{D + B}, {B}, {B}});
+    return exl3_verify_drafts_step(p.data_ptr(), ps, q, qs, dt, (int)vocab, (int)B, (int)D,
+                                   static_cast<const int32_t*>(cu.data_ptr()),
+                                   static_cast<const int32_t*>(draft.data_ptr()),
+                                   static_cast<const float*>(au.data_ptr()),
+                                   static_cast<const float*>(su.data_ptr()), lens,
+                                   static_cast<int32_t*>(out[0].data_ptr()),
+                                   static_cast<int32_t*>(out[1].data_ptr()),
+                                   static_cast<int32_t*>(out[2].data_ptr()), st.launch.stream());
+  });
+  check(s, "exl3_verify_drafts");
+  return tuple({out[0], out[1], out[2]});
 }
 
 const at::Tensor& rows_named(PyObject* o, const exl3_page_pool* pool) {
@@ -202,18 +216,22 @@ PyObject* pages_extend(PyObject* const* a) {
   if (tokens < 0 || tokens > INT32_MAX)
     raise(PyExc_ValueError, "%s must not be negative", "max_tokens");
   if (max_q < 0 || max_q > INT32_MAX) raise(PyExc_ValueError, "%s must not be negative", "max_q");
+  void* const ws = address<void>(a[1]);
+  const size_t bytes = (size_t)whole(a[2]);
   const Stream st(a[7], seqs);
-  const auto [slots, pos, cu, lens, table] =
-      st.words<5>({{tokens}, {tokens}, {n + 1}, {n}, {n, pool->max_pages}}, true);
-  check(exl3_pages_extend(pool, (int)n, static_cast<const int32_t*>(seqs.data_ptr()),
-                          static_cast<const int32_t*>(q.data_ptr()), (int)tokens,
-                          static_cast<int32_t*>(cu.data_ptr()),
-                          static_cast<int32_t*>(lens.data_ptr()),
-                          static_cast<int32_t*>(table.data_ptr()),
-                          static_cast<int32_t*>(pos.data_ptr()),
-                          static_cast<int64_t*>(slots.data_ptr()), address<void>(a[1]),
-                          (size_t)whole(a[2]), st.launch.stream()),
-        "exl3_pages_extend");
+  at::Tensor slots, pos, cu, lens, table;
+  const exl3_status s = unlocked([&] {
+    std::tie(slots, pos, cu, lens, table) = std::tuple_cat(
+        st.words<5>({{tokens}, {tokens}, {n + 1}, {n}, {n, pool->max_pages}}, true));
+    return exl3_pages_extend(pool, (int)n, static_cast<const int32_t*>(seqs.data_ptr()),
+                             static_cast<const int32_t*>(q.data_ptr()), (int)tokens,
+                             static_cast<int32_t*>(cu.data_ptr()),
+                             static_cast<int32_t*>(lens.data_ptr()),
+                             static_cast<int32_t*>(table.data_ptr()),
+                             static_cast<int32_t*>(pos.data_ptr()),
+                             static_cast<int64_t*>(slots.data_ptr()), ws, bytes, st.launch.stream());
+  });
+  check(s, "exl3_pages_extend");
   exl3_kv_batch batch{};
   batch.num_seqs = (int)n;
   batch.max_q = (int)max_q;
@@ -235,10 +253,14 @@ PyObject* pages_trim(PyObject* const* a) {
   if (a[4] != Py_None)
     drop = static_cast<const int32_t*>(vector(a[4], "drop", at::kInt, seqs.size(0)).data_ptr());
   const int32_t* lens = lens_of(a[7], seqs.size(0));
+  void* const ws = address<void>(a[1]);
+  const size_t bytes = (size_t)whole(a[2]);
   const Stream st(a[5], seqs);
-  check(exl3_pages_trim_step(pool, (int)seqs.size(0), static_cast<const int32_t*>(seqs.data_ptr()),
-                             drop, lens, address<void>(a[1]), (size_t)whole(a[2]), st.launch.stream()),
-        "exl3_pages_trim");
+  const exl3_status s = unlocked([&] {
+    return exl3_pages_trim_step(pool, (int)seqs.size(0), static_cast<const int32_t*>(seqs.data_ptr()),
+                                drop, lens, ws, bytes, st.launch.stream());
+  });
+  check(s, "exl3_pages_trim");
   Py_RETURN_NONE;
 }
 
@@ -289,8 +311,8 @@ PyObject* kv_append(PyObject* const* a) {
   v.x = vt.data_ptr();
   k.heads = v.heads = (int)kt.size(1);
   k.weight = weight_of(a[6], "k_weight", kt.scalar_type(), dim);
-  const Stream st(a[14], kt);
   at::Tensor out;
+  const at::Tensor* made = nullptr;  // q, where its place is to be made
   if (a[7] != Py_None) {
     const at::Tensor& qt = heads_of(a[7], "q", dim, &q.token_stride, &q.head_stride);
     if (qt.scalar_type() != kt.scalar_type() || qt.size(0) != T)
@@ -299,15 +321,15 @@ PyObject* kv_append(PyObject* const* a) {
     q.heads = (int)qt.size(1);
     q.weight = weight_of(a[8], "q_weight", qt.scalar_type(), dim);
     if (a[9] == Py_None) {
-      out = st.empty(qt.sizes(), qt.scalar_type());
+      made = &qt;
       q.out_token_stride = qt.size(1) * dim;
       q.out_head_stride = dim;
     } else {
       out = heads_of(a[9], "q_out", dim, &q.out_token_stride, &q.out_head_stride);
       if (out.scalar_type() != qt.scalar_type() || out.sizes() != qt.sizes())
         raise(PyExc_ValueError, "%s must have q's shape and dtype", "q_out");
+      q.out = out.data_ptr();
     }
-    q.out = out.data_ptr();
   }
   exl3_rope rope{};
   if (a[5] != Py_None) {
@@ -324,14 +346,20 @@ PyObject* kv_append(PyObject* const* a) {
   if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
   const exl3_heads* qp = a[7] != Py_None ? &q : nullptr;
   const exl3_rope* rp = rope.inv_freq || a[5] != Py_None ? &rope : nullptr;
-  if (scales)
-    check(exl3_kv_append_blocks(cache, scales, batch_of(a[2]), qp, &k, &v, code_of(kt), (int)T, rp,
-                                positions, (float)eps, address<int32_t>(a[13]), st.launch.stream()),
-          "exl3_kv_append_blocks");
-  else
-    check(exl3_kv_append(cache, batch_of(a[2]), qp, &k, &v, code_of(kt), (int)T, rp, positions,
-                         (float)eps, address<int32_t>(a[13]), st.launch.stream()),
-          "exl3_kv_append");
+  const exl3_kv_batch* const batch = batch_of(a[2]);
+  int32_t* const status = address<int32_t>(a[13]);
+  const Stream st(a[14], kt);
+  const exl3_status s = unlocked([&] {
+    if (made) {
+      out = st.empty(made->sizes(), made->scalar_type());
+      q.out = out.data_ptr();
+    }
+    return scales ? exl3_kv_append_blocks(cache, scales, batch, qp, &k, &v, code_of(kt), (int)T, rp,
+                                          positions, (float)eps, status, st.launch.stream())
+                  : exl3_kv_append(cache, batch, qp, &k, &v, code_of(kt), (int)T, rp, positions,
+                                   (float)eps, status, st.launch.stream());
+  });
+  check(s, scales ? "exl3_kv_append_blocks" : "exl3_kv_append");
   if (!out.defined()) {  // (no q: what was given as its place comes back)
     Py_INCREF(a[9]);
     return a[9];
@@ -354,33 +382,32 @@ PyObject* paged_attention(PyObject* const* a) {
   const bool with_lse = PyObject_IsTrue(a[8]);
   if (window < INT32_MIN || window > INT32_MAX || path < INT32_MIN || path > INT32_MAX)
     raise(PyExc_ValueError, "%s out of range", "window or path");
-  const Stream st(a[12], q);
-  at::Tensor out;
-  if (a[7] == Py_None) {
-    out = st.empty(q.sizes(), q.scalar_type());
-  } else {
+  at::Tensor out, lse;
+  if (a[7] != Py_None) {
     out = tensor(a[7], "out");
     if (out.scalar_type() != q.scalar_type()) raise(PyExc_TypeError, "%s must have q's dtype", "out");
     if (out.sizes() != q.sizes()) raise(PyExc_ValueError, "%s must have q's shape", "out");
     if (!out.is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", "out");
   }
-  at::Tensor lse;
-  if (with_lse) lse = st.empty({q.size(0), q.size(1)}, at::kFloat);
-  float* l = with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
   void* const ws = address<void>(a[10]);
   const size_t bytes = (size_t)whole(a[11]);
   const int causal = PyObject_IsTrue(a[5]);
-  if (scales)
-    check(exl3_paged_attention_blocks(cache, scales, batch_of(a[2]), q.data_ptr(), ts, hs, code_of(q),
-                                      (int)q.size(0), (int)q.size(1), (float)scale, causal,
-                                      (int)window, out.data_ptr(), l, (int)path, ws, bytes,
-                                      st.launch.stream()),
-          "exl3_paged_attention_blocks");
-  else
-    check(exl3_paged_attention(cache, batch_of(a[2]), q.data_ptr(), ts, hs, code_of(q),
-                               (int)q.size(0), (int)q.size(1), (float)scale, causal, (int)window,
-                               out.data_ptr(), l, (int)path, ws, bytes, st.launch.stream()),
-          "exl3_paged_attention");
+  const exl3_kv_batch* const batch = batch_of(a[2]);
+  const Stream st(a[12], q);
+  const exl3_status s = unlocked([&] {
+    if (!out.defined()) out = st.empty(q.sizes(), q.scalar_type());
+    if (with_lse) lse = st.empty({q.size(0), q.size(1)}, at::kFloat);
+    float* const l = with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
+    return scales ? exl3_paged_attention_blocks(cache, scales, batch, q.data_ptr(), ts, hs, code_of(q),
+                                                (int)q.size(0), (int)q.size(1), (float)scale, causal,
+                                                (int)window, out.data_ptr(), l, (int)path, ws, bytes,
+                                                st.launch.stream())
+                  : exl3_paged_attention(cache, batch, q.data_ptr(), ts, hs, code_of(q),
+                                         (int)q.size(0), (int)q.size(1), (float)scale, causal,
+                                         (int)window, out.data_ptr(), l, (int)path, ws, bytes,
+                                         st.launch.stream());
+  });
+  check(s, scales ? "exl3_paged_attention_blocks" : "exl3_paged_attention");
   if (with_lse) return tuple({out, lse});
   return THPVariable_Wrap(out);
 }
