@@ -63,3 +63,81 @@ def test_other_threads_run_while_a_call_waits_for_the_queue(name):
     torch.cuda.synchronize()
     assert took > 0.2, "the queue never filled"
     assert max(gaps) < 0.1, max(gaps)
+
+
+def given(g):
+    """Calls by name: fresh tensors, and the call on them with stream=."""
+    from trellis_quantized_moe_exl3_gb300 import qk_norm_rope
+    n = 60000  # (sizes of their own, larger than what small tensors share)
+
+    def cache():
+        return PagedKVCache(*[torch.zeros(40, 16, 2, 64, dtype=BF, device="cuda") for _ in range(2)])
+
+    def batch(rows):
+        return PagedBatch(ints([0, rows]), ints([rows]), ints([list(range(40))]), rows)
+
+    def x(rows, heads):
+        return torch.randn(rows, heads, 64, generator=g, device="cuda").to(BF)
+
+    fixed = cache()
+    plain = batch(600)
+    w = lambda: 1 + torch.rand(64, generator=g, device="cuda").to(BF)  # noqa: E731
+    f = lambda: torch.rand(32, generator=g, device="cuda", dtype=torch.float64)  # noqa: E731
+    pos = lambda: torch.arange(600, dtype=torch.int32, device="cuda")  # noqa: E731
+    return {
+        "verify": (lambda: [torch.rand(3, n, device="cuda"), ints([1, 2]), ints([0, 2]),
+                            torch.rand(2, device="cuda"), torch.rand(1, device="cuda"),
+                            torch.rand(2, n, device="cuda")],
+                   lambda t, st: verify_drafts(*t[:5], q=t[5], stream=st)),
+        "append": (lambda: [x(600, 2), x(600, 2), f(), w(), x(600, 4), w(), x(600, 4), pos()],
+                   lambda t, st: kv_append(fixed, plain, t[0], t[1], t[2], t[3], t[4], t[5], t[6], t[7],
+                                           stream=st)),
+        "append to a handle": (lambda: (lambda c, b: [c, b, c.k, c.v, b.cu_q, b.seq_lens, b.block_table])(
+                                   cache(), batch(600)),
+                               lambda t, st: kv_append(t[0], t[1], kept[0], kept[1], stream=st)),
+        "attention": (lambda: [x(600, 4), torch.empty(600, 4, 64, dtype=BF, device="cuda"),
+                               torch.zeros(fixed.workspace_size(600, 4, 1), dtype=torch.uint8, device="cuda")],
+                      lambda t, st: paged_attention(t[0], fixed, plain, out=t[1], ws=t[2], stream=st)),
+        "attention of a handle": (lambda: (lambda c, b: [c, b, c.k, c.v, b.cu_q, b.seq_lens, b.block_table])(
+                                      cache(), batch(600)),
+                                  lambda t, st: paged_attention(kept[2], t[0], t[1], stream=st)),
+        "norm": (lambda: [x(600, 4), x(600, 2), pos(), f(), w(), w()],
+                 lambda t, st: qk_norm_rope(*t, stream=st)),
+        "extend": (lambda: (lambda p: [p, ints([0, 1]), ints([5, 3]), p.table, p.lens, p.free, p.count])(
+                       PagePool(90000, 16, 30, 900)),
+                   lambda t, st: t[0].extend(t[1], t[2], 5, 8, stream=st)),
+        "trim": (lambda: (lambda p: [p, ints([0, 1]), ints([0, 0]), p.table, p.lens, p.free, p.count])(
+                     PagePool(90000, 16, 30, 900)),
+                 lambda t, st: t[0].trim(t[1], t[2], stream=st)),
+    }
+
+
+kept = []
+
+
+@pytest.mark.parametrize("name", ["verify", "append", "append to a handle", "attention",
+                                  "attention of a handle", "norm", "extend", "trim"])
+def test_tensors_freed_after_a_call_on_another_stream(name):
+    """Tensors (a handle's own among them) that the program drops right after a call with
+    stream= are not handed out again while that stream has yet to run it."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kept[:] = [torch.randn(600, h, 64, generator=g, device="cuda").to(BF) for h in (2, 2, 4)]
+    make, call = given(g)[name]
+    side = torch.cuda.Stream()
+    call(make(), side)                        # (workspaces made)
+    t = make()
+    torch.cuda.synchronize()
+    tensors = [x for x in t if isinstance(x, torch.Tensor)]
+    at = {(x.untyped_storage().data_ptr()): x.untyped_storage().nbytes() for x in tensors}
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)        # 0.2 s before the call's turn
+    out = call(t, side)
+    del t, tensors
+    again = []
+    for size in list(at.values()) * 3:
+        again.append(torch.empty(size, dtype=torch.uint8, device="cuda"))
+    assert not side.query(), "the stream was done too early for the test to say anything"
+    taken = {x.data_ptr() for x in again} & set(at)
+    torch.cuda.synchronize()
+    assert not taken
+    del out

@@ -8,7 +8,7 @@
 ``qk_norm_rope`` is the norm and rotation alone, for keys that go to no cache.
 PyTorch supplies device memory and streams only; every call is one or a few
 kernels of the library on the current stream (or on stream=, which the inputs
-must then be ready on), allocates nothing but its outputs, and can be captured
+must then be ready on, and which keeps their memory until it is done), allocates nothing but its outputs, and can be captured
 in a CUDA graph.
 """
 from __future__ import annotations
@@ -51,6 +51,28 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _lend(stream, *tensors):
+    """Memory of the tensors (None: none) that a call on stream uses is not handed
+    out again before the stream is done with it."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+class _Lent:
+    """A handle whose tensors are lent to the streams that its calls name (once for
+    all calls: the memory waits for all that the stream has then)."""
+    _lent = frozenset()
+
+    def _lend(self, stream):
+        if stream is not None and stream.cuda_stream not in self._lent:
+            _lend(stream, *self._tensors())
+            self._lent |= {stream.cuda_stream}
+
+
 def _empty(shape, dtype, device, stream):
     """An uninitialised contiguous tensor that the launch stream may write at
     once, for use on the current stream later."""
@@ -90,7 +112,7 @@ def _beside(cache, batch):
         raise ValueError("the batch is on another device than the cache")
 
 
-class PagedKVCache:
+class PagedKVCache(_Lent):
     """A paged cache: k and v [pages, page_size, kv_heads, head_dim], fp16, bf16
     or float8_e4m3fn, channels contiguous, the other strides free but alike (a
     permuted view of [pages, kv_heads, page_size, head_dim] works).  k_scale,
@@ -151,6 +173,9 @@ class PagedKVCache:
         self._spaces = {}  # raw stream -> the workspace of its calls
         self._all = []     # every one so far: a graph may hold an outgrown one
         self._spaces[_current_stream(k.get_device())] = self._space(_lib.EXL3_ATTENTION_HEAD_BYTES)
+
+    def _tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
 
     def _space(self, n):
         if n == _lib.EXL3_ATTENTION_HEAD_BYTES:
@@ -226,7 +251,7 @@ class _Space:
         self.ws, self.ptr, self.bytes, self.graph, self.fits = ws, ws.data_ptr(), ws.numel(), False, None
 
 
-class PagedBatch:
+class PagedBatch(_Lent):
     """The sequences of one step.  Sequence b has the new tokens cu_q[b] ..
     cu_q[b+1]-1 and seq_lens[b] tokens in all, the new ones last, so new token
     i of n stands at position seq_lens[b] - n + i; position p is in place
@@ -252,6 +277,10 @@ class PagedBatch:
         d.cu_q, d.seq_lens = cu_q.data_ptr(), seq_lens.data_ptr()
         d.block_table = block_table.data_ptr()
         self._d, self._ref, self._at = d, ctypes.byref(d), ctypes.addressof(d)
+
+
+    def _tensors(self):
+        return self.cu_q, self.seq_lens, self.block_table
 
 
 def _strides(t):
@@ -340,6 +369,7 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
         k_out, p, ots, ohs = _out(k_out, k, T, Hk, dim, "k_out", stream)
         hk = _HEADS.pack(k.data_ptr(), p, _weight(k_weight, "k_weight", dtype, dim), Hk, ts, hs, ots,
                          ohs)
+    _lend(stream, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
     check(_lib.lib().exl3_qk_norm_rope(hq, hk, _ACT[dtype], T, dim, _positions(positions, T),
                                        _rope(inv_freq, interleaved), eps, _stream(stream, q)),
           "exl3_qk_norm_rope")
@@ -358,6 +388,8 @@ def kv_append(cache: PagedKVCache, batch: PagedBatch, k, v, inv_freq=None, k_wei
     if not k.is_cuda:
         _cuda(k, "k", _ACT)
     _beside(cache, batch)
+    cache._lend(stream)
+    batch._lend(stream)
     raw = _stream(stream, k)
     w = cache._spaces.get(raw) or cache._room(stream, raw, None)
     return _lib.native().kv_append(cache._at, cache._scales_at, batch._at, k, v, inv_freq, k_weight, q,
@@ -383,6 +415,8 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
     if not q.is_cuda:
         _cuda(q, "q", _ACT)
     _beside(cache, batch)
+    cache._lend(stream)
+    batch._lend(stream)
     dim = cache.head_dim
     if ws is None:
         raw = _stream(stream, q)
@@ -394,6 +428,7 @@ def paged_attention(q, cache: PagedKVCache, batch: PagedBatch, scale=None, causa
     else:
         _dense(ws, "ws", torch.uint8, ws.shape)
         _one_device(cache=cache.k, ws=ws)
+        _lend(stream, ws)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     return _lib.native().paged_attention(cache._at, cache._scales_at, batch._at, q,
                                          dim ** -0.5 if scale is None else scale, causal, window, out,

@@ -26,6 +26,9 @@ struct Raised {};
 
 // The device of a call: its cache's or pool's, else its first tensor's (-1: none yet).
 thread_local int t_device;
+// The tensors that a call was given.
+thread_local std::array<const at::Tensor*, 16> t_given;
+thread_local size_t t_count;
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) raise(PyExc_TypeError, "%s must be a tensor", name);
@@ -34,6 +37,7 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   if (t_device < 0) t_device = t.get_device();
   if (t.get_device() != t_device)
     raise(PyExc_ValueError, "%s is on another device than the rest of the call", name);
+  t_given[t_count++] = &t;
   return t;
 }
 // A contiguous vector of n values (n < 0: any number).
@@ -64,7 +68,8 @@ T* address(PyObject* o) {
 }
 
 // The stream of a call: stream= (an object with a cuda_stream) or the device's
-// current one.  Outputs are made on it, and are for use on the current one later.
+// current one.  Outputs are made on it, and are for use on the current one later;
+// what the call was given stays its own until the stream is done with it.
 // The tensors' device is the current one as long as it lives: a raw default stream
 // is the current device's, whichever that is.
 struct Stream {
@@ -75,6 +80,8 @@ struct Stream {
       : current(c10::cuda::getCurrentCUDAStream(t.get_device())), launch(current), other(false) {
     if (c10::cuda::current_device() != t.get_device()) device.set_index(t.get_device());
     if (given == Py_None) return;
+    const auto tensors = t_given;  // (what Python runs below may make calls of its own)
+    const size_t count = t_count;
     PyObject* raw = PyObject_GetAttrString(given, "cuda_stream");
     if (!raw) throw Raised{};
     const auto s = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(raw));
@@ -82,6 +89,8 @@ struct Stream {
     if (PyErr_Occurred()) throw Raised{};
     launch = c10::cuda::getStreamFromExternal(s, t.get_device());
     other = s != current.stream();
+    if (other)
+      for (size_t i = 0; i < count; i++) tensors[i]->record_stream(launch);
   }
   // Tensors of 32-bit words (the first of 64-bit ones where asked) side by side in
   // one allocation: each one's own costs as much as the rest of a small call.
@@ -419,6 +428,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   t_device = -1;
+  t_count = 0;
   try {
     return F(args);
   } catch (const Raised&) {

@@ -9,7 +9,8 @@
 
 Nothing of it is read on the host, so a whole step can be captured in a CUDA
 graph.  Every call is one or two kernels on the current stream (or on stream=,
-which the inputs must then be ready on).
+which the inputs must then be ready on, and which keeps their memory until it
+is done).
 """
 from __future__ import annotations
 
@@ -19,7 +20,7 @@ import torch
 
 from . import _lib
 from .api import device_status
-from .attention import PagedBatch, _capturing
+from .attention import PagedBatch, _capturing, _Lent
 
 
 class PagedStep(PagedBatch):
@@ -34,7 +35,7 @@ class PagedStep(PagedBatch):
         self._at = self._ref = batch  # exl3_kv_batch, its bytes
 
 
-class PagePool:
+class PagePool(_Lent):
     """The pages of a cache and the sequences that hold them, on the GPU: `table`
     [max_seqs, max_pages], `lens` [max_seqs], `free` [num_pages] and `count` [1],
     int32.  A sequence is a row of the table; free[0 .. count - 1] are the free
@@ -72,12 +73,16 @@ class PagePool:
             torch.cuda.current_stream(device).synchronize()
         self._native = _lib.native()
 
+    def _tensors(self):
+        return self.table, self.lens, self.free, self.count, self.ws
+
     def extend(self, seqs, q_lens, max_q: int, max_tokens: int, stream=None) -> PagedStep:
         """Begins a step: row seqs[i] of the pool gets q_lens[i] new tokens and the
         pages for them (int32 [sequences]).  max_tokens: rows of the step's token
         tensors, at least the sum of q_lens; max_q: as PagedBatch's.  A sequence
         for which there are no pages left keeps its rows, but has length 0 in the
         step and stays as it was in the pool."""
+        self._lend(stream)
         return PagedStep(self._device, max_q, *self._native.pages_extend(
             self._at, self._ws, self._ws_bytes, seqs, q_lens, max_tokens, max_q, stream, self._device))
 
@@ -87,6 +92,7 @@ class PagePool:
         seqs that these tokens are of (extend's); rows that it did not serve got
         none, and are left alone.  Without it a drop of tokens that never came
         takes older ones."""
+        self._lend(stream)
         self._native.pages_trim(self._at, self._ws, self._ws_bytes, seqs, drop, stream, self._device,
                                 None if step is None else step.seq_lens)
 
