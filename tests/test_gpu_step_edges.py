@@ -1,5 +1,6 @@
 """What a speculative step does where its calls meet: sequences without pages,
 bounds that make no sense, odd probabilities, tensors that are freed or saved."""
+import io
 import math
 
 import pytest
@@ -212,3 +213,64 @@ def test_acceptance_holds_probabilities_to_0_and_1(dtype, u):
     t, accepted, _ = verify_drafts(p.cuda(), draft.cuda(), ints(list(range(n + 1))),
                                    torch.full((n,), u, device="cuda"), torch.full((n,), 0.5, device="cuda"))
     assert accepted.tolist() == [int(u < held(a)) for a, _ in pairs]
+
+
+# ------------------------------------------------------------ a step's tensors afterwards
+def test_a_step_can_be_saved():
+    """All of a step's and of a verification's tensors, together and one by one."""
+    pool = PagePool(500, 16, 64, 40)
+    step = pool.extend(ints(list(range(0, 64, 2))), ints([3] * 32), 3, 100)
+    p, u = torch.full((5, 9), 1 / 9, device="cuda"), torch.full((3,), 0.5, device="cuda")
+    got = verify_drafts(p, ints([1, 2, 3]), ints([0, 1, 3]), u, u[:2])
+    of = {n: getattr(step, n) for n in ("cu_q", "seq_lens", "block_table", "positions", "slots")}
+    of |= dict(zip(("tokens", "accepted", "dropped"), got))
+    for what in [of] + [{n: t} for n, t in of.items()]:
+        f = io.BytesIO()
+        torch.save(what, f)
+        f.seek(0)
+        back = torch.load(f)
+        assert all(torch.equal(back[n], t) and back[n].dtype == t.dtype for n, t in what.items())
+        if "block_table" not in what:
+            assert len(f.getvalue()) < 4000     # (the table is 5120 bytes)
+
+
+def test_what_is_kept_of_a_step_does_not_keep_its_table():
+    pool = PagePool(100, 16, 64, 60000)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    step = pool.extend(ints(list(range(64))), ints([1] * 64), 1, 64)
+    assert torch.cuda.memory_allocated() - before > 64 * 60000 * 4
+    kept = step.cu_q, step.seq_lens, step.positions, step.slots
+    del step
+    assert torch.cuda.memory_allocated() - before < 100000
+    assert kept[0].tolist() == list(range(65)) and kept[1].tolist() == [1] * 64
+
+
+def test_outputs_are_ordinary_tensors():
+    """Also made inside torch.inference_mode, of no elements, and on another stream."""
+    pool = PagePool(9, 16, 4, 3)
+    side = torch.cuda.Stream()
+    seqs, q = ints([0, 1]), ints([2, 1])
+    torch.cuda.synchronize()
+    step = pool.extend(seqs, q, 2, 3)
+    t = step.block_table
+    assert t.device == pool.table.device and t.is_contiguous() and not t.requires_grad and t._version == 0
+    assert torch.equal(t + 0, t) and t.stride() == (3, 1) and step.slots.dtype == torch.int64
+    t += 1                                    # (versions count, memory can be resized)
+    assert t._version == 1
+    t.resize_(7, 3)
+    f = torch.zeros(3, device="cuda", requires_grad=True)
+    (f * step.positions).sum().backward()
+    assert f.grad.tolist() == [0.0, 1.0, 0.0]
+    with torch.inference_mode():
+        step = pool.extend(seqs, q, 2, 0)
+        assert step.slots.is_inference() and step.slots.shape == step.positions.shape == (0,)
+    with pytest.raises(RuntimeError, match="[Ii]nference"):
+        step.slots.requires_grad_(False).add_(1)
+    pool.clear_status()
+    step = pool.extend(seqs, q, 2, 3, stream=side)
+    torch.cuda.synchronize()
+    assert step.cu_q.tolist() == [0, 2, 3] and step.block_table.cpu()[:, 0].min() >= 0
+    n = torch.cuda.memory_allocated()
+    del step, t
+    assert torch.cuda.memory_allocated() < n

@@ -4,8 +4,9 @@
 // because through ctypes and torch's Python side a call's own cost was two to three
 // times its kernel's (verification 16 us around 5, a step of the pool 23 around 10,
 // the append of 64 tokens 15 around 4).
-#include <ATen/ops/empty.h>
+#include <ATen/core/Tensor.h>
 #include <array>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -92,35 +93,51 @@ struct Stream {
     if (other)
       for (size_t i = 0; i < count; i++) tensors[i]->record_stream(launch);
   }
-  // Tensors of 32-bit words (the first of 64-bit ones where asked) side by side in
-  // one allocation: each one's own costs as much as the rest of a small call.
+  // Small int32 tensors side by side in one allocation: each one's own costs as much
+  // as the rest of a small call.  (Of one type: torch saves no two that share memory
+  // as different ones.  Small: what is kept of them keeps all.)
   template <int N>
-  std::array<at::Tensor, N> words(const at::IntArrayRef (&shapes)[N], bool first64 = false) const {
+  std::array<at::Tensor, N> words(const at::IntArrayRef (&shapes)[N]) const {
     int64_t at[N], n = 0;
     for (int i = 0; i < N; i++) {
       at[i] = n;
       int64_t size = 1;
       for (const int64_t d : shapes[i]) size *= d;
-      n += ((first64 && i == 0 ? 2 * size : size) + 3) & ~(int64_t)3;  // 16 bytes aligned
+      n += (size + 3) & ~(int64_t)3;  // 16 bytes aligned
     }
-    const at::Tensor all = empty({n}, at::kInt);
+    const c10::Storage all = memory(4 * n);
     std::array<at::Tensor, N> r;
     for (int i = 0; i < N; i++) {
-      const bool wide = first64 && i == 0;
-      r[i] = at::detail::make_tensor<c10::TensorImpl>(
-          c10::Storage(all.storage()), all.key_set(),
-          caffe2::TypeMeta::fromScalarType(wide ? at::kLong : at::kInt));
-      r[i].unsafeGetTensorImpl()->set_sizes_contiguous(shapes[i]);
-      r[i].unsafeGetTensorImpl()->set_storage_offset(wide ? at[i] / 2 : at[i]);
+      r[i] = view(all, shapes[i], at::kInt);
+      r[i].unsafeGetTensorImpl()->set_storage_offset(at[i]);
     }
     return r;
   }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    const auto options = at::TensorOptions().dtype(type).device(launch.device());
-    if (!other) return at::empty(shape, options);
+    int64_t size = (int64_t)c10::elementSize(type);
+    for (const int64_t d : shape) size *= d;
+    return view(memory(size), shape, type);
+  }
+
+ private:
+  // From torch's allocator as it is: at::empty takes as long again on the way to it.
+  c10::Storage memory(int64_t bytes) const {
+    c10::Allocator* const from = c10::cuda::CUDACachingAllocator::get();
+    const auto make = [&] {
+      return c10::Storage(c10::Storage::use_byte_size_t(), (size_t)bytes, from->allocate((size_t)bytes),
+                          from, /*resizable=*/true);
+    };
+    if (!other) return make();
     c10::cuda::CUDAStreamGuard guard(launch);
-    at::Tensor t = at::empty(shape, options);
-    t.record_stream(current);
+    c10::Storage s = make();
+    c10::cuda::CUDACachingAllocator::recordStream(s.data_ptr(), current);
+    return s;
+  }
+  static at::Tensor view(const c10::Storage& of, at::IntArrayRef shape, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(of), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+        caffe2::TypeMeta::fromScalarType(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
     return t;
   }
 };
@@ -230,8 +247,9 @@ PyObject* pages_extend(PyObject* const* a) {
   const Stream st(a[7], seqs);
   at::Tensor slots, pos, cu, lens, table;
   const exl3_status s = unlocked([&] {
-    std::tie(slots, pos, cu, lens, table) = std::tuple_cat(
-        st.words<5>({{tokens}, {tokens}, {n + 1}, {n}, {n, pool->max_pages}}, true));
+    std::tie(pos, cu, lens) = std::tuple_cat(st.words<3>({{tokens}, {n + 1}, {n}}));
+    table = st.empty({n, pool->max_pages}, at::kInt);
+    slots = st.empty({tokens}, at::kLong);
     return exl3_pages_extend(pool, (int)n, static_cast<const int32_t*>(seqs.data_ptr()),
                              static_cast<const int32_t*>(q.data_ptr()), (int)tokens,
                              static_cast<int32_t*>(cu.data_ptr()),

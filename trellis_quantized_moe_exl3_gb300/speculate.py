@@ -26,7 +26,9 @@ from .attention import PagedBatch, _capturing, _Lent
 class PagedStep(PagedBatch):
     """A step as PagePool.extend lays it out: a PagedBatch (cu_q, seq_lens,
     block_table) with positions [max_tokens] int32 and slots [max_tokens] int64
-    (page * page_size + place) of its new tokens, -1 in rows that are none's."""
+    (page * page_size + place) of its new tokens, -1 in rows that are none's.
+    cu_q, seq_lens and positions share an allocation: one that is kept, or saved,
+    keeps the others (clone it)."""
 
     def __init__(self, device, max_q, cu_q, seq_lens, block_table, positions, slots, batch):
         self.cu_q, self.seq_lens, self.block_table = cu_q, seq_lens, block_table
@@ -127,6 +129,7 @@ def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None, s
     Returns int32 (tokens [drafts + sequences], accepted [sequences], dropped
     [sequences]): from place cu_draft[b] + b on, the accepted drafts, the drawn
     token, then -1; accepted drafts, and the others (what PagePool.trim takes).
+    They share an allocation: one that is kept, or saved, keeps the others.
 
     step: the step (PagePool.extend's) that p was computed for.  A sequence that
     it did not serve, for want of pages, has seen nothing: it gets tokens -1, and
