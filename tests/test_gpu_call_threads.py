@@ -141,3 +141,54 @@ def test_tensors_freed_after_a_call_on_another_stream(name):
     torch.cuda.synchronize()
     assert not taken
     del out
+
+
+class _Elsewhere:
+    """A tensor that says it is on the next device."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.t.get_device() + 1
+
+
+@pytest.mark.parametrize("which", ["k", "positions", "inv_freq", "q_weight", "k_weight", "q_out", "k_out"])
+def test_norm_refuses_tensors_of_another_device(which):
+    """Before anything is launched (there may be one device only)."""
+    from trellis_quantized_moe_exl3_gb300 import _lib, qk_norm_rope
+    x = torch.randn(4, 2, 64, device="cuda").to(BF)
+    a = dict(q=x, k=x.clone(), positions=torch.arange(4, dtype=torch.int32, device="cuda"),
+             inv_freq=torch.ones(32, dtype=torch.float64, device="cuda"),
+             q_weight=torch.ones(64, device="cuda").to(BF), k_weight=torch.ones(64, device="cuda").to(BF),
+             q_out=torch.empty_like(x), k_out=torch.empty_like(x))
+    want = [t.clone() for t in qk_norm_rope(**a)]
+    n = _lib.lib().exl3_launch_count()
+    with pytest.raises(ValueError, match="another device"):
+        qk_norm_rope(**{**a, which: _Elsewhere(a[which])})
+    assert _lib.lib().exl3_launch_count() == n
+    assert all(torch.equal(g, w) for g, w in zip(qk_norm_rope(**a), want))
+
+
+def test_norm_makes_its_tensors_device_current(monkeypatch):
+    """Where another device is current, the launch is inside a guard of the tensors'."""
+    from trellis_quantized_moe_exl3_gb300 import attention, qk_norm_rope
+    x = torch.randn(4, 2, 64, device="cuda").to(BF)
+    w = torch.ones(64, device="cuda").to(BF)
+    want = qk_norm_rope(x, None, q_weight=w)[0]
+    entered = []
+    real = torch.cuda.device
+
+    class Guard(real):
+        def __enter__(self):
+            entered.append(self.idx)
+            return super().__enter__()
+
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    assert torch.equal(qk_norm_rope(x, None, q_weight=w)[0], want) and not entered
+    monkeypatch.setattr(attention, "_current_device", lambda: x.get_device() + 1)
+    assert torch.equal(qk_norm_rope(x, None, q_weight=w)[0], want)
+    assert entered == [x.get_device()]

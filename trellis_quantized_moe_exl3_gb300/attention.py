@@ -36,6 +36,7 @@ _ROPE = struct.Struct("@Qii")
 assert _HEADS.size == ctypes.sizeof(_lib.Heads) and _ROPE.size == ctypes.sizeof(_lib.Rope)
 _current_stream = torch._C._cuda_getCurrentRawStream
 _capturing = torch._C._cuda_isCurrentStreamCapturing
+_current_device = torch._C._cuda_getDevice
 
 
 def _stream(stream, t):
@@ -369,10 +370,18 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
         k_out, p, ots, ohs = _out(k_out, k, T, Hk, dim, "k_out", stream)
         hk = _HEADS.pack(k.data_ptr(), p, _weight(k_weight, "k_weight", dtype, dim), Hk, ts, hs, ots,
                          ohs)
-    _lend(stream, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
-    check(_lib.lib().exl3_qk_norm_rope(hq, hk, _ACT[dtype], T, dim, _positions(positions, T),
-                                       _rope(inv_freq, interleaved), eps, _stream(stream, q)),
-          "exl3_qk_norm_rope")
+    device = q.get_device()
+    used = (q_out, positions, inv_freq, q_weight) + (() if k is None else (k, k_out, k_weight))
+    for t in used:
+        if t is not None and t.get_device() != device:
+            raise ValueError("a tensor is on another device than q")
+    if stream is not None:
+        _lend(stream, q, *used)
+    # (a raw default stream is the current device's, whichever that is)
+    with contextlib.nullcontext() if device == _current_device() else torch.cuda.device(device):
+        check(_lib.lib().exl3_qk_norm_rope(hq, hk, _ACT[dtype], T, dim, _positions(positions, T),
+                                           _rope(inv_freq, interleaved), eps, _stream(stream, q)),
+              "exl3_qk_norm_rope")
     return q_out, k_out
 
 
