@@ -1066,17 +1066,12 @@ cudaError_t launch_cfg(const AttnParams& p, cudaStream_t st) {
   static_assert(C::RT * C::kGrid * 4 <= C::kRing, "join weights");
   static_assert(C::kCtasPerSm * (C::kSmem + 1200) <= 227 * 1024, "resident CTAs");
   static_assert(C::kGrid <= kRowsCounters, "counters");
-  static bool init = false;
-  if (!init) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_rows_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    init = true;
-  }
-  const cudaError_t err =
-      launch_pdl(attn_rows_kernel<C>, dim3(C::kGrid), dim3(kThreads), C::kSmem, st, p);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(attn_rows_kernel<C>, C::kSmem, &done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_rows_kernel<C>, dim3(C::kGrid), dim3(kThreads), C::kSmem, st, p);
   note_launches(1);
-  return err;
+  return e;
 }
 
 template <int D, int NB>

@@ -1775,14 +1775,10 @@ template <class C>
 cudaError_t launch_cfg(const AttnParams& p, const Maps& maps, const Plan& pl, int max_unit,
                        cudaStream_t st) {
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
-  static bool init = false;
-  if (!init) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_tiles_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    init = true;
-  }
-  cudaError_t e = launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, pl, max_unit);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(attn_tiles_kernel<C>, C::kSmem, &done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, pl, max_unit);
   note_launches(1);
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_tiles_kernel<C>, dim3(kGrid), dim3(C::kThreads), C::kSmem, st, maps, p, pl);
