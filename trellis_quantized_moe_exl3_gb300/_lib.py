@@ -10,7 +10,7 @@ import ctypes
 import os
 import re
 
-from .build import LIB_PATH, NATIVE_PATH
+from .build import LIB_PATH, NATIVE_PATH, built_stamp, native_stamp
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                       "exl3.h")
@@ -192,6 +192,9 @@ def native():
         if not os.path.exists(NATIVE_PATH):
             raise ImportError(f"{NATIVE_PATH} is missing: build it with "
                               "trellis_quantized_moe_exl3_gb300.build.build()")
+        if built_stamp() != native_stamp():
+            raise ImportError(f"{NATIVE_PATH} was built against {built_stamp()}, this is {native_stamp()}: "
+                              "build it again with trellis_quantized_moe_exl3_gb300.build.build()")
         import importlib.util
         spec = importlib.util.spec_from_file_location(__package__ + "._native", NATIVE_PATH)
         _native = importlib.util.module_from_spec(spec)

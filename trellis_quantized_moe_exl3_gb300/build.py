@@ -1,6 +1,6 @@
 """Build the CUDA library libexl3_gb300.so in-tree with nvcc (sm_103a only), and
 _native.so, the Python calls of its smallest operators, with g++ against the
-installed torch.
+installed torch and Python (and again when these are others).
 
 Every translation unit compiles in parallel; the link uses the static CUDA
 runtime so the library has no runtime search-path dependency.
@@ -12,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -40,6 +41,27 @@ def _stale(obj: str, src: str, headers) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(f) > t for f in [src] + headers)
+
+
+def native_stamp() -> str:
+    """What _native.so is built against (torch's C++ side and Python's have no
+    stable ABI): written beside it, and compared before it is loaded."""
+    import torch
+    return (f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"Python {'.'.join(map(str, sys.version_info[:3]))} {sysconfig.get_config_var('SOABI')}")
+
+
+def _stamp_path() -> str:
+    return os.path.splitext(NATIVE_PATH)[0] + ".stamp"
+
+
+def built_stamp():
+    """native_stamp() of the built _native.so, None where there is none."""
+    try:
+        with open(_stamp_path()) as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
 
 
 def _native_commands(tmp: str):
@@ -77,7 +99,8 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed: {' '.join(cmd)}\n{r.stdout}\n"
+                               f"{r.stderr}")
         return r.stdout + r.stderr
 
     def compile_one(job):
@@ -88,7 +111,9 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
 
     binding = os.path.join(CSRC, "binding.cpp")
     native = native_obj = None
-    if force or jobs or _stale(NATIVE_PATH, binding, headers) or not os.path.exists(LIB_PATH):
+    stamp = native_stamp()
+    if force or jobs or _stale(NATIVE_PATH, binding, headers) or not os.path.exists(LIB_PATH) or \
+            built_stamp() != stamp:
         native = NATIVE_PATH + f".tmp{os.getpid()}"
         native_obj, compile_cmd, link_cmd = _native_commands(native)
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
@@ -96,16 +121,21 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> str:
         for out in ex.map(compile_one, jobs):
             if verbose and out.strip():
                 print(out)
+        # (the library, which C programs use, needs nothing of the binding)
+        if force or jobs or not os.path.exists(LIB_PATH):
+            tmp = LIB_PATH + f".tmp{os.getpid()}"
+            run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"])
+            os.replace(tmp, LIB_PATH)
         if also:
             also.result()
-    if force or jobs or not os.path.exists(LIB_PATH):
-        tmp = LIB_PATH + f".tmp{os.getpid()}"
-        run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"])
-        os.replace(tmp, LIB_PATH)
     if native:
         run(link_cmd)
         os.remove(native_obj)
         os.replace(native, NATIVE_PATH)
+        tmp = _stamp_path() + f".tmp{os.getpid()}"
+        with open(tmp, "w") as f:
+            f.write(stamp)
+        os.replace(tmp, _stamp_path())
     return LIB_PATH
 
 
