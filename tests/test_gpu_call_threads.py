@@ -192,3 +192,27 @@ def test_norm_makes_its_tensors_device_current(monkeypatch):
     monkeypatch.setattr(attention, "_current_device", lambda: x.get_device() + 1)
     assert torch.equal(qk_norm_rope(x, None, q_weight=w)[0], want)
     assert entered == [x.get_device()]
+
+
+class _NoTruth:
+    def __bool__(self):
+        raise KeyError("neither true nor false")
+
+
+def test_errors_of_arguments_come_through():
+    """What an argument raises when it is looked at is what the caller sees."""
+    cache = PagedKVCache(*[torch.zeros(2, 16, 1, 64, dtype=BF, device="cuda") for _ in range(2)])
+    batch = PagedBatch(ints([0, 1]), ints([5]), ints([[0, 1]]), 1)
+    x = torch.randn(1, 1, 64, device="cuda").to(BF)
+    f = torch.ones(32, dtype=torch.float64, device="cuda")
+    want = paged_attention(x, cache, batch)
+    for kw in (dict(causal=_NoTruth()), dict(return_lse=_NoTruth())):
+        with pytest.raises(KeyError):
+            paged_attention(x, cache, batch, **kw)
+    with pytest.raises(KeyError):
+        kv_append(cache, batch, x, x, inv_freq=f, interleaved=_NoTruth())
+    for kw in (dict(window="3"), dict(scale="1"), dict(path=None)):
+        with pytest.raises(TypeError):
+            paged_attention(x, cache, batch, **kw)
+    assert torch.equal(paged_attention(x, cache, batch, causal=5, window=0), want)
+    assert cache.status() == 0

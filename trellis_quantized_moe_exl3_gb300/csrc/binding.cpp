@@ -61,6 +61,11 @@ int64_t whole(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw Raised{};
   return v;
 }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v;
+}
 template <class T>
 T* address(PyObject* o) {
   void* p = PyLong_AsVoidPtr(o);
@@ -364,7 +369,7 @@ PyObject* kv_append(PyObject* const* a) {
     if (f.size(0) > INT32_MAX / 2) raise(PyExc_ValueError, "%s is too long", "inv_freq");
     rope.inv_freq = static_cast<const double*>(f.data_ptr());
     rope.rotary_dim = 2 * (int)f.size(0);
-    rope.interleaved = PyObject_IsTrue(a[12]);
+    rope.interleaved = truth(a[12]);
   }
   const int32_t* positions =
       a[10] == Py_None ? nullptr
@@ -406,7 +411,7 @@ PyObject* paged_attention(PyObject* const* a) {
   const double scale = PyFloat_AsDouble(a[4]);
   if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
   const int64_t window = whole(a[6]), path = whole(a[9]);
-  const bool with_lse = PyObject_IsTrue(a[8]);
+  const bool with_lse = truth(a[8]);
   if (window < INT32_MIN || window > INT32_MAX || path < INT32_MIN || path > INT32_MAX)
     raise(PyExc_ValueError, "%s out of range", "window or path");
   at::Tensor out, lse;
@@ -418,7 +423,7 @@ PyObject* paged_attention(PyObject* const* a) {
   }
   void* const ws = address<void>(a[10]);
   const size_t bytes = (size_t)whole(a[11]);
-  const int causal = PyObject_IsTrue(a[5]);
+  const int causal = truth(a[5]);
   const exl3_kv_batch* const batch = batch_of(a[2]);
   const Stream st(a[12], q);
   const exl3_status s = unlocked([&] {
