@@ -287,35 +287,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyParams p
   const int b = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;
   pdl_wait();
   const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
-  // the drafts that belong to sequences (a bound out of range says nothing)
+  // the drafts that belong to sequences, and whether the step served this one (asked
+  // for now, looked at once the drafts have been decided on: 0.1 us less than at once)
   int lo = __ldg(p.cu), hi = __ldg(p.cu + p.num_seqs);
-  if (lo < 0 || lo > p.drafts) lo = 0;
-  if (hi < 0 || hi > p.drafts) hi = p.drafts;
-  const bool good = c0 >= lo && c1 >= c0 && c1 <= hi;
-  auto none = [&](int64_t from, int64_t to) {  // places of no token
-    for (int64_t j = from + threadIdx.x; j < to; j += kThreads) p.tokens[j] = -1;
-  };
-  if (rank == 0) {
-    if (b == 0) none(0, lo);
-    if (b == p.num_seqs - 1) none((int64_t)hi + p.num_seqs, (int64_t)p.drafts + p.num_seqs);
-  }
-  // Left out: bounds that do not ascend, or a sequence that the step did not
-  // serve, whose rows of p are those of no token: nothing is drawn, nothing came
-  // that could be dropped.  (The bounds, held to lo .. hi, lead from the first
-  // place to the last in steps up and down, and every place lies in a step up: of
-  // a sequence that writes its own, or of one that is left out.)
-  if (!good || (p.step_lens && __ldg(p.step_lens + b) <= 0)) {
-    if (rank == 0) {
-      const int from = b == 0 ? lo : min(max(c0, lo), hi);
-      const int to = b == p.num_seqs - 1 ? hi : min(max(c1, lo), hi);
-      none((int64_t)from + b, (int64_t)to + b + 1);
-      if (threadIdx.x == 0) p.accepted[b] = p.dropped[b] = 0;
-    }
-    return;  // (the whole cluster: it waits for no one)
-  }
-  const int d = c1 - c0;
+  const int len = p.step_lens ? __ldg(p.step_lens + b) : 1;
+  const int d = c0 >= 0 && c1 >= c0 && c1 <= p.drafts ? c1 - c0 : 0;
   // ---- the first refusal (every CTA for itself)
   const bool few = d < 32;  // (the drafts then stay in the lanes of the first warp)
+  int mine = -1;
   if (warp == 0) {
     int a = d, x = 0;
     for (int j0 = 0; j0 < d; j0 += 32) {
@@ -340,8 +319,35 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_kernel(VerifyParams p
       }
     }
     if (lane == 0) s_accepted = a;
-    if (rank == 0 && few && lane <= d) p.tokens[c0 + b + lane] = lane < a ? x : -1;
+    mine = lane < a ? x : -1;
   }
+  // (a bound out of range says nothing)
+  if (lo < 0 || lo > p.drafts) lo = 0;
+  if (hi < 0 || hi > p.drafts) hi = p.drafts;
+  const bool good = c0 >= lo && c1 >= c0 && c1 <= hi && len > 0;
+  auto none = [&](int64_t from, int64_t to) {  // places of no token
+#pragma unroll 1
+    for (int64_t j = from + threadIdx.x; j < to; j += kThreads) p.tokens[j] = -1;
+  };
+  if (rank == 1) {  // (the first CTA has the tokens to write)
+    if (b == 0) none(0, lo);
+    if (b == p.num_seqs - 1) none((int64_t)hi + p.num_seqs, (int64_t)p.drafts + p.num_seqs);
+  }
+  // Left out: bounds that do not ascend, or a sequence that the step did not
+  // serve, whose rows of p are those of no token: nothing is drawn, nothing came
+  // that could be dropped.  (The bounds, held to lo .. hi, lead from the first
+  // place to the last in steps up and down, and every place lies in a step up: of
+  // a sequence that writes its own, or of one that is left out.)
+  if (!good) {
+    if (rank == 0) {
+      const int from = b == 0 ? lo : min(max(c0, lo), hi);
+      const int to = b == p.num_seqs - 1 ? hi : min(max(c1, lo), hi);
+      none((int64_t)from + b, (int64_t)to + b + 1);
+      if (threadIdx.x == 0) p.accepted[b] = p.dropped[b] = 0;
+    }
+    return;  // (the whole cluster: it waits for no one)
+  }
+  if (rank == 0 && warp == 0 && few && lane <= d) p.tokens[c0 + b + lane] = mine;
   __syncthreads();
   const int a = s_accepted;
   if (rank == 0) {
