@@ -274,3 +274,16 @@ def test_outputs_are_ordinary_tensors():
     n = torch.cuda.memory_allocated()
     del step, t
     assert torch.cuda.memory_allocated() < n
+
+
+def test_pages_of_a_pool_whose_count_is_the_largest():
+    """A count of 2^31 - 1 and the like is held to the pool's pages."""
+    for count in ((1 << 31) - 1, -(1 << 31), 7):
+        pool = PagePool(6, 16, 3, 4)
+        pool.count.fill_(count)
+        for _ in range(3):
+            step = pool.extend(ints([0, 1, 2]), ints([30, 1, 0]), 30, 31)
+            assert step.seq_lens.tolist() in ([30, 1, 0], [0, 0, 0])
+            pool.trim(ints([2, 1, 0]), ints([5, 70, 1]))
+            pool.trim(ints([0, 1, 2]))
+            assert 0 <= int(pool.count) <= 6 and pool.lens.tolist() == [0, 0, 0]
