@@ -287,3 +287,20 @@ def test_pages_of_a_pool_whose_count_is_the_largest():
             pool.trim(ints([2, 1, 0]), ints([5, 70, 1]))
             pool.trim(ints([0, 1, 2]))
             assert 0 <= int(pool.count) <= 6 and pool.lens.tolist() == [0, 0, 0]
+
+
+def test_a_step_of_another_pools_pages_is_refused():
+    """A pool whose pages have another size than the cache's, or of which the cache has
+    fewer, would put tokens into the wrong places, or nowhere."""
+    x = torch.randn(5, 1, 64, device="cuda").to(BF)
+    cache = PagedKVCache(*[torch.zeros(9, 32, 1, 64, dtype=BF, device="cuda") for _ in range(2)])
+    for pool in (PagePool(9, 16, 2, 4), PagePool(9, 64, 2, 4), PagePool(10, 32, 2, 4)):
+        step = pool.extend(ints([0, 1]), ints([2, 3]), 3, 5)
+        with pytest.raises(ValueError, match="pages of another size"):
+            kv_append(cache, step, x, x)
+        with pytest.raises(ValueError, match="pages of another size"):
+            paged_attention(x, cache, step)
+    for pages in (9, 5):
+        step = PagePool(pages, 32, 2, 4).extend(ints([0, 1]), ints([2, 3]), 3, 5)
+        kv_append(cache, step, x, x)
+        assert bool((paged_attention(x, cache, step) != 0).all()) and cache.status() == 0

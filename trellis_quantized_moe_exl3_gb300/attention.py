@@ -111,6 +111,9 @@ def _one_device(**tensors):
 def _beside(cache, batch):
     if batch._device != cache._device:
         raise ValueError("the batch is on another device than the cache")
+    size, pages = batch._pages
+    if size is not None and (size != cache.page_size or pages > cache.num_pages):
+        raise ValueError("the step's pool has pages of another size, or more of them, than the cache")
 
 
 class PagedKVCache(_Lent):
@@ -160,6 +163,7 @@ class PagedKVCache(_Lent):
         self.kv_heads, self.head_dim, self.dtype = k.shape[2], k.shape[3], k.dtype
         d = _lib.KVCache()
         d.k, d.v, d.dtype = k.data_ptr(), v.data_ptr(), _CODES[k.dtype]
+        self.num_pages, self.page_size = k.shape[:2]
         d.num_pages, d.page_size, d.kv_heads, d.head_dim = k.shape
         d.page_stride, d.token_stride, d.head_stride = _strides(k)
         self._scales, self._scales_at = None, 0  # exl3_kv_scales, where there are block scales
@@ -260,6 +264,7 @@ class PagedBatch(_Lent):
     [B + 1], [B], [B, max_pages]; their values may change between calls (they
     are read on the device).  max_q: the most new tokens of a sequence, a hint
     that picks the kernel."""
+    _pages = None, 0  # a step's: the page size and the pages of its pool
 
     def __init__(self, cu_q, seq_lens, block_table, max_q: int):
         n = seq_lens.shape[0]

@@ -30,10 +30,10 @@ class PagedStep(PagedBatch):
     cu_q, seq_lens and positions share an allocation: one that is kept, or saved,
     keeps the others (clone it)."""
 
-    def __init__(self, device, max_q, cu_q, seq_lens, block_table, positions, slots, batch):
+    def __init__(self, device, pages, max_q, cu_q, seq_lens, block_table, positions, slots, batch):
         self.cu_q, self.seq_lens, self.block_table = cu_q, seq_lens, block_table
         self.positions, self.slots = positions, slots
-        self.num_seqs, self.max_q, self._device = len(seq_lens), max_q, device
+        self.num_seqs, self.max_q, self._device, self._pages = len(seq_lens), max_q, device, pages
         self._at = self._ref = batch  # exl3_kv_batch, its bytes
 
 
@@ -85,7 +85,7 @@ class PagePool(_Lent):
         for which there are no pages left keeps its rows, but has length 0 in the
         step and stays as it was in the pool."""
         self._lend(stream)
-        return PagedStep(self._device, max_q, *self._native.pages_extend(
+        return PagedStep(self._device, (self.page_size, self.num_pages), max_q, *self._native.pages_extend(
             self._at, self._ws, self._ws_bytes, seqs, q_lens, max_tokens, max_q, stream, self._device))
 
     def trim(self, seqs, drop=None, stream=None, step=None):
