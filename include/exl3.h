@@ -545,8 +545,9 @@ size_t exl3_pages_workspace_size(int max_seqs, int num);
  * cu_q, seq_lens and block_table are what exl3_kv_batch takes.  Sequences are
  * served in order; one whose pages, with those of all before it, are more than
  * the free ones gets none, nor do later ones that need any.  A sequence that is
- * not served keeps its rows but has seq_lens 0 (nothing is appended, and its
- * tokens see nothing), and the pool's row stays as it was. */
+ * not served keeps its rows but has seq_lens 0 (nothing is appended, which the
+ * append's status reports as tokens before position 0, and its tokens see
+ * nothing), and the pool's row stays as it was. */
 exl3_status exl3_pages_extend(const exl3_page_pool *pool, int num, const int32_t *seqs,
                               const int32_t *q_lens, int max_tokens, int32_t *cu_q,
                               int32_t *seq_lens, int32_t *block_table, int32_t *positions,
@@ -578,7 +579,8 @@ exl3_status exl3_pages_trim_step(const exl3_page_pool *pool, int num, const int3
  *   the last draft from p: the first token whose cumulative weight is above
  *   sample_u times the total.
  * Both are decided exactly: probabilities are rounded to units of 2^-46 and
- * summed as whole numbers, so results do not depend on the order of sums.
+ * summed as whole numbers, so results do not depend on the order of sums (a
+ * token below 2^-47 is never drawn; bits of sample_u below 2^-64 do not count).
  *   p, q      device, rows of vocab probabilities in dt (fp16, bf16 or fp32),
  *             strides in elements.  NaN and what is negative count as 0, what
  *             is above 1 as 1; a row sums to less than 2^16
@@ -593,7 +595,9 @@ exl3_status exl3_pages_trim_step(const exl3_page_pool *pool, int num, const int3
  * A sequence whose cu_draft does not ascend within 0 .. drafts, or leaves
  * cu_draft[0] .. cu_draft[num_seqs] (as far as these are in that range), is left
  * out: accepted and dropped 0, tokens -1 (a place that such bounds give to two
- * sequences holds what either has there).  vocab at most 2^24.  Errors: EXL3_ERR_ARG (null or misaligned pointers, strides below vocab, bad enum), EXL3_ERR_SHAPE. */
+ * sequences holds what either has there).  vocab at most 2^24.  Errors:
+ * EXL3_ERR_ARG (null or misaligned pointers, strides below vocab, bad enum),
+ * EXL3_ERR_SHAPE. */
 exl3_status exl3_verify_drafts(const void *p, int64_t p_stride, const void *q, int64_t q_stride,
                                exl3_dtype dt, int vocab, int num_seqs, int drafts,
                                const int32_t *cu_draft, const int32_t *draft,

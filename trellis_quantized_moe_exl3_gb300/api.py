@@ -4,6 +4,9 @@
     out = layer.forward(x, logits, top_k=8)                # one MoE layer
     ids, w, seg_offsets, seg_pairs = route(logits, top_k)  # routing tables
     dense = layer.decode_dense(expert, proj)               # fp16 [in][out]
+
+With stream= a call runs there: what it is given, and its outputs, must be ready on
+that stream and live until it is done.
 """
 from __future__ import annotations
 

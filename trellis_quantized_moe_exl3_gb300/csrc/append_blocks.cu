@@ -26,7 +26,7 @@
 namespace exl3 {
 namespace {
 
-// three CTAs of 80 registers on an SM (7000 tokens 40.9 us; four of 64 44.6, two 47)
+// three CTAs of 80 registers on an SM (7000 tokens 40.5 us; four of 64 44.6, two 47)
 constexpr int kThreads = 256, kPerSm = 3;
 
 // the least 2^e >= top / 448, within the range of scales
@@ -94,9 +94,11 @@ struct Lane {
     unpack8<BF16>(w.b, v + 4);
   }
   // cosines and sines of its pairs 2 e, 2 e + 1 at a position.  The fraction of a
-  // turn is exact; the fast functions of it are off by 2^-21, a row's values by
-  // 1e-6 of its largest: nothing beside the rounding to 8 or 16 bits that follows
-  // (and a fifth of the instructions of the exact ones).
+  // turn is exact; the fast functions of it are off by 2^-21, a row's values, keys and
+  // queries alike, by 1e-6 of its largest (a cache with a scale per head has exact
+  // ones, 1e-7).  An 8-bit key cannot tell; a 16-bit query can where it is below a
+  // 500th of its row's largest in fp16, a 4000th in bf16, and no score, a sum over the
+  // row, can.  (A fifth of the instructions of the exact ones.)
   __device__ __forceinline__ void angles(const uint64_t* turns, int pos, int e, float2* c,
                                          float2* s) const {
     float x[2];
@@ -434,9 +436,9 @@ cudaError_t launch_hold(const NormRopeParams& p, cudaStream_t st) {
 
 template <int LPR>
 cudaError_t launch_lpr(const NormRopeParams& p, cudaStream_t st) {
-  // one row per lane group keeps a step of a few tokens short (64 of one token 3.8 us,
-  // with two 4.4), two keep a block of 64 tokens in registers (7000 tokens 40.9 us,
-  // with one, formed twice, 43.4)
+  // one row per lane group keeps a step of a few tokens short (64 of one token 3.6 us,
+  // with two 4.3), two keep a block of 64 tokens in registers (7000 tokens 40.5 us,
+  // with one, formed twice, 42.7)
   return p.batch.max_q <= 8 ? launch_hold<LPR, 1>(p, st) : launch_hold<LPR, 2>(p, st);
 }
 

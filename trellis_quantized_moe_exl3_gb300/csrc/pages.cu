@@ -20,8 +20,8 @@ namespace {
 
 constexpr int kThreads = 512, kCtas = 8;
 // Words a step writes up to which it is one launch: a step and its way back, us in
-// one / two launches of extend, 8 sequences of 128 pages 9.7 / 9.9, 256 of 2048
-// 18.4 / 12.2.
+// one / two launches of extend, 8 sequences of 128 pages 7.9 / 8.7, 64 of 256 8.7 /
+// 9.1, 128 of 512 (65536 words) 9.2 / 9.1, 256 of 2048 17.1 / 10.3.
 constexpr long long kFused = 65536;
 constexpr int kOwners = 8192;  // rows of a pool whose claims fit shared memory
 

@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kPerSm = 1024 / kThreads;
 // of a cluster, one cluster per sequence.  64 pairs of rows of 131072 fp32 (floor 10
-// us): 16.5 us; 16 CTAs of 128 threads as fast, 16 of 256 and 8 of 128 slower
+// us): 16.6 us; 16 CTAs of 128 threads as fast, 16 of 256 and 8 of 128 slower
 constexpr int kCtas = 8;
 constexpr int kGroups = 8;  // parts of a warp's run whose sums are kept (draw: four lanes each)
 constexpr int kUnroll = 4;  // 16-byte loads of p (and of q) in flight per thread

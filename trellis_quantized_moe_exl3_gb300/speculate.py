@@ -83,7 +83,8 @@ class PagePool(_Lent):
         pages for them (int32 [sequences]).  max_tokens: rows of the step's token
         tensors, at least the sum of q_lens; max_q: as PagedBatch's.  A sequence
         for which there are no pages left keeps its rows, but has length 0 in the
-        step and stays as it was in the pool."""
+        step and stays as it was in the pool (give the step to verify_drafts, or to
+        trim, so that it stays so; kv_append's status reports its tokens)."""
         self._lend(stream)
         return PagedStep(self._device, (self.page_size, self.num_pages), max_q, *self._native.pages_extend(
             self._at, self._ws, self._ws_bytes, seqs, q_lens, max_tokens, max_q, stream, self._device))
@@ -123,12 +124,17 @@ def verify_drafts(p, draft, cu_draft, accept_u, sample_u, q=None, stream=None, s
 
     Draft x is accepted, after all before it, if accept_u * q(x) < p(x).  After
     the first refusal a token is drawn from max(p - q, 0), after the last draft
-    from p: the first whose cumulative weight is above sample_u of the total
-    (both exactly, whatever the size of the vocabulary).
+    from p: the first whose cumulative weight is above sample_u of the total.
+    The first is decided exactly; weights are rounded to units of 2^-46 (a token
+    below 2^-47 is never drawn) and summed without a further rounding, whatever
+    the size of the vocabulary.  NaN and what is negative count as 0, what is
+    above 1 as 1; a row may sum to less than 2^16.  Where p - q leaves nothing, p
+    itself counts; a row of p without weight gives -1 for the token.
 
     Returns int32 (tokens [drafts + sequences], accepted [sequences], dropped
     [sequences]): from place cu_draft[b] + b on, the accepted drafts, the drawn
     token, then -1; accepted drafts, and the others (what PagePool.trim takes).
+    Places of no sequence hold -1, those of one whose cu_draft does not ascend too.
     They share an allocation: one that is kept, or saved, keeps the others.
 
     step: the step (PagePool.extend's) that p was computed for.  A sequence that
