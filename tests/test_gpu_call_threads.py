@@ -34,7 +34,7 @@ def calls():
 
 @pytest.mark.parametrize("name", ["extend", "trim", "append", "attention", "verify"])
 def test_other_threads_run_while_a_call_waits_for_the_queue(name):
-    """A call that waits for room among the launches under way (behind half a second of
+    """A call that waits for room among the launches under way (behind a second of
     work) leaves the interpreter to other threads."""
     call = calls()[name]
     call()
@@ -52,7 +52,7 @@ def test_other_threads_run_while_a_call_waits_for_the_queue(name):
     ticker = threading.Thread(target=tick)
     ticker.start()
     try:
-        torch.cuda._sleep(1_000_000_000)
+        torch.cuda._sleep(2_000_000_000)
         t0 = time.perf_counter()
         for _ in range(3000):
             call()
@@ -61,8 +61,8 @@ def test_other_threads_run_while_a_call_waits_for_the_queue(name):
         stop.set()
         ticker.join()
     torch.cuda.synchronize()
-    assert took > 0.2, "the queue never filled"
-    assert max(gaps) < 0.1, max(gaps)
+    assert took > 0.6, "the queue never filled"
+    assert max(gaps) < 0.3, max(gaps)
 
 
 def given(g):
@@ -130,7 +130,7 @@ def test_tensors_freed_after_a_call_on_another_stream(name):
     tensors = [x for x in t if isinstance(x, torch.Tensor)]
     at = {(x.untyped_storage().data_ptr()): x.untyped_storage().nbytes() for x in tensors}
     with torch.cuda.stream(side):
-        torch.cuda._sleep(400_000_000)        # 0.2 s before the call's turn
+        torch.cuda._sleep(1_000_000_000)      # half a second before the call's turn
     out = call(t, side)
     del t, tensors
     again = []
